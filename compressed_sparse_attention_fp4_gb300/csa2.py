@@ -23,6 +23,9 @@ MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
 MAX_QLEN = 4
 IDX_EARLY_INPUTS = 1
 KV_EARLY_INPUTS = 1
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_PARTS, ROPE_BASE = 0, 1, 2, 3
+DENSE_ALL_POSITIONS = 1
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED_SHAPE",
           3: "CSA2_ERR_WORKSPACE_TOO_SMALL", 4: "CSA2_ERR_CUDA",
@@ -42,6 +45,12 @@ class CDims(ctypes.Structure):
                 ("topk", ctypes.c_int32), ("heads", ctypes.c_int32), ("swa", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int64),
                 ("max_ctx", ctypes.c_int64)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_ctx", ctypes.c_double), ("turns_lo", ctypes.c_double), ("turns_hi", ctypes.c_double)]
 
 
 SIGNATURES = {
@@ -67,6 +76,12 @@ SIGNATURES = {
                                           _P, _P, _P, _P, _F, _P, _P, _P, _SZ, _P]),
     "csa2_sparse_attn_decode_noalloc": (_I32, [ctypes.POINTER(CDims), _I32, _I32, _P, _P, _P, _P,
                                                _P, _P, _P, _P, _P, _F, _P, _P, _P, _P]),
+    "csa2_rope_apply": (_I32, [ctypes.POINTER(CRope), _I32, _P, _P, _P, _I64, _I32, _I32, _I32, _I64, _I64, _I64,
+                               _I64, _I32, _P]),
+    "csa2_kv_append": (_I32, [ctypes.POINTER(CRope), _P, _I64, _I64, _P, _F, _P, _P, _P, _P, _P, _I64, _P, _P]),
+    "csa2_dense_attn_workspace_size": (_I32, [ctypes.POINTER(CDims), _I32, _I64, ctypes.POINTER(_SZ)]),
+    "csa2_dense_attn_chunk": (_I32, [ctypes.POINTER(CDims), _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _F, _I32, _I32,
+                                     _P, _P, _P, _SZ, _P]),
     "csa2_get_device_status": (_I32, [_P, _P, ctypes.POINTER(_I32)]),
     "csa2_profile_enable": (_I32, [_I32]),
     "csa2_profile_read": (_I32, [ctypes.POINTER(CKernelTime), _I32, ctypes.POINTER(_I32)]),
@@ -261,6 +276,133 @@ def csa2_sparse_attn_decode_noalloc(dims: Dims, batch: int, mode: int, q, kv_cod
         ctypes.byref(dims.c()), batch, mode, _ptr(q), _ptr(kv_codes), _ptr(kv_scales),
         _ptr(kv_rope), _ptr(page_table), _ptr(ctx_len), _ptr(topk), _ptr(swa_kv), _ptr(swa_len),
         float(scale), _ptr(out), _ptr(lse), _ptr(err_word), _stream(stream)))
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Python view of ``csa2_rope``: a rotary configuration (see include/csa2.h)."""
+    rot: int = ROPE
+    theta: float = 10000.0
+    layout: int = ROPE_INTERLEAVED
+    scaling: int = ROPE_PLAIN
+    factor: float = 1.0
+    orig_ctx: float = 0.0
+    turns_lo: float = 1.0
+    turns_hi: float = 32.0
+    mscale: float = 1.0
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", CRope(self.rot, self.layout, self.scaling, self.mscale, self.theta, self.factor,
+                                             self.orig_ctx, self.turns_lo, self.turns_hi))
+
+    def c(self) -> CRope:
+        return self._c
+
+
+def _need(fn: str, ok: bool):
+    """A tensor that the C call cannot check (type, shape, stride, device): the same error as its own checks."""
+    if not ok:
+        raise Csa2Error(fn, 1)
+
+
+def _plane(t, dtype, rows, width, dev) -> bool:
+    """A contiguous [rows, width] (or more leading axes) tensor of dtype on dev."""
+    return t.dtype == dtype and t.device == dev and t.is_contiguous() and t.numel() == rows * width
+
+
+class _On:
+    """The tensors' device made current for a call (a library call launches on the current device)."""
+
+    def __init__(self, dev):
+        self.dev = dev
+        self.other = dev.type == "cuda" and dev.index != torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.other:
+            self.was = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.other:
+            torch.cuda.set_device(self.was)
+
+
+def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor | None = None, offset: int = 0,
+                    inverse: bool = False, stream=None) -> torch.Tensor:
+    """Rotary positions on channels [offset, offset + cfg.rot) of x [tokens, heads, dim]
+    (bf16 or fp32, any strides but the last axis's 1) into y (a new tensor; y=x: in
+    place).  pos: int32 [tokens].  inverse=True is the gradient's turn."""
+    fn = "csa2_rope_apply"
+    _need(fn, x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32) and (x.shape[2] <= 1 or x.stride(2) == 1))
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need(fn, y.shape == x.shape and y.dtype == x.dtype and y.device == x.device and (y.shape[2] <= 1 or y.stride(2) == 1))
+    _need(fn, pos.dtype == torch.int32 and pos.device == x.device and pos.is_contiguous() and pos.numel() == x.shape[0])
+    with _On(x.device):
+        _check(fn, _lib.csa2_rope_apply(
+            ctypes.byref(cfg.c()), 1 if x.dtype == torch.float32 else 0, _ptr(x), _ptr(y), _ptr(pos), x.shape[0],
+            x.shape[1], x.shape[2], int(offset), x.stride(0), x.stride(1), y.stride(0), y.stride(1), int(bool(inverse)),
+            _stream(stream)))
+    return y
+
+
+def csa2_kv_append(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, dst_rows: torch.Tensor, codes: torch.Tensor,
+                   scales: torch.Tensor, rope: torch.Tensor, norm_w: torch.Tensor | None = None, eps: float = 1e-6,
+                   entry: torch.Tensor | None = None, stream=None):
+    """Norm, rotate, quantize and write row i of x (bf16 [n, 576], rows strided) to cache
+    row dst_rows[i] (int64; outside the cache: no cache row) of the planes codes
+    [rows, 256], scales [rows, 32], rope [rows, 64]; entry (bf16 [n, 576]) also
+    receives the row in bf16."""
+    fn = "csa2_kv_append"
+    _need(fn, x.dim() == 2 and x.shape[1] == DQK and x.dtype == torch.bfloat16 and x.stride(1) == 1)
+    n, dev, rows = x.shape[0], x.device, codes.numel() // (LATENT // 2)
+    _need(fn, _plane(pos, torch.int32, n, 1, dev) and _plane(dst_rows, torch.int64, n, 1, dev))
+    _need(fn, _plane(codes, torch.uint8, rows, LATENT // 2, dev) and _plane(scales, torch.uint8, rows, LATENT // 16, dev)
+          and _plane(rope, torch.bfloat16, rows, ROPE, dev))
+    _need(fn, norm_w is None or _plane(norm_w, torch.bfloat16, 1, LATENT, dev))
+    _need(fn, entry is None or _plane(entry, torch.bfloat16, n, DQK, dev))
+    with _On(dev):
+        _check(fn, _lib.csa2_kv_append(
+            ctypes.byref(cfg.c()), _ptr(x), n, x.stride(0), _ptr(norm_w), float(eps), _ptr(pos), _ptr(dst_rows),
+            _ptr(codes), _ptr(scales), _ptr(rope), rows, _ptr(entry), _stream(stream)))
+
+
+def dense_attn_workspace_size(dims: Dims, batch: int, total_q: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("csa2_dense_attn_workspace_size",
+           _lib.csa2_dense_attn_workspace_size(ctypes.byref(dims.c()), batch, total_q, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_dense_attn_workspace(dims: Dims, batch: int, total_q: int, device="cuda") -> torch.Tensor:
+    """Workspace of csa2_dense_attn_chunk (uint8; its error word zeroed)."""
+    ws = torch.empty(dense_attn_workspace_size(dims, batch, total_q), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def csa2_dense_attn_chunk(dims: Dims, batch: int, q, q_start, kv_codes, kv_scales, kv_rope, page_table, ctx_len,
+                          scale: float, out, lse, ws, window: int = 0, flags: int = 0, stream=None):
+    """Dense attention of packed query tokens q bf16 [total_q, H, 576] over every visible
+    cache position: out bf16 [total_q, H, 512], lse fp32 [total_q, H].  flags:
+    DENSE_ALL_POSITIONS (no causal mask) or 0; window > 0: the last `window` positions."""
+    fn = "csa2_dense_attn_chunk"
+    total, h, dev = q.shape[0], dims.heads, q.device
+    _need(fn, _plane(q, torch.bfloat16, total, h * DQK, dev) and _plane(out, torch.bfloat16, total, h * LATENT, dev)
+          and _plane(lse, torch.float32, total, h, dev))
+    _need(fn, _plane(q_start, torch.int32, batch + 1, 1, dev) and _plane(ctx_len, torch.int32, batch, 1, dev))
+    if page_table is not None:
+        _need(fn, _plane(page_table, torch.int32, batch, dims.max_pages, dev))
+    rows = batch * dims.max_ctx if page_table is None else dims.num_pages * PAGE
+    _need(fn, kv_codes.dtype == torch.uint8 and kv_scales.dtype == torch.uint8 and kv_rope.dtype == torch.bfloat16)
+    for t, width in ((kv_codes, LATENT // 2), (kv_scales, LATENT // 16), (kv_rope, ROPE)):
+        _need(fn, t.device == dev and t.is_contiguous() and t.numel() >= rows * width)
+    _need(fn, ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous())
+    with _On(dev):
+        _check(fn, _lib.csa2_dense_attn_chunk(
+            ctypes.byref(dims.c()), batch, total, _ptr(q), _ptr(q_start), _ptr(kv_codes), _ptr(kv_scales), _ptr(kv_rope),
+            _ptr(page_table), _ptr(ctx_len), float(scale), int(window), int(flags), _ptr(out), _ptr(lse), _ptr(ws),
+            ws.numel(), _stream(stream)))
 
 
 def get_device_status(ws: torch.Tensor, stream=None) -> int:

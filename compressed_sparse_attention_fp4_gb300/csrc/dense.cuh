@@ -1,0 +1,63 @@
+// dense.cuh -- arguments and workspace layout of the dense chunk attention.
+#pragma once
+
+#include "common.cuh"
+
+namespace csa2 {
+
+constexpr int kDenseTile = 128;          // rows (query token, head) of a tile
+constexpr int kDenseBlk = 64;            // positions of a block: one page
+constexpr int kDenseMaxClusters = 76;    // CTA pairs: one CTA on each of 152 SMs
+constexpr int kDenseMinBlocks = 4;       // least blocks a run is cut to (one SM pair fills in ~1 us a block; a cut costs a merge)
+static_assert(kDenseBlk == kPage, "a block never crosses a page");
+
+struct DensePlan {
+  int4* head;          // tiles, runs in use
+  int4* runs;          // per cluster: first tile, blocks of it before the run, blocks
+  int4* seqs;          // per sequence: first tile, first query, queries, context
+  int4* tiles;         // two per tile (see Item)
+  int64_t* before;     // per tile: blocks before it
+};
+
+struct DenseArgs {
+  csa2_dims d;
+  int batch, total_q, causal, window, clusters;
+  const uint16_t* q;
+  const int32_t* q_start;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const uint16_t* rope;
+  const int32_t* page_table;
+  const int32_t* ctx_len;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  uint8_t* ws;
+  DensePlan plan;
+  float* part_o;       // [2 * clusters][512][128]
+  float* part_lse;     // [2 * clusters][128]
+};
+
+// Byte offsets in the workspace: error word, plan, partial outputs.
+struct DenseLayout {
+  int64_t head, runs, seqs, tiles, before, part_lse, part_o, total;
+};
+
+inline DenseLayout make_dense_layout(const csa2_dims& d, int64_t batch, int64_t total_q) {
+  DenseLayout L;
+  int64_t off = 256;
+  const int64_t tiles = (total_q * d.heads + kDenseTile - 1) / kDenseTile + batch;
+  L.head = off;     off += 256;
+  L.runs = off;     off = align256(off + kDenseMaxClusters * 16);
+  L.seqs = off;     off = align256(off + batch * 16);
+  L.tiles = off;    off = align256(off + tiles * 32);
+  L.before = off;   off = align256(off + tiles * 8);
+  L.part_lse = off; off = align256(off + int64_t(2 * kDenseMaxClusters) * kDenseTile * 4);
+  L.part_o = off;   off = align256(off + int64_t(2 * kDenseMaxClusters) * kDenseTile * kLatent * 4);
+  L.total = off;
+  return L;
+}
+
+cudaError_t launch_dense(DenseArgs a, cudaStream_t st);
+
+}  // namespace csa2

@@ -121,6 +121,34 @@ struct AttnArgs {
   int q_len;                   // queries per sequence (1; 2..4 for a multi-query call, cluster path only)
 };
 
+struct RopeArgs {
+  csa2_rope cfg;
+  bool fp32, inverse;
+  const void* x;
+  void* y;
+  const int32_t* pos;
+  int64_t tokens;
+  int heads, dim, offset;
+  int64_t x_token, x_head, y_token, y_head;   // elements
+};
+
+struct AppendArgs {
+  csa2_rope cfg;
+  const uint16_t* x;
+  int64_t n, x_stride;
+  const uint16_t* norm_w;
+  float eps;
+  const int32_t* pos;
+  const int64_t* dst_rows;
+  uint8_t* codes;
+  uint8_t* scales;
+  uint16_t* rope;
+  int64_t cache_rows;
+  uint16_t* entry;
+};
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_quantize(const uint16_t* x, int64_t n, const int64_t* dst_rows, uint8_t* codes,
                             uint8_t* scales, bool early, cudaStream_t st);
 cudaError_t launch_quantize_idx(const uint16_t* x, int64_t n, const int64_t* dst_rows, uint8_t* idx_k,

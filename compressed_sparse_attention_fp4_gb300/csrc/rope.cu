@@ -1,0 +1,342 @@
+// rope.cu -- rotary positions of query / key heads, and the cache append that
+// norms, rotates and quantizes a token's row in one pass.
+//
+// Both kernels are bound by memory: every value is read once and written once,
+// and the arithmetic between is kept under the time of the bytes.
+#include "fp4.cuh"
+#include "kernels.cuh"
+#include "profile.cuh"
+#include "rope.cuh"
+
+namespace csa2 {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Rotary positions: y = m R(angle) x on channels [offset, offset + rot) of every
+// head, the other channels copied (or left, in place).
+//
+// A CTA takes kTok tokens and a range of heads: it forms the (cos, sin) of its
+// tokens once in shared memory (rot / 2 of them a token, against heads * rot
+// values to turn) and then walks 16-byte pieces.
+// ---------------------------------------------------------------------------
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTok = 8;
+
+template <typename T> struct Io;
+template <> struct Io<float> {
+  static constexpr int kVec = 4;
+  __device__ static void unpack(uint4 v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+  __device__ static uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  __device__ static float get(float v) { return v; }
+  __device__ static float put(float v) { return v; }
+};
+__device__ inline uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <> struct Io<uint16_t> {
+  static constexpr int kVec = 8;
+  __device__ static void unpack(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static uint4 pack(const float (&f)[8]) {
+    return make_uint4(bf16x2_rn(f[0], f[1]), bf16x2_rn(f[2], f[3]), bf16x2_rn(f[4], f[5]), bf16x2_rn(f[6], f[7]));
+  }
+  __device__ static float get(uint16_t v) { return bf16_to_f32(v); }
+  __device__ static uint16_t put(float v) { return uint16_t(bf16x2_rn(v, 0.0f)); }
+};
+
+// x, y and the strides count elements of T; sign is -1 for the inverse.
+template <typename T, bool kHalf>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_kernel(const __grid_constant__ RopeTable tab, const T* x, T* y, const int32_t* __restrict__ pos, int64_t tokens,
+                int heads, int dim, int offset, int64_t xt, int64_t xh, int64_t yt, int64_t yh, int heads_per, int copy,
+                int vec, float sign) {
+  __shared__ float2 cs[kRopeTok * kMaxPairs];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int pairs = tab.pairs, tid = threadIdx.x;
+  const int64_t t0 = int64_t(blockIdx.x) * kRopeTok;
+  const int nt = int(min64(kRopeTok, tokens - t0));
+  const int h0 = blockIdx.y * heads_per, nh = min(heads_per, heads - h0);
+  for (int i = tid; i < nt * pairs; i += kRopeThreads) {
+    const int t = i / pairs, p = i - t * pairs;
+    float2 v = rope_cs(tab, p, __ldg(pos + t0 + t));
+    v.y *= sign;
+    cs[t * kMaxPairs + p] = v;
+  }
+  __syncthreads();
+  if (vec) {
+    constexpr int V = Io<T>::kVec;
+    // pieces of a head: turned (kHalf: two pieces rot / 2 apart at once), then copied
+    const int nturn = kHalf ? pairs / V : 2 * pairs / V, ncopy = copy ? (dim - 2 * pairs) / V : 0;
+    const int per = nturn + ncopy, per_t = nh * per, all = nt * per_t;
+    for (int i = tid; i < all; i += kRopeThreads) {
+      const int t = i / per_t, r = i - t * per_t, h = r / per, c = r - h * per;
+      const T* xs = x + (t0 + t) * xt + int64_t(h0 + h) * xh;
+      T* ys = y + (t0 + t) * yt + int64_t(h0 + h) * yh;
+      const float2* a = cs + t * kMaxPairs;
+      if (c >= nturn) {
+        int at = (c - nturn) * V;
+        if (at >= offset) at += 2 * pairs;
+        *reinterpret_cast<uint4*>(ys + at) = *reinterpret_cast<const uint4*>(xs + at);
+      } else if (kHalf) {
+        float u[V], v[V];
+        const int p = c * V;
+        Io<T>::unpack(*reinterpret_cast<const uint4*>(xs + offset + p), u);
+        Io<T>::unpack(*reinterpret_cast<const uint4*>(xs + offset + pairs + p), v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float2 e = a[p + k];
+          const float w = u[k];
+          u[k] = w * e.x - v[k] * e.y;
+          v[k] = w * e.y + v[k] * e.x;
+        }
+        *reinterpret_cast<uint4*>(ys + offset + p) = Io<T>::pack(u);
+        *reinterpret_cast<uint4*>(ys + offset + pairs + p) = Io<T>::pack(v);
+      } else {
+        float u[V];
+        Io<T>::unpack(*reinterpret_cast<const uint4*>(xs + offset + c * V), u);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+          const float2 e = a[c * (V / 2) + k];
+          const float w = u[2 * k];
+          u[2 * k] = w * e.x - u[2 * k + 1] * e.y;
+          u[2 * k + 1] = w * e.y + u[2 * k + 1] * e.x;
+        }
+        *reinterpret_cast<uint4*>(ys + offset + c * V) = Io<T>::pack(u);
+      }
+    }
+  } else {
+    // odd sizes, strides or addresses: one pair, or one copied channel, at a time
+    const int ncopy = copy ? dim - 2 * pairs : 0;
+    const int per = pairs + ncopy, per_t = nh * per, all = nt * per_t;
+    for (int i = tid; i < all; i += kRopeThreads) {
+      const int t = i / per_t, r = i - t * per_t, h = r / per, c = r - h * per;
+      const T* xs = x + (t0 + t) * xt + int64_t(h0 + h) * xh;
+      T* ys = y + (t0 + t) * yt + int64_t(h0 + h) * yh;
+      if (c >= pairs) {
+        int at = c - pairs;
+        if (at >= offset) at += 2 * pairs;
+        ys[at] = xs[at];
+      } else {
+        const float2 e = cs[t * kMaxPairs + c];
+        const int iu = offset + (kHalf ? c : 2 * c), iv = offset + (kHalf ? c + pairs : 2 * c + 1);
+        const float u = Io<T>::get(xs[iu]), v = Io<T>::get(xs[iv]);
+        ys[iu] = Io<T>::put(u * e.x - v * e.y);
+        ys[iv] = Io<T>::put(u * e.y + v * e.x);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Cache append: one warp a row.  Lane l holds latent channels 8 l .. 8 l + 7 of
+// both halves (the layout of the FP4 write) and rotary pair l.
+//
+// RMS norm y = x w / sqrt(mean x^2 + eps), rounded once, from the exact value,
+// to bf16: the FP4 codes then follow the 64-bit definition bit for bit, as the
+// codec's do.  fp32 arithmetic alone would round some thousandths of a percent
+// of the values the other way, so
+//   * x is scaled by the power of two that brings the row's largest value into
+//     [1, 2); a lane adds its 16 squares to 64 (each step's rounding error is
+//     then exact in fp32 and summed beside it), and both sums are added over
+//     the warp as integers;
+//   * 1/sqrt is rsqrtf and one Newton step kept as a second fp32 part;
+//   * x w is exact in fp32 (8 + 8 bits); only a product within 8 units of a
+//     bf16 midpoint (one in 4,000) needs the low parts.
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 256;
+
+// xw * (r + rl) rounded once to bf16, for a product p = xw * r near a midpoint.
+__device__ __noinline__ float near_midpoint(float xw, float r, float rl, float p) {
+  const float e = __fmaf_rn(xw, r, -p) + xw * rl;
+  float q = p + e;
+  const float rest = (p - q) + e;
+  if ((__float_as_uint(q) & 0xFFFFu) == 0x8000u && rest != 0.0f)
+    q = __uint_as_float(__float_as_uint(q) + (((rest < 0.0f) == (q < 0.0f)) ? 1u : 0xFFFFFFFFu));
+  return q;
+}
+
+__device__ inline uint4 norm8(uint4 xv, uint4 wv, float up, float r, float rl) {
+  float x[8], w[8], y[8];
+  Io<uint16_t>::unpack(xv, x);
+  Io<uint16_t>::unpack(wv, w);
+  uint32_t near = 0xFFFFu;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = (x[i] * up) * w[i];
+    y[i] = x[i] * r;
+    near = min(near, (__float_as_uint(y[i]) - 0x7FF8u) & 0xFFFFu);
+  }
+  if (near <= 16u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (((__float_as_uint(y[i]) - 0x7FF8u) & 0xFFFFu) <= 16u) y[i] = near_midpoint(x[i], r, rl, y[i]);
+  }
+  return Io<uint16_t>::pack(y);
+}
+
+template <bool kHalf>
+__global__ void __launch_bounds__(kAppendThreads)
+    append_kernel(const __grid_constant__ RopeTable tab, const uint16_t* __restrict__ x, int64_t n, int64_t stride,
+                  const uint16_t* __restrict__ norm_w, float eps, const int32_t* __restrict__ pos,
+                  const int64_t* __restrict__ dst_rows, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                  uint16_t* __restrict__ rope, int64_t cache_rows, uint16_t* __restrict__ entry) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t nwarps = (int64_t(gridDim.x) * blockDim.x) >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  uint4 w[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    w[r] = norm_w ? __ldg(reinterpret_cast<const uint4*>(norm_w) + r * 32 + lane) : make_uint4(0, 0, 0, 0);
+  for (int64_t row = warp; row < n; row += nwarps) {
+    const uint16_t* xr = x + row * stride;
+    uint4 v[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) v[r] = __ldcs(reinterpret_cast<const uint4*>(xr) + r * 32 + lane);
+    float u0, u1;
+    if (kHalf) {
+      u0 = bf16_to_f32(__ldcs(xr + kLatent + lane));
+      u1 = bf16_to_f32(__ldcs(xr + kLatent + 32 + lane));
+    } else {
+      const uint32_t p = __ldcs(reinterpret_cast<const uint32_t*>(xr + kLatent) + lane);
+      u0 = __uint_as_float(p << 16);
+      u1 = __uint_as_float(p & 0xFFFF0000u);
+    }
+    const int32_t ps = __ldg(pos + row);
+    const int64_t dst = __ldg(dst_rows + row);
+    if (norm_w) {
+      const uint32_t a[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(bf16x8_amax(a), bf16x8_amax(b))));
+      // exponent of the row's largest value, at least -40 (eps then outweighs the squares by far)
+      const int ex = max(int(top >> 23) - 127, -40);
+      const float up = __uint_as_float(uint32_t(127 - ex) << 23 | (ex == 127 ? 0x00400000u : 0u));
+      float s = 64.0f, e = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float f[8];
+        Io<uint16_t>::unpack(v[r], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float g = f[i] * up;
+          const float t = __fmaf_rn(g, g, s);
+          e += __fmaf_rn(g, g, s - t);
+          s = t;
+        }
+      }
+      // s - 64 < 64 in steps of 2^-17, |e| < 2^-13: integer sums over the warp
+      const int hi = __reduce_add_sync(0xFFFFFFFFu, int((s - 64.0f) * 131072.0f));
+      const int lo = __reduce_add_sync(0xFFFFFFFFu, __float2int_rn(e * 274877906944.0f));       // 2^38
+      // mean + eps, scaled like x^2, as two fp32 parts
+      const float m0 = float(hi & ~31) * 1.4901161193847656e-8f;                               // 2^-26
+      const float m1 = float(hi & 31) * 1.4901161193847656e-8f + float(lo) * 7.105427357601002e-15f;   // 2^-47
+      const float es = eps * up * up;
+      const float ms = m0 + es, back = ms - m0;
+      const float ml0 = (m0 - (ms - back)) + (es - back) + m1;
+      const float mh = ms + ml0, ml = (ms - mh) + ml0;
+      const float r0 = rsqrtf(mh);
+      const float p = r0 * r0, pe = __fmaf_rn(r0, r0, -p);
+      const float d = __fmaf_rn(-mh, p, 1.0f) - __fmaf_rn(mh, pe, ml * p);
+      const float rl = 0.5f * r0 * d;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) v[r] = norm8(v[r], w[r], up, r0, rl);
+    }
+    const float2 cs = rope_cs(tab, lane, ps);
+    const uint32_t turned = bf16x2_rn(u0 * cs.x - u1 * cs.y, u0 * cs.y + u1 * cs.x);
+    if (entry) {
+      uint16_t* er = entry + row * kDqk;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) __stcs(reinterpret_cast<uint4*>(er) + r * 32 + lane, v[r]);
+      if (kHalf) {
+        er[kLatent + lane] = uint16_t(turned);
+        er[kLatent + 32 + lane] = uint16_t(turned >> 16);
+      } else {
+        __stcs(reinterpret_cast<uint32_t*>(er + kLatent) + lane, turned);
+      }
+    }
+    const bool keep = dst >= 0 && dst < cache_rows;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t sc;
+      const uint32_t packed = fp4_quantize_half_group(v[r], &sc);
+      if (keep) {
+        codes[dst * 64 + r * 32 + lane] = packed;
+        if ((lane & 1) == 0) scales[dst * 32 + r * 16 + (lane >> 1)] = uint8_t(sc);
+      }
+    }
+    if (keep) {
+      uint16_t* rr = rope + dst * kRope;
+      if (kHalf) {
+        rr[lane] = uint16_t(turned);
+        rr[32 + lane] = uint16_t(turned >> 16);
+      } else {
+        reinterpret_cast<uint32_t*>(rr)[lane] = turned;
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t rope_typed(const RopeArgs& a, cudaStream_t st) {
+  constexpr int V = Io<T>::kVec;
+  const RopeTable tab = make_rope_table(a.cfg);
+  const bool half = a.cfg.layout == CSA2_ROPE_HALF;
+  const int rot = a.cfg.rot;
+  const bool copy = a.x != a.y;
+  // 16-byte pieces wherever every piece of every head is whole and aligned
+  const int64_t strides = a.x_token | a.x_head | a.y_token | a.y_head | a.offset | (half ? rot / 2 : rot) |
+                          (copy ? a.dim : 0);
+  const bool vec = strides % V == 0 && (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y)) % 16 == 0;
+  const int64_t gx = (a.tokens + kRopeTok - 1) / kRopeTok;
+  // few tokens: the heads are spread over CTAs (down to one a CTA), up to about four CTAs an SM
+  int hper = a.heads;
+  const int64_t want = int64_t(device_sms()) * 4;
+  if (gx < want) {
+    const int64_t split = min64(a.heads, (want + gx - 1) / gx);
+    hper = int((a.heads + split - 1) / split);
+  }
+  const unsigned gy = unsigned((a.heads + hper - 1) / hper);
+  cudaError_t e;
+  auto kernel = half ? rope_kernel<T, true> : rope_kernel<T, false>;
+  CSA2_PROFILED(st, "rope",
+                (e = launch_pdl(kernel, dim3(unsigned(gx), gy), dim3(kRopeThreads), 0, st, 1, tab,
+                                static_cast<const T*>(a.x), static_cast<T*>(a.y), a.pos, a.tokens, a.heads, a.dim,
+                                a.offset, a.x_token, a.x_head, a.y_token, a.y_head, hper, copy ? 1 : 0, vec ? 1 : 0,
+                                a.inverse ? -1.0f : 1.0f)));
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
+  return a.fp32 ? rope_typed<float>(a, st) : rope_typed<uint16_t>(a, st);
+}
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
+  const RopeTable tab = make_rope_table(a.cfg);
+  const int64_t want = (a.n + 7) / 8, cap = int64_t(device_sms()) * 8;
+  const unsigned grid = unsigned(want < cap ? want : cap);
+  auto kernel = a.cfg.layout == CSA2_ROPE_HALF ? append_kernel<true> : append_kernel<false>;
+  cudaError_t e;
+  CSA2_PROFILED(st, "kv_append",
+                (e = launch_pdl(kernel, dim3(grid), dim3(kAppendThreads), 0, st, 1, tab, a.x, a.n, a.x_stride, a.norm_w,
+                                a.eps, a.pos, a.dst_rows, reinterpret_cast<uint32_t*>(a.codes), a.scales, a.rope,
+                                a.cache_rows, a.entry)));
+  return e;
+}
+
+}  // namespace csa2

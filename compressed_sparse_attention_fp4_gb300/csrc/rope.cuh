@@ -1,0 +1,82 @@
+// rope.cuh -- rotary positions: per-pair frequencies (host) and angles (device).
+//
+// Pair i of a rotated part of `rot` channels turns by the angle pos * f_i.  The
+// pages apply rotary positions to the 64 bf16 key channels and the matching
+// query channels before the cache and the attention are reached; the layouts
+// and the context scalings here are the published ones (rotary embedding;
+// position interpolation; the base change and the by-parts rule of YaRN).
+//
+// Angles: pos reaches 2^20 and more, where an fp32 product pos * f_i is off by
+// hundredths of a radian.  f_i / 2 pi is therefore held as a 64-bit fraction of
+// a turn, and pos * F_i modulo 2^64 is the angle modulo one turn, exactly: one
+// integer multiply in place of 64-bit floating point, which this GPU runs at a
+// small part of its fp32 rate.  The top 32 bits give the angle to 2^-32 turns;
+// the sine and cosine are fp32.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace csa2 {
+
+constexpr int kMaxRot = 256;
+constexpr int kMaxPairs = kMaxRot / 2;
+
+// By value into the kernels (constant bank): the turn fraction of every pair.
+struct RopeTable {
+  uint64_t turn[kMaxPairs];    // f_i / (2 pi) * 2^64
+  float mscale;                // multiplies cosine and sine
+  int pairs;
+};
+
+// The frequencies of `r` (host, 64 bits).  The caller has checked `r`.
+inline RopeTable make_rope_table(const csa2_rope& r) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  RopeTable t;
+  t.mscale = r.mscale;
+  t.pairs = r.rot / 2;
+  double theta = r.theta;
+  if (r.scaling == CSA2_ROPE_BASE && r.rot > 2) theta *= std::pow(r.factor, double(r.rot) / double(r.rot - 2));
+  for (int i = 0; i < t.pairs; ++i) {
+    double f = std::pow(theta, -2.0 * i / r.rot);
+    if (r.scaling == CSA2_ROPE_LINEAR) f /= r.factor;
+    if (r.scaling == CSA2_ROPE_PARTS) {
+      // turns the pair makes over the original context: above turns_hi the
+      // frequency stays, below turns_lo it is divided, linear between
+      const double turns = r.orig_ctx * f / kTwoPi;
+      double keep = (turns - r.turns_lo) / (r.turns_hi - r.turns_lo);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      f = f * keep + f / r.factor * (1.0 - keep);
+    }
+    t.turn[i] = uint64_t(std::ldexp(f / kTwoPi, 64));   // f <= 1: below a sixth of a turn
+  }
+  return t;
+}
+
+// Checks of a rotary configuration (host).
+inline csa2_status check_rope(const csa2_rope* r) {
+  if (!r) return CSA2_ERR_INVALID_ARG;
+  if (r->layout != CSA2_ROPE_INTERLEAVED && r->layout != CSA2_ROPE_HALF) return CSA2_ERR_INVALID_ARG;
+  if (r->scaling < CSA2_ROPE_PLAIN || r->scaling > CSA2_ROPE_BASE) return CSA2_ERR_INVALID_ARG;
+  if (r->rot < 2 || r->rot > kMaxRot || (r->rot & 1)) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (!(r->theta > 1.0) || !std::isfinite(r->theta) || !std::isfinite(r->mscale)) return CSA2_ERR_INVALID_ARG;
+  if (r->scaling != CSA2_ROPE_PLAIN && (!(r->factor >= 1.0) || !std::isfinite(r->factor))) return CSA2_ERR_INVALID_ARG;
+  if (r->scaling == CSA2_ROPE_PARTS &&
+      (!(r->orig_ctx > 0.0) || !std::isfinite(r->orig_ctx) || !(r->turns_lo >= 0.0) || !(r->turns_hi > r->turns_lo) ||
+       !std::isfinite(r->turns_hi)))
+    return CSA2_ERR_INVALID_ARG;
+  return CSA2_OK;
+}
+
+// (cos, sin) * mscale of pair i at position pos.
+__device__ inline float2 rope_cs(const RopeTable& t, int i, int32_t pos) {
+  const uint64_t a = uint64_t(int64_t(pos)) * t.turn[i];       // modulo one turn
+  const float half_turns = float(int32_t(a >> 32)) * 4.656612873077393e-10f;   // 2^-31: [-1, 1)
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c * t.mscale, s * t.mscale);
+}
+
+}  // namespace csa2

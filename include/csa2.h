@@ -84,6 +84,7 @@ typedef enum {
 #define CSA2_DEV_SWA_LEN   0x08  /* swa_len[b] outside [0, dims.swa]         */
 #define CSA2_DEV_POOL      0x10  /* pool id / pool_len out of range          */
 #define CSA2_DEV_TIMEOUT   0x20  /* a bounded wait gave up                   */
+#define CSA2_DEV_Q_START   0x40  /* q_start falls back or leaves [0, total_q] */
 
 typedef enum {
   CSA2_IDXK_E4M3 = 0,   /* indexer K E4M3 [rows][idx_dim], query bf16 */
@@ -349,6 +350,117 @@ csa2_status csa2_sparse_attn_decode_noalloc(const csa2_dims* d, int32_t batch, i
                                             const int32_t* topk, const uint16_t* swa_kv,
                                             const int32_t* swa_len, float scale, float* out,
                                             float* lse, int32_t* err_word, void* stream);
+
+/* Rotary positions (the pages apply them to the 64 bf16 key channels and the
+ * matching query channels before this library's cache and attention are
+ * reached: foosynaptic atlas, section 3.2; the layouts and scalings are the
+ * published ones).  Pair i of the `rot` rotated channels, i = 0 .. rot/2 - 1,
+ * turns by the angle pos * f_i:
+ *   (u, v) -> mscale * (u cos - v sin, u sin + v cos),   f_i = theta^(-2 i / rot)
+ * with the pair's channels
+ *   CSA2_ROPE_INTERLEAVED: 2 i and 2 i + 1;   CSA2_ROPE_HALF: i and rot/2 + i
+ * and, for contexts longer than the original one, f_i scaled by
+ *   CSA2_ROPE_LINEAR: f_i / factor (position interpolation);
+ *   CSA2_ROPE_PARTS:  by the turns n_i = orig_ctx * f_i / (2 pi) that the pair makes
+ *     over the original context (the by-parts rule of YaRN): with k = (n_i - turns_lo)
+ *     / (turns_hi - turns_lo) limited to [0, 1], f_i * k + f_i / factor * (1 - k);
+ *   CSA2_ROPE_BASE:   theta replaced by theta * factor^(rot / (rot - 2)) (rot > 2).
+ * Angles are exact modulo one turn for every int32 position (to 2^-32 turns). */
+typedef enum { CSA2_ROPE_INTERLEAVED = 0, CSA2_ROPE_HALF = 1 } csa2_rope_layout;
+typedef enum {
+  CSA2_ROPE_PLAIN = 0,
+  CSA2_ROPE_LINEAR = 1,
+  CSA2_ROPE_PARTS = 2,
+  CSA2_ROPE_BASE = 3
+} csa2_rope_scaling;
+typedef struct {
+  int32_t rot;        /* rotated channels, even, 2..256                        */
+  int32_t layout;     /* csa2_rope_layout                                      */
+  int32_t scaling;    /* csa2_rope_scaling                                     */
+  float mscale;       /* multiplies cosine and sine (1: a rotation), finite    */
+  double theta;       /* base, > 1                                             */
+  double factor;      /* context factor, >= 1 (not PLAIN)                      */
+  double orig_ctx;    /* original context, > 0 (PARTS)                         */
+  double turns_lo;    /* >= 0 (PARTS; usually 1)                               */
+  double turns_hi;    /* > turns_lo (PARTS; usually 32)                        */
+} csa2_rope;
+
+/* y = rotary(x) on channels [offset, offset + rot) of every head; the other
+ * channels are copied, or left alone when y == x (in place, equal strides).
+ *   dtype:  CSA2_ROPE_BF16 or CSA2_ROPE_F32, of x and y (device)
+ *   pos:    device int32 [tokens]: the position of each token (any value)
+ *   x[t][h][c] at x + t * x_token + h * x_head + c (strides in elements; x may
+ *   repeat rows with stride 0); y likewise, without overlap of its rows.
+ *   inverse: 0, or 1 for the transpose mscale * R(-angle): the gradient with
+ *     respect to x of a forward call, applied to the gradient of y.
+ * x and y must be the same buffer with the same strides, or blocks (first to last
+ * element) that do not overlap.
+ * Errors: CSA2_ERR_INVALID_ARG (also: y's rows overlap), CSA2_ERR_UNSUPPORTED_SHAPE
+ * (rot outside 2..256 or odd, offset + rot > dim, sizes below 0, more than 2^31
+ * positions, heads > 65535), CSA2_ERR_CUDA. */
+#define CSA2_ROPE_BF16 0
+#define CSA2_ROPE_F32 1
+csa2_status csa2_rope_apply(const csa2_rope* r, int32_t dtype, const void* x, void* y, const int32_t* pos,
+                            int64_t tokens, int32_t heads, int32_t dim, int32_t offset, int64_t x_token,
+                            int64_t x_head, int64_t y_token, int64_t y_head, int32_t inverse, void* stream);
+
+/* Cache append from a layer's projection: row i of x (bf16, x + i * x_stride, 576
+ * channels: 512 latent, then 64 rotary) is normed, rotated, quantized and written
+ * to cache row dst_rows[i] in one pass:
+ *   latent = bf16(x w / sqrt(mean(x^2) + eps)), rounded once from the exact value
+ *            (x itself when norm_w is NULL);
+ *   codes, scales of the latent exactly as fp4_kv_quantize forms them;
+ *   rope   = bf16(rotary(x[512..575], pos[i])) with r (r->rot must be 64).
+ * A row whose destination is negative or not below cache_rows writes no cache row.
+ * Destinations must differ from each other (of two rows with the same one, which
+ * bytes of which row remain is not specified).
+ *   norm_w:   device bf16 [512], or NULL;  eps > 0, finite
+ *   pos:      device int32 [n];  dst_rows: device int64 [n]
+ *   codes, scales, rope: the cache planes (layout above; 16-, 2- and 16-byte aligned)
+ *   entry:    device bf16 [n][576], or NULL: also receives every row i as
+ *             [latent ; rope] in bf16 (an SWA window row), whatever dst_rows[i] is
+ *   x: 16-byte aligned, x_stride a multiple of 8, at least 576 for n > 1
+ * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (rot != 64), CSA2_ERR_CUDA. */
+csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int64_t x_stride,
+                           const uint16_t* norm_w, float eps, const int32_t* pos, const int64_t* dst_rows,
+                           uint8_t* codes, uint8_t* scales, uint16_t* rope, int64_t cache_rows, uint16_t* entry,
+                           void* stream);
+
+/* Dense attention of a chunk of new tokens over the main-KV cache: every visible
+ * position of the cache takes part (no Top-K set, no separate window; the new
+ * tokens' own rows have been appended before).  The queries of `batch` sequences
+ * are packed: sequence b owns tokens q_start[b] .. q_start[b + 1] of q.  Its token i
+ * (0-based, of n) stands at position ctx_len[b] - n + i and sees
+ *   the positions 0 .. ctx_len[b] - n + i (causal; with window > 0 only the last
+ *   `window` of them), or, with CSA2_DENSE_ALL_POSITIONS, 0 .. ctx_len[b] - 1.
+ * For each of its heads h:
+ *   logit_t = scale * q . [dq(latent_t) ; rope_t],  out = sum_t softmax(logit)_t dq(latent_t),
+ *   lse = ln sum_t exp(logit_t);  a token that sees nothing: out 0, lse -inf.
+ * Any number of tokens per sequence, none included: one (a decode step), a few
+ * (drafts), a prompt's chunk, a whole prompt.  Tokens of q before q_start[0] or
+ * from q_start[batch] on are not touched.  Results do not change from call to call.
+ *   Dimensions read: heads, max_ctx, max_pages, num_pages (the others must be valid
+ *   only for the calls that use them).
+ *   q:        device bf16 [total_q][H][576], 16-byte aligned
+ *   q_start:  device int32 [batch + 1], not decreasing, within 0 .. total_q
+ *   kv_codes, kv_scales, kv_rope, page_table, ctx_len: as csa2_sparse_attn_decode;
+ *             a block of positions whose page id is out of range is skipped and reported
+ *   out:      device bf16 [total_q][H][512], 16-byte aligned;  lse: device fp32 [total_q][H]
+ *   ws:       workspace of csa2_dense_attn_workspace_size(d, batch, total_q) bytes, its
+ *             first 256 the error word as elsewhere.  Calls that may run at the same
+ *             time need a workspace each.
+ *   P is rounded to fp16 (2^-11) and the output to bf16; everything between is fp32.
+ * Limits: total_q * H < 2^31, batch <= 2^20.
+ * Errors: CSA2_ERR_INVALID_ARG (window < 0, window with CSA2_DENSE_ALL_POSITIONS,
+ *         unknown flags, pointers, NaN scale), CSA2_ERR_UNSUPPORTED_SHAPE,
+ *         CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
+#define CSA2_DENSE_ALL_POSITIONS 1
+csa2_status csa2_dense_attn_workspace_size(const csa2_dims* d, int32_t batch, int64_t total_q, size_t* bytes);
+csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t total_q, const uint16_t* q,
+                                  const int32_t* q_start, const uint8_t* kv_codes, const uint8_t* kv_scales,
+                                  const uint16_t* kv_rope, const int32_t* page_table, const int32_t* ctx_len,
+                                  float scale, int32_t window, int32_t flags, uint16_t* out, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
 
 /* Kernel timing, a tracing aid.  While enabled, the library brackets every
  * kernel it launches with a pair of CUDA events on the launching stream
