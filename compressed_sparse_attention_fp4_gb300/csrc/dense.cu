@@ -13,11 +13,12 @@
 // of an SM, so scores and outputs cannot live on one SM.  A cluster of two CTAs
 // divides the work by kind instead:
 //   scores CTA (rank 0)   queries resident in tensor memory (288 columns); a block of
-//       64 positions is widened from FP4 to bf16 (exact) in shared memory,
-//       S[128 x 64] = Q . K^T (M 128, N 64, K 576, bf16 -> fp32); softmax, one thread a
-//       row; P as fp16 goes to the other CTA by an asynchronous shared-memory copy;
-//   values CTA (rank 1)   widens the same block's latents to fp16 (exact: 6
-//       significant bits, 2^-10 .. 2688), O[128 x 512] += P . V (M 128, N 2 x 256, K 64).
+//       64 positions is widened from FP4 to fp16 (exact: 6 significant bits, 2^-10 ..
+//       2688) in shared memory, its rope keys stay bf16; S[128 x 64] = Q . K^T (M 128,
+//       N 64, K 512 fp16 + 64 bf16 -> fp32); softmax, one thread a row; P as fp16 goes to
+//       the other CTA by an asynchronous shared-memory copy;
+//   values CTA (rank 1)   widens the same block's latents to fp16,
+//       O[128 x 512] += P . V (M 128, N 2 x 256, K 64).
 // Data flow one way only, so each side runs ahead through its rings (2 blocks of
 // keys, 2 score buffers, 3 blocks of P, 2 blocks of values).  Tensor work a block:
 // 1,152 and 1,024 cycles; the halves are balanced and nothing is computed twice but
@@ -51,26 +52,25 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kConvWarps = 8;
-constexpr int kRowWarp0 = 8;                        // warps 8..11: one row a thread (lane quarters 0..3)
-constexpr int kMmaWarp = 12;
-constexpr int kAuxWarp = 13;
-constexpr int kDenseThreads = 14 * 32;
+constexpr int kConvWarps = 16;                      // two groups of 8, one for each ring stage
+constexpr int kRowWarp0 = kConvWarps;               // eight warps: lane quarter (w % 4) x half of the columns
+constexpr int kRowWarps = 8;
+constexpr int kMmaWarp = kRowWarp0 + kRowWarps;
+constexpr int kDenseThreads = (kMmaWarp + 2) * 32;  // the last warp: copies (scores CTA), slots (values CTA)
 
 constexpr int kReg = kDenseBlk * 128;               // 64 channels x 64 positions of 16-bit: 8 KB
 constexpr int kPSlots = 3;
-constexpr int kPBytes = kDenseTile * 128;           // P[128 x 64] fp16
+constexpr int kPBytes = kDenseTile * 128;           // P[128 x 64] fp16: two halves of 32 positions
 constexpr int kKStages = 2;
-constexpr int kKBytes = 9 * kReg;                   // 576 channels
+constexpr int kKBytes = 9 * kReg;                   // 576 channels of 64 positions, or of 64 query rows
 constexpr int kVBytes = 8 * kReg;                   // 512 channels
-constexpr int kQSlots = 3;
-constexpr int kQPiece = kDenseTile * 64;            // 32 channels x 128 rows of bf16
-constexpr int kQPieces = kDqk / 32;
+constexpr int kRawBytes = kConvWarps * 32 * 32;     // the next block's codes, 32 bytes a widening thread
 constexpr int kPOff = 0;
 constexpr int kKvOff = kPOff + kPSlots * kPBytes;
-constexpr int kQOff = kKvOff + kKStages * kKBytes;  // scores CTA: query pieces; values CTA: output staging
-constexpr int kDenseSmem = kQOff + kQSlots * kQPiece;
-static_assert(4 * 4096 <= kQSlots * kQPiece, "output staging of the values CTA");
+constexpr int kRawOff = kKvOff + kKStages * kKBytes;
+constexpr int kStageOff = kKvOff + kKStages * kVBytes;   // values CTA: output staging, 2 KB a warp
+constexpr int kDenseSmem = kRawOff + kRawBytes;
+static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
 constexpr uint32_t kTmemAll = 512;
@@ -80,7 +80,6 @@ struct DenseSmall {
   uint64_t kv_full[kKStages], kv_empty[kKStages];
   uint64_t s_full[2], s_empty[2];
   uint64_t q_full;
-  uint64_t qc_full[kQSlots], qc_empty[kQSlots];
   uint64_t p_free[kPSlots];                         // scores CTA: slot read by the values CTA (remote arrival)
   uint64_t p_full[kPSlots];                         // values CTA: bytes of P and meta have arrived
   uint64_t corr[kPSlots];                           // values CTA: outputs brought to the slot's reference
@@ -89,8 +88,8 @@ struct DenseSmall {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
-  int page_ok[4];                                   // of the block n & 3
-  __align__(16) float meta[kPSlots][4][3][32];
+  __align__(16) float meta[kPSlots][kRowWarps][3][32];
+  uint32_t swap[2][2][kDenseTile];                  // row maxima between the two halves' warps
 };
 
 __device__ inline uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -163,6 +162,22 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
          (uint32_t(M >> 4) << 24);
 }
 
+__device__ inline bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ inline void some_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// 16 bytes of global memory into shared memory, asynchronously; zeros where !have.
+__device__ inline void cp_async16(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16u : 0u) : "memory");
+}
+__device__ inline void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ inline void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
+
 __device__ inline void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -208,9 +223,6 @@ __device__ inline uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// fp16 values (normal or zero) as the bf16 of 2^-112 times them: the 5-bit
-// exponent moved into the 8-bit field, the top 7 mantissa bits kept
-__device__ inline uint32_t f16x2_as_bf16x2(uint32_t h) { return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u); }
 
 // ---------------------------------------------------------------------------
 // The blocks of a cluster's run, walked alike by every role.
@@ -248,243 +260,312 @@ struct Walk {
   }
 };
 
-// ---------------------------------------------------------------------------
-// Widening warps (both CTAs).  Warp w takes the block's rows 8 w .. 8 w + 7, lane
-// = 8 * piece + row: a quarter-warp stores one 16-byte chunk of 8 rows (all 32 banks,
-// 128-byte swizzle), a load instruction reads 64 contiguous bytes of 8 rows.
-// The next block is loaded before the current one waits for its stage.
-// ---------------------------------------------------------------------------
-struct Raw {
-  uint4 cw[4];
-  uint32_t sc[2];     // four pairs of E4M3 scales
-  uint4 rp[2];
-  int ok;             // the page is valid
+// The blocks of a run one after the other, with their cache rows.  A warp keeps the
+// page ids of up to 32 blocks, one a lane.
+struct Cursor {
+  Walk walk;
+  Item it;
+  int i, pages, lane;
+  __device__ Cursor(const DensePlan& p, int c, int lane_) : walk(p, c), i(0), pages(0), lane(lane_) {}
+  __device__ void load_pages(const DenseArgs& a) {
+    const int at = (i & ~31) + lane;
+    if (a.page_table && at < it.n) pages = __ldg(a.page_table + int64_t(it.a.x) * a.d.max_pages + it.blk + at);
+  }
+  __device__ bool item(const DenseArgs& a, int first = 0) {
+    if (!walk.next(it)) return false;
+    i = first;
+    load_pages(a);
+    return true;
+  }
+  // `by` (1 or 2) blocks on within the item; false behind its end
+  __device__ bool step(const DenseArgs& a, int by) {
+    const int was = i;
+    i += by;
+    if (i >= it.n) return false;
+    if ((i ^ was) & 32) load_pages(a);
+    return true;
+  }
+  // first cache row of the block, -1 for a page id out of range (all lanes)
+  __device__ int64_t row0(const DenseArgs& a) const {
+    if (!a.page_table) return int64_t(it.a.x) * a.d.max_ctx + (it.blk + i) * kDenseBlk;
+    const int pg = __shfl_sync(0xFFFFFFFFu, pages, i & 31);
+    return pg < 0 || pg >= a.d.num_pages ? -1 : int64_t(pg) * kPage;
+  }
 };
 
-template <bool kScores>
-__device__ inline void load_raw(const DenseArgs& a, int4 ta, int4 tb, int blk, int w, int lane, Raw& r) {
-  const int b = ta.x, t = blk * kDenseBlk + 8 * w + (lane & 7), p = lane >> 3;
-  int64_t row = -1;
-  r.ok = 1;
-  if (a.page_table) {
-    const int pg = __ldg(a.page_table + int64_t(b) * a.d.max_pages + blk);
-    if (pg < 0 || pg >= a.d.num_pages) {
-      r.ok = 0;
-      if (kScores && lane == 0 && w == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
-    } else {
-      row = int64_t(pg) * kPage + (t & (kPage - 1));
-    }
-  } else {
-    row = int64_t(b) * a.d.max_ctx + t;
-  }
-  // rows behind the context hold anything: they are zeros (0 * P stays 0)
-  if (t >= tb.x || row < 0) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.cw[j] = make_uint4(0, 0, 0, 0);
-    r.sc[0] = r.sc[1] = 0;
-    if (kScores) r.rp[0] = r.rp[1] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const uint4* cp = reinterpret_cast<const uint4*>(a.codes + row * kCodesPerRow);
-  const uint16_t* sp = reinterpret_cast<const uint16_t*>(a.scales + row * kScalesPerRow);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r.cw[j] = __ldg(cp + 4 * j + p);
-  r.sc[0] = uint32_t(__ldg(sp + p)) | uint32_t(__ldg(sp + 4 + p)) << 16;
-  r.sc[1] = uint32_t(__ldg(sp + 8 + p)) | uint32_t(__ldg(sp + 12 + p)) << 16;
-  if (kScores) {
-    const uint4* rp = reinterpret_cast<const uint4*>(a.rope + row * kRope);
-    r.rp[0] = __ldg(rp + p);
-    r.rp[1] = __ldg(rp + 4 + p);
-  }
-}
-
-// Four FP4 words' worth of one 16-byte chunk: 8 channels under one scale.
-template <bool kScores>
+// ---------------------------------------------------------------------------
+// Widening warps (both CTAs): E2M1 x E4M3 -> fp16, exact (6 significant bits, 2^-10 ..
+// 2688).  Group g = w / 8 fills ring stage g (every other block); warp w takes rows
+// 8 (w % 8) .. + 7, lane = 8 * piece + row, four times: a quarter-warp stores one
+// 16-byte chunk of 8 rows (all 32 banks, 128-byte swizzle), a load reads 64 contiguous
+// bytes of 8 rows.  Codes are copied asynchronously into the thread's own 32 bytes of
+// shared memory, two pieces (a whole block period) ahead: no registers held, a short
+// loop.  (Straight-line code with the loads in registers stalls on the instruction
+// cache: 3.0 ms where the loop took 2.1, 1,216 tokens x 64 heads over 9,408 positions.)
+// ---------------------------------------------------------------------------
+// One 4-byte word of codes: 8 channels under one scale (twice in sc2).
 __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
-  uint32_t h[4] = {e2m1_byte_f16x2<0>(w), e2m1_byte_f16x2<1>(w), e2m1_byte_f16x2<2>(w), e2m1_byte_f16x2<3>(w)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = kScores ? mul_bf16x2(f16x2_as_bf16x2(h[i]), sc2) : mul_f16x2(h[i], sc2);
-  return make_uint4(h[0], h[1], h[2], h[3]);
-}
-
-template <bool kScores>
-__device__ inline void store_wide(uint8_t* dst, const Raw& r, int w, int lane) {
-  const int row = 8 * w + (lane & 7), p = lane >> 3;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int piece = 4 * j + p;                     // 16 code bytes: channels 32 piece .. + 31
-    const uint32_t two = e4m3x2_to_f16x2(uint16_t(r.sc[j >> 1] >> (16 * (j & 1))));
-    uint32_t s0, s1;
-    if (kScores) {
-      // scale * 2^112 in bf16 (exact: 4 significant bits, below 2^121), twice
-      const __half2 hh = *reinterpret_cast<const __half2*>(&two);
-      const float f0 = __low2float(hh) * 5.192296858534828e33f, f1 = __high2float(hh) * 5.192296858534828e33f;
-      s0 = __byte_perm(__float_as_uint(f0), 0, 0x3232);
-      s1 = __byte_perm(__float_as_uint(f1), 0, 0x3232);
-    } else {
-      s0 = __byte_perm(two, 0, 0x1010);
-      s1 = __byte_perm(two, 0, 0x3232);
-    }
-    uint8_t* reg = dst + (piece >> 1) * kReg;
-    const int c0 = (piece & 1) * 4;
-    const uint32_t w4[4] = {r.cw[j].x, r.cw[j].y, r.cw[j].z, r.cw[j].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(reg + tc::sw128_offset(row, c0 + i)) = widen8<kScores>(w4[i], i < 2 ? s0 : s1);
-  }
-  if (kScores) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<uint4*>(dst + 8 * kReg + tc::sw128_offset(row, 4 * j + p)) = r.rp[j];
-  }
+  return make_uint4(mul_f16x2(e2m1_byte_f16x2<0>(w), sc2), mul_f16x2(e2m1_byte_f16x2<1>(w), sc2),
+                    mul_f16x2(e2m1_byte_f16x2<2>(w), sc2), mul_f16x2(e2m1_byte_f16x2<3>(w), sc2));
 }
 
 template <bool kScores>
 __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int w, int lane) {
-  Walk walk(a.plan, cl);
-  Item it;
-  if (!walk.next(it)) return;
-  Raw cur;
-  load_raw<kScores>(a, it.a, it.b, it.blk, w, lane, cur);
-  for (uint32_t n = 0;; ++n) {
-    // the next block's loads
-    Raw nxt;
-    bool more = true;
-    ++it.blk;
-    if (--it.n == 0) more = walk.next(it);
-    if (more) load_raw<kScores>(a, it.a, it.b, it.blk, w, lane, nxt);
-    const uint32_t st = n % kKStages;
-    if (!wait_warp(sm, &sm.kv_empty[st], ((n / kKStages) & 1) ^ 1, a.ws)) return;
-    store_wide<kScores>(base + kKvOff + st * (kScores ? kKBytes : kVBytes), cur, w, lane);
-    if (kScores && w == 0 && lane == 0) sm.page_ok[n & 3] = cur.ok;
+  const int g = w >> 3, rw = 8 * (w & 7) + (lane & 7), p = lane >> 3;
+  constexpr int kLead = kScores ? 2 : 0;       // ring places of a tile's queries before its blocks
+  Cursor cur(a.plan, cl, lane);
+  int place = 0;                               // ring place (mod 2) of the item's start
+  int lead = 0;                                // query places of this stage to pass before the next block
+  const uint32_t slot = tc::smem_u32(base + kRawOff + (w * 32 + lane) * 16);        // and + kConvWarps * 512
+  const uint8_t* src = nullptr;                // this lane's codes in the next block
+  uint32_t sc_a = 0, sc_b = 0;                 // its four pairs of scales
+  bool have = false;
+  // the run's next block of this stage; false at its end
+  const auto next_block = [&](bool first) {
+    bool in = !first && cur.step(a, 2);
+    while (!in) {
+      if (!first) place = (place + kLead + cur.it.n) & 1;
+      first = false;
+      if (!cur.item(a, (g - place) & 1)) return false;
+      lead += kLead / 2;
+      in = cur.i < cur.it.n;
+    }
+    const int64_t row0 = cur.row0(a);
+    // rows behind the context hold anything: they are zeros (0 * P stays 0)
+    have = row0 >= 0 && (cur.it.blk + cur.i) * kDenseBlk + rw < cur.it.b.x;
+    if (kScores && row0 < 0 && (w & 7) == 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
+    const int64_t row = have ? row0 + rw : 0;
+    src = a.codes + row * kCodesPerRow + p * 16;
+    sc_a = sc_b = 0;
+    if (have) {
+      const uint16_t* s = reinterpret_cast<const uint16_t*>(a.scales + row * kScalesPerRow) + p;
+      sc_a = uint32_t(__ldg(s)) | uint32_t(__ldg(s + 4)) << 16;
+      sc_b = uint32_t(__ldg(s + 8)) | uint32_t(__ldg(s + 12)) << 16;
+    }
+    return true;
+  };
+  bool more = next_block(true);
+  if (more) {
+    cp_async16(slot, src, have);
+    cp_async_commit();
+    cp_async16(slot + kConvWarps * 512, src + 64, have);
+    cp_async_commit();
+  }
+  uint8_t* const stage = base + kKvOff + g * (kScores ? kKBytes : kVBytes) + (p >> 1) * kReg;
+  const uint32_t o0 = tc::sw128_offset(rw, (p & 1) * 4);                            // chunk i of the four: o0 ^ 16 i
+  uint32_t u = 0;                              // uses of the stage
+  while (true) {
+    // the tiles' queries pass through the same ring: nothing to widen
+    for (; lead > 0; --lead, ++u) {
+      if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
+      if (lane == 0) arrive(&sm.kv_full[g]);
+    }
+    if (!more) return;
+    const uint8_t* const src_now = src;
+    const bool have_now = have;
+    uint32_t sc = sc_a, sc_hi = sc_b;
+    more = next_block(false);
+    if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
+    uint8_t* reg = stage;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t raw = slot + (j & 1) * (kConvWarps * 512);
+      cp_async_wait<1>();
+      uint4 cw;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(cw.x), "=r"(cw.y), "=r"(cw.z), "=r"(cw.w) : "r"(raw) : "memory");
+      const uint32_t two = e4m3x2_to_f16x2(uint16_t(sc));
+      sc = __funnelshift_r(sc, sc_hi, 16);
+      sc_hi >>= 16;
+      const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+      // 16 code bytes: channels 32 (4 j + p) .. + 31, four chunks of region 2 j + p / 2
+      *reinterpret_cast<uint4*>(reg + o0) = widen8(cw.x, s0);
+      *reinterpret_cast<uint4*>(reg + (o0 ^ 16)) = widen8(cw.y, s0);
+      *reinterpret_cast<uint4*>(reg + (o0 ^ 32)) = widen8(cw.z, s1);
+      *reinterpret_cast<uint4*>(reg + (o0 ^ 48)) = widen8(cw.w, s1);
+      reg += 2 * kReg;
+      if (j < 2) cp_async16(raw, src_now + (j + 2) * 64, have_now);
+      else if (more) cp_async16(raw, src + (j - 2) * 64, have);
+      cp_async_commit();
+    }
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) arrive(&sm.kv_full[st]);
-    if (!more) return;
-    cur = nxt;
+    if (lane == 0) arrive(&sm.kv_full[g]);
+    ++u;
   }
 }
 
 // ---------------------------------------------------------------------------
 // Scores CTA
 // ---------------------------------------------------------------------------
+// Copies by TMA into the ring: a tile's queries as two "blocks" of 64 rows, then
+// the rope keys of each block of positions (their region needs no widening; rows
+// behind the context are masked scores, whatever they hold).
+__device__ inline void scores_copy_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int lane,
+                                        const CUtensorMap* qmap, const CUtensorMap* rmap) {
+  Cursor cur(a.plan, cl, lane);
+  uint32_t m = 0;
+  bool more = cur.item(a);
+  while (more) {
+    if (cur.i == 0) {
+      const int y = cur.it.a.z * a.d.heads + cur.it.a.y;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k, ++m) {
+        const uint32_t st = m % kKStages;
+        if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
+        if (lane == 0) {
+          tc::mbar_expect_tx(&sm.kv_full[st], kKBytes);
+#pragma unroll 1
+          for (int kb = 0; kb < 9; ++kb)
+            tc::tma_load_2d(qmap, base + kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.kv_full[st]);
+        }
+        __syncwarp();
+      }
+    }
+    const uint32_t st = m % kKStages;
+    const int64_t row0 = cur.row0(a);
+    if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
+    if (lane == 0) {
+      tc::mbar_expect_tx(&sm.kv_full[st], kReg);
+      tc::tma_load_2d(rmap, base + kKvOff + st * kKBytes + 8 * kReg, 0, row0 < 0 ? 0 : int(row0), &sm.kv_full[st]);
+    }
+    __syncwarp();
+    ++m;
+    more = cur.step(a, 1) || cur.item(a);
+  }
+}
+
 __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, uint32_t tmem) {
-  constexpr uint32_t id = tc::idesc_bf16(kDenseTile, kDenseBlk, 0, 0);
+  // latents are fp16, rope keys bf16 (each with queries of its type; one accumulator)
+  constexpr uint32_t id_lat = idesc_f16(kDenseTile, kDenseBlk, 0, 0), id_rope = tc::idesc_bf16(kDenseTile, kDenseBlk, 0, 0);
   Walk walk(a.plan, cl);
   Item it;
-  uint32_t n = 0;
+  uint32_t n = 0, m = 0;
+  const bool leader = elect_one();
   for (uint32_t k = 0; walk.next(it); ++k) {
-    if (!wait_on(sm, &sm.q_full, k & 1, a.ws)) return;
-    for (int j = 0; j < it.n; ++j, ++n) {
-      const uint32_t st = n % kKStages, buf = n & 1;
-      if (!wait_on(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
-      if (!wait_on(sm, &sm.s_empty[buf], ((n >> 1) & 1) ^ 1, a.ws)) return;
+    m += 2;
+    if (!wait_warp(sm, &sm.q_full, k & 1, a.ws)) return;
+    for (int j = 0; j < it.n; ++j, ++n, ++m) {
+      const uint32_t st = m % kKStages, buf = n & 1;
+      if (!wait_warp(sm, &sm.kv_full[st], (m / kKStages) & 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.s_empty[buf], ((n >> 1) & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
-      const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kKBytes), 16, 1024, 2);
-      const uint32_t d = tmem + kSCol + buf * kDenseBlk;
+      if (leader) {
+        const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kKBytes), 16, 1024, 2);
+        const uint32_t d = tmem + kSCol + buf * kDenseBlk;
+#pragma unroll 1
+        for (int kb = 0; kb < 9; ++kb)
 #pragma unroll
-      for (int ks = 0; ks < kDqk / 16; ++ks)
-        mma_ts(d, tmem + ks * 8, bd + (((ks >> 2) * kReg + (ks & 3) * 32) >> 4), id, ks > 0);
-      tc::mma_commit(&sm.kv_empty[st]);
-      tc::mma_commit(&sm.s_full[buf]);
+          for (int k4 = 0; k4 < 4; ++k4)
+            mma_ts(d, tmem + kb * 32 + k4 * 8, bd + ((kb * kReg + k4 * 32) >> 4), kb < 8 ? id_lat : id_rope, kb + k4 > 0);
+        tc::mma_commit(&sm.kv_empty[st]);
+        tc::mma_commit(&sm.s_full[buf]);
+      }
+      __syncwarp();
     }
   }
 }
 
-__device__ inline void query_tma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, const CUtensorMap* map) {
-  Walk walk(a.plan, cl);
-  Item it;
-  uint32_t n = 0;
-  while (walk.next(it)) {
-    const int y = it.a.z * a.d.heads + it.a.y;
-    for (int c = 0; c < kQPieces; ++c, ++n) {
-      const uint32_t s = n % kQSlots;
-      if (!wait_on(sm, &sm.qc_empty[s], ((n / kQSlots) & 1) ^ 1, a.ws)) return;
-      tc::mbar_expect_tx(&sm.qc_full[s], kQPiece);
-      tc::tma_load_2d(map, base + kQOff + s * kQPiece, 32 * c, y, &sm.qc_full[s]);
-    }
-  }
-}
-
-__device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int wq, int lane,
+// Warp rw: rows 32 (rw % 4) .. + 31 (one a lane), positions 32 (rw / 4) .. + 31 of a block.
+__device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int rw, int lane,
                                     uint32_t tmem) {
+  const int wq = rw & 3, half = rw >> 2;
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
   const int r = wq * 32 + lane;
   const float c2 = a.scale * 1.4426950408889634f;
-  const bool neg = c2 < 0.0f;
-  const float c = fmaxf(fabsf(c2), 1.17549435e-38f);
-  uint32_t n = 0, nq = 0;
-  Walk walk(a.plan, cl);
-  Item it;
-  uint32_t peer_p[kPSlots], peer_meta[kPSlots], peer_bar[kPSlots];
+  uint32_t n = 0, m = 0, ev = 0;
+  Cursor cur(a.plan, cl, lane);
+  while (cur.item(a)) {
+    // The tile's queries into tensor memory (rows 0..63 in the first half, 64..127 in the
+    // second); the MMAs that read the previous tile's are done (their scores have been
+    // read).  Each row is scaled by the power of two that brings its largest value into
+    // [2^14, 2^15), so that the 512 latent channels are fp16: the 8 bits of bf16 are kept
+    // for all values down to 2^-28 of the largest, smaller ones are off by 2^-39 of it.
+    float c;
+    {
+      const uint32_t mh = m + (wq >> 1), st = mh % kKStages;
+      if (!wait_warp(sm, &sm.kv_full[st], (mh / kKStages) & 1, a.ws)) return;
+      const uint8_t* src = base + kKvOff + st * kKBytes;
+      uint32_t big = 0;
+#pragma unroll 1
+      for (int q = 9 * half; q < 9 * half + 9; ++q)
 #pragma unroll
-  for (int s = 0; s < kPSlots; ++s) {
-    peer_p[s] = peer_addr(base + kPOff + s * kPBytes + wq * 4096, 1);
-    peer_meta[s] = peer_addr(&sm.meta[s][wq][0][0], 1);
-    peer_bar[s] = peer_addr(&sm.p_full[s], 1);
-  }
-  while (walk.next(it)) {
-    // the tile's queries into tensor memory, 32 channels (16 columns) at a time; the
-    // MMAs that read the previous tile's are done (their scores have been read)
-    for (int q = 0; q < kQPieces; ++q, ++nq) {
-      const uint32_t s = nq % kQSlots;
-      if (!wait_warp(sm, &sm.qc_full[s], (nq / kQSlots) & 1, a.ws)) return;
-      uint32_t v[16];
-      const uint8_t* src = base + kQOff + s * kQPiece + r * 64;      // 64-byte swizzle: chunk ^ (row / 2) % 4
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + (q >> 1) * kReg + tc::sw128_offset(r & 63, (q & 1) * 4 + i));
+          big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+        }
+      // the row's maximum over both halves (buffers alternate: the other warp has read
+      // the one before last when it comes to this barrier)
+      sm.swap[ev & 1][half][r] = big;
+      some_sync(1 + wq, 64);
+      big = __vmaxu2(big, sm.swap[ev & 1][half ^ 1][r]);
+      ++ev;
+      const int ex = int(max(big & 0xFFFFu, big >> 16) >> 7);              // biased exponent of the largest
+      const int k = min(14 + 127 - ex, 126);
+      const float up = __uint_as_float(uint32_t(127 + k) << 23) * (c2 < 0.0f ? -1.0f : 1.0f);   // a negative scale negates the queries
+      c = fmaxf(fabsf(c2) * __uint_as_float(uint32_t(127 - k) << 23), 1.17549435e-38f);
+      const uint32_t up2 = (__float_as_uint(up) >> 16) * 0x10001u;
+#pragma unroll 1
+      for (int q = 9 * half; q < 9 * half + 9; ++q) {
+        uint32_t v[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + ((i ^ ((r >> 1) & 3)) << 4));
-        v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + (q >> 1) * kReg + tc::sw128_offset(r & 63, (q & 1) * 4 + i));
+          v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+        }
+        if (q < 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = f16x2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], up2);
+        }
+        tmem_st16_nowait(lanes + q * 16, v);
       }
-      tmem_st16_nowait(lanes + q * 16, v);
+      tmem_wait_st();
+      tc::tc_fence_before_sync();
+      some_sync(5 + (wq >> 1), 128);
+      if (lane == 0) {
+        if ((wq & 1) == 0 && half == 0) arrive(&sm.kv_empty[st]);
+        arrive(&sm.q_full);
+      }
       __syncwarp();
-      if (lane == 0) arrive(&sm.qc_empty[s]);
+      m += 2 + cur.it.n;
     }
-    tmem_wait_st();
-    tc::tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) arrive(&sm.q_full);
-
     // positions this row sees: first .. last
-    const int lr = it.a.y + r, tok = lr / a.d.heads;
+    const int lr = cur.it.a.y + r, tok = lr / a.d.heads;
     int last = -1, first = 0;
-    if (tok < it.a.w) {
-      last = a.causal ? it.b.x - it.a.w + tok : it.b.x - 1;
+    if (tok < cur.it.a.w) {
+      last = a.causal ? cur.it.b.x - cur.it.a.w + tok : cur.it.b.x - 1;
       if (a.window > 0) first = max(0, last - a.window + 1);
     }
     float ref = -INFINITY, sum = 0.0f;
-    for (int j = 0; j < it.n; ++j, ++n) {
+    bool more = true;
+#pragma unroll 1
+    for (; more; ++n) {
       const uint32_t buf = n & 1, slot = n % kPSlots;
+      const int t0 = (cur.it.blk + cur.i) * kDenseBlk + 32 * half;
+      const int lo = first - t0, hi = cur.row0(a) < 0 ? -1 : last - t0;
       if (!wait_warp(sm, &sm.s_full[buf], (n >> 1) & 1, a.ws)) return;
       tc::tc_fence_after_sync();
-      float x[64];
-      {
-        float h[32];
-        tc::tmem_ld32(lanes + kSCol + buf * kDenseBlk, h);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = h[i];
-        tc::tmem_ld32(lanes + kSCol + buf * kDenseBlk + 32, h);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[32 + i] = h[i];
-      }
-      const int t0 = (it.blk + j) * kDenseBlk;
-      int lo = first - t0, hi = last - t0;
-      if (!sm.page_ok[n & 3]) hi = -1;
+      float x[32];
+      tc::tmem_ld32(lanes + kSCol + buf * kDenseBlk + 32 * half, x);
       tc::tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive(&sm.s_empty[buf]);
-      if (neg) {
+      if (__any_sync(0xFFFFFFFFu, lo > 0 || hi < 31)) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] = -x[i];
+        for (int i = 0; i < 32; ++i) x[i] = (i >= lo && i <= hi) ? x[i] : -INFINITY;
       }
-      if (__any_sync(0xFFFFFFFFu, lo > 0 || hi < kDenseBlk - 1)) {
+      float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] = (i >= lo && i <= hi) ? x[i] : -INFINITY;
-      }
-      float m[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int i = 4; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], x[i]);
-      const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
+      for (int i = 4; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
+      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      sm.swap[ev & 1][half][r] = __float_as_uint(top);
+      some_sync(1 + wq, 64);
+      top = fmaxf(top, __uint_as_float(sm.swap[ev & 1][half ^ 1][r])) * c;
+      ++ev;
       float alpha = 1.0f;
       if (top > ref + 8.0f) {
         const float now = ceilf(top);
@@ -493,10 +574,10 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
         ref = now;
       }
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
-      uint32_t pk[32];
       float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      uint32_t pk[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 16; ++i) {
         const float p0 = ex2(__fmaf_rn(x[2 * i], c, -sub)), p1 = ex2(__fmaf_rn(x[2 * i + 1], c, -sub));
         s4[(2 * i) & 3] += p0;
         s4[(2 * i + 1) & 3] += p1;
@@ -504,21 +585,24 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       }
       sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
-      uint8_t* ps = base + kPOff + slot * kPBytes;
+      // 64-byte rows, 64-byte swizzle (chunk ^ (row / 2) % 4): the warp's 32 rows are 2 KB in one piece
+      uint8_t* ps = base + kPOff + slot * kPBytes + half * (kPBytes / 2) + wq * 2048;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4*>(ps + tc::sw128_offset(r, i)) =
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(ps + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
             make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-      sm.meta[slot][wq][0][lane] = alpha;
-      sm.meta[slot][wq][1][lane] = sum;
-      sm.meta[slot][wq][2][lane] = sub;
+      sm.meta[slot][rw][0][lane] = alpha;
+      sm.meta[slot][rw][1][lane] = sum;
+      sm.meta[slot][rw][2][lane] = sub;
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        copy_to_peer(peer_p[slot], ps + wq * 4096, 4096, peer_bar[slot]);
-        copy_to_peer(peer_meta[slot], &sm.meta[slot][wq][0][0], kMetaWarp, peer_bar[slot]);
+        const uint32_t bar = peer_addr(&sm.p_full[slot], 1);
+        copy_to_peer(peer_addr(ps, 1), ps, 2048, bar);
+        copy_to_peer(peer_addr(&sm.meta[slot][rw][0][0], 1), &sm.meta[slot][rw][0][0], kMetaWarp, bar);
       }
       __syncwarp();
+      more = cur.step(a, 1);
     }
   }
 }
@@ -531,23 +615,28 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
   Walk walk(a.plan, cl);
   Item it;
   uint32_t n = 0;
+  const bool leader = elect_one();
   for (uint32_t k = 0; walk.next(it); ++k) {
-    if (!wait_on(sm, &sm.o_free, (k & 1) ^ 1, a.ws)) return;
+    if (!wait_warp(sm, &sm.o_free, (k & 1) ^ 1, a.ws)) return;
     for (int j = 0; j < it.n; ++j, ++n) {
       const uint32_t st = n % kKStages, slot = n % kPSlots, ph = (n / kPSlots) & 1;
-      if (!wait_on(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
-      if (!wait_on(sm, &sm.p_full[slot], ph, a.ws)) return;
-      if (!wait_on(sm, &sm.corr[slot], ph, a.ws)) return;
+      if (!wait_warp(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.p_full[slot], ph, a.ws)) return;
+      if (!wait_warp(sm, &sm.corr[slot], ph, a.ws)) return;
       tc::tc_fence_after_sync();
-      const uint64_t ad = tc::smem_desc(tc::smem_u32(base + kPOff + slot * kPBytes), 16, 1024, 2);
-      const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kVBytes), kReg, 1024, 2);
+      if (leader) {
+        const uint64_t ad = tc::smem_desc(tc::smem_u32(base + kPOff + slot * kPBytes), 16, 512, 4);   // 64-byte swizzle
+        const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kVBytes), kReg, 1024, 2);
 #pragma unroll
-      for (int ks = 0; ks < kDenseBlk / 16; ++ks)
+        for (int ks = 0; ks < kDenseBlk / 16; ++ks)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          tc::mma_bf16(tmem + h * 256, ad + ((ks * 32) >> 4), bd + ((h * 4 * kReg + ks * 2048) >> 4), id, j > 0 || ks > 0);
-      tc::mma_commit(&sm.kv_empty[st]);
-      tc::mma_commit(&sm.pv_done[slot]);
+          for (int h = 0; h < 2; ++h)
+            tc::mma_bf16(tmem + h * 256, ad + (((ks >> 1) * (kPBytes / 2) + (ks & 1) * 32) >> 4), bd + ((h * 4 * kReg + ks * 2048) >> 4), id,
+                         j > 0 || ks > 0);
+        tc::mma_commit(&sm.kv_empty[st]);
+        tc::mma_commit(&sm.pv_done[slot]);
+      }
+      __syncwarp();
     }
   }
 }
@@ -559,17 +648,19 @@ __device__ inline void slot_role(const DenseArgs& a, DenseSmall& sm, int cl) {
     const uint32_t slot = uint32_t(n) % kPSlots;
     if (!wait_on(sm, &sm.pv_done[slot], (uint32_t(n) / kPSlots) & 1, a.ws)) return;
     if (n + kPSlots < all) {
-      tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
+      tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + kRowWarps * kMetaWarp);
       arrive_remote(peer_addr(&sm.p_free[slot], 0));
     }
   }
 }
 
-__device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int wq, int lane,
+// Warp rw: rows 32 (rw % 4) .. + 31 (one a lane), channels 256 (rw / 4) .. + 255.
+__device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int rw, int lane,
                                    uint32_t tmem) {
-  const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
+  const int wq = rw & 3, col0 = 256 * (rw >> 2);
+  const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16) + uint32_t(col0);
   const int r = wq * 32 + lane;
-  uint8_t* stage = base + kQOff + wq * 4096;
+  uint8_t* stage = base + kStageOff + rw * 2048;
   Walk walk(a.plan, cl);
   Item it;
   uint32_t n = 0;
@@ -579,7 +670,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
       const uint32_t slot = n % kPSlots;
       if (!wait_warp(sm, &sm.p_full[slot], (n / kPSlots) & 1, a.ws)) return;
       const float alpha = sm.meta[slot][wq][0][lane];
-      sum = sm.meta[slot][wq][1][lane];
+      sum = sm.meta[slot][wq][1][lane] + sm.meta[slot][wq + 4][1][lane];
       sub = sm.meta[slot][wq][2][lane];
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
         // the outputs so far, once their products are done, to the new reference
@@ -587,7 +678,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
         if (!wait_warp(sm, &sm.pv_done[m % kPSlots], (m / kPSlots) & 1, a.ws)) return;
         tc::tc_fence_after_sync();
 #pragma unroll 1
-        for (int col = 0; col < kLatent; col += 8) {
+        for (int col = 0; col < 256; col += 8) {
           float v[8];
           tc::tmem_ld8(lanes + col, v);
 #pragma unroll
@@ -607,10 +698,10 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     const int lr = it.a.y + r, rows = it.a.w * a.d.heads;
     if (it.head || it.tail) {
       const int slot = 2 * cl + (it.head ? 0 : 1);
-      float* po = a.part_o + int64_t(slot) * kLatent * kDenseTile + r;
-      a.part_lse[slot * kDenseTile + r] = lse;
+      float* po = a.part_o + (int64_t(slot) * kLatent + col0) * kDenseTile + r;
+      if (col0 == 0) a.part_lse[slot * kDenseTile + r] = lse;
 #pragma unroll 1
-      for (int col = 0; col < kLatent; col += 32) {
+      for (int col = 0; col < 256; col += 32) {
         float v[32];
         tc::tmem_ld32(lanes + col, v);
 #pragma unroll
@@ -618,29 +709,27 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
       }
     } else {
       const int64_t g0 = int64_t(it.a.z) * a.d.heads + it.a.y + wq * 32;    // the warp's first row
-      const int have = min(32, rows - it.a.y - wq * 32);                    // rows of it that exist
-      if (lr < rows) a.lse[g0 + lane] = lse;
+      const int have = rows - it.a.y - wq * 32;                             // rows of it that exist (any number)
+      if (col0 == 0 && lr < rows) a.lse[g0 + lane] = lse;
+      uint16_t* dst = a.out + g0 * kLatent + col0 + 8 * (lane & 3);
 #pragma unroll 1
-      for (int col = 0; col < kLatent; col += 64) {
+      for (int col = 0; col < 256; col += 32) {
+        float v[32];
+        tc::tmem_ld32(lanes + col, v);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float v[32];
-          tc::tmem_ld32(lanes + col + 32 * half, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(stage + tc::sw128_offset(lane, 4 * half + i)) =
-                make_uint4(bf16x2_rn(v[8 * i] * inv, v[8 * i + 1] * inv), bf16x2_rn(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                           bf16x2_rn(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                           bf16x2_rn(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(bf16x2_rn(v[8 * i] * inv, v[8 * i + 1] * inv), bf16x2_rn(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                         bf16x2_rn(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                         bf16x2_rn(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
         __syncwarp();
-        // four rows of 128 bytes an instruction
+        // eight rows of 64 bytes an instruction
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + (lane >> 3);
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + (lane >> 2);
           if (row < have)
-            *reinterpret_cast<uint4*>(a.out + (g0 + row) * kLatent + col + 8 * (lane & 7)) =
-                *reinterpret_cast<const uint4*>(stage + tc::sw128_offset(row, lane & 7));
+            *reinterpret_cast<uint4*>(dst + int64_t(row) * kLatent + col) =
+                *reinterpret_cast<const uint4*>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
         }
         __syncwarp();
       }
@@ -652,7 +741,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
-    dense_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap) {
+    dense_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ DenseSmall sm;
@@ -661,30 +750,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
   if (wid == 0) tc::tmem_alloc(&sm.tmem_slot, kTmemAll);
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      tc::mbar_init(&sm.kv_full[i], kConvWarps);
+      tc::mbar_init(&sm.kv_full[i], rank == 0 ? 9 : 8);   // a group's warps, and the copying thread
       tc::mbar_init(&sm.kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.s_empty[i], 4);
+      tc::mbar_init(&sm.s_empty[i], kRowWarps);
     }
-    tc::mbar_init(&sm.q_full, 4);
-    for (int i = 0; i < kQSlots; ++i) {
-      tc::mbar_init(&sm.qc_full[i], 1);
-      tc::mbar_init(&sm.qc_empty[i], 4);
-    }
+    tc::mbar_init(&sm.q_full, kRowWarps);
     for (int i = 0; i < kPSlots; ++i) {
       tc::mbar_init(&sm.p_free[i], 1);
       tc::mbar_init(&sm.p_full[i], 1);
-      tc::mbar_init(&sm.corr[i], 4);
+      tc::mbar_init(&sm.corr[i], kRowWarps);
       tc::mbar_init(&sm.pv_done[i], 1);
     }
-    tc::mbar_init(&sm.o_free, 4);
+    tc::mbar_init(&sm.o_free, kRowWarps);
     tc::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     tc::fence_mbar_init();
     if (rank == 1)
-      for (int i = 0; i < kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + 4 * kMetaWarp);
+      for (int i = 0; i < kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + kRowWarps * kMetaWarp);
   }
   tc::tc_fence_before_sync();
   __syncthreads();
@@ -697,21 +782,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
   pdl_launch_dependents();
   if (rank == 0) {
     if (wid < kConvWarps) widen_role<true>(a, sm, base, cl, wid, lane);
-    else if (wid < kRowWarp0 + 4) softmax_role(a, sm, base, cl, wid - kRowWarp0, lane, tmem);
-    else if (wid == kMmaWarp && lane == 0) scores_mma_role(a, sm, base, cl, tmem);
-    else if (wid == kAuxWarp && lane == 0) query_tma_role(a, sm, base, cl, &qmap);
+    else if (wid < kRowWarp0 + kRowWarps) softmax_role(a, sm, base, cl, wid - kRowWarp0, lane, tmem);
+    else if (wid == kMmaWarp) scores_mma_role(a, sm, base, cl, tmem);
+    else scores_copy_role(a, sm, base, cl, lane, &qmap, &rmap);
   } else {
     if (wid < kConvWarps) widen_role<false>(a, sm, base, cl, wid, lane);
-    else if (wid < kRowWarp0 + 4) output_role(a, sm, base, cl, wid - kRowWarp0, lane, tmem);
-    else if (wid == kMmaWarp && lane == 0) values_mma_role(a, sm, base, cl, tmem);
-    else if (wid == kAuxWarp && lane == 0) slot_role(a, sm, cl);
+    else if (wid < kRowWarp0 + kRowWarps) output_role(a, sm, base, cl, wid - kRowWarp0, lane, tmem);
+    else if (wid == kMmaWarp) values_mma_role(a, sm, base, cl, tmem);
+    else if (lane == 0) slot_role(a, sm, cl);
   }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
-  if (wid == kMmaWarp && lane == 0) {
-    tc::mma_commit(&sm.drain);
-    wait_slow(sm, &sm.drain, 0, a.ws);
-  }
   __syncwarp();
+  if (wid == kMmaWarp) {
+    if (elect_one()) {
+      tc::mma_commit(&sm.drain);
+      wait_slow(sm, &sm.drain, 0, a.ws);
+    }
+    __syncwarp();
+  }
   tc::tc_fence_before_sync();
   __syncthreads();
   tc::tc_fence_after_sync();
@@ -949,10 +1037,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   a.clusters = int(min64(kDenseMaxClusters, device_sms() / 2));
   if (a.clusters < 1) a.clusters = 1;
-  CUtensorMap qmap;
+  CUtensorMap qmap, rmap;
   if (!encode_2d_cached(tensor_map_encoder(), &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk,
-                        uint64_t(a.total_q) * a.d.heads, kDqk * 2, 32, kDenseTile, CU_TENSOR_MAP_SWIZZLE_64B,
+                        uint64_t(a.total_q) * a.d.heads, kDqk * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return cudaErrorUnknown;
+  const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
+  if (!encode_2d_cached(tensor_map_encoder(), &rmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rope, kRope, rows, kRope * 2, 64,
+                        64, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
     return cudaErrorUnknown;
   static KernelAttrs attrs;
   constexpr size_t smem = size_t(kDenseSmem) + 1024;
@@ -961,7 +1053,8 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   CSA2_PROFILED(st, "dense_plan", (e = launch_pdl(dense_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_attn",
-                (e = launch_pdl(dense_kernel, dim3(unsigned(2 * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, qmap)));
+                (e = launch_pdl(dense_kernel, dim3(unsigned(2 * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, qmap,
+                                rmap)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_merge",
                 (e = launch_pdl(dense_merge_kernel, dim3(kLatent / kMergeCh, unsigned(a.clusters)), dim3(kDenseTile), 0,
