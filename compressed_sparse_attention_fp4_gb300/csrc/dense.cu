@@ -53,14 +53,15 @@ namespace csa2 {
 namespace {
 
 constexpr int kConvWarps = 16;                      // two groups of 8, one for each ring stage
-constexpr int kRowWarp0 = kConvWarps;               // eight warps: lane quarter (w % 4) x half of the columns
+constexpr int kRowWarp0 = kConvWarps;               // eight warps: lane quarter (w % 4) x (w / 4): the scores of every
+                                                    // other block (rank 0), half of the output channels (rank 1)
 constexpr int kRowWarps = 8;
 constexpr int kMmaWarp = kRowWarp0 + kRowWarps;
 constexpr int kDenseThreads = (kMmaWarp + 2) * 32;  // the last warp: copies (scores CTA), slots (values CTA)
 
 constexpr int kReg = kDenseBlk * 128;               // 64 channels x 64 positions of 16-bit: 8 KB
 constexpr int kPSlots = 3;
-constexpr int kPBytes = kDenseTile * 128;           // P[128 x 64] fp16: two halves of 32 positions
+constexpr int kPBytes = kDenseTile * 128;           // P[128 x 64] fp16
 constexpr int kKStages = 2;
 constexpr int kKBytes = 9 * kReg;                   // 576 channels of 64 positions, or of 64 query rows
 constexpr int kVBytes = 8 * kReg;                   // 512 channels
@@ -73,12 +74,13 @@ constexpr int kDenseSmem = kRawOff + kRawBytes;
 static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
+constexpr int kSBufs = 3;
 constexpr uint32_t kTmemAll = 512;
 constexpr int kMetaWarp = 3 * 32 * 4;               // alpha, sum, reference of a warp's rows
 
 struct DenseSmall {
   uint64_t kv_full[kKStages], kv_empty[kKStages];
-  uint64_t s_full[2], s_empty[2];
+  uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t q_full;
   uint64_t p_free[kPSlots];                         // scores CTA: slot read by the values CTA (remote arrival)
   uint64_t p_full[kPSlots];                         // values CTA: bytes of P and meta have arrived
@@ -88,8 +90,9 @@ struct DenseSmall {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
-  __align__(16) float meta[kPSlots][kRowWarps][3][32];
-  uint32_t swap[2][2][kDenseTile];                  // row maxima between the two halves' warps
+  __align__(16) float meta[kPSlots][4][3][32];
+  uint32_t swap[2][kDenseTile];                     // row maxima of the queries, between a row's two warps
+  float ref[2][kDenseTile];                         // softmax reference, handed from block to block
 };
 
 __device__ inline uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -168,6 +171,7 @@ __device__ inline bool elect_one() {
   return p != 0;
 }
 
+__device__ inline void some_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ inline void some_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // 16 bytes of global memory into shared memory, asynchronously; zeros where !have.
@@ -446,9 +450,9 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
     m += 2;
     if (!wait_warp(sm, &sm.q_full, k & 1, a.ws)) return;
     for (int j = 0; j < it.n; ++j, ++n, ++m) {
-      const uint32_t st = m % kKStages, buf = n & 1;
+      const uint32_t st = m % kKStages, buf = n % kSBufs;
       if (!wait_warp(sm, &sm.kv_full[st], (m / kKStages) & 1, a.ws)) return;
-      if (!wait_warp(sm, &sm.s_empty[buf], ((n >> 1) & 1) ^ 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.s_empty[buf], ((n / kSBufs) & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
       if (leader) {
         const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kKBytes), 16, 1024, 2);
@@ -466,23 +470,31 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
   }
 }
 
-// Warp rw: rows 32 (rw % 4) .. + 31 (one a lane), positions 32 (rw / 4) .. + 31 of a block.
+// Warp rw: rows 32 (rw % 4) .. + 31 (one a lane) of every block n with n % 2 = rw / 4: the
+// two warps of a row take turns, each with two block periods for the latencies of a
+// block.  What must go in order is the reference: block n's warp takes it from block
+// n - 1's as soon as that one has its maximum, and hands it on.
 __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int rw, int lane,
                                     uint32_t tmem) {
   const int wq = rw & 3, half = rw >> 2;
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
   const int r = wq * 32 + lane;
   const float c2 = a.scale * 1.4426950408889634f;
-  uint32_t n = 0, m = 0, ev = 0;
+  uint32_t n = 0, m = 0;
   Cursor cur(a.plan, cl, lane);
   while (cur.item(a)) {
     // The tile's queries into tensor memory (rows 0..63 in the first half, 64..127 in the
-    // second); the MMAs that read the previous tile's are done (their scores have been
-    // read).  Each row is scaled by the power of two that brings its largest value into
-    // [2^14, 2^15), so that the 512 latent channels are fp16: the 8 bits of bf16 are kept
-    // for all values down to 2^-28 of the largest, smaller ones are off by 2^-39 of it.
+    // second; a row's two warps take half of the channels each); the MMAs that read the
+    // previous tile's are done (its last scores have been read, by one of the two warps,
+    // and both meet at the barrier).  Each row is scaled by the power of two that brings
+    // its largest value into [2^14, 2^15), so that the 512 latent channels are fp16: the 8
+    // bits of bf16 are kept for all values down to 2^-28 of the largest, smaller ones are
+    // off by 2^-39 of it.
     float c;
     {
+      // both warps of a row are through the tile before: a wait for a parity must not
+      // start while the use before it is open
+      some_sync(11 + wq, 64);
       const uint32_t mh = m + (wq >> 1), st = mh % kKStages;
       if (!wait_warp(sm, &sm.kv_full[st], (mh / kKStages) & 1, a.ws)) return;
       const uint8_t* src = base + kKvOff + st * kKBytes;
@@ -494,12 +506,9 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
           const uint4 x = *reinterpret_cast<const uint4*>(src + (q >> 1) * kReg + tc::sw128_offset(r & 63, (q & 1) * 4 + i));
           big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
         }
-      // the row's maximum over both halves (buffers alternate: the other warp has read
-      // the one before last when it comes to this barrier)
-      sm.swap[ev & 1][half][r] = big;
-      some_sync(1 + wq, 64);
-      big = __vmaxu2(big, sm.swap[ev & 1][half ^ 1][r]);
-      ++ev;
+      sm.swap[half][r] = big;
+      some_sync(11 + wq, 64);
+      big = __vmaxu2(big, sm.swap[half ^ 1][r]);
       const int ex = int(max(big & 0xFFFFu, big >> 16) >> 7);              // biased exponent of the largest
       const int k = min(14 + 127 - ex, 126);
       const float up = __uint_as_float(uint32_t(127 + k) << 23) * (c2 < 0.0f ? -1.0f : 1.0f);   // a negative scale negates the queries
@@ -525,7 +534,7 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       }
       tmem_wait_st();
       tc::tc_fence_before_sync();
-      some_sync(5 + (wq >> 1), 128);
+      some_sync(9 + (wq >> 1), 128);
       if (lane == 0) {
         if ((wq & 1) == 0 && half == 0) arrive(&sm.kv_empty[st]);
         arrive(&sm.q_full);
@@ -540,70 +549,95 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       last = a.causal ? cur.it.b.x - cur.it.a.w + tok : cur.it.b.x - 1;
       if (a.window > 0) first = max(0, last - a.window + 1);
     }
-    float ref = -INFINITY, sum = 0.0f;
-    bool more = true;
+    float own = -INFINITY, sum = 0.0f;               // reference of this warp's last block, its sum under it
+    const uint32_t n0 = n, n1 = n + cur.it.n;
+    cur.i = int((half ^ n0) & 1);
+    n += uint32_t(cur.i);
 #pragma unroll 1
-    for (; more; ++n) {
-      const uint32_t buf = n & 1, slot = n % kPSlots;
-      const int t0 = (cur.it.blk + cur.i) * kDenseBlk + 32 * half;
+    for (; n < n1; n += 2) {
+      const uint32_t buf = n % kSBufs, slot = n % kPSlots;
+      const int t0 = (cur.it.blk + cur.i) * kDenseBlk;
       const int lo = first - t0, hi = cur.row0(a) < 0 ? -1 : last - t0;
-      if (!wait_warp(sm, &sm.s_full[buf], (n >> 1) & 1, a.ws)) return;
+      const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kDenseBlk - 1);
+      if (!wait_warp(sm, &sm.s_full[buf], (n / kSBufs) & 1, a.ws)) return;
       tc::tc_fence_after_sync();
-      float x[32];
-      tc::tmem_ld32(lanes + kSCol + buf * kDenseBlk + 32 * half, x);
-      tc::tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive(&sm.s_empty[buf]);
-      if (__any_sync(0xFFFFFFFFu, lo > 0 || hi < 31)) {
+      const uint32_t scol = lanes + kSCol + buf * kDenseBlk;
+      // two short passes over the scores in tensor memory: maximum, then weights
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float x[32];
+        tc::tmem_ld32(scol + 32 * h, x);
+        if (edge) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = (i >= lo && i <= hi) ? x[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) x[i] = (32 * h + i >= lo && 32 * h + i <= hi) ? x[i] : -INFINITY;
+        }
+        float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int i = 4; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
+        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
       }
-      float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int i = 4; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
-      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-      sm.swap[ev & 1][half][r] = __float_as_uint(top);
-      some_sync(1 + wq, 64);
-      top = fmaxf(top, __uint_as_float(sm.swap[ev & 1][half ^ 1][r])) * c;
-      ++ev;
-      float alpha = 1.0f;
+      top *= c;
+      // the reference so far, from the other warp (barriers 1..4 to the odd blocks' warps,
+      // 5..8 back; each arrival is awaited before the next on the same barrier)
+      float before = -INFINITY;
+      if (n != n0) {
+        some_sync(1 + 4 * (half ^ 1) + wq, 64);
+        before = sm.ref[half ^ 1][r];
+      }
+      float ref = before, alpha = 1.0f;
       if (top > ref + 8.0f) {
-        const float now = ceilf(top);
-        if (ref != -INFINITY) alpha = ex2(ref - now);
-        sum *= alpha;
-        ref = now;
+        ref = ceilf(top);
+        if (before != -INFINITY) alpha = ex2(before - ref);
       }
+      if (n + 1 != n1) {
+        sm.ref[half][r] = ref;
+        some_arrive(1 + 4 * half + wq, 64);
+      }
+      if (own != ref) sum = own == -INFINITY ? 0.0f : sum * ex2(own - ref);
+      own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
-      float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      uint32_t pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p0 = ex2(__fmaf_rn(x[2 * i], c, -sub)), p1 = ex2(__fmaf_rn(x[2 * i + 1], c, -sub));
-        s4[(2 * i) & 3] += p0;
-        s4[(2 * i + 1) & 3] += p1;
-        pk[i] = f16x2_rn(p0, p1);
-      }
-      sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
       if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
-      // 64-byte rows, 64-byte swizzle (chunk ^ (row / 2) % 4): the warp's 32 rows are 2 KB in one piece
-      uint8_t* ps = base + kPOff + slot * kPBytes + half * (kPBytes / 2) + wq * 2048;
+      uint8_t* ps = base + kPOff + slot * kPBytes;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float x[32];
+        tc::tmem_ld32(scol + 32 * h, x);
+        if (edge) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(ps + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-      sm.meta[slot][rw][0][lane] = alpha;
-      sm.meta[slot][rw][1][lane] = sum;
-      sm.meta[slot][rw][2][lane] = sub;
+          for (int i = 0; i < 32; ++i) x[i] = (32 * h + i >= lo && 32 * h + i <= hi) ? x[i] : -INFINITY;
+        }
+        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p0 = ex2(__fmaf_rn(x[2 * i], c, -sub)), p1 = ex2(__fmaf_rn(x[2 * i + 1], c, -sub));
+          s4[(2 * i) & 3] += p0;
+          s4[(2 * i + 1) & 3] += p1;
+          pk[i] = f16x2_rn(p0, p1);
+        }
+        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(ps + tc::sw128_offset(r, 4 * h + i)) =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+      }
+      tc::tc_fence_before_sync();
+      sm.meta[slot][wq][0][lane] = alpha;
+      sm.meta[slot][wq][1][lane] = sum;
+      sm.meta[slot][wq][2][lane] = sub;
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
+        arrive(&sm.s_empty[buf]);
         const uint32_t bar = peer_addr(&sm.p_full[slot], 1);
-        copy_to_peer(peer_addr(ps, 1), ps, 2048, bar);
-        copy_to_peer(peer_addr(&sm.meta[slot][rw][0][0], 1), &sm.meta[slot][rw][0][0], kMetaWarp, bar);
+        copy_to_peer(peer_addr(ps + wq * 4096, 1), ps + wq * 4096, 4096, bar);
+        copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], 1), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
       }
       __syncwarp();
-      more = cur.step(a, 1);
+      cur.step(a, 2);
     }
+    n = n1;
   }
 }
 
@@ -625,13 +659,13 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
       if (!wait_warp(sm, &sm.corr[slot], ph, a.ws)) return;
       tc::tc_fence_after_sync();
       if (leader) {
-        const uint64_t ad = tc::smem_desc(tc::smem_u32(base + kPOff + slot * kPBytes), 16, 512, 4);   // 64-byte swizzle
+        const uint64_t ad = tc::smem_desc(tc::smem_u32(base + kPOff + slot * kPBytes), 16, 1024, 2);
         const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kVBytes), kReg, 1024, 2);
 #pragma unroll
         for (int ks = 0; ks < kDenseBlk / 16; ++ks)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            tc::mma_bf16(tmem + h * 256, ad + (((ks >> 1) * (kPBytes / 2) + (ks & 1) * 32) >> 4), bd + ((h * 4 * kReg + ks * 2048) >> 4), id,
+            tc::mma_bf16(tmem + h * 256, ad + ((ks * 32) >> 4), bd + ((h * 4 * kReg + ks * 2048) >> 4), id,
                          j > 0 || ks > 0);
         tc::mma_commit(&sm.kv_empty[st]);
         tc::mma_commit(&sm.pv_done[slot]);
@@ -648,7 +682,7 @@ __device__ inline void slot_role(const DenseArgs& a, DenseSmall& sm, int cl) {
     const uint32_t slot = uint32_t(n) % kPSlots;
     if (!wait_on(sm, &sm.pv_done[slot], (uint32_t(n) / kPSlots) & 1, a.ws)) return;
     if (n + kPSlots < all) {
-      tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + kRowWarps * kMetaWarp);
+      tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
       arrive_remote(peer_addr(&sm.p_free[slot], 0));
     }
   }
@@ -665,12 +699,15 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
   Item it;
   uint32_t n = 0;
   while (walk.next(it)) {
-    float sum = 0.0f, sub = 0.0f;
+    // sums of the even and the odd blocks, each under the reference of its last block
+    float sum = 0.0f, sub = 0.0f, sum_b = 0.0f, sub_b = 0.0f;
     for (int j = 0; j < it.n; ++j, ++n) {
       const uint32_t slot = n % kPSlots;
       if (!wait_warp(sm, &sm.p_full[slot], (n / kPSlots) & 1, a.ws)) return;
       const float alpha = sm.meta[slot][wq][0][lane];
-      sum = sm.meta[slot][wq][1][lane] + sm.meta[slot][wq + 4][1][lane];
+      sum_b = sum;
+      sub_b = sub;
+      sum = sm.meta[slot][wq][1][lane];
       sub = sm.meta[slot][wq][2][lane];
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
         // the outputs so far, once their products are done, to the new reference
@@ -693,6 +730,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     const uint32_t m = n - 1;
     if (!wait_warp(sm, &sm.pv_done[m % kPSlots], (m / kPSlots) & 1, a.ws)) return;
     tc::tc_fence_after_sync();
+    if (sum_b > 0.0f) sum += sum_b * ex2(sub_b - sub);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const float lse = sum > 0.0f ? (sub + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     const int lr = it.a.y + r, rows = it.a.w * a.d.heads;
@@ -753,9 +791,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
       tc::mbar_init(&sm.kv_full[i], rank == 0 ? 9 : 8);   // a group's warps, and the copying thread
       tc::mbar_init(&sm.kv_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSBufs; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.s_empty[i], kRowWarps);
+      tc::mbar_init(&sm.s_empty[i], 4);
     }
     tc::mbar_init(&sm.q_full, kRowWarps);
     for (int i = 0; i < kPSlots; ++i) {
@@ -769,7 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
     sm.abort = 0;
     tc::fence_mbar_init();
     if (rank == 1)
-      for (int i = 0; i < kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + kRowWarps * kMetaWarp);
+      for (int i = 0; i < kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + 4 * kMetaWarp);
   }
   tc::tc_fence_before_sync();
   __syncthreads();
