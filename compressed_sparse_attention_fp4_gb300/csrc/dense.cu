@@ -63,24 +63,22 @@ constexpr int kReg = kDenseBlk * 128;               // 64 channels x 64 position
 constexpr int kPSlots = 3;
 constexpr int kPBytes = kDenseTile * 128;           // P[128 x 64] fp16
 constexpr int kKStages = 2;
-constexpr int kKBytes = 9 * kReg;                   // 576 channels of 64 positions, or of 64 query rows
+constexpr int kKBytes = 9 * kReg;                   // 576 channels of a block's positions, or of 64 query rows
 constexpr int kVBytes = 8 * kReg;                   // 512 channels
-constexpr int kRawBytes = kConvWarps * 32 * 32;     // the next block's codes, 32 bytes a widening thread
 constexpr int kPOff = 0;
 constexpr int kKvOff = kPOff + kPSlots * kPBytes;
-constexpr int kRawOff = kKvOff + kKStages * kKBytes;
 constexpr int kStageOff = kKvOff + kKStages * kVBytes;   // values CTA: output staging, 2 KB a warp
-constexpr int kDenseSmem = kRawOff + kRawBytes;
-static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
+constexpr int kDenseSmem = kKvOff + kKStages * kKBytes;
+static_assert(kStageOff + kRowWarps * 2048 <= kDenseSmem, "output staging of the values CTA");
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
 constexpr int kSBufs = 3;
-constexpr uint32_t kTmemAll = 512;
 constexpr int kMetaWarp = 3 * 32 * 4;               // alpha, sum, reference of a warp's rows
 
 struct DenseSmall {
   uint64_t kv_full[kKStages], kv_empty[kKStages];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
+  uint64_t q_place[kKStages];                       // queries in a ring stage (and the group's turn passed)
   uint64_t q_full;
   uint64_t p_free[kPSlots];                         // scores CTA: slot read by the values CTA (remote arrival)
   uint64_t p_full[kPSlots];                         // values CTA: bytes of P and meta have arrived
@@ -107,56 +105,112 @@ __device__ inline void copy_to_peer(uint32_t raddr, const void* src, uint32_t by
                : "memory");
 }
 
+// Arrival on another CTA's barrier.  What it hands over is never read by ordinary loads
+// of that CTA: shared memory that the tensor cores read (made visible to them by the
+// writer's proxy fence before this), tensor memory (ordered by the tcgen05 fences on
+// both sides), or a place that is free.  A release at cluster scope, which waits for
+// every earlier store of the thread, costs a fifth of the kernel's time instead
+// (1.55 against 1.28 ms, 1,216 tokens over 9,408 positions).
 __device__ inline void arrive_remote(uint32_t rbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(rbar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(rbar) : "memory");
 }
 
 __device__ inline void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
-__device__ inline bool try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+// One try, which suspends the thread for a while the hardware chooses.
+__device__ inline bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
       : "memory");
   return done != 0;
 }
 
-// Every wait of the kernel: bounded (200 ms against microseconds), and cut short
-// once another role of the CTA has given up.  False: the caller's role ends.
+// Arrive on a barrier of the pair's leading CTA (the one that issues its MMAs).
+template <int G>
+__device__ inline void arrive_leader(uint64_t* bar, int leader) {
+  if constexpr (G == 1) arrive(bar);
+  else arrive_remote(peer_addr(bar, uint32_t(leader)));
+}
+
+// Every wait of the kernel: bounded (200 ms against microseconds; the clock is only read
+// after some tries, it takes longer than most waits), and cut short once another role
+// of the CTA has given up.  False: the caller's role ends.
 __device__ __noinline__ bool wait_slow(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
-  const uint64_t t0 = tc::globaltimer_ns();
-  while (true) {
-    if (try_wait_cluster(bar, parity, 20000u)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
-    if (tc::globaltimer_ns() - t0 > 200ull * 1000 * 1000) {
-      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-      raise_err(ws, CSA2_DEV_TIMEOUT);
-      return false;
+    if ((i & 31u) == 0) {
+      const uint64_t t = tc::globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > 200ull * 1000 * 1000) {
+        *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+        raise_err(ws, CSA2_DEV_TIMEOUT);
+        return false;
+      }
     }
   }
 }
 __device__ inline bool wait_on(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
-  return try_wait_cluster(bar, parity, 0u) || wait_slow(sm, bar, parity, ws);
+  return try_wait_cluster(bar, parity) || wait_slow(sm, bar, parity, ws);
 }
 // the same for a converged warp: one answer for all lanes
 __device__ inline bool wait_warp(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
   return __all_sync(0xFFFFFFFFu, wait_on(sm, bar, parity, ws));
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T
+// D[tmem] (+)= A * B[smem]^T over one CTA (G 1) or a pair (G 2: rows of both, B
+// shared, each CTA holding half of its columns); A in tensor or shared memory.
+template <int G>
 __device__ inline void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
-      : "memory");
+  if constexpr (G == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)) : "memory");
+}
+template <int G>
+__device__ inline void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  if constexpr (G == 1) tc::mma_bf16(d, a, b, idesc, acc);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)) : "memory");
+}
+// Arrive on `bar` of this CTA (G 1), or of both CTAs in `mask`, once the MMAs so far are done.
+template <int G>
+__device__ inline void commit_to(uint64_t* bar, uint16_t mask) {
+  if constexpr (G == 1) tc::mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(tc::smem_u32(bar)), "h"(mask) : "memory");
+}
+template <int G>
+__device__ inline void tmem_alloc_all(uint32_t* slot) {
+  if constexpr (G == 1) tc::tmem_alloc(slot, 512);
+  else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int G>
+__device__ inline void tmem_free_all(uint32_t taddr) {
+  if constexpr (G == 1) tc::tmem_dealloc(taddr, 512);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512u) : "memory");
 }
 
 // Instruction descriptor with fp16 A/B and fp32 accumulation.
@@ -173,14 +227,6 @@ __device__ inline bool elect_one() {
 
 __device__ inline void some_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ inline void some_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
-
-// 16 bytes of global memory into shared memory, asynchronously; zeros where !have.
-__device__ inline void cp_async16(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16u : 0u) : "memory");
-}
-__device__ inline void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ inline void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
 __device__ inline void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -298,14 +344,16 @@ struct Cursor {
 };
 
 // ---------------------------------------------------------------------------
-// Widening warps (both CTAs): E2M1 x E4M3 -> fp16, exact (6 significant bits, 2^-10 ..
-// 2688).  Group g = w / 8 fills ring stage g (every other block); warp w takes rows
-// 8 (w % 8) .. + 7, lane = 8 * piece + row, four times: a quarter-warp stores one
-// 16-byte chunk of 8 rows (all 32 banks, 128-byte swizzle), a load reads 64 contiguous
-// bytes of 8 rows.  Codes are copied asynchronously into the thread's own 32 bytes of
-// shared memory, two pieces (a whole block period) ahead: no registers held, a short
-// loop.  (Straight-line code with the loads in registers stalls on the instruction
-// cache: 3.0 ms where the loop took 2.1, 1,216 tokens x 64 heads over 9,408 positions.)
+// Widening warps (every CTA): E2M1 x E4M3 -> fp16, exact (6 significant bits, 2^-10 ..
+// 2688).  Group g = w / 8 fills ring stage g (every other block).  A lane takes 16
+// bytes of codes (32 channels) of one row at a time, lane = 8 * piece + row: a
+// quarter-warp stores one 16-byte chunk of 8 rows (all 32 banks, 128-byte swizzle), a
+// load reads 64 contiguous bytes of 8 rows.  A block's codes, scales and rope keys are
+// loaded into registers as soon as the block before (of this stage) is stored, two
+// block periods before they are used.
+//   G 1: scores and values CTA each take 64 rows x 512 channels (4 pieces a lane);
+//   G 2: a scores CTA takes its 32 of the 64 rows, a values CTA its 256 of the 512
+//        channels (128 of each 256-column product): 2 pieces a lane.
 // ---------------------------------------------------------------------------
 // One 4-byte word of codes: 8 channels under one scale (twice in sc2).
 __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
@@ -313,16 +361,29 @@ __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
                     mul_f16x2(e2m1_byte_f16x2<2>(w), sc2), mul_f16x2(e2m1_byte_f16x2<3>(w), sc2));
 }
 
-template <bool kScores>
-__device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int w, int lane) {
-  const int g = w >> 3, rw = 8 * (w & 7) + (lane & 7), p = lane >> 3;
+template <int G, bool kScores>
+__device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int w, int lane) {
+  constexpr int kPieces = 4 / G, kRopePieces = kScores ? 2 / G : 0;
   constexpr int kLead = kScores ? 2 : 0;       // ring places of a tile's queries before its blocks
+  constexpr int kLeader = kScores ? 0 : G;
+  const int g = w >> 3, w8 = w & 7, p = lane >> 3;
+  // row in the stage, row in the block, first piece of 16 code bytes and the step to the next, region of the first piece
+  const int srow = 8 * (G == 2 && kScores ? w8 & 3 : w8) + (lane & 7);
+  const int brow = G == 2 && kScores ? 32 * part + srow : srow;
+  const int piece = G == 1 ? p : kScores ? 8 * (w8 >> 2) + p : 4 * part + p;
+  constexpr int kStep = G == 2 && !kScores ? 8 : 4;
+  constexpr int kStageRows = G == 2 && kScores ? 32 : 64;
+  constexpr int kRegion = kStageRows * 128;
+  const int region = (G == 2 && !kScores ? 0 : 2 * (piece >> 2)) + (p >> 1);
+  const int rpiece = G == 1 ? p : (w8 >> 2) * 4 + p;                                // rope: 16 bytes, 8 channels
+  uint8_t* const stage = base + kKvOff + g * (kScores ? kKBytes : kVBytes);
+  uint8_t* const reg = stage + region * kRegion;
+  const uint32_t o0 = tc::sw128_offset(srow, (p & 1) * 4);                         // chunk i of the four: o0 ^ 16 i
   Cursor cur(a.plan, cl, lane);
   int place = 0;                               // ring place (mod 2) of the item's start
   int lead = 0;                                // query places of this stage to pass before the next block
-  const uint32_t slot = tc::smem_u32(base + kRawOff + (w * 32 + lane) * 16);        // and + kConvWarps * 512
-  const uint8_t* src = nullptr;                // this lane's codes in the next block
-  uint32_t sc_a = 0, sc_b = 0;                 // its four pairs of scales
+  uint4 cw[kPieces], rp[kRopePieces + 1];
+  uint16_t sc[kPieces];
   bool have = false;
   // the run's next block of this stage; false at its end
   const auto next_block = [&](bool first) {
@@ -335,123 +396,104 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
       in = cur.i < cur.it.n;
     }
     const int64_t row0 = cur.row0(a);
-    // rows behind the context hold anything: they are zeros (0 * P stays 0)
-    have = row0 >= 0 && (cur.it.blk + cur.i) * kDenseBlk + rw < cur.it.b.x;
-    if (kScores && row0 < 0 && (w & 7) == 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
-    const int64_t row = have ? row0 + rw : 0;
-    src = a.codes + row * kCodesPerRow + p * 16;
-    sc_a = sc_b = 0;
-    if (have) {
-      const uint16_t* s = reinterpret_cast<const uint16_t*>(a.scales + row * kScalesPerRow) + p;
-      sc_a = uint32_t(__ldg(s)) | uint32_t(__ldg(s + 4)) << 16;
-      sc_b = uint32_t(__ldg(s + 8)) | uint32_t(__ldg(s + 12)) << 16;
+    if (kScores && part == 0 && row0 < 0 && w8 == 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
+    // rows behind the context hold anything: their scale is taken as 0 (0 * P stays 0; their
+    // scores are masked).  The loads are unconditional, from row 0 in their place, so that
+    // nothing waits for them here.
+    have = row0 >= 0 && (cur.it.blk + cur.i) * kDenseBlk + brow < cur.it.b.x;
+    const int64_t row = have ? row0 + brow : 0;
+    const uint4* c = reinterpret_cast<const uint4*>(a.codes + row * kCodesPerRow) + piece;
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(a.scales + row * kScalesPerRow) + piece;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) cw[j] = __ldg(c + kStep * j);
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) sc[j] = __ldg(s + kStep * j);
+    if (kScores) {
+      const uint4* r = reinterpret_cast<const uint4*>(a.rope + row * kRope) + rpiece;
+#pragma unroll
+      for (int j = 0; j < kRopePieces; ++j) rp[j] = __ldg(r + 4 * j);
     }
     return true;
   };
   bool more = next_block(true);
-  if (more) {
-    cp_async16(slot, src, have);
-    cp_async_commit();
-    cp_async16(slot + kConvWarps * 512, src + 64, have);
-    cp_async_commit();
-  }
-  uint8_t* const stage = base + kKvOff + g * (kScores ? kKBytes : kVBytes) + (p >> 1) * kReg;
-  const uint32_t o0 = tc::sw128_offset(rw, (p & 1) * 4);                            // chunk i of the four: o0 ^ 16 i
   uint32_t u = 0;                              // uses of the stage
   while (true) {
     // the tiles' queries pass through the same ring: nothing to widen
     for (; lead > 0; --lead, ++u) {
       if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
-      if (lane == 0) arrive(&sm.kv_full[g]);
+      if (lane == 0) arrive(&sm.q_place[g]);
     }
     if (!more) return;
-    const uint8_t* const src_now = src;
-    const bool have_now = have;
-    uint32_t sc = sc_a, sc_hi = sc_b;
-    more = next_block(false);
     if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
-    uint8_t* reg = stage;
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t raw = slot + (j & 1) * (kConvWarps * 512);
-      cp_async_wait<1>();
-      uint4 cw;
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(cw.x), "=r"(cw.y), "=r"(cw.z), "=r"(cw.w) : "r"(raw) : "memory");
-      const uint32_t two = e4m3x2_to_f16x2(uint16_t(sc));
-      sc = __funnelshift_r(sc, sc_hi, 16);
-      sc_hi >>= 16;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const uint32_t two = e4m3x2_to_f16x2(have ? sc[j] : uint16_t(0));
       const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-      // 16 code bytes: channels 32 (4 j + p) .. + 31, four chunks of region 2 j + p / 2
-      *reinterpret_cast<uint4*>(reg + o0) = widen8(cw.x, s0);
-      *reinterpret_cast<uint4*>(reg + (o0 ^ 16)) = widen8(cw.y, s0);
-      *reinterpret_cast<uint4*>(reg + (o0 ^ 32)) = widen8(cw.z, s1);
-      *reinterpret_cast<uint4*>(reg + (o0 ^ 48)) = widen8(cw.w, s1);
-      reg += 2 * kReg;
-      if (j < 2) cp_async16(raw, src_now + (j + 2) * 64, have_now);
-      else if (more) cp_async16(raw, src + (j - 2) * 64, have);
-      cp_async_commit();
+      uint8_t* d = reg + 2 * j * kRegion;
+      *reinterpret_cast<uint4*>(d + o0) = widen8(cw[j].x, s0);
+      *reinterpret_cast<uint4*>(d + (o0 ^ 16)) = widen8(cw[j].y, s0);
+      *reinterpret_cast<uint4*>(d + (o0 ^ 32)) = widen8(cw[j].z, s1);
+      *reinterpret_cast<uint4*>(d + (o0 ^ 48)) = widen8(cw[j].w, s1);
+    }
+    if (kScores) {
+#pragma unroll
+      for (int j = 0; j < kRopePieces; ++j)
+        *reinterpret_cast<uint4*>(stage + 8 * kRegion + tc::sw128_offset(srow, rpiece + 4 * j)) = rp[j];
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) arrive(&sm.kv_full[g]);
+    if (lane == 0) arrive_leader<G>(&sm.kv_full[g], kLeader);
     ++u;
+    more = next_block(false);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Scores CTA
 // ---------------------------------------------------------------------------
-// Copies by TMA into the ring: a tile's queries as two "blocks" of 64 rows, then
-// the rope keys of each block of positions (their region needs no widening; rows
-// behind the context are masked scores, whatever they hold).
-__device__ inline void scores_copy_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int lane,
-                                        const CUtensorMap* qmap, const CUtensorMap* rmap) {
-  Cursor cur(a.plan, cl, lane);
+// Copies a tile's queries by TMA into the ring, as two places of 64 rows.
+template <int G>
+__device__ inline void query_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int lane,
+                                  const CUtensorMap* qmap) {
+  Walk walk(a.plan, cl);
+  Item it;
   uint32_t m = 0;
-  bool more = cur.item(a);
-  while (more) {
-    if (cur.i == 0) {
-      const int y = cur.it.a.z * a.d.heads + cur.it.a.y;
+  while (walk.next(it)) {
+    const int y = it.a.z * a.d.heads + it.a.y + kDenseTile * part;
 #pragma unroll 1
-      for (int k = 0; k < 2; ++k, ++m) {
-        const uint32_t st = m % kKStages;
-        if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
-        if (lane == 0) {
-          tc::mbar_expect_tx(&sm.kv_full[st], kKBytes);
+    for (int k = 0; k < 2; ++k, ++m) {
+      const uint32_t st = m % kKStages;
+      if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
+      if (lane == 0) {
+        tc::mbar_expect_tx(&sm.q_place[st], kKBytes);
 #pragma unroll 1
-          for (int kb = 0; kb < 9; ++kb)
-            tc::tma_load_2d(qmap, base + kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.kv_full[st]);
-        }
-        __syncwarp();
+        for (int kb = 0; kb < 9; ++kb)
+          tc::tma_load_2d(qmap, base + kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.q_place[st]);
       }
+      __syncwarp();
     }
-    const uint32_t st = m % kKStages;
-    const int64_t row0 = cur.row0(a);
-    if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
-    if (lane == 0) {
-      tc::mbar_expect_tx(&sm.kv_full[st], kReg);
-      tc::tma_load_2d(rmap, base + kKvOff + st * kKBytes + 8 * kReg, 0, row0 < 0 ? 0 : int(row0), &sm.kv_full[st]);
-    }
-    __syncwarp();
-    ++m;
-    more = cur.step(a, 1) || cur.item(a);
+    // the places of the tile's blocks: only waited for, so that no parity is mistaken for an earlier one
+    for (int j = 0; j < it.n; ++j, ++m)
+      if (!wait_warp(sm, &sm.kv_empty[m % kKStages], ((m / kKStages) & 1) ^ 1, a.ws)) return;
   }
 }
 
+template <int G>
 __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, uint32_t tmem) {
   // latents are fp16, rope keys bf16 (each with queries of its type; one accumulator)
-  constexpr uint32_t id_lat = idesc_f16(kDenseTile, kDenseBlk, 0, 0), id_rope = tc::idesc_bf16(kDenseTile, kDenseBlk, 0, 0);
+  constexpr uint32_t id_lat = idesc_f16(kDenseTile * G, kDenseBlk, 0, 0);
+  constexpr uint32_t id_rope = tc::idesc_bf16(kDenseTile * G, kDenseBlk, 0, 0);
+  constexpr int kRegion = kReg / G;                  // 64 channels of the 64 / G positions of a CTA
+  constexpr uint16_t kBoth = 0x3;
   Walk walk(a.plan, cl);
   Item it;
-  uint32_t n = 0, m = 0;
+  uint32_t n = 0;
   const bool leader = elect_one();
   for (uint32_t k = 0; walk.next(it); ++k) {
-    m += 2;
     if (!wait_warp(sm, &sm.q_full, k & 1, a.ws)) return;
-    for (int j = 0; j < it.n; ++j, ++n, ++m) {
-      const uint32_t st = m % kKStages, buf = n % kSBufs;
-      if (!wait_warp(sm, &sm.kv_full[st], (m / kKStages) & 1, a.ws)) return;
+    for (int j = 0; j < it.n; ++j, ++n) {
+      const uint32_t st = n % kKStages, buf = n % kSBufs;
+      if (!wait_warp(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
       if (!wait_warp(sm, &sm.s_empty[buf], ((n / kSBufs) & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
       if (leader) {
@@ -461,9 +503,9 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
         for (int kb = 0; kb < 9; ++kb)
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4)
-            mma_ts(d, tmem + kb * 32 + k4 * 8, bd + ((kb * kReg + k4 * 32) >> 4), kb < 8 ? id_lat : id_rope, kb + k4 > 0);
-        tc::mma_commit(&sm.kv_empty[st]);
-        tc::mma_commit(&sm.s_full[buf]);
+            mma_ts<G>(d, tmem + kb * 32 + k4 * 8, bd + ((kb * kRegion + k4 * 32) >> 4), kb < 8 ? id_lat : id_rope, kb + k4 > 0);
+        commit_to<G>(&sm.kv_empty[st], kBoth);
+        commit_to<G>(&sm.s_full[buf], kBoth);
       }
       __syncwarp();
     }
@@ -474,15 +516,17 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
 // two warps of a row take turns, each with two block periods for the latencies of a
 // block.  What must go in order is the reference: block n's warp takes it from block
 // n - 1's as soon as that one has its maximum, and hands it on.
-__device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int rw, int lane,
+template <int G>
+__device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int rw, int lane,
                                     uint32_t tmem) {
   const int wq = rw & 3, half = rw >> 2;
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
   const int r = wq * 32 + lane;
   const float c2 = a.scale * 1.4426950408889634f;
   uint32_t n = 0, m = 0;
+  uint32_t zeroed = 0;                               // slots in which this warp's rows of P are zeros
   Cursor cur(a.plan, cl, lane);
-  while (cur.item(a)) {
+  for (uint32_t k_item = 0; cur.item(a); ++k_item) {
     // The tile's queries into tensor memory (rows 0..63 in the first half, 64..127 in the
     // second; a row's two warps take half of the channels each); the MMAs that read the
     // previous tile's are done (its last scores have been read, by one of the two warps,
@@ -496,7 +540,7 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       // start while the use before it is open
       some_sync(11 + wq, 64);
       const uint32_t mh = m + (wq >> 1), st = mh % kKStages;
-      if (!wait_warp(sm, &sm.kv_full[st], (mh / kKStages) & 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.q_place[st], k_item & 1, a.ws)) return;
       const uint8_t* src = base + kKvOff + st * kKBytes;
       uint32_t big = 0;
 #pragma unroll 1
@@ -537,13 +581,14 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       some_sync(9 + (wq >> 1), 128);
       if (lane == 0) {
         if ((wq & 1) == 0 && half == 0) arrive(&sm.kv_empty[st]);
-        arrive(&sm.q_full);
+        arrive_leader<G>(&sm.q_full, 0);
       }
       __syncwarp();
       m += 2 + cur.it.n;
     }
     // positions this row sees: first .. last
-    const int lr = cur.it.a.y + r, tok = lr / a.d.heads;
+    const int lr = cur.it.a.y + kDenseTile * part + r, tok = lr / a.d.heads;
+    const bool live = __any_sync(0xFFFFFFFFu, tok < cur.it.a.w);     // some row of this warp (and of its other half) exists
     int last = -1, first = 0;
     if (tok < cur.it.a.w) {
       last = a.causal ? cur.it.b.x - cur.it.a.w + tok : cur.it.b.x - 1;
@@ -559,7 +604,32 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       const int t0 = (cur.it.blk + cur.i) * kDenseBlk;
       const int lo = first - t0, hi = cur.row0(a) < 0 ? -1 : last - t0;
       const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kDenseBlk - 1);
+      uint8_t* ps = base + kPOff + slot * kPBytes;
       if (!wait_warp(sm, &sm.s_full[buf], (n / kSBufs) & 1, a.ws)) return;
+      if (!live) {
+        // no row at all (a decode tile of few heads): P stays zero
+        if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
+        if (!(zeroed >> slot & 1)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(ps + wq * 4096 + i * 512 + lane * 16) = make_uint4(0, 0, 0, 0);
+          sm.meta[slot][wq][0][lane] = 1.0f;
+          sm.meta[slot][wq][1][lane] = 0.0f;
+          sm.meta[slot][wq][2][lane] = 0.0f;
+          tc::fence_proxy_async_smem();
+          zeroed |= 1u << slot;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          arrive_leader<G>(&sm.s_empty[buf], 0);
+          const uint32_t bar = peer_addr(&sm.p_full[slot], uint32_t(G + part));
+          copy_to_peer(peer_addr(ps + wq * 4096, uint32_t(G + part)), ps + wq * 4096, 4096, bar);
+          copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], uint32_t(G + part)), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
+        }
+        __syncwarp();
+        cur.step(a, 2);
+        continue;
+      }
+      zeroed &= ~(1u << slot);
       tc::tc_fence_after_sync();
       const uint32_t scol = lanes + kSCol + buf * kDenseBlk;
       // two short passes over the scores in tensor memory: maximum, then weights
@@ -598,7 +668,6 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
       if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
-      uint8_t* ps = base + kPOff + slot * kPBytes;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float x[32];
@@ -629,10 +698,10 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive(&sm.s_empty[buf]);
-        const uint32_t bar = peer_addr(&sm.p_full[slot], 1);
-        copy_to_peer(peer_addr(ps + wq * 4096, 1), ps + wq * 4096, 4096, bar);
-        copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], 1), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
+        arrive_leader<G>(&sm.s_empty[buf], 0);
+        const uint32_t bar = peer_addr(&sm.p_full[slot], uint32_t(G + part));
+        copy_to_peer(peer_addr(ps + wq * 4096, uint32_t(G + part)), ps + wq * 4096, 4096, bar);
+        copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], uint32_t(G + part)), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
       }
       __syncwarp();
       cur.step(a, 2);
@@ -644,8 +713,10 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
 // ---------------------------------------------------------------------------
 // Values CTA
 // ---------------------------------------------------------------------------
+template <int G>
 __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, uint32_t tmem) {
-  constexpr uint32_t id = idesc_f16(kDenseTile, 256, 0, 1);
+  constexpr uint32_t id = idesc_f16(kDenseTile * G, 256, 0, 1);
+  constexpr uint16_t kBoth = 0xC;
   Walk walk(a.plan, cl);
   Item it;
   uint32_t n = 0;
@@ -655,8 +726,8 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
     for (int j = 0; j < it.n; ++j, ++n) {
       const uint32_t st = n % kKStages, slot = n % kPSlots, ph = (n / kPSlots) & 1;
       if (!wait_warp(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
-      if (!wait_warp(sm, &sm.p_full[slot], ph, a.ws)) return;
-      if (!wait_warp(sm, &sm.corr[slot], ph, a.ws)) return;
+      if (G == 1 && !wait_warp(sm, &sm.p_full[slot], ph, a.ws)) return;
+      if (!wait_warp(sm, &sm.corr[slot], ph, a.ws)) return;       // of a pair: both have seen their P arrive
       tc::tc_fence_after_sync();
       if (leader) {
         const uint64_t ad = tc::smem_desc(tc::smem_u32(base + kPOff + slot * kPBytes), 16, 1024, 2);
@@ -665,10 +736,10 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
         for (int ks = 0; ks < kDenseBlk / 16; ++ks)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            tc::mma_bf16(tmem + h * 256, ad + ((ks * 32) >> 4), bd + ((h * 4 * kReg + ks * 2048) >> 4), id,
-                         j > 0 || ks > 0);
-        tc::mma_commit(&sm.kv_empty[st]);
-        tc::mma_commit(&sm.pv_done[slot]);
+            mma_ss<G>(tmem + h * 256, ad + ((ks * 32) >> 4), bd + ((h * (4 / G) * kReg + ks * 2048) >> 4), id,
+                      j > 0 || ks > 0);
+        commit_to<G>(&sm.kv_empty[st], kBoth);
+        commit_to<G>(&sm.pv_done[slot], kBoth);
       }
       __syncwarp();
     }
@@ -676,20 +747,22 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
 }
 
 // Hands each slot of P back once its products are done.
-__device__ inline void slot_role(const DenseArgs& a, DenseSmall& sm, int cl) {
+template <int G>
+__device__ inline void slot_role(const DenseArgs& a, DenseSmall& sm, int cl, int part) {
   Walk walk(a.plan, cl);
   for (int n = 0, all = walk.left; n < all; ++n) {
     const uint32_t slot = uint32_t(n) % kPSlots;
     if (!wait_on(sm, &sm.pv_done[slot], (uint32_t(n) / kPSlots) & 1, a.ws)) return;
     if (n + kPSlots < all) {
       tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
-      arrive_remote(peer_addr(&sm.p_free[slot], 0));
+      arrive_remote(peer_addr(&sm.p_free[slot], uint32_t(part)));
     }
   }
 }
 
 // Warp rw: rows 32 (rw % 4) .. + 31 (one a lane), channels 256 (rw / 4) .. + 255.
-__device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int rw, int lane,
+template <int G>
+__device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int rw, int lane,
                                    uint32_t tmem) {
   const int wq = rw & 3, col0 = 256 * (rw >> 2);
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16) + uint32_t(col0);
@@ -725,7 +798,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
         tc::tc_fence_before_sync();
       }
       __syncwarp();
-      if (lane == 0) arrive(&sm.corr[slot]);
+      if (lane == 0) arrive_leader<G>(&sm.corr[slot], G);
     }
     const uint32_t m = n - 1;
     if (!wait_warp(sm, &sm.pv_done[m % kPSlots], (m / kPSlots) & 1, a.ws)) return;
@@ -733,9 +806,9 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     if (sum_b > 0.0f) sum += sum_b * ex2(sub_b - sub);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const float lse = sum > 0.0f ? (sub + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-    const int lr = it.a.y + r, rows = it.a.w * a.d.heads;
+    const int lr = it.a.y + kDenseTile * part + r, rows = it.a.w * a.d.heads;
     if (it.head || it.tail) {
-      const int slot = 2 * cl + (it.head ? 0 : 1);
+      const int slot = (2 * cl + (it.head ? 0 : 1)) * G + part;
       float* po = a.part_o + (int64_t(slot) * kLatent + col0) * kDenseTile + r;
       if (col0 == 0) a.part_lse[slot * kDenseTile + r] = lse;
 #pragma unroll 1
@@ -746,8 +819,8 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
         for (int i = 0; i < 32; ++i) po[(col + i) * kDenseTile] = v[i] * inv;
       }
     } else {
-      const int64_t g0 = int64_t(it.a.z) * a.d.heads + it.a.y + wq * 32;    // the warp's first row
-      const int have = rows - it.a.y - wq * 32;                             // rows of it that exist (any number)
+      const int64_t g0 = int64_t(it.a.z) * a.d.heads + lr - lane;           // the warp's first row
+      const int have = rows - (lr - lane);                                  // rows from it on that exist
       if (col0 == 0 && lr < rows) a.lse[g0 + lane] = lse;
       uint16_t* dst = a.out + g0 * kLatent + col0 + 8 * (lane & 3);
 #pragma unroll 1
@@ -774,66 +847,68 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     }
     tc::tc_fence_before_sync();
     __syncwarp();
-    if (lane == 0) arrive(&sm.o_free);
+    if (lane == 0) arrive_leader<G>(&sm.o_free, G);
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
-    dense_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap) {
+template <int G>
+__device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ DenseSmall sm;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int rank = blockIdx.x & 1, cl = blockIdx.x >> 1;
-  if (wid == 0) tc::tmem_alloc(&sm.tmem_slot, kTmemAll);
+  const int rank = blockIdx.x % (2 * G), cl = blockIdx.x / (2 * G), part = rank % G;
+  const bool scores = rank < G;
+  if (wid == 0) tmem_alloc_all<G>(&sm.tmem_slot);
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      tc::mbar_init(&sm.kv_full[i], rank == 0 ? 9 : 8);   // a group's warps, and the copying thread
+      tc::mbar_init(&sm.kv_full[i], 8 * G);          // a group's warps of every CTA of the pair
       tc::mbar_init(&sm.kv_empty[i], 1);
+      tc::mbar_init(&sm.q_place[i], 9);              // a group's warps and the copying thread
     }
     for (int i = 0; i < kSBufs; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.s_empty[i], 4);
+      tc::mbar_init(&sm.s_empty[i], 4 * G);
     }
-    tc::mbar_init(&sm.q_full, kRowWarps);
+    tc::mbar_init(&sm.q_full, kRowWarps * G);
     for (int i = 0; i < kPSlots; ++i) {
       tc::mbar_init(&sm.p_free[i], 1);
       tc::mbar_init(&sm.p_full[i], 1);
-      tc::mbar_init(&sm.corr[i], kRowWarps);
+      tc::mbar_init(&sm.corr[i], kRowWarps * G);
       tc::mbar_init(&sm.pv_done[i], 1);
     }
-    tc::mbar_init(&sm.o_free, kRowWarps);
+    tc::mbar_init(&sm.o_free, kRowWarps * G);
     tc::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     tc::fence_mbar_init();
-    if (rank == 1)
+    if (!scores)
       for (int i = 0; i < kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + 4 * kMetaWarp);
   }
   tc::tc_fence_before_sync();
   __syncthreads();
   tc::tc_fence_after_sync();
-  // both CTAs' barriers stand before either writes into the other
+  // every CTA's barriers stand before another writes into it
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const uint32_t tmem = sm.tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
-  if (rank == 0) {
-    if (wid < kConvWarps) widen_role<true>(a, sm, base, cl, wid, lane);
-    else if (wid < kRowWarp0 + kRowWarps) softmax_role(a, sm, base, cl, wid - kRowWarp0, lane, tmem);
-    else if (wid == kMmaWarp) scores_mma_role(a, sm, base, cl, tmem);
-    else scores_copy_role(a, sm, base, cl, lane, &qmap, &rmap);
+  if (scores) {
+    if (wid < kConvWarps) widen_role<G, true>(a, sm, base, cl, part, wid, lane);
+    else if (wid < kRowWarp0 + kRowWarps) softmax_role<G>(a, sm, base, cl, part, wid - kRowWarp0, lane, tmem);
+    else if (wid > kMmaWarp) query_role<G>(a, sm, base, cl, part, lane, qmap);
+    else if (part == 0) scores_mma_role<G>(a, sm, base, cl, tmem);
   } else {
-    if (wid < kConvWarps) widen_role<false>(a, sm, base, cl, wid, lane);
-    else if (wid < kRowWarp0 + kRowWarps) output_role(a, sm, base, cl, wid - kRowWarp0, lane, tmem);
-    else if (wid == kMmaWarp) values_mma_role(a, sm, base, cl, tmem);
-    else if (lane == 0) slot_role(a, sm, cl);
+    if (wid < kConvWarps) widen_role<G, false>(a, sm, base, cl, part, wid, lane);
+    else if (wid < kRowWarp0 + kRowWarps) output_role<G>(a, sm, base, cl, part, wid - kRowWarp0, lane, tmem);
+    else if (wid == kMmaWarp && part == 0) values_mma_role<G>(a, sm, base, cl, tmem);
+    else if (wid > kMmaWarp && lane == 0) slot_role<G>(a, sm, cl, part);
   }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
   __syncwarp();
-  if (wid == kMmaWarp) {
+  if (wid == kMmaWarp && part == 0) {
     if (elect_one()) {
-      tc::mma_commit(&sm.drain);
+      commit_to<G>(&sm.drain, uint16_t(1u << rank));
       wait_slow(sm, &sm.drain, 0, a.ws);
     }
     __syncwarp();
@@ -841,11 +916,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
   tc::tc_fence_before_sync();
   __syncthreads();
   tc::tc_fence_after_sync();
-  // neither CTA leaves while the other may still write into it
+  // no CTA leaves (or frees a pair's tensor memory) while another may still write into it
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (wid == 0) tc::tmem_dealloc(tmem, kTmemAll);
+  if (wid == 0) tmem_free_all<G>(tmem);
 }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
+    dense_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap) { dense_body<1>(a, &qmap); }
+
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kDenseThreads, 1)
+    dense_pair_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap) { dense_body<2>(a, &qmap); }
 
 // ---------------------------------------------------------------------------
 // Plan: one CTA.  Sequences -> tiles of 128 rows -> blocks each tile sees ->
@@ -922,7 +1003,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a
     __syncthreads();
     if ((tid & 31) == 0) from = tid == 0 ? reach : edge[(tid >> 5) - 1];
     const int len = b < a.batch ? upto - from : 0;
-    const int64_t tiles = (int64_t(len) * H + kDenseTile - 1) / kDenseTile;
+    const int64_t tiles = (int64_t(len) * H + a.tile - 1) / a.tile;
     int64_t all;
     const int64_t at = block_scan_sum(tiles, buf, all);
     if (b < a.batch) {
@@ -946,8 +1027,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a
         else hi = mid - 1;
       }
       const int4 s = a.plan.seqs[lo];
-      const int row0 = (t - s.x) * kDenseTile;
-      const int tok0 = row0 / H, tok1 = min(s.z - 1, (row0 + kDenseTile - 1) / H);
+      const int row0 = (t - s.x) * a.tile;
+      const int tok0 = row0 / H, tok1 = min(s.z - 1, (row0 + a.tile - 1) / H);
       int first = 0, last = s.w - 1;
       if (a.causal) {
         last = s.w - s.z + tok1;
@@ -996,17 +1077,17 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int r = threadIdx.x, g = blockIdx.x, c = blockIdx.y;
+  const int G = a.tile / kDenseTile, part = blockIdx.z;
   const int4 head = __ldg(a.plan.head);
   if (c < head.y) {
     const int4 run = __ldg(a.plan.runs + c);
     const int64_t w0 = run.y;                        // blocks of the tile before this run
     if (w0 > 0) {
       const int4 ta = __ldg(a.plan.tiles + 2 * run.x), tb = __ldg(a.plan.tiles + 2 * run.x + 1);
-      const int64_t before = __ldg(a.plan.before + run.x);
       const int4 prev = __ldg(a.plan.runs + c - 1);
       // first boundary inside: the run before starts at or before the tile's first block
       const bool mine = prev.x != run.x || prev.y == 0;
-      const int lr = ta.y + r;
+      const int lr = ta.y + kDenseTile * part + r;
       if (mine && lr < ta.w * a.d.heads) {
         // last run that touches the tile
         int c1 = c;
@@ -1015,10 +1096,9 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
           ++c1;
           done += __ldg(a.plan.runs + c1).z;
         }
-        (void)before;
         const int n = c1 - c + 2;                    // pieces: runs c - 1 .. c1
         // the first piece ends the run before (its tail); the others start theirs
-        const auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i); };
+        const auto slot = [&](int i) { return (i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * G + part; };
         float top = -INFINITY;
         for (int i = 0; i < n; ++i) top = fmaxf(top, a.part_lse[slot(i) * kDenseTile + r]);
         float o[kMergeCh], total = 0.0f;
@@ -1045,15 +1125,15 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
       }
     }
   }
-  const int ctas = gridDim.x * gridDim.y;
-  for (int t = blockIdx.y * gridDim.x + blockIdx.x; t < head.x; t += ctas) {
+  const int ctas = gridDim.x * gridDim.y * gridDim.z;
+  for (int t = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x; t < head.x; t += ctas) {
     if (__ldg(a.plan.tiles + 2 * t + 1).z != 0) continue;
     const int4 ta = __ldg(a.plan.tiles + 2 * t);
-    const int rows = min(kDenseTile, ta.w * a.d.heads - ta.y);
+    const int rows = min(a.tile, ta.w * a.d.heads - ta.y);
     const int64_t row = int64_t(ta.z) * a.d.heads + ta.y;
     for (int i = r; i < rows * (kLatent / 8); i += kDenseTile)
       reinterpret_cast<uint4*>(a.out + row * kLatent)[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows) a.lse[row + r] = -INFINITY;
+    for (int i = r; i < rows; i += kDenseTile) a.lse[row + i] = -INFINITY;
   }
 }
 
@@ -1070,33 +1150,66 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// Clusters of 2 G CTAs that run at the same time on the current device (asked once per
+// device): the runs of a call are cut for that many.  Fewer fit than SMs / (2 G) where
+// a GPU processing cluster's SM count is no multiple of 2 G.
+int resident_clusters(void (*kernel)(DenseArgs, const CUtensorMap), int G, size_t smem) {
+  static std::atomic<int> known[2][kMaxDevices];
+  const int most = kDenseMaxClusters / G;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return most;
+  const bool slot = dev >= 0 && dev < kMaxDevices;
+  if (slot) {
+    const int n = known[G - 1][dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(unsigned(2 * G * most));
+  cfg.blockDim = dim3(kDenseThreads);
+  cfg.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(2 * G);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = int(min64(most, device_sms() / (2 * G)));
+  }
+  n = n < 1 ? 1 : n > most ? most : n;
+  if (slot) known[G - 1][dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace
 
 cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
-  a.clusters = int(min64(kDenseMaxClusters, device_sms() / 2));
-  if (a.clusters < 1) a.clusters = 1;
-  CUtensorMap qmap, rmap;
+  // Tiles of 128 rows on 2 SMs or of 256 rows on 4: the larger one widens each block
+  // once for twice the rows, and wastes up to 255 rows of a sequence instead of 127.
+  const int G = dense_pairs(a.d.heads, a.batch, a.total_q) ? 2 : 1;
+  a.tile = kDenseTile * G;
+  CUtensorMap qmap;
   if (!encode_2d_cached(tensor_map_encoder(), &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk,
                         uint64_t(a.total_q) * a.d.heads, kDqk * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
-  const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
-  if (!encode_2d_cached(tensor_map_encoder(), &rmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rope, kRope, rows, kRope * 2, 64,
-                        64, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
-    return cudaErrorUnknown;
-  static KernelAttrs attrs;
+  static KernelAttrs attrs[2];
   constexpr size_t smem = size_t(kDenseSmem) + 1024;
-  cudaError_t e = prepare_kernel(dense_kernel, smem, false, attrs);
+  auto kernel = G == 2 ? dense_pair_kernel : dense_kernel;
+  cudaError_t e = prepare_kernel(kernel, smem, false, attrs[G - 1]);
   if (e != cudaSuccess) return e;
+  a.clusters = resident_clusters(kernel, G, smem);
   CSA2_PROFILED(st, "dense_plan", (e = launch_pdl(dense_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_attn",
-                (e = launch_pdl(dense_kernel, dim3(unsigned(2 * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, qmap,
-                                rmap)));
+                (e = launch_pdl(kernel, dim3(unsigned(2 * G * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, qmap)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_merge",
-                (e = launch_pdl(dense_merge_kernel, dim3(kLatent / kMergeCh, unsigned(a.clusters)), dim3(kDenseTile), 0,
-                                st, 1, a)));
+                (e = launch_pdl(dense_merge_kernel, dim3(kLatent / kMergeCh, unsigned(a.clusters), unsigned(G)),
+                                dim3(kDenseTile), 0, st, 1, a)));
   return e;
 }
 

@@ -22,6 +22,7 @@ struct DensePlan {
 struct DenseArgs {
   csa2_dims d;
   int batch, total_q, causal, window, clusters;
+  int tile;            // rows of a tile: 128, or 256 on twice the SMs
   const uint16_t* q;
   const int32_t* q_start;
   const uint8_t* codes;
@@ -34,8 +35,8 @@ struct DenseArgs {
   float* lse;
   uint8_t* ws;
   DensePlan plan;
-  float* part_o;       // [2 * clusters][512][128]
-  float* part_lse;     // [2 * clusters][128]
+  float* part_o;       // [2 * clusters * tile / 128][512][128]
+  float* part_lse;     // [2 * clusters * tile / 128][128]
 };
 
 // Byte offsets in the workspace: error word, plan, partial outputs.
@@ -56,6 +57,11 @@ inline DenseLayout make_dense_layout(const csa2_dims& d, int64_t batch, int64_t 
   L.part_o = off;   off = align256(off + int64_t(2 * kDenseMaxClusters) * kDenseTile * kLatent * 4);
   L.total = off;
   return L;
+}
+
+// Whether a call takes tiles of 256 rows.
+inline bool dense_pairs(int heads, int batch, int64_t total_q) {
+  return total_q * heads >= int64_t(512) * batch;
 }
 
 cudaError_t launch_dense(DenseArgs a, cudaStream_t st);
