@@ -52,12 +52,13 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kConvWarps = 16;                      // two groups of 8, one for each ring stage
-constexpr int kRowWarp0 = kConvWarps;               // eight warps: lane quarter (w % 4) x (w / 4): the scores of every
-                                                    // other block (rank 0), half of the output channels (rank 1)
-constexpr int kRowWarps = 8;
-constexpr int kMmaWarp = kRowWarp0 + kRowWarps;
-constexpr int kDenseThreads = (kMmaWarp + 2) * 32;  // the last warp: copies (scores CTA), slots (values CTA)
+constexpr int kRowWarps = 8;                        // lane quarter (w % 4) x (w / 4): the scores of every other block
+                                                    // (scores CTA), half of the output channels (values CTA)
+constexpr int kConvWarp0 = kRowWarps, kConvWarps = 16;   // two groups of 8, one for each ring stage
+constexpr int kMmaWarp = kRowWarps + kConvWarps;
+// warp kMmaWarp: query copies and MMAs (scores CTA), MMAs and slots (values CTA); the next
+// one: copies from the cache; two more make them a warpgroup and only give their registers
+constexpr int kDenseThreads = (kMmaWarp + 4) * 32;
 
 constexpr int kReg = kDenseBlk * 128;               // 64 channels x 64 positions of 16-bit: 8 KB
 constexpr int kPSlots = 3;
@@ -68,17 +69,23 @@ constexpr int kVBytes = 8 * kReg;                   // 512 channels
 constexpr int kPOff = 0;
 constexpr int kKvOff = kPOff + kPSlots * kPBytes;
 constexpr int kStageOff = kKvOff + kKStages * kVBytes;   // values CTA: output staging, 2 KB a warp
-constexpr int kDenseSmem = kKvOff + kKStages * kKBytes;
-static_assert(kStageOff + kRowWarps * 2048 <= kDenseSmem, "output staging of the values CTA");
+// Raw bytes of the blocks to widen, as they come from the cache: G stages of 64 / G rows
+// (scores CTA) or of 64 rows x 1 / G of the codes (values CTA): rope keys, codes, scales.
+constexpr int kRawOff = kKvOff + kKStages * kKBytes;
+constexpr int kRawRope = kDenseBlk * kRope * 2, kRawCodes = kDenseBlk * kCodesPerRow, kRawScales = kDenseBlk * kScalesPerRow;
+constexpr int kRawBytes = kRawRope + kRawCodes + kRawScales;
+constexpr int kDenseSmem = kRawOff + kRawBytes;
+static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
 constexpr int kSBufs = 3;
 constexpr int kMetaWarp = 3 * 32 * 4;               // alpha, sum, reference of a warp's rows
 
 struct DenseSmall {
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t kv_full[kKStages], kv_empty[kKStages];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
-  uint64_t q_place[kKStages];                       // queries in a ring stage (and the group's turn passed)
+  uint64_t q_turn[kKStages], q_place[kKStages];     // a ring stage free for queries; holding them
   uint64_t q_full;
   uint64_t p_free[kPSlots];                         // scores CTA: slot read by the values CTA (remote arrival)
   uint64_t p_full[kPSlots];                         // values CTA: bytes of P and meta have arrived
@@ -88,6 +95,7 @@ struct DenseSmall {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
+  int raw_rows[2];                                  // rows of the raw block before the context's end (0: bad page)
   __align__(16) float meta[kPSlots][4][3][32];
   uint32_t swap[2][kDenseTile];                     // row maxima of the queries, between a row's two warps
   float ref[2][kDenseTile];                         // softmax reference, handed from block to block
@@ -119,33 +127,34 @@ __device__ inline void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
-// One try, which suspends the thread for a while the hardware chooses.
-__device__ inline bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// One try, which suspends the thread for a while the hardware chooses.  kCluster: acquires
+// what another CTA wrote.
+template <bool kCluster>
+__device__ inline bool try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(tc::smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
   return done != 0;
-}
-
-// Arrive on a barrier of the pair's leading CTA (the one that issues its MMAs).
-template <int G>
-__device__ inline void arrive_leader(uint64_t* bar, int leader) {
-  if constexpr (G == 1) arrive(bar);
-  else arrive_remote(peer_addr(bar, uint32_t(leader)));
 }
 
 // Every wait of the kernel: bounded (200 ms against microseconds; the clock is only read
 // after some tries, it takes longer than most waits), and cut short once another role
 // of the CTA has given up.  False: the caller's role ends.
-__device__ __noinline__ bool wait_slow(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
+template <bool kCluster>
+__device__ __forceinline__ bool wait_slow(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (try_wait<kCluster>(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
     if ((i & 31u) == 0) {
       const uint64_t t = tc::globaltimer_ns();
@@ -158,12 +167,17 @@ __device__ __noinline__ bool wait_slow(DenseSmall& sm, uint64_t* bar, uint32_t p
     }
   }
 }
-__device__ inline bool wait_on(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
-  return try_wait_cluster(bar, parity) || wait_slow(sm, bar, parity, ws);
-}
-// the same for a converged warp: one answer for all lanes
+// for a converged warp: one answer for all lanes
+template <bool kCluster = false>
 __device__ inline bool wait_warp(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
-  return __all_sync(0xFFFFFFFFu, wait_on(sm, bar, parity, ws));
+  return __all_sync(0xFFFFFFFFu, try_wait<kCluster>(bar, parity) || wait_slow<kCluster>(sm, bar, parity, ws));
+}
+
+// Arrive on a barrier of the pair's leading CTA (the one that issues its MMAs).
+template <int G>
+__device__ inline void arrive_leader(uint64_t* bar, int leader) {
+  if constexpr (G == 1) arrive(bar);
+  else arrive_remote(peer_addr(bar, uint32_t(leader)));
 }
 
 // D[tmem] (+)= A * B[smem]^T over one CTA (G 1) or a pair (G 2: rows of both, B
@@ -228,6 +242,20 @@ __device__ inline bool elect_one() {
 __device__ inline void some_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ inline void some_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
+__device__ inline void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ inline uint32_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ inline uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ inline void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -237,6 +265,35 @@ __device__ inline void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16])
       : "memory");
 }
 __device__ inline void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations an instruction.
+__device__ inline uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ inline void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Registers a thread of the calling warpgroup.  72 a thread are launched (seven warps on
+// a quarter of the SM allow no more): the widening warps give 16 each and the last
+// warpgroup 32, the 8 row warps, which hold 64 scores a thread, take 48.
+template <int n>
+__device__ inline void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
+template <int n>
+__device__ inline void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
+constexpr int kLaunchRegs = 72, kConvRegs = 56, kRowRegs = 120, kMmaRegs = 40;
+static_assert(kConvWarps * kConvRegs + kRowWarps * kRowRegs + 4 * kMmaRegs <= kLaunchRegs * (kDenseThreads / 32),
+              "a split above what was launched would wait for ever");
 
 __device__ inline float ex2(float x) {
   float y;
@@ -316,7 +373,7 @@ struct Cursor {
   Walk walk;
   Item it;
   int i, pages, lane;
-  __device__ Cursor(const DensePlan& p, int c, int lane_) : walk(p, c), i(0), pages(0), lane(lane_) {}
+  __device__ Cursor(const DensePlan& p, int c, int lane_) : walk(p, c), it{}, i(0), pages(0), lane(lane_) {}
   __device__ void load_pages(const DenseArgs& a) {
     const int at = (i & ~31) + lane;
     if (a.page_table && at < it.n) pages = __ldg(a.page_table + int64_t(it.a.x) * a.d.max_pages + it.blk + at);
@@ -344,17 +401,56 @@ struct Cursor {
 };
 
 // ---------------------------------------------------------------------------
+// A block's bytes come from the cache by TMA, asked for by a warp that runs ahead
+// (raw_role), so the widening warps hold no addresses and wait for no loads.  (The same
+// bytes by the widening threads' own loads, into registers or by cp.async, 16 bytes
+// each: the SM's load path takes half of the kernel's time; 387 against 229 us without
+// any loads, 128K decode batch.)
+//
 // Widening warps (every CTA): E2M1 x E4M3 -> fp16, exact (6 significant bits, 2^-10 ..
-// 2688).  Group g = w / 8 fills ring stage g (every other block).  A lane takes 16
-// bytes of codes (32 channels) of one row at a time, lane = 8 * piece + row: a
-// quarter-warp stores one 16-byte chunk of 8 rows (all 32 banks, 128-byte swizzle), a
-// load reads 64 contiguous bytes of 8 rows.  A block's codes, scales and rope keys are
-// loaded into registers as soon as the block before (of this stage) is stored, two
-// block periods before they are used.
-//   G 1: scores and values CTA each take 64 rows x 512 channels (4 pieces a lane);
-//   G 2: a scores CTA takes its 32 of the 64 rows, a values CTA its 256 of the 512
-//        channels (128 of each 256-column product): 2 pieces a lane.
+// 2688).  A lane takes 16 bytes of codes (32 channels) of one row at a time, lane = 8 *
+// piece + row: a quarter-warp reads and stores one 16-byte chunk of 8 rows (all 32 banks,
+// 64- and 128-byte swizzle).  Two such pieces a lane and block:
+//   G 1: the 16 warps take every block together, 64 rows x 512 channels;
+//   G 2: 8 warps take every other block (those of one ring stage); a scores CTA has 32
+//        of the 64 rows, a values CTA 256 of the 512 channels (128 of each 256-column
+//        product).
 // ---------------------------------------------------------------------------
+// Copies the run's blocks into the raw stages.
+template <int G, bool kScores>
+__device__ inline void raw_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int lane,
+                                const CUtensorMap* codes, const CUtensorMap* scales, const CUtensorMap* rope) {
+  constexpr int kRows = G == 2 && kScores ? 32 : 64;
+  constexpr uint32_t kBytes = (kScores ? kRawRope / G : 0) + kRawCodes / G + kRows * kScalesPerRow;
+  Cursor cur(a.plan, cl, lane);
+  uint32_t n = 0;
+  for (bool more = cur.item(a); more; more = cur.step(a, 1) || cur.item(a), ++n) {
+    const uint32_t st = n % G;
+    const int64_t row0 = cur.row0(a);
+    if (kScores && part == 0 && row0 < 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
+    const int first = G == 2 && kScores ? 32 * part : 0;              // first of this CTA's rows in the block
+    const int rows = row0 < 0 ? 0 : max(0, min(kRows, cur.it.b.x - (cur.it.blk + cur.i) * kDenseBlk - first));
+    if (!wait_warp(sm, &sm.raw_empty[st], ((n / G) & 1) ^ 1, a.ws)) return;
+    if (lane == 0) {
+      uint8_t* raw = base + kRawOff + st * (kRawBytes / G);
+      uint64_t* bar = &sm.raw_full[st];
+      const int y = int(row0 < 0 ? 0 : row0) + first;
+      sm.raw_rows[st] = rows;
+      tc::mbar_expect_tx(bar, kBytes);
+#pragma unroll 1
+      for (int h = 0; h < kRows / 32; ++h) {
+        if (kScores) tc::tma_load_2d(rope, raw + h * 4096, 0, y + 32 * h, bar);
+        uint8_t* c = raw + kRawRope / G + h * 2048;
+#pragma unroll 1
+        for (int k = 0; k < (G == 2 && !kScores ? 2 : 4); ++k)        // 64 code bytes (128 channels) of 32 rows
+          tc::tma_load_2d(codes, c + k * kRows * 64, G == 2 && !kScores ? 128 * k + 64 * part : 64 * k, y + 32 * h, bar);
+        tc::tma_load_2d(scales, raw + kRawRope / G + kRawCodes / G + h * 1024, 0, y + 32 * h, bar);
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // One 4-byte word of codes: 8 channels under one scale (twice in sc2).
 __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
   return make_uint4(mul_f16x2(e2m1_byte_f16x2<0>(w), sc2), mul_f16x2(e2m1_byte_f16x2<1>(w), sc2),
@@ -363,133 +459,116 @@ __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
 
 template <int G, bool kScores>
 __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int w, int lane) {
-  constexpr int kPieces = 4 / G, kRopePieces = kScores ? 2 / G : 0;
+  constexpr int kPieces = 2;
   constexpr int kLead = kScores ? 2 : 0;       // ring places of a tile's queries before its blocks
   constexpr int kLeader = kScores ? 0 : G;
-  const int g = w >> 3, w8 = w & 7, p = lane >> 3;
-  // row in the stage, row in the block, first piece of 16 code bytes and the step to the next, region of the first piece
-  const int srow = 8 * (G == 2 && kScores ? w8 & 3 : w8) + (lane & 7);
-  const int brow = G == 2 && kScores ? 32 * part + srow : srow;
-  const int piece = G == 1 ? p : kScores ? 8 * (w8 >> 2) + p : 4 * part + p;
-  constexpr int kStep = G == 2 && !kScores ? 8 : 4;
-  constexpr int kStageRows = G == 2 && kScores ? 32 : 64;
-  constexpr int kRegion = kStageRows * 128;
-  const int region = (G == 2 && !kScores ? 0 : 2 * (piece >> 2)) + (p >> 1);
-  const int rpiece = G == 1 ? p : (w8 >> 2) * 4 + p;                                // rope: 16 bytes, 8 channels
-  uint8_t* const stage = base + kKvOff + g * (kScores ? kKBytes : kVBytes);
-  uint8_t* const reg = stage + region * kRegion;
-  const uint32_t o0 = tc::sw128_offset(srow, (p & 1) * 4);                         // chunk i of the four: o0 ^ 16 i
-  Cursor cur(a.plan, cl, lane);
+  constexpr bool kColumns = G == 2 && !kScores;
+  constexpr int kRows = G == 2 && kScores ? 32 : 64;
+  constexpr int kRegion = kRows * 128;
+  constexpr uint32_t kStageBytes = kScores ? kKBytes : kVBytes;
+  const int g = G == 2 ? w >> 3 : 0;           // G 2: the warp's ring and raw stage
+  const int w8 = w & 7, p = lane >> 3;
+  const int hi = G == 1 ? w >> 3 : kScores ? w8 >> 2 : 0;             // half of the channels (256) this warp takes
+  const int row = 8 * (G == 2 && kScores ? w8 & 3 : w8) + (lane & 7);  // in the stage
+  // first raw piece (64-byte group; the next is one on), its scales, first region (the next is two on)
+  const uint32_t raw = tc::smem_u32(base) + kRawOff + g * (kRawBytes / G);
+  const uint32_t src = raw + kRawRope / G + 2 * hi * kRows * 64 + row * 64 + ((p ^ ((row >> 1) & 3)) << 4);
+  const uint32_t ssrc = raw + kRawRope / G + kRawCodes / G + row * kScalesPerRow + 2 * (kColumns ? 4 * part + p : 8 * hi + p);
+  constexpr uint32_t kScaleStep = kColumns ? 16 : 8;
+  const uint32_t o_rope = tc::sw128_offset(row, hi * 4 + p);          // rope: one 16-byte chunk a lane
+  const uint32_t dst = tc::smem_u32(base) + kKvOff + (4 * hi + (p >> 1)) * kRegion;
+  const uint32_t o0 = tc::sw128_offset(row, (p & 1) * 4);             // chunk i of a piece's four: o0 ^ 16 i
+  Walk walk(a.plan, cl);
+  Item it = {};
+  uint32_t u = 0, v = 0;                       // uses of the ring (G 1: places, G 2: of the stage) and of the raw stage
+  const auto stage_of = [&]() { return G == 1 ? u % kKStages : uint32_t(g); };
+  const auto parity_of = [&]() { return ((G == 1 ? u / kKStages : u) & 1) ^ 1; };
   int place = 0;                               // ring place (mod 2) of the item's start
-  int lead = 0;                                // query places of this stage to pass before the next block
-  uint4 cw[kPieces], rp[kRopePieces + 1];
-  uint16_t sc[kPieces];
-  bool have = false;
-  // the run's next block of this stage; false at its end
-  const auto next_block = [&](bool first) {
-    bool in = !first && cur.step(a, 2);
-    while (!in) {
-      if (!first) place = (place + kLead + cur.it.n) & 1;
-      first = false;
-      if (!cur.item(a, (g - place) & 1)) return false;
-      lead += kLead / 2;
-      in = cur.i < cur.it.n;
+  while (walk.next(it)) {
+    // the tile's queries pass through the same ring: nothing to widen
+#pragma unroll 1
+    for (int k = 0; k < kLead / G; ++k, ++u) {
+      if (!wait_warp(sm, &sm.kv_empty[stage_of()], parity_of(), a.ws)) return;
+      if (lane == 0) arrive(&sm.q_turn[stage_of()]);
     }
-    const int64_t row0 = cur.row0(a);
-    if (kScores && part == 0 && row0 < 0 && w8 == 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
-    // rows behind the context hold anything: their scale is taken as 0 (0 * P stays 0; their
-    // scores are masked).  The loads are unconditional, from row 0 in their place, so that
-    // nothing waits for them here.
-    have = row0 >= 0 && (cur.it.blk + cur.i) * kDenseBlk + brow < cur.it.b.x;
-    const int64_t row = have ? row0 + brow : 0;
-    const uint4* c = reinterpret_cast<const uint4*>(a.codes + row * kCodesPerRow) + piece;
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(a.scales + row * kScalesPerRow) + piece;
+#pragma unroll 1
+    for (int i = G == 2 ? (g - place) & 1 : 0; i < it.n; i += G, ++u, ++v) {
+      if (!wait_warp(sm, &sm.raw_full[g], v & 1, a.ws)) return;
+      uint4 cw[kPieces], rp;
+      uint32_t sc[kPieces];
+      const bool have = row < sm.raw_rows[g];
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) cw[j] = __ldg(c + kStep * j);
+      for (int j = 0; j < kPieces; ++j) {
+        cw[j] = ld_shared16(src + j * kRows * 64);
+        sc[j] = ld_shared_u16(ssrc + j * kScaleStep);
+      }
+      if (kScores) rp = ld_shared16(raw + o_rope);
+      __syncwarp();
+      if (lane == 0) arrive(&sm.raw_empty[g]);
+      const uint32_t st = stage_of();
+      if (!wait_warp(sm, &sm.kv_empty[st], parity_of(), a.ws)) return;
+      const uint32_t d = dst + st * kStageBytes;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) sc[j] = __ldg(s + kStep * j);
-    if (kScores) {
-      const uint4* r = reinterpret_cast<const uint4*>(a.rope + row * kRope) + rpiece;
-#pragma unroll
-      for (int j = 0; j < kRopePieces; ++j) rp[j] = __ldg(r + 4 * j);
+      for (int j = 0; j < kPieces; ++j) {
+        // rows behind the context hold anything: their scale is taken as 0 (0 * P stays 0; their scores are masked)
+        const uint32_t two = e4m3x2_to_f16x2(uint16_t(have ? sc[j] : 0u));
+        const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+        st_shared16(d + 2 * j * kRegion + o0, widen8(cw[j].x, s0));
+        st_shared16(d + 2 * j * kRegion + (o0 ^ 16), widen8(cw[j].y, s0));
+        st_shared16(d + 2 * j * kRegion + (o0 ^ 32), widen8(cw[j].z, s1));
+        st_shared16(d + 2 * j * kRegion + (o0 ^ 48), widen8(cw[j].w, s1));
+      }
+      if (kScores) st_shared16(tc::smem_u32(base) + kKvOff + st * kStageBytes + 8 * kRegion + o_rope, rp);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_leader<G>(&sm.kv_full[st], kLeader);
     }
-    return true;
-  };
-  bool more = next_block(true);
-  uint32_t u = 0;                              // uses of the stage
-  while (true) {
-    // the tiles' queries pass through the same ring: nothing to widen
-    for (; lead > 0; --lead, ++u) {
-      if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
-      if (lane == 0) arrive(&sm.q_place[g]);
-    }
-    if (!more) return;
-    if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const uint32_t two = e4m3x2_to_f16x2(have ? sc[j] : uint16_t(0));
-      const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-      uint8_t* d = reg + 2 * j * kRegion;
-      *reinterpret_cast<uint4*>(d + o0) = widen8(cw[j].x, s0);
-      *reinterpret_cast<uint4*>(d + (o0 ^ 16)) = widen8(cw[j].y, s0);
-      *reinterpret_cast<uint4*>(d + (o0 ^ 32)) = widen8(cw[j].z, s1);
-      *reinterpret_cast<uint4*>(d + (o0 ^ 48)) = widen8(cw[j].w, s1);
-    }
-    if (kScores) {
-#pragma unroll
-      for (int j = 0; j < kRopePieces; ++j)
-        *reinterpret_cast<uint4*>(stage + 8 * kRegion + tc::sw128_offset(srow, rpiece + 4 * j)) = rp[j];
-    }
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) arrive_leader<G>(&sm.kv_full[g], kLeader);
-    ++u;
-    more = next_block(false);
+    place = (place + kLead + it.n) & 1;
   }
 }
 
 // ---------------------------------------------------------------------------
 // Scores CTA
 // ---------------------------------------------------------------------------
-// Copies a tile's queries by TMA into the ring, as two places of 64 rows.
-template <int G>
-__device__ inline void query_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int lane,
-                                  const CUtensorMap* qmap) {
-  Walk walk(a.plan, cl);
-  Item it;
-  uint32_t m = 0;
-  while (walk.next(it)) {
-    const int y = it.a.z * a.d.heads + it.a.y + kDenseTile * part;
+// Copies a tile's queries by TMA into the ring, as two places of 64 rows from place m
+// on, once the widening warps, which follow the ring place by place, have found them free.
+__device__ inline bool copy_queries(const DenseArgs& a, DenseSmall& sm, uint8_t* base, const Item& it, int part, uint32_t m,
+                                    uint32_t k_item, bool one, const CUtensorMap* qmap) {
+  const int y = it.a.z * a.d.heads + it.a.y + kDenseTile * part;
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k, ++m) {
-      const uint32_t st = m % kKStages;
-      if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
-      if (lane == 0) {
-        tc::mbar_expect_tx(&sm.q_place[st], kKBytes);
+  for (int k = 0; k < 2; ++k, ++m) {
+    const uint32_t st = m % kKStages;
+    if (!wait_warp(sm, &sm.q_turn[st], k_item & 1, a.ws)) return false;
+    if (one) {
+      tc::mbar_expect_tx(&sm.q_place[st], kKBytes);
 #pragma unroll 1
-        for (int kb = 0; kb < 9; ++kb)
-          tc::tma_load_2d(qmap, base + kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.q_place[st]);
-      }
-      __syncwarp();
+      for (int kb = 0; kb < 9; ++kb)
+        tc::tma_load_2d(qmap, base + kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.q_place[st]);
     }
-    // the places of the tile's blocks: only waited for, so that no parity is mistaken for an earlier one
-    for (int j = 0; j < it.n; ++j, ++m)
-      if (!wait_warp(sm, &sm.kv_empty[m % kKStages], ((m / kKStages) & 1) ^ 1, a.ws)) return;
+    __syncwarp();
   }
+  return true;
 }
 
+// The copying and issuing warp; in the second CTA of a pair it only copies.
 template <int G>
-__device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, uint32_t tmem) {
+__device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, uint32_t tmem,
+                                       const CUtensorMap* qmap) {
   // latents are fp16, rope keys bf16 (each with queries of its type; one accumulator)
   constexpr uint32_t id_lat = idesc_f16(kDenseTile * G, kDenseBlk, 0, 0);
   constexpr uint32_t id_rope = tc::idesc_bf16(kDenseTile * G, kDenseBlk, 0, 0);
   constexpr int kRegion = kReg / G;                  // 64 channels of the 64 / G positions of a CTA
   constexpr uint16_t kBoth = 0x3;
   Walk walk(a.plan, cl);
-  Item it;
+  Item it = {};
   uint32_t n = 0;
   const bool leader = elect_one();
   for (uint32_t k = 0; walk.next(it); ++k) {
+    if (!copy_queries(a, sm, base, it, part, n, k, leader, qmap)) return;      // two places a tile: place and block number have one parity
+    if (part != 0) {
+      n += it.n;
+      continue;
+    }
     if (!wait_warp(sm, &sm.q_full, k & 1, a.ws)) return;
     for (int j = 0; j < it.n; ++j, ++n) {
       const uint32_t st = n % kKStages, buf = n % kSBufs;
@@ -631,23 +710,28 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       }
       zeroed &= ~(1u << slot);
       tc::tc_fence_after_sync();
-      const uint32_t scol = lanes + kSCol + buf * kDenseBlk;
-      // two short passes over the scores in tensor memory: maximum, then weights
-      float top = -INFINITY;
-#pragma unroll 1
+      float x[64];
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x[32];
-        tc::tmem_ld32(scol + 32 * h, x);
-        if (edge) {
+        float y[32];
+        tc::tmem_ld32(lanes + kSCol + buf * kDenseBlk + 32 * h, y);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (32 * h + i >= lo && 32 * h + i <= hi) ? x[i] : -INFINITY;
-        }
-        float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int i = 4; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
-        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+        for (int i = 0; i < 32; ++i) x[32 * h + i] = y[i];
       }
-      top *= c;
+      tc::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_leader<G>(&sm.s_empty[buf], 0);
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] = (i >= lo && i <= hi) ? x[i] : -INFINITY;
+      }
+      float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < 64; i += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t4[k] = i + 4 + k < 64 ? fmaxf(fmaxf(t4[k], x[i + k]), x[i + 4 + k]) : fmaxf(t4[k], x[i + k]);
+      }
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
       // the reference so far, from the other warp (barriers 1..4 to the odd blocks' warps,
       // 5..8 back; each arrival is awaited before the next on the same barrier)
       float before = -INFINITY;
@@ -668,37 +752,33 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
       if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float x[32];
-        tc::tmem_ld32(scol + 32 * h, x);
-        if (edge) {
+      const uint64_t cc = pack2(c, c), ss = pack2(-sub, -sub);
+      uint64_t acc[2] = {0, 0};                      // +0, +0
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (32 * h + i >= lo && 32 * h + i <= hi) ? x[i] : -INFINITY;
+      for (int i = 0; i < 8; ++i) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float p0, p1;
+          unpack2(fma2(pack2(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]), cc, ss), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          acc[k & 1] = add2(acc[k & 1], pack2(p0, p1));
+          pk[k] = f16x2_rn(p0, p1);
         }
-        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p0 = ex2(__fmaf_rn(x[2 * i], c, -sub)), p1 = ex2(__fmaf_rn(x[2 * i + 1], c, -sub));
-          s4[(2 * i) & 3] += p0;
-          s4[(2 * i + 1) & 3] += p1;
-          pk[i] = f16x2_rn(p0, p1);
-        }
-        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(ps + tc::sw128_offset(r, 4 * h + i)) =
-              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        *reinterpret_cast<uint4*>(ps + tc::sw128_offset(r, i)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
-      tc::tc_fence_before_sync();
+      {
+        float s0, s1;
+        unpack2(add2(acc[0], acc[1]), s0, s1);
+        sum += s0 + s1;
+      }
       sm.meta[slot][wq][0][lane] = alpha;
       sm.meta[slot][wq][1][lane] = sum;
       sm.meta[slot][wq][2][lane] = sub;
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_leader<G>(&sm.s_empty[buf], 0);
         const uint32_t bar = peer_addr(&sm.p_full[slot], uint32_t(G + part));
         copy_to_peer(peer_addr(ps + wq * 4096, uint32_t(G + part)), ps + wq * 4096, 4096, bar);
         copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], uint32_t(G + part)), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
@@ -713,18 +793,39 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
 // ---------------------------------------------------------------------------
 // Values CTA
 // ---------------------------------------------------------------------------
+// Hands the slot of P of block n back once its products are done; false after a timeout.
+__device__ inline bool free_slot(const DenseArgs& a, DenseSmall& sm, int part, int n, int all, bool one) {
+  const uint32_t slot = uint32_t(n) % kPSlots;
+  if (!wait_warp(sm, &sm.pv_done[slot], (uint32_t(n) / kPSlots) & 1, a.ws)) return false;
+  if (one && n + kPSlots < all) {
+    tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
+    arrive_remote(peer_addr(&sm.p_free[slot], uint32_t(part)));
+  }
+  __syncwarp();
+  return true;
+}
+
+// The issuing warp, which also hands slots back, one block behind (the next block's
+// products are in the queue by then); in the second CTA of a pair it only does that.
 template <int G>
-__device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, uint32_t tmem) {
+__device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, uint32_t tmem) {
   constexpr uint32_t id = idesc_f16(kDenseTile * G, 256, 0, 1);
   constexpr uint16_t kBoth = 0xC;
   Walk walk(a.plan, cl);
-  Item it;
-  uint32_t n = 0;
+  Item it = {};
+  int n = 0;
+  const int all = walk.left;
   const bool leader = elect_one();
+  if (part != 0) {
+    for (; n < all; ++n)
+      if (!free_slot(a, sm, part, n, all, leader)) return;
+    return;
+  }
   for (uint32_t k = 0; walk.next(it); ++k) {
+    if (n > 0 && k > 0 && !free_slot(a, sm, part, n - 1, all, leader)) return;   // before the outputs are waited for
     if (!wait_warp(sm, &sm.o_free, (k & 1) ^ 1, a.ws)) return;
     for (int j = 0; j < it.n; ++j, ++n) {
-      const uint32_t st = n % kKStages, slot = n % kPSlots, ph = (n / kPSlots) & 1;
+      const uint32_t st = n % kKStages, slot = uint32_t(n) % kPSlots, ph = (uint32_t(n) / kPSlots) & 1;
       if (!wait_warp(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
       if (G == 1 && !wait_warp(sm, &sm.p_full[slot], ph, a.ws)) return;
       if (!wait_warp(sm, &sm.corr[slot], ph, a.ws)) return;       // of a pair: both have seen their P arrive
@@ -742,20 +843,7 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
         commit_to<G>(&sm.pv_done[slot], kBoth);
       }
       __syncwarp();
-    }
-  }
-}
-
-// Hands each slot of P back once its products are done.
-template <int G>
-__device__ inline void slot_role(const DenseArgs& a, DenseSmall& sm, int cl, int part) {
-  Walk walk(a.plan, cl);
-  for (int n = 0, all = walk.left; n < all; ++n) {
-    const uint32_t slot = uint32_t(n) % kPSlots;
-    if (!wait_on(sm, &sm.pv_done[slot], (uint32_t(n) / kPSlots) & 1, a.ws)) return;
-    if (n + kPSlots < all) {
-      tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
-      arrive_remote(peer_addr(&sm.p_free[slot], uint32_t(part)));
+      if (j > 0 && !free_slot(a, sm, part, n - 1, all, leader)) return;
     }
   }
 }
@@ -769,14 +857,14 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
   const int r = wq * 32 + lane;
   uint8_t* stage = base + kStageOff + rw * 2048;
   Walk walk(a.plan, cl);
-  Item it;
+  Item it = {};
   uint32_t n = 0;
   while (walk.next(it)) {
     // sums of the even and the odd blocks, each under the reference of its last block
     float sum = 0.0f, sub = 0.0f, sum_b = 0.0f, sub_b = 0.0f;
     for (int j = 0; j < it.n; ++j, ++n) {
       const uint32_t slot = n % kPSlots;
-      if (!wait_warp(sm, &sm.p_full[slot], (n / kPSlots) & 1, a.ws)) return;
+      if (!wait_warp<true>(sm, &sm.p_full[slot], (n / kPSlots) & 1, a.ws)) return;
       const float alpha = sm.meta[slot][wq][0][lane];
       sum_b = sum;
       sub_b = sub;
@@ -852,7 +940,8 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
 }
 
 template <int G>
-__device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap) {
+__device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, const CUtensorMap* codes,
+                                  const CUtensorMap* scales, const CUtensorMap* rope) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ DenseSmall sm;
@@ -861,10 +950,15 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap) {
   const bool scores = rank < G;
   if (wid == 0) tmem_alloc_all<G>(&sm.tmem_slot);
   if (tid == 0) {
+    for (int i = 0; i < G; ++i) {
+      tc::mbar_init(&sm.raw_full[i], 1);
+      tc::mbar_init(&sm.raw_empty[i], kConvWarps / G);
+    }
     for (int i = 0; i < kKStages; ++i) {
-      tc::mbar_init(&sm.kv_full[i], 8 * G);          // a group's warps of every CTA of the pair
+      tc::mbar_init(&sm.kv_full[i], kConvWarps);     // G 1: all; G 2: 8 in each CTA of the pair
       tc::mbar_init(&sm.kv_empty[i], 1);
-      tc::mbar_init(&sm.q_place[i], 9);              // a group's warps and the copying thread
+      tc::mbar_init(&sm.q_turn[i], kConvWarps / G);
+      tc::mbar_init(&sm.q_place[i], 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
@@ -894,25 +988,45 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap) {
   pdl_wait();
   pdl_launch_dependents();
   if (scores) {
-    if (wid < kConvWarps) widen_role<G, true>(a, sm, base, cl, part, wid, lane);
-    else if (wid < kRowWarp0 + kRowWarps) softmax_role<G>(a, sm, base, cl, part, wid - kRowWarp0, lane, tmem);
-    else if (wid > kMmaWarp) query_role<G>(a, sm, base, cl, part, lane, qmap);
-    else if (part == 0) scores_mma_role<G>(a, sm, base, cl, tmem);
+    if (wid < kRowWarps) {
+      regs_up<kRowRegs>();
+      softmax_role<G>(a, sm, base, cl, part, wid, lane, tmem);
+    } else if (wid < kMmaWarp) {
+      regs_down<kConvRegs>();
+      widen_role<G, true>(a, sm, base, cl, part, wid - kConvWarp0, lane);
+    } else {
+      regs_down<kMmaRegs>();
+      if (wid == kMmaWarp) scores_mma_role<G>(a, sm, base, cl, part, tmem, qmap);
+      else if (wid == kMmaWarp + 1) raw_role<G, true>(a, sm, base, cl, part, lane, codes, scales, rope);
+    }
   } else {
-    if (wid < kConvWarps) widen_role<G, false>(a, sm, base, cl, part, wid, lane);
-    else if (wid < kRowWarp0 + kRowWarps) output_role<G>(a, sm, base, cl, part, wid - kRowWarp0, lane, tmem);
-    else if (wid == kMmaWarp && part == 0) values_mma_role<G>(a, sm, base, cl, tmem);
-    else if (wid > kMmaWarp && lane == 0) slot_role<G>(a, sm, cl, part);
+    if (wid < kRowWarps) {
+      output_role<G>(a, sm, base, cl, part, wid, lane, tmem);
+    } else if (wid < kMmaWarp) {
+      regs_down<kConvRegs>();
+      widen_role<G, false>(a, sm, base, cl, part, wid - kConvWarp0, lane);
+    } else {
+      regs_down<kMmaRegs>();
+      if (wid == kMmaWarp) values_mma_role<G>(a, sm, base, cl, part, tmem);
+      else if (wid == kMmaWarp + 1) raw_role<G, false>(a, sm, base, cl, part, lane, codes, scales, rope);
+    }
   }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
   __syncwarp();
   if (wid == kMmaWarp && part == 0) {
     if (elect_one()) {
       commit_to<G>(&sm.drain, uint16_t(1u << rank));
-      wait_slow(sm, &sm.drain, 0, a.ws);
+      wait_slow<false>(sm, &sm.drain, 0, a.ws);
     }
     __syncwarp();
   }
+  // after a wait that gave up, copies may still be on their way: they land within microseconds
+  if (*reinterpret_cast<volatile int*>(&sm.abort)) {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  __syncwarp();
   tc::tc_fence_before_sync();
   __syncthreads();
   tc::tc_fence_after_sync();
@@ -922,11 +1036,19 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap) {
   if (wid == 0) tmem_free_all<G>(tmem);
 }
 
+struct DenseMaps {
+  CUtensorMap q, codes, scales, rope;
+};
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
-    dense_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap) { dense_body<1>(a, &qmap); }
+    dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ DenseMaps m) {
+  dense_body<1>(a, &m.q, &m.codes, &m.scales, &m.rope);
+}
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kDenseThreads, 1)
-    dense_pair_kernel(DenseArgs a, const __grid_constant__ CUtensorMap qmap) { dense_body<2>(a, &qmap); }
+    dense_pair_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ DenseMaps m) {
+  dense_body<2>(a, &m.q, &m.codes, &m.scales, &m.rope);
+}
 
 // ---------------------------------------------------------------------------
 // Plan: one CTA.  Sequences -> tiles of 128 rows -> blocks each tile sees ->
@@ -1152,17 +1274,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // Clusters of 2 G CTAs that run at the same time on the current device (asked once per
 // device): the runs of a call are cut for that many.  Fewer fit than SMs / (2 G) where
-// a GPU processing cluster's SM count is no multiple of 2 G.
-int resident_clusters(void (*kernel)(DenseArgs, const CUtensorMap), int G, size_t smem) {
+// a GPU processing cluster's SM count is no multiple of 2 G.  0: not to be launched.
+int resident_clusters(void (*kernel)(const DenseArgs, const DenseMaps), int G, size_t smem) {
   static std::atomic<int> known[2][kMaxDevices];
   const int most = kDenseMaxClusters / G;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return most;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   const bool slot = dev >= 0 && dev < kMaxDevices;
   if (slot) {
     const int n = known[G - 1][dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
   }
+  // the register split of the roles counts on this many a thread
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kLaunchRegs) return 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(unsigned(2 * G * most));
@@ -1191,10 +1316,17 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   // once for twice the rows, and wastes up to 255 rows of a sequence instead of 127.
   const int G = dense_pairs(a.d.heads, a.batch, a.total_q) ? 2 : 1;
   a.tile = kDenseTile * G;
-  CUtensorMap qmap;
-  if (!encode_2d_cached(tensor_map_encoder(), &qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk,
-                        uint64_t(a.total_q) * a.d.heads, kDqk * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+  DenseMaps m;
+  const auto enc = tensor_map_encoder();
+  const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
+  if (!encode_2d_cached(enc, &m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, uint64_t(a.total_q) * a.d.heads, kDqk * 2,
+                        64, 64, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !encode_2d_cached(enc, &m.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, kCodesPerRow, rows, kCodesPerRow, 64, 32,
+                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !encode_2d_cached(enc, &m.scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.scales, kScalesPerRow, rows, kScalesPerRow,
+                        kScalesPerRow, 32, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !encode_2d_cached(enc, &m.rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rope, kRope, rows, kRope * 2, 64, 32,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
   static KernelAttrs attrs[2];
   constexpr size_t smem = size_t(kDenseSmem) + 1024;
@@ -1202,10 +1334,11 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   cudaError_t e = prepare_kernel(kernel, smem, false, attrs[G - 1]);
   if (e != cudaSuccess) return e;
   a.clusters = resident_clusters(kernel, G, smem);
+  if (a.clusters < 1) return cudaErrorInvalidConfiguration;
   CSA2_PROFILED(st, "dense_plan", (e = launch_pdl(dense_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_attn",
-                (e = launch_pdl(kernel, dim3(unsigned(2 * G * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, qmap)));
+                (e = launch_pdl(kernel, dim3(unsigned(2 * G * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, m)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_merge",
                 (e = launch_pdl(dense_merge_kernel, dim3(kLatent / kMergeCh, unsigned(a.clusters), unsigned(G)),

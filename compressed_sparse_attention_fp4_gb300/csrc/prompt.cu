@@ -137,12 +137,12 @@ csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t tot
   if (!ws || !is_aligned(ws, 256)) return CSA2_ERR_INVALID_ARG;
   const DenseLayout L = make_dense_layout(*d, batch, total_q);
   if (ws_bytes < size_t(L.total)) return CSA2_ERR_WORKSPACE_TOO_SMALL;
-  // the rope keys are addressed by 32-bit row coordinates
+  // the cache is addressed by 32-bit row coordinates
   const __int128 rows = page_table ? __int128(d->num_pages) * kPage : __int128(batch) * d->max_ctx;
   if (rows > INT32_MAX) return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (batch == 0 || total_q == 0) return CSA2_OK;
   if (!q || !q_start || !kv_codes || !kv_scales || !kv_rope || !ctx_len || !out || !lse) return CSA2_ERR_INVALID_ARG;
-  if (!is_aligned(q, 16) || !is_aligned(q_start, 4) || !is_aligned(kv_codes, 16) || !is_aligned(kv_scales, 2) ||
+  if (!is_aligned(q, 16) || !is_aligned(q_start, 4) || !is_aligned(kv_codes, 16) || !is_aligned(kv_scales, 16) ||
       !is_aligned(kv_rope, 16) || !is_aligned(ctx_len, 4) || !is_aligned(out, 16) || !is_aligned(lse, 4))
     return CSA2_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);

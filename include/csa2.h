@@ -443,14 +443,16 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
  *   only for the calls that use them).
  *   q:        device bf16 [total_q][H][576], 16-byte aligned
  *   q_start:  device int32 [batch + 1], not decreasing, within 0 .. total_q
- *   kv_codes, kv_scales, kv_rope, page_table, ctx_len: as csa2_sparse_attn_decode;
+ *   kv_codes, kv_scales, kv_rope, page_table, ctx_len: as csa2_sparse_attn_decode, all
+ *             three planes 16-byte aligned;
  *             a block of positions whose page id is out of range is skipped and reported
  *   out:      device bf16 [total_q][H][512], 16-byte aligned;  lse: device fp32 [total_q][H]
  *   ws:       workspace of csa2_dense_attn_workspace_size(d, batch, total_q) bytes, its
  *             first 256 the error word as elsewhere.  Calls that may run at the same
  *             time need a workspace each.
  *   P is rounded to fp16 (2^-11) and the output to bf16; everything between is fp32.
- * Limits: total_q * H < 2^31, batch <= 2^20.
+ * Limits: total_q * H < 2^31, batch <= 2^20, cache rows (batch * max_ctx, or num_pages *
+ * 64) < 2^31.
  * Errors: CSA2_ERR_INVALID_ARG (window < 0, window with CSA2_DENSE_ALL_POSITIONS,
  *         unknown flags, pointers, NaN scale), CSA2_ERR_UNSUPPORTED_SHAPE,
  *         CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
