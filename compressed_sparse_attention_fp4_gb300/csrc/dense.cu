@@ -410,42 +410,50 @@ struct Cursor {
 // Widening warps (every CTA): E2M1 x E4M3 -> fp16, exact (6 significant bits, 2^-10 ..
 // 2688).  A lane takes 16 bytes of codes (32 channels) of one row at a time, lane = 8 *
 // piece + row: a quarter-warp reads and stores one 16-byte chunk of 8 rows (all 32 banks,
-// 64- and 128-byte swizzle).  Two such pieces a lane and block:
+// 128-byte swizzle).  Two such pieces a lane and block:
 //   G 1: the 16 warps take every block together, 64 rows x 512 channels;
 //   G 2: 8 warps take every other block (those of one ring stage); a scores CTA has 32
-//        of the 64 rows, a values CTA 256 of the 512 channels (128 of each 256-column
-//        product).
+//        of the 64 rows, a values CTA its half of the 512 channels.
 // ---------------------------------------------------------------------------
-// Copies the run's blocks into the raw stages.
+// Copies the run's blocks into the raw stages: boxes of 128 bytes x 32 rows (64-byte boxes
+// take the copy engine nearly twice as long), scales in one piece.
 template <int G, bool kScores>
 __device__ inline void raw_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int lane,
-                                const CUtensorMap* codes, const CUtensorMap* scales, const CUtensorMap* rope) {
+                                const CUtensorMap* codes, const CUtensorMap* rope) {
   constexpr int kRows = G == 2 && kScores ? 32 : 64;
-  constexpr uint32_t kBytes = (kScores ? kRawRope / G : 0) + kRawCodes / G + kRows * kScalesPerRow;
+  constexpr uint32_t kBytes = (kScores ? kRawRope / G : 0) + kRawCodes / G;
   Cursor cur(a.plan, cl, lane);
   uint32_t n = 0;
   for (bool more = cur.item(a); more; more = cur.step(a, 1) || cur.item(a), ++n) {
     const uint32_t st = n % G;
-    const int64_t row0 = cur.row0(a);
+    int64_t row0 = cur.row0(a);
     if (kScores && part == 0 && row0 < 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
     const int first = G == 2 && kScores ? 32 * part : 0;              // first of this CTA's rows in the block
     const int rows = row0 < 0 ? 0 : max(0, min(kRows, cur.it.b.x - (cur.it.blk + cur.i) * kDenseBlk - first));
+    row0 = (row0 < 0 ? 0 : row0) + first;
     if (!wait_warp(sm, &sm.raw_empty[st], ((n / G) & 1) ^ 1, a.ws)) return;
     if (lane == 0) {
       uint8_t* raw = base + kRawOff + st * (kRawBytes / G);
       uint64_t* bar = &sm.raw_full[st];
-      const int y = int(row0 < 0 ? 0 : row0) + first;
       sm.raw_rows[st] = rows;
-      tc::mbar_expect_tx(bar, kBytes);
+      tc::mbar_expect_tx(bar, kBytes + uint32_t(rows * kScalesPerRow));
 #pragma unroll 1
       for (int h = 0; h < kRows / 32; ++h) {
-        if (kScores) tc::tma_load_2d(rope, raw + h * 4096, 0, y + 32 * h, bar);
-        uint8_t* c = raw + kRawRope / G + h * 2048;
-#pragma unroll 1
-        for (int k = 0; k < (G == 2 && !kScores ? 2 : 4); ++k)        // 64 code bytes (128 channels) of 32 rows
-          tc::tma_load_2d(codes, c + k * kRows * 64, G == 2 && !kScores ? 128 * k + 64 * part : 64 * k, y + 32 * h, bar);
-        tc::tma_load_2d(scales, raw + kRawRope / G + kRawCodes / G + h * 1024, 0, y + 32 * h, bar);
+        uint8_t* c = raw + kRawRope / G + h * 4096;
+        if (G == 2 && !kScores) {
+          tc::tma_load_2d(codes, c, 128 * part, int(row0) + 32 * h, bar);
+        } else {
+          tc::tma_load_2d(codes, c, 0, int(row0) + 32 * h, bar);
+          tc::tma_load_2d(codes, c + kRows * 128, 128, int(row0) + 32 * h, bar);
+        }
+        if (kScores) tc::tma_load_2d(rope, raw + h * 4096, 0, int(row0) + 32 * h, bar);
       }
+      // valid rows only: the plane may end behind them
+      if (rows > 0)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     ::"r"(tc::smem_u32(raw + kRawRope / G + kRawCodes / G)), "l"(a.scales + row0 * kScalesPerRow),
+                       "r"(rows * kScalesPerRow), "r"(tc::smem_u32(bar))
+                     : "memory");
     }
     __syncwarp();
   }
@@ -470,11 +478,10 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
   const int w8 = w & 7, p = lane >> 3;
   const int hi = G == 1 ? w >> 3 : kScores ? w8 >> 2 : 0;             // half of the channels (256) this warp takes
   const int row = 8 * (G == 2 && kScores ? w8 & 3 : w8) + (lane & 7);  // in the stage
-  // first raw piece (64-byte group; the next is one on), its scales, first region (the next is two on)
+  // raw codes (128 bytes of a row; the second piece is 64 bytes on), its scales, first region (the next is two on)
   const uint32_t raw = tc::smem_u32(base) + kRawOff + g * (kRawBytes / G);
-  const uint32_t src = raw + kRawRope / G + 2 * hi * kRows * 64 + row * 64 + ((p ^ ((row >> 1) & 3)) << 4);
-  const uint32_t ssrc = raw + kRawRope / G + kRawCodes / G + row * kScalesPerRow + 2 * (kColumns ? 4 * part + p : 8 * hi + p);
-  constexpr uint32_t kScaleStep = kColumns ? 16 : 8;
+  const uint32_t src = raw + kRawRope / G + hi * kRows * 128 + tc::sw128_offset(row, p);
+  const uint32_t ssrc = raw + kRawRope / G + kRawCodes / G + row * kScalesPerRow + 2 * (8 * (kColumns ? part : hi) + p);
   const uint32_t o_rope = tc::sw128_offset(row, hi * 4 + p);          // rope: one 16-byte chunk a lane
   const uint32_t dst = tc::smem_u32(base) + kKvOff + (4 * hi + (p >> 1)) * kRegion;
   const uint32_t o0 = tc::sw128_offset(row, (p & 1) * 4);             // chunk i of a piece's four: o0 ^ 16 i
@@ -499,8 +506,8 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
       const bool have = row < sm.raw_rows[g];
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
-        cw[j] = ld_shared16(src + j * kRows * 64);
-        sc[j] = ld_shared_u16(ssrc + j * kScaleStep);
+        cw[j] = ld_shared16(src ^ (64 * j));
+        sc[j] = ld_shared_u16(ssrc + 8 * j);
       }
       if (kScores) rp = ld_shared16(raw + o_rope);
       __syncwarp();
@@ -856,6 +863,8 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16) + uint32_t(col0);
   const int r = wq * 32 + lane;
   uint8_t* stage = base + kStageOff + rw * 2048;
+  // channel of output column col0 + c: in order at G 1; at G 2 a product's 256 columns are 128 channels from each CTA's half
+  const auto channel = [&](int c) { return G == 1 ? col0 + c : (col0 >> 1) + (c & 127) + ((c & 128) << 1); };
   Walk walk(a.plan, cl);
   Item it = {};
   uint32_t n = 0;
@@ -897,20 +906,20 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     const int lr = it.a.y + kDenseTile * part + r, rows = it.a.w * a.d.heads;
     if (it.head || it.tail) {
       const int slot = (2 * cl + (it.head ? 0 : 1)) * G + part;
-      float* po = a.part_o + (int64_t(slot) * kLatent + col0) * kDenseTile + r;
+      float* po = a.part_o + int64_t(slot) * kLatent * kDenseTile + r;
       if (col0 == 0) a.part_lse[slot * kDenseTile + r] = lse;
 #pragma unroll 1
       for (int col = 0; col < 256; col += 32) {
         float v[32];
         tc::tmem_ld32(lanes + col, v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) po[(col + i) * kDenseTile] = v[i] * inv;
+        for (int i = 0; i < 32; ++i) po[(channel(col) + i) * kDenseTile] = v[i] * inv;
       }
     } else {
       const int64_t g0 = int64_t(it.a.z) * a.d.heads + lr - lane;           // the warp's first row
       const int have = rows - (lr - lane);                                  // rows from it on that exist
       if (col0 == 0 && lr < rows) a.lse[g0 + lane] = lse;
-      uint16_t* dst = a.out + g0 * kLatent + col0 + 8 * (lane & 3);
+      uint16_t* dst = a.out + g0 * kLatent + 8 * (lane & 3);
 #pragma unroll 1
       for (int col = 0; col < 256; col += 32) {
         float v[32];
@@ -927,7 +936,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
         for (int i = 0; i < 4; ++i) {
           const int row = 8 * i + (lane >> 2);
           if (row < have)
-            *reinterpret_cast<uint4*>(dst + int64_t(row) * kLatent + col) =
+            *reinterpret_cast<uint4*>(dst + int64_t(row) * kLatent + channel(col)) =
                 *reinterpret_cast<const uint4*>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
         }
         __syncwarp();
@@ -941,7 +950,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
 
 template <int G>
 __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, const CUtensorMap* codes,
-                                  const CUtensorMap* scales, const CUtensorMap* rope) {
+                                  const CUtensorMap* rope) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ DenseSmall sm;
@@ -997,7 +1006,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
     } else {
       regs_down<kMmaRegs>();
       if (wid == kMmaWarp) scores_mma_role<G>(a, sm, base, cl, part, tmem, qmap);
-      else if (wid == kMmaWarp + 1) raw_role<G, true>(a, sm, base, cl, part, lane, codes, scales, rope);
+      else if (wid == kMmaWarp + 1) raw_role<G, true>(a, sm, base, cl, part, lane, codes, rope);
     }
   } else {
     if (wid < kRowWarps) {
@@ -1008,7 +1017,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
     } else {
       regs_down<kMmaRegs>();
       if (wid == kMmaWarp) values_mma_role<G>(a, sm, base, cl, part, tmem);
-      else if (wid == kMmaWarp + 1) raw_role<G, false>(a, sm, base, cl, part, lane, codes, scales, rope);
+      else if (wid == kMmaWarp + 1) raw_role<G, false>(a, sm, base, cl, part, lane, codes, rope);
     }
   }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
@@ -1037,17 +1046,17 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
 }
 
 struct DenseMaps {
-  CUtensorMap q, codes, scales, rope;
+  CUtensorMap q, codes, rope;
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
     dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ DenseMaps m) {
-  dense_body<1>(a, &m.q, &m.codes, &m.scales, &m.rope);
+  dense_body<1>(a, &m.q, &m.codes, &m.rope);
 }
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kDenseThreads, 1)
     dense_pair_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ DenseMaps m) {
-  dense_body<2>(a, &m.q, &m.codes, &m.scales, &m.rope);
+  dense_body<2>(a, &m.q, &m.codes, &m.rope);
 }
 
 // ---------------------------------------------------------------------------
@@ -1321,10 +1330,8 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
   if (!encode_2d_cached(enc, &m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, uint64_t(a.total_q) * a.d.heads, kDqk * 2,
                         64, 64, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-      !encode_2d_cached(enc, &m.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, kCodesPerRow, rows, kCodesPerRow, 64, 32,
-                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-      !encode_2d_cached(enc, &m.scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.scales, kScalesPerRow, rows, kScalesPerRow,
-                        kScalesPerRow, 32, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !encode_2d_cached(enc, &m.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, kCodesPerRow, rows, kCodesPerRow, 128, 32,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
       !encode_2d_cached(enc, &m.rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.rope, kRope, rows, kRope * 2, 64, 32,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
