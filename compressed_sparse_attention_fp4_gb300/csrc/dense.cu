@@ -56,26 +56,37 @@ constexpr int kRowWarps = 8;                        // lane quarter (w % 4) x (w
                                                     // (scores CTA), half of the output channels (values CTA)
 constexpr int kConvWarp0 = kRowWarps, kConvWarps = 16;   // two groups of 8, one for each ring stage
 constexpr int kMmaWarp = kRowWarps + kConvWarps;
-// warp kMmaWarp: query copies and MMAs (scores CTA), MMAs and slots (values CTA); the next
-// one: copies from the cache; two more make them a warpgroup and only give their registers
+// warp kMmaWarp: query copies and MMAs (scores CTA), MMAs (values CTA); then copies from
+// the cache, and rope keys (scores CTA, G 1) or slots of P (values CTA); one more makes
+// them a warpgroup and only gives its registers
 constexpr int kDenseThreads = (kMmaWarp + 4) * 32;
 
 constexpr int kReg = kDenseBlk * 128;               // 64 channels x 64 positions of 16-bit: 8 KB
-constexpr int kPSlots = 3;
+constexpr int kMaxPSlots = 3;
 constexpr int kPBytes = kDenseTile * 128;           // P[128 x 64] fp16
 constexpr int kKStages = 2;
 constexpr int kKBytes = 9 * kReg;                   // 576 channels of a block's positions, or of 64 query rows
 constexpr int kVBytes = 8 * kReg;                   // 512 channels
-constexpr int kPOff = 0;
-constexpr int kKvOff = kPOff + kPSlots * kPBytes;
-constexpr int kStageOff = kKvOff + kKStages * kVBytes;   // values CTA: output staging, 2 KB a warp
-// Raw bytes of the blocks to widen, as they come from the cache: G stages of 64 / G rows
-// (scores CTA) or of 64 rows x 1 / G of the codes (values CTA): rope keys, codes, scales.
-constexpr int kRawOff = kKvOff + kKStages * kKBytes;
-constexpr int kRawRope = kDenseBlk * kRope * 2, kRawCodes = kDenseBlk * kCodesPerRow, kRawScales = kDenseBlk * kScalesPerRow;
-constexpr int kRawBytes = kRawRope + kRawCodes + kRawScales;
-constexpr int kDenseSmem = kRawOff + kRawBytes;
-static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
+
+// Shared memory of a CTA: slots of P, the ring of keys or values, raw bytes of the
+// blocks to widen as they come from the cache (64 / G rows in a scores CTA, 1 / G of the
+// codes in a values CTA).  At G 1, where a block is twice the bytes, the rope keys go
+// straight into the ring.
+template <int G>
+struct Lay {
+  static constexpr int kPSlots = 3;
+  static constexpr int kRawStages = G;
+  static constexpr int kKvOff = kPSlots * kPBytes;
+  static constexpr int kRawOff = kKvOff + kKStages * kKBytes;
+  static constexpr int kRawRope = G == 1 ? 0 : kDenseBlk * kRope * 2 / G;       // scores CTA only
+  static constexpr int kRawCodes = kDenseBlk * kCodesPerRow / G;
+  static constexpr int kRawStage = kRawRope + kRawCodes + kDenseBlk * kScalesPerRow / G;   // (a values CTA at G 2: all scales, no rope)
+  static constexpr int kStageOff = kKvOff + kKStages * kVBytes;       // values CTA: output staging, 2 KB a warp
+  static constexpr int kSmem = kRawOff + kRawStages * kRawStage;
+  static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
+  static_assert(kRawCodes + kDenseBlk * kScalesPerRow <= kRawStage, "raw bytes of a values CTA");
+  static_assert(kRawStage % 1024 == 0 && kSmem + 1024 + 7168 <= 232448, "alignment and size of shared memory");
+};
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
 constexpr int kSBufs = 3;
@@ -87,16 +98,16 @@ struct DenseSmall {
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t q_turn[kKStages], q_place[kKStages];     // a ring stage free for queries; holding them
   uint64_t q_full;
-  uint64_t p_free[kPSlots];                         // scores CTA: slot read by the values CTA (remote arrival)
-  uint64_t p_full[kPSlots];                         // values CTA: bytes of P and meta have arrived
-  uint64_t corr[kPSlots];                           // values CTA: outputs brought to the slot's reference
-  uint64_t pv_done[kPSlots];
+  uint64_t p_free[kMaxPSlots];                         // scores CTA: slot read by the values CTA (remote arrival)
+  uint64_t p_full[kMaxPSlots];                         // values CTA: bytes of P and meta have arrived
+  uint64_t corr[kMaxPSlots];                           // values CTA: outputs brought to the slot's reference
+  uint64_t pv_done[kMaxPSlots];
   uint64_t o_free;
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
   int raw_rows[2];                                  // rows of the raw block before the context's end (0: bad page)
-  __align__(16) float meta[kPSlots][4][3][32];
+  __align__(16) float meta[kMaxPSlots][4][3][32];
   uint32_t swap[2][kDenseTile];                     // row maxima of the queries, between a row's two warps
   float ref[2][kDenseTile];                         // softmax reference, handed from block to block
 };
@@ -421,41 +432,65 @@ template <int G, bool kScores>
 __device__ inline void raw_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int lane,
                                 const CUtensorMap* codes, const CUtensorMap* rope) {
   constexpr int kRows = G == 2 && kScores ? 32 : 64;
-  constexpr uint32_t kBytes = (kScores ? kRawRope / G : 0) + kRawCodes / G;
+  constexpr int kCodesAt = kScores ? Lay<G>::kRawRope : 0, kScalesAt = kCodesAt + Lay<G>::kRawCodes;
+  constexpr uint32_t kBytes = kScalesAt;
   Cursor cur(a.plan, cl, lane);
   uint32_t n = 0;
   for (bool more = cur.item(a); more; more = cur.step(a, 1) || cur.item(a), ++n) {
-    const uint32_t st = n % G;
+    const uint32_t st = n % Lay<G>::kRawStages;
     int64_t row0 = cur.row0(a);
     if (kScores && part == 0 && row0 < 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
     const int first = G == 2 && kScores ? 32 * part : 0;              // first of this CTA's rows in the block
     const int rows = row0 < 0 ? 0 : max(0, min(kRows, cur.it.b.x - (cur.it.blk + cur.i) * kDenseBlk - first));
     row0 = (row0 < 0 ? 0 : row0) + first;
-    if (!wait_warp(sm, &sm.raw_empty[st], ((n / G) & 1) ^ 1, a.ws)) return;
+    if (!wait_warp(sm, &sm.raw_empty[st], ((n / Lay<G>::kRawStages) & 1) ^ 1, a.ws)) return;
     if (lane == 0) {
-      uint8_t* raw = base + kRawOff + st * (kRawBytes / G);
+      uint8_t* raw = base + Lay<G>::kRawOff + st * Lay<G>::kRawStage;
       uint64_t* bar = &sm.raw_full[st];
       sm.raw_rows[st] = rows;
       tc::mbar_expect_tx(bar, kBytes + uint32_t(rows * kScalesPerRow));
 #pragma unroll 1
       for (int h = 0; h < kRows / 32; ++h) {
-        uint8_t* c = raw + kRawRope / G + h * 4096;
+        uint8_t* c = raw + kCodesAt + h * 4096;
         if (G == 2 && !kScores) {
           tc::tma_load_2d(codes, c, 128 * part, int(row0) + 32 * h, bar);
         } else {
           tc::tma_load_2d(codes, c, 0, int(row0) + 32 * h, bar);
           tc::tma_load_2d(codes, c + kRows * 128, 128, int(row0) + 32 * h, bar);
         }
-        if (kScores) tc::tma_load_2d(rope, raw + h * 4096, 0, int(row0) + 32 * h, bar);
+        if (kScores && G == 2) tc::tma_load_2d(rope, raw + h * 4096, 0, int(row0) + 32 * h, bar);
       }
       // valid rows only: the plane may end behind them
       if (rows > 0)
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                     ::"r"(tc::smem_u32(raw + kRawRope / G + kRawCodes / G)), "l"(a.scales + row0 * kScalesPerRow),
+                     ::"r"(tc::smem_u32(raw + kScalesAt)), "l"(a.scales + row0 * kScalesPerRow),
                        "r"(rows * kScalesPerRow), "r"(tc::smem_u32(bar))
                      : "memory");
     }
     __syncwarp();
+  }
+}
+
+// G 1: the rope keys of each block, straight into the ring (they need no widening; rows
+// behind the context are masked scores, whatever they hold).  Follows the ring place by place.
+__device__ inline void rope_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int lane, const CUtensorMap* rope) {
+  Cursor cur(a.plan, cl, lane);
+  uint32_t m = 0;
+  for (bool more = cur.item(a); more; more = cur.step(a, 1) || cur.item(a)) {
+    const int64_t row0 = cur.row0(a);
+    for (int k = cur.i == 0 ? 2 : 0; k >= 0; --k, ++m) {              // the tile's two query places, then the block's
+      const uint32_t st = m % kKStages;
+      if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
+      if (k > 0) {
+        if (lane == 0) arrive(&sm.q_turn[st]);
+      } else if (lane == 0) {
+        uint8_t* dst = base + Lay<1>::kKvOff + st * kKBytes + 8 * kReg;
+        tc::mbar_expect_tx(&sm.kv_full[st], kReg);
+        tc::tma_load_2d(rope, dst, 0, row0 < 0 ? 0 : int(row0), &sm.kv_full[st]);
+        tc::tma_load_2d(rope, dst + kReg / 2, 0, row0 < 0 ? 32 : int(row0) + 32, &sm.kv_full[st]);
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -479,11 +514,12 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
   const int hi = G == 1 ? w >> 3 : kScores ? w8 >> 2 : 0;             // half of the channels (256) this warp takes
   const int row = 8 * (G == 2 && kScores ? w8 & 3 : w8) + (lane & 7);  // in the stage
   // raw codes (128 bytes of a row; the second piece is 64 bytes on), its scales, first region (the next is two on)
-  const uint32_t raw = tc::smem_u32(base) + kRawOff + g * (kRawBytes / G);
-  const uint32_t src = raw + kRawRope / G + hi * kRows * 128 + tc::sw128_offset(row, p);
-  const uint32_t ssrc = raw + kRawRope / G + kRawCodes / G + row * kScalesPerRow + 2 * (8 * (kColumns ? part : hi) + p);
+  const uint32_t raw0 = tc::smem_u32(base) + Lay<G>::kRawOff;
+  constexpr uint32_t kCodesAt = kScores ? Lay<G>::kRawRope : 0;
+  const uint32_t src = kCodesAt + hi * kRows * 128 + tc::sw128_offset(row, p);
+  const uint32_t ssrc = kCodesAt + Lay<G>::kRawCodes + row * kScalesPerRow + 2 * (8 * (kColumns ? part : hi) + p);
   const uint32_t o_rope = tc::sw128_offset(row, hi * 4 + p);          // rope: one 16-byte chunk a lane
-  const uint32_t dst = tc::smem_u32(base) + kKvOff + (4 * hi + (p >> 1)) * kRegion;
+  const uint32_t dst = tc::smem_u32(base) + Lay<G>::kKvOff + (4 * hi + (p >> 1)) * kRegion;
   const uint32_t o0 = tc::sw128_offset(row, (p & 1) * 4);             // chunk i of a piece's four: o0 ^ 16 i
   Walk walk(a.plan, cl);
   Item it = {};
@@ -500,18 +536,20 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
     }
 #pragma unroll 1
     for (int i = G == 2 ? (g - place) & 1 : 0; i < it.n; i += G, ++u, ++v) {
-      if (!wait_warp(sm, &sm.raw_full[g], v & 1, a.ws)) return;
+      // raw stages: G 1: in turn; G 2: the warp's own
+      const uint32_t rs = G == 1 ? v % Lay<G>::kRawStages : uint32_t(g), raw = raw0 + rs * Lay<G>::kRawStage;
+      if (!wait_warp(sm, &sm.raw_full[rs], (G == 1 ? v / Lay<G>::kRawStages : v) & 1, a.ws)) return;
       uint4 cw[kPieces], rp;
       uint32_t sc[kPieces];
-      const bool have = row < sm.raw_rows[g];
+      const bool have = row < sm.raw_rows[rs];
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
-        cw[j] = ld_shared16(src ^ (64 * j));
-        sc[j] = ld_shared_u16(ssrc + 8 * j);
+        cw[j] = ld_shared16((raw + src) ^ (64 * j));
+        sc[j] = ld_shared_u16(raw + ssrc + 8 * j);
       }
-      if (kScores) rp = ld_shared16(raw + o_rope);
+      if (kScores && G == 2) rp = ld_shared16(raw + o_rope);
       __syncwarp();
-      if (lane == 0) arrive(&sm.raw_empty[g]);
+      if (lane == 0) arrive(&sm.raw_empty[rs]);
       const uint32_t st = stage_of();
       if (!wait_warp(sm, &sm.kv_empty[st], parity_of(), a.ws)) return;
       const uint32_t d = dst + st * kStageBytes;
@@ -525,7 +563,7 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
         st_shared16(d + 2 * j * kRegion + (o0 ^ 32), widen8(cw[j].z, s1));
         st_shared16(d + 2 * j * kRegion + (o0 ^ 48), widen8(cw[j].w, s1));
       }
-      if (kScores) st_shared16(tc::smem_u32(base) + kKvOff + st * kStageBytes + 8 * kRegion + o_rope, rp);
+      if (kScores && G == 2) st_shared16(tc::smem_u32(base) + Lay<G>::kKvOff + st * kStageBytes + 8 * kRegion + o_rope, rp);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader<G>(&sm.kv_full[st], kLeader);
@@ -539,6 +577,7 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
 // ---------------------------------------------------------------------------
 // Copies a tile's queries by TMA into the ring, as two places of 64 rows from place m
 // on, once the widening warps, which follow the ring place by place, have found them free.
+template <int G>
 __device__ inline bool copy_queries(const DenseArgs& a, DenseSmall& sm, uint8_t* base, const Item& it, int part, uint32_t m,
                                     uint32_t k_item, bool one, const CUtensorMap* qmap) {
   const int y = it.a.z * a.d.heads + it.a.y + kDenseTile * part;
@@ -550,7 +589,7 @@ __device__ inline bool copy_queries(const DenseArgs& a, DenseSmall& sm, uint8_t*
       tc::mbar_expect_tx(&sm.q_place[st], kKBytes);
 #pragma unroll 1
       for (int kb = 0; kb < 9; ++kb)
-        tc::tma_load_2d(qmap, base + kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.q_place[st]);
+        tc::tma_load_2d(qmap, base + Lay<G>::kKvOff + st * kKBytes + kb * kReg, 64 * kb, y + 64 * k, &sm.q_place[st]);
     }
     __syncwarp();
   }
@@ -571,7 +610,7 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
   uint32_t n = 0;
   const bool leader = elect_one();
   for (uint32_t k = 0; walk.next(it); ++k) {
-    if (!copy_queries(a, sm, base, it, part, n, k, leader, qmap)) return;      // two places a tile: place and block number have one parity
+    if (!copy_queries<G>(a, sm, base, it, part, n, k, leader, qmap)) return;      // two places a tile: place and block number have one parity
     if (part != 0) {
       n += it.n;
       continue;
@@ -583,7 +622,7 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
       if (!wait_warp(sm, &sm.s_empty[buf], ((n / kSBufs) & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
       if (leader) {
-        const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kKBytes), 16, 1024, 2);
+        const uint64_t bd = tc::smem_desc(tc::smem_u32(base + Lay<G>::kKvOff + st * kKBytes), 16, 1024, 2);
         const uint32_t d = tmem + kSCol + buf * kDenseBlk;
 #pragma unroll 1
         for (int kb = 0; kb < 9; ++kb)
@@ -627,7 +666,7 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       some_sync(11 + wq, 64);
       const uint32_t mh = m + (wq >> 1), st = mh % kKStages;
       if (!wait_warp(sm, &sm.q_place[st], k_item & 1, a.ws)) return;
-      const uint8_t* src = base + kKvOff + st * kKBytes;
+      const uint8_t* src = base + Lay<G>::kKvOff + st * kKBytes;
       uint32_t big = 0;
 #pragma unroll 1
       for (int q = 9 * half; q < 9 * half + 9; ++q)
@@ -686,15 +725,15 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
     n += uint32_t(cur.i);
 #pragma unroll 1
     for (; n < n1; n += 2) {
-      const uint32_t buf = n % kSBufs, slot = n % kPSlots;
+      const uint32_t buf = n % kSBufs, slot = n % Lay<G>::kPSlots;
       const int t0 = (cur.it.blk + cur.i) * kDenseBlk;
       const int lo = first - t0, hi = cur.row0(a) < 0 ? -1 : last - t0;
       const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kDenseBlk - 1);
-      uint8_t* ps = base + kPOff + slot * kPBytes;
+      uint8_t* ps = base + slot * kPBytes;
       if (!wait_warp(sm, &sm.s_full[buf], (n / kSBufs) & 1, a.ws)) return;
       if (!live) {
         // no row at all (a decode tile of few heads): P stays zero
-        if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) return;
         if (!(zeroed >> slot & 1)) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(ps + wq * 4096 + i * 512 + lane * 16) = make_uint4(0, 0, 0, 0);
@@ -758,7 +797,7 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       if (own != ref) sum = own == -INFINITY ? 0.0f : sum * ex2(own - ref);
       own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
-      if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) return;
       const uint64_t cc = pack2(c, c), ss = pack2(-sub, -sub);
       uint64_t acc[2] = {0, 0};                      // +0, +0
 #pragma unroll
@@ -800,46 +839,40 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
 // ---------------------------------------------------------------------------
 // Values CTA
 // ---------------------------------------------------------------------------
-// Hands the slot of P of block n back once its products are done; false after a timeout.
-__device__ inline bool free_slot(const DenseArgs& a, DenseSmall& sm, int part, int n, int all, bool one) {
-  const uint32_t slot = uint32_t(n) % kPSlots;
-  if (!wait_warp(sm, &sm.pv_done[slot], (uint32_t(n) / kPSlots) & 1, a.ws)) return false;
-  if (one && n + kPSlots < all) {
-    tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
-    arrive_remote(peer_addr(&sm.p_free[slot], uint32_t(part)));
+// Hands each slot of P back once its products are done.
+template <int G>
+__device__ inline void slot_role(const DenseArgs& a, DenseSmall& sm, int cl, int part, int lane) {
+  const int all = Walk(a.plan, cl).left;
+  for (int n = 0; n + Lay<G>::kPSlots < all; ++n) {
+    const uint32_t slot = uint32_t(n) % Lay<G>::kPSlots;
+    if (!wait_warp(sm, &sm.pv_done[slot], (uint32_t(n) / Lay<G>::kPSlots) & 1, a.ws)) return;
+    if (lane == 0) {
+      tc::mbar_expect_tx(&sm.p_full[slot], kPBytes + 4 * kMetaWarp);
+      arrive_remote(peer_addr(&sm.p_free[slot], uint32_t(part)));
+    }
+    __syncwarp();
   }
-  __syncwarp();
-  return true;
 }
 
-// The issuing warp, which also hands slots back, one block behind (the next block's
-// products are in the queue by then); in the second CTA of a pair it only does that.
 template <int G>
-__device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, uint32_t tmem) {
+__device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, uint32_t tmem) {
   constexpr uint32_t id = idesc_f16(kDenseTile * G, 256, 0, 1);
   constexpr uint16_t kBoth = 0xC;
   Walk walk(a.plan, cl);
   Item it = {};
-  int n = 0;
-  const int all = walk.left;
+  uint32_t n = 0;
   const bool leader = elect_one();
-  if (part != 0) {
-    for (; n < all; ++n)
-      if (!free_slot(a, sm, part, n, all, leader)) return;
-    return;
-  }
   for (uint32_t k = 0; walk.next(it); ++k) {
-    if (n > 0 && k > 0 && !free_slot(a, sm, part, n - 1, all, leader)) return;   // before the outputs are waited for
     if (!wait_warp(sm, &sm.o_free, (k & 1) ^ 1, a.ws)) return;
     for (int j = 0; j < it.n; ++j, ++n) {
-      const uint32_t st = n % kKStages, slot = uint32_t(n) % kPSlots, ph = (uint32_t(n) / kPSlots) & 1;
+      const uint32_t st = n % kKStages, slot = n % Lay<G>::kPSlots, ph = (n / Lay<G>::kPSlots) & 1;
       if (!wait_warp(sm, &sm.kv_full[st], (n / kKStages) & 1, a.ws)) return;
       if (G == 1 && !wait_warp(sm, &sm.p_full[slot], ph, a.ws)) return;
       if (!wait_warp(sm, &sm.corr[slot], ph, a.ws)) return;       // of a pair: both have seen their P arrive
       tc::tc_fence_after_sync();
       if (leader) {
-        const uint64_t ad = tc::smem_desc(tc::smem_u32(base + kPOff + slot * kPBytes), 16, 1024, 2);
-        const uint64_t bd = tc::smem_desc(tc::smem_u32(base + kKvOff + st * kVBytes), kReg, 1024, 2);
+        const uint64_t ad = tc::smem_desc(tc::smem_u32(base + slot * kPBytes), 16, 1024, 2);
+        const uint64_t bd = tc::smem_desc(tc::smem_u32(base + Lay<G>::kKvOff + st * kVBytes), kReg, 1024, 2);
 #pragma unroll
         for (int ks = 0; ks < kDenseBlk / 16; ++ks)
 #pragma unroll
@@ -850,7 +883,6 @@ __device__ inline void values_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
         commit_to<G>(&sm.pv_done[slot], kBoth);
       }
       __syncwarp();
-      if (j > 0 && !free_slot(a, sm, part, n - 1, all, leader)) return;
     }
   }
 }
@@ -862,7 +894,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
   const int wq = rw & 3, col0 = 256 * (rw >> 2);
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16) + uint32_t(col0);
   const int r = wq * 32 + lane;
-  uint8_t* stage = base + kStageOff + rw * 2048;
+  uint8_t* stage = base + Lay<G>::kStageOff + rw * 2048;
   // channel of output column col0 + c: in order at G 1; at G 2 a product's 256 columns are 128 channels from each CTA's half
   const auto channel = [&](int c) { return G == 1 ? col0 + c : (col0 >> 1) + (c & 127) + ((c & 128) << 1); };
   Walk walk(a.plan, cl);
@@ -872,8 +904,8 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     // sums of the even and the odd blocks, each under the reference of its last block
     float sum = 0.0f, sub = 0.0f, sum_b = 0.0f, sub_b = 0.0f;
     for (int j = 0; j < it.n; ++j, ++n) {
-      const uint32_t slot = n % kPSlots;
-      if (!wait_warp<true>(sm, &sm.p_full[slot], (n / kPSlots) & 1, a.ws)) return;
+      const uint32_t slot = n % Lay<G>::kPSlots;
+      if (!wait_warp<true>(sm, &sm.p_full[slot], (n / Lay<G>::kPSlots) & 1, a.ws)) return;
       const float alpha = sm.meta[slot][wq][0][lane];
       sum_b = sum;
       sub_b = sub;
@@ -882,7 +914,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
         // the outputs so far, once their products are done, to the new reference
         const uint32_t m = n - 1;
-        if (!wait_warp(sm, &sm.pv_done[m % kPSlots], (m / kPSlots) & 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.pv_done[m % Lay<G>::kPSlots], (m / Lay<G>::kPSlots) & 1, a.ws)) return;
         tc::tc_fence_after_sync();
 #pragma unroll 1
         for (int col = 0; col < 256; col += 8) {
@@ -898,7 +930,7 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
       if (lane == 0) arrive_leader<G>(&sm.corr[slot], G);
     }
     const uint32_t m = n - 1;
-    if (!wait_warp(sm, &sm.pv_done[m % kPSlots], (m / kPSlots) & 1, a.ws)) return;
+    if (!wait_warp(sm, &sm.pv_done[m % Lay<G>::kPSlots], (m / Lay<G>::kPSlots) & 1, a.ws)) return;
     tc::tc_fence_after_sync();
     if (sum_b > 0.0f) sum += sum_b * ex2(sub_b - sub);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -959,14 +991,15 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
   const bool scores = rank < G;
   if (wid == 0) tmem_alloc_all<G>(&sm.tmem_slot);
   if (tid == 0) {
-    for (int i = 0; i < G; ++i) {
+    for (int i = 0; i < Lay<G>::kRawStages; ++i) {
       tc::mbar_init(&sm.raw_full[i], 1);
       tc::mbar_init(&sm.raw_empty[i], kConvWarps / G);
     }
     for (int i = 0; i < kKStages; ++i) {
-      tc::mbar_init(&sm.kv_full[i], kConvWarps);     // G 1: all; G 2: 8 in each CTA of the pair
+      // G 1: all widening warps, and the rope keys' thread; G 2: 8 in each CTA of the pair
+      tc::mbar_init(&sm.kv_full[i], G == 1 && scores ? kConvWarps + 1 : kConvWarps);
       tc::mbar_init(&sm.kv_empty[i], 1);
-      tc::mbar_init(&sm.q_turn[i], kConvWarps / G);
+      tc::mbar_init(&sm.q_turn[i], G == 1 ? kConvWarps + 1 : kConvWarps / 2);
       tc::mbar_init(&sm.q_place[i], 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
@@ -974,7 +1007,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
       tc::mbar_init(&sm.s_empty[i], 4 * G);
     }
     tc::mbar_init(&sm.q_full, kRowWarps * G);
-    for (int i = 0; i < kPSlots; ++i) {
+    for (int i = 0; i < Lay<G>::kPSlots; ++i) {
       tc::mbar_init(&sm.p_free[i], 1);
       tc::mbar_init(&sm.p_full[i], 1);
       tc::mbar_init(&sm.corr[i], kRowWarps * G);
@@ -985,7 +1018,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
     sm.abort = 0;
     tc::fence_mbar_init();
     if (!scores)
-      for (int i = 0; i < kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + 4 * kMetaWarp);
+      for (int i = 0; i < Lay<G>::kPSlots; ++i) tc::mbar_expect_tx(&sm.p_full[i], kPBytes + 4 * kMetaWarp);
   }
   tc::tc_fence_before_sync();
   __syncthreads();
@@ -1007,6 +1040,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
       regs_down<kMmaRegs>();
       if (wid == kMmaWarp) scores_mma_role<G>(a, sm, base, cl, part, tmem, qmap);
       else if (wid == kMmaWarp + 1) raw_role<G, true>(a, sm, base, cl, part, lane, codes, rope);
+      else if (G == 1 && wid == kMmaWarp + 2) rope_role(a, sm, base, cl, lane, rope);
     }
   } else {
     if (wid < kRowWarps) {
@@ -1016,7 +1050,8 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
       widen_role<G, false>(a, sm, base, cl, part, wid - kConvWarp0, lane);
     } else {
       regs_down<kMmaRegs>();
-      if (wid == kMmaWarp) values_mma_role<G>(a, sm, base, cl, part, tmem);
+      if (wid == kMmaWarp && part == 0) values_mma_role<G>(a, sm, base, cl, tmem);
+      else if (wid == kMmaWarp + 2) slot_role<G>(a, sm, cl, part, lane);
       else if (wid == kMmaWarp + 1) raw_role<G, false>(a, sm, base, cl, part, lane, codes, rope);
     }
   }
@@ -1336,7 +1371,7 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
   static KernelAttrs attrs[2];
-  constexpr size_t smem = size_t(kDenseSmem) + 1024;
+  const size_t smem = size_t(G == 2 ? Lay<2>::kSmem : Lay<1>::kSmem) + 1024;
   auto kernel = G == 2 ? dense_pair_kernel : dense_kernel;
   cudaError_t e = prepare_kernel(kernel, smem, false, attrs[G - 1]);
   if (e != cudaSuccess) return e;
