@@ -1100,6 +1100,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kDenseThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
+// Exclusive sum over the block; buf: one value a warp.
 __device__ inline int64_t block_scan_sum(int64_t v, int64_t* buf, int64_t& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int64_t x = v;
@@ -1111,15 +1112,18 @@ __device__ inline int64_t block_scan_sum(int64_t v, int64_t* buf, int64_t& total
   __syncthreads();
   if (lane == 31) buf[w] = x;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int i = 0; i < kPlanThreads / 32; ++i) {
-    if (i < w) before += buf[i];
-    all += buf[i];
+  const int64_t mine = lane < int(blockDim.x >> 5) ? buf[lane] : 0;
+  int64_t z = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, z, o);
+    if (lane >= o) z += y;
   }
-  total = all;
-  return before + x - v;      // exclusive
+  total = __shfl_sync(0xFFFFFFFFu, z, 31);
+  return __shfl_sync(0xFFFFFFFFu, z - mine, w) + x - v;
 }
 
+// Inclusive maximum over the block.
 __device__ inline int block_scan_max(int v, int64_t* buf, int& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int x = v;
@@ -1131,27 +1135,106 @@ __device__ inline int block_scan_max(int v, int64_t* buf, int& total) {
   __syncthreads();
   if (lane == 31) buf[w] = x;
   __syncthreads();
+  const int warps = int(blockDim.x >> 5);
   int before = INT32_MIN, all = INT32_MIN;
-  for (int i = 0; i < kPlanThreads / 32; ++i) {
+  for (int i = 0; i < warps; ++i) {
     if (i < w) before = max(before, int(buf[i]));
     all = max(all, int(buf[i]));
   }
   total = all;
-  return max(before, x);      // inclusive
+  return max(before, x);
+}
+
+// The last of n (at least 1) ascending values that is at most x.
+template <typename F>
+__device__ inline int last_at_most(int n, int64_t x, F value) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (value(mid) <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Tile t of a sequence: its two records, and how many blocks it sees.
+__device__ inline int make_tile(const DenseArgs& a, int t, int seq, int4 s, int4* out) {
+  const int H = a.d.heads, row0 = (t - s.x) * a.tile;
+  const int tok0 = row0 / H, tok1 = min(s.z - 1, (row0 + a.tile - 1) / H);
+  int first = 0, last = s.w - 1, nb = 0, fb = 0;
+  if (a.causal) {
+    last = s.w - s.z + tok1;
+    if (a.window > 0) first = max(0, s.w - s.z + tok0 - a.window + 1);
+  }
+  if (last >= first) {
+    fb = first / kDenseBlk;
+    nb = last / kDenseBlk - fb + 1;
+  }
+  out[2 * t] = make_int4(seq, row0, s.y, s.z);
+  out[2 * t + 1] = make_int4(s.w, fb, nb, 0);
+  return nb;
+}
+
+__device__ inline int active_runs(const DenseArgs& a, int64_t blocks) {
+  const int64_t want = (blocks + kDenseMinBlocks - 1) / kDenseMinBlocks;
+  return blocks > 0 ? int(min64(a.clusters, want)) : 0;
+}
+
+// Run c: first tile, blocks of it before the run, blocks.
+template <typename F>
+__device__ inline int4 make_run(int c, int active, int64_t blocks, int ntiles, F before) {
+  if (c >= active) return make_int4(0, 0, 0, 0);
+  const int64_t w0 = blocks * c / active, w1 = blocks * (c + 1) / active;
+  const int t = last_at_most(ntiles, w0, before);
+  return make_int4(t, int(w0 - before(t)), int(w1 - w0), 0);
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a) {
-  __shared__ int64_t buf[kPlanThreads / 32];
-  const int tid = threadIdx.x, H = a.d.heads;
+  __shared__ int64_t buf[32];
+  __shared__ int4 s_seq[kPlanThreads];
+  __shared__ int s_before[kPlanThreads];
+  const int tid = threadIdx.x, H = a.d.heads, threads = int(blockDim.x);
+  const bool paged = a.page_table != nullptr;
   pdl_wait();
   pdl_launch_dependents();
-  // sequences: a q_start that falls back or leaves [0, total_q] is reported and
-  // replaced by the nearest value that keeps the order
+  // One sequence and one tile a thread, all in shared memory, where that is enough and
+  // the starts are in order.
+  if (a.batch <= threads && a.max_tiles <= threads) {
+    const bool in = tid < a.batch;
+    const int from = in ? __ldg(a.q_start + tid) : 0, end = in ? __ldg(a.q_start + tid + 1) : 0;
+    const int len = end - from;
+    const int64_t raw_ctx = in ? __ldg(a.ctx_len + tid) : 0;
+    if (__syncthreads_and(from >= 0 && end >= from && end <= a.total_q)) {
+      const int ctx = in ? int(check_ctx(raw_ctx, a.d, paged, a.ws)) : 0;
+      int64_t all, blocks;
+      const int64_t at = block_scan_sum((int64_t(len) * H + a.tile - 1) / a.tile, buf, all);
+      if (in) s_seq[tid] = make_int4(int(at), from, len, ctx);
+      __syncthreads();
+      const int ntiles = int(all);
+      int nb = 0;
+      if (tid < ntiles) {
+        const int b = last_at_most(a.batch, tid, [&](int i) { return int64_t(s_seq[i].x); });
+        nb = make_tile(a, tid, b, s_seq[b], a.plan.tiles);
+      }
+      const int64_t before = block_scan_sum(nb, buf, blocks);
+      s_before[tid] = int(before);                   // at most 1,024 tiles of 16,384 blocks
+      __syncthreads();
+      const int active = active_runs(a, blocks);
+      if (tid == 0) *a.plan.head = make_int4(ntiles, active, int(blocks), int(blocks >> 32));
+      if (tid < ntiles) a.plan.before[tid] = before;
+      for (int c = tid; c < a.clusters; c += threads)
+        a.plan.runs[c] = make_run(c, active, blocks, ntiles, [&](int i) { return int64_t(s_before[i]); });
+      return;
+    }
+  }
+  // Any number of them.  A q_start that falls back or leaves [0, total_q] is reported and
+  // replaced by the nearest value that keeps the order.
   const int s0 = __ldg(a.q_start);
   int reach = min(max(s0, 0), a.total_q);
   if (tid == 0 && reach != s0) raise_err(a.ws, CSA2_DEV_Q_START);
   int ntiles = 0;
-  for (int base = 0; base < a.batch; base += kPlanThreads) {
+  __shared__ int edge[kPlanThreads / 32];
+  for (int base = 0; base < a.batch; base += threads) {
     const int b = base + tid;
     int end = INT32_MIN, raw = 0;
     if (b < a.batch) {
@@ -1163,49 +1246,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a
     if (b < a.batch && upto != raw) raise_err(a.ws, CSA2_DEV_Q_START);
     // this sequence's first query: the reach before it
     int from = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
-    __shared__ int edge[kPlanThreads / 32];
     __syncthreads();
     if ((tid & 31) == 31) edge[tid >> 5] = upto;
     __syncthreads();
     if ((tid & 31) == 0) from = tid == 0 ? reach : edge[(tid >> 5) - 1];
     const int len = b < a.batch ? upto - from : 0;
-    const int64_t tiles = (int64_t(len) * H + a.tile - 1) / a.tile;
     int64_t all;
-    const int64_t at = block_scan_sum(tiles, buf, all);
-    if (b < a.batch) {
-      const int64_t ctx = checked_ctx(a.ctx_len, a.d, b, a.page_table != nullptr, a.ws);
-      a.plan.seqs[b] = make_int4(ntiles + int(at), from, len, int(ctx));
-    }
+    const int64_t at = block_scan_sum((int64_t(len) * H + a.tile - 1) / a.tile, buf, all);
+    if (b < a.batch)
+      a.plan.seqs[b] = make_int4(ntiles + int(at), from, len, int(checked_ctx(a.ctx_len, a.d, b, paged, a.ws)));
     ntiles += int(all);
     reach = max(reach, top);
   }
   __syncthreads();
-  // tiles
   int64_t blocks = 0;
-  for (int base = 0; base < ntiles; base += kPlanThreads) {
+  for (int base = 0; base < ntiles; base += threads) {
     const int t = base + tid;
-    int nb = 0, fb = 0;
+    int nb = 0;
     if (t < ntiles) {
-      int lo = 0, hi = a.batch - 1;                  // the last sequence whose first tile is <= t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.plan.seqs[mid].x <= t) lo = mid;
-        else hi = mid - 1;
-      }
-      const int4 s = a.plan.seqs[lo];
-      const int row0 = (t - s.x) * a.tile;
-      const int tok0 = row0 / H, tok1 = min(s.z - 1, (row0 + a.tile - 1) / H);
-      int first = 0, last = s.w - 1;
-      if (a.causal) {
-        last = s.w - s.z + tok1;
-        if (a.window > 0) first = max(0, s.w - s.z + tok0 - a.window + 1);
-      }
-      if (last >= first) {
-        fb = first / kDenseBlk;
-        nb = last / kDenseBlk - fb + 1;
-      }
-      a.plan.tiles[2 * t] = make_int4(lo, row0, s.y, s.z);
-      a.plan.tiles[2 * t + 1] = make_int4(s.w, fb, nb, 0);
+      const int b = last_at_most(a.batch, t, [&](int i) { return int64_t(a.plan.seqs[i].x); });
+      nb = make_tile(a, t, b, a.plan.seqs[b], a.plan.tiles);
     }
     int64_t all;
     const int64_t at = block_scan_sum(nb, buf, all);
@@ -1213,86 +1273,68 @@ __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a
     blocks += all;
   }
   __syncthreads();
-  const int64_t want = (blocks + kDenseMinBlocks - 1) / kDenseMinBlocks;
-  const int active = int(min64(a.clusters, max64(want, 1)));
-  if (tid == 0) *a.plan.head = make_int4(ntiles, blocks > 0 ? active : 0, 0, 0);
-  for (int c = tid; c < a.clusters; c += kPlanThreads) {
-    int4 run = make_int4(0, 0, 0, 0);
-    const int64_t w0 = c < active ? blocks * c / active : blocks, w1 = c < active ? blocks * (c + 1) / active : blocks;
-    if (w1 > w0) {
-      int lo = 0, hi = ntiles - 1;                   // the last tile whose first block is <= w0
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.plan.before[mid] <= w0) lo = mid;
-        else hi = mid - 1;
-      }
-      run = make_int4(lo, int(w0 - a.plan.before[lo]), int(w1 - w0), 0);
-    }
-    a.plan.runs[c] = run;
-  }
+  const int active = active_runs(a, blocks);
+  if (tid == 0) *a.plan.head = make_int4(ntiles, active, int(blocks), int(blocks >> 32));
+  for (int c = tid; c < a.clusters; c += threads)
+    a.plan.runs[c] = make_run(c, active, blocks, ntiles, [&](int i) { return a.plan.before[i]; });
 }
 
 // ---------------------------------------------------------------------------
-// Merge: CTA (g, c) joins 16 channels of the tile that the boundary before run c
+// Merge: CTA (g, c) joins 8 channels of the tile that the boundary before run c
 // cuts, if c is the first boundary inside it.  Thread = row.  It also writes the
 // rows of tiles that see nothing.
 // ---------------------------------------------------------------------------
-constexpr int kMergeCh = 16;
+constexpr int kMergeCh = 8;
 
 __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int r = threadIdx.x, g = blockIdx.x, c = blockIdx.y;
   const int G = a.tile / kDenseTile, part = blockIdx.z;
-  const int4 head = __ldg(a.plan.head);
-  if (c < head.y) {
-    const int4 run = __ldg(a.plan.runs + c);
-    const int64_t w0 = run.y;                        // blocks of the tile before this run
-    if (w0 > 0) {
-      const int4 ta = __ldg(a.plan.tiles + 2 * run.x), tb = __ldg(a.plan.tiles + 2 * run.x + 1);
-      const int4 prev = __ldg(a.plan.runs + c - 1);
-      // first boundary inside: the run before starts at or before the tile's first block
-      const bool mine = prev.x != run.x || prev.y == 0;
-      const int lr = ta.y + kDenseTile * part + r;
-      if (mine && lr < ta.w * a.d.heads) {
-        // last run that touches the tile
-        int c1 = c;
-        int64_t done = w0 + run.z;
-        while (done < tb.z) {
-          ++c1;
-          done += __ldg(a.plan.runs + c1).z;
-        }
-        const int n = c1 - c + 2;                    // pieces: runs c - 1 .. c1
-        // the first piece ends the run before (its tail); the others start theirs
-        const auto slot = [&](int i) { return (i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * G + part; };
-        float top = -INFINITY;
-        for (int i = 0; i < n; ++i) top = fmaxf(top, a.part_lse[slot(i) * kDenseTile + r]);
-        float o[kMergeCh], total = 0.0f;
+  // independent loads first: each level of dependent ones is most of a microsecond
+  const int4 head = __ldg(a.plan.head), run = __ldg(a.plan.runs + c), prev = __ldg(a.plan.runs + max(c - 1, 0));
+  const int ctas = gridDim.x * gridDim.y * gridDim.z;
+  const int t0 = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  // a boundary inside a tile, the first there: the run before starts at or before the tile's first block
+  if (c < head.y && run.y > 0 && (prev.x != run.x || prev.y == 0)) {
+    const int4 ta = __ldg(a.plan.tiles + 2 * run.x), tb = __ldg(a.plan.tiles + 2 * run.x + 1);
+    const int64_t last = __ldg(a.plan.before + run.x) + tb.z - 1;               // the tile's last block
+    const int64_t blocks = int64_t(uint32_t(head.z)) | int64_t(head.w) << 32;
+    const int lr = ta.y + kDenseTile * part + r;
+    if (lr < ta.w * a.d.heads) {
+      const int c1 = int(((last + 1) * head.y - 1) / blocks);                  // the run it is in (see make_run)
+      const int n = c1 - c + 2;                      // pieces: runs c - 1 .. c1
+      // the first piece ends the run before (its tail); the others start theirs
+      const auto slot = [&](int i) { return (i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * G + part; };
+      float top = -INFINITY;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) top = fmaxf(top, __ldg(a.part_lse + slot(i) * kDenseTile + r));
+      float o[kMergeCh], total = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kMergeCh; ++k) o[k] = 0.0f;
-        for (int i = 0; i < n; ++i) {
-          const int s = slot(i);
-          const float l = a.part_lse[s * kDenseTile + r];
-          const float w = l == -INFINITY ? 0.0f : exp2f((l - top) * 1.4426950408889634f);
-          total += w;
-          const float* po = a.part_o + (int64_t(s) * kLatent + g * kMergeCh) * kDenseTile + r;
+      for (int k = 0; k < kMergeCh; ++k) o[k] = 0.0f;
+#pragma unroll 2
+      for (int i = 0; i < n; ++i) {
+        const int s = slot(i);
+        const float l = __ldg(a.part_lse + s * kDenseTile + r);
+        const float w = l == -INFINITY ? 0.0f : exp2f((l - top) * 1.4426950408889634f);
+        total += w;
+        const float* po = a.part_o + (int64_t(s) * kLatent + g * kMergeCh) * kDenseTile + r;
 #pragma unroll
-          for (int k = 0; k < kMergeCh; ++k) o[k] = fmaf(w, po[k * kDenseTile], o[k]);
-        }
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-        const int64_t row = int64_t(ta.z) * a.d.heads + lr;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + row * kLatent + g * kMergeCh);
-#pragma unroll
-        for (int k = 0; k < kMergeCh / 8; ++k)
-          dst[k] = make_uint4(bf16x2_rn(o[8 * k] * inv, o[8 * k + 1] * inv), bf16x2_rn(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                              bf16x2_rn(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                              bf16x2_rn(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-        if (g == 0) a.lse[row] = total > 0.0f ? top + logf(total) : -INFINITY;
+        for (int k = 0; k < kMergeCh; ++k) o[k] = fmaf(w, __ldg(po + k * kDenseTile), o[k]);
       }
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      const int64_t row = int64_t(ta.z) * a.d.heads + lr;
+      uint4* dst = reinterpret_cast<uint4*>(a.out + row * kLatent + g * kMergeCh);
+#pragma unroll
+      for (int k = 0; k < kMergeCh / 8; ++k)
+        dst[k] = make_uint4(bf16x2_rn(o[8 * k] * inv, o[8 * k + 1] * inv), bf16x2_rn(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                            bf16x2_rn(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                            bf16x2_rn(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+      if (g == 0) a.lse[row] = total > 0.0f ? top + logf(total) : -INFINITY;
     }
   }
-  const int ctas = gridDim.x * gridDim.y * gridDim.z;
-  for (int t = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x; t < head.x; t += ctas) {
+  // tiles that see nothing
+  for (int t = t0; t < head.x; t += ctas) {
     if (__ldg(a.plan.tiles + 2 * t + 1).z != 0) continue;
     const int4 ta = __ldg(a.plan.tiles + 2 * t);
     const int rows = min(a.tile, ta.w * a.d.heads - ta.y);
@@ -1377,7 +1419,11 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.clusters = resident_clusters(kernel, G, smem);
   if (a.clusters < 1) return cudaErrorInvalidConfiguration;
-  CSA2_PROFILED(st, "dense_plan", (e = launch_pdl(dense_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a)));
+  // as many threads as there can be sequences or tiles, up to the most
+  a.max_tiles = int(min64((int64_t(a.total_q) * a.d.heads + a.tile - 1) / a.tile + a.batch, INT32_MAX));
+  const int64_t want = max64(max64(a.max_tiles, a.batch), 128);
+  const unsigned threads = want >= kPlanThreads ? kPlanThreads : unsigned((want + 31) / 32 * 32);
+  CSA2_PROFILED(st, "dense_plan", (e = launch_pdl(dense_plan_kernel, dim3(1), dim3(threads), 0, st, 1, a)));
   if (e != cudaSuccess) return e;
   CSA2_PROFILED(st, "dense_attn",
                 (e = launch_pdl(kernel, dim3(unsigned(2 * G * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, m)));

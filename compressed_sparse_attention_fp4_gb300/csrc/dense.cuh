@@ -12,7 +12,7 @@ constexpr int kDenseMinBlocks = 4;       // least blocks a run is cut to (one SM
 static_assert(kDenseBlk == kPage, "a block never crosses a page");
 
 struct DensePlan {
-  int4* head;          // tiles, runs in use
+  int4* head;          // tiles, runs in use, blocks (low, high word)
   int4* runs;          // per cluster: first tile, blocks of it before the run, blocks
   int4* seqs;          // per sequence: first tile, first query, queries, context
   int4* tiles;         // two per tile (see Item)
@@ -23,6 +23,7 @@ struct DenseArgs {
   csa2_dims d;
   int batch, total_q, causal, window, clusters;
   int tile;            // rows of a tile: 128, or 256 on twice the SMs
+  int max_tiles;       // bound of their number
   const uint16_t* q;
   const int32_t* q_start;
   const uint8_t* codes;
