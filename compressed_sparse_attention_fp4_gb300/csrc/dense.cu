@@ -81,11 +81,12 @@ struct Lay {
   static constexpr int kRawRope = G == 1 ? 0 : kDenseBlk * kRope * 2 / G;       // scores CTA only
   static constexpr int kRawCodes = kDenseBlk * kCodesPerRow / G;
   static constexpr int kRawStage = kRawRope + kRawCodes + kDenseBlk * kScalesPerRow / G;   // (a values CTA at G 2: all scales, no rope)
-  static constexpr int kStageOff = kKvOff + kKStages * kVBytes;       // values CTA: output staging, 2 KB a warp
+  // values CTA: output staging, 2 G KB a warp, behind the values (at G 2 they are half of a stage)
+  static constexpr int kStageOff = G == 1 ? kKvOff + kKStages * kVBytes : kKvOff + (kKStages - 1) * kVBytes + kVBytes / 2;
   static constexpr int kSmem = kRawOff + kRawStages * kRawStage;
-  static_assert(kStageOff + kRowWarps * 2048 <= kRawOff, "output staging of the values CTA");
+  static_assert(kStageOff + kRowWarps * 2048 * G <= kRawOff, "output staging of the values CTA");
   static_assert(kRawCodes + kDenseBlk * kScalesPerRow <= kRawStage, "raw bytes of a values CTA");
-  static_assert(kRawStage % 1024 == 0 && kSmem + 1024 + 7168 <= 232448, "alignment and size of shared memory");
+  static_assert(kRawStage % 1024 == 0 && kSmem + 1024 + 8192 <= 232448, "alignment and size of shared memory");
 };
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
@@ -108,7 +109,8 @@ struct DenseSmall {
   int abort;
   int raw_rows[2];                                  // rows of the raw block before the context's end (0: bad page)
   __align__(16) float meta[kMaxPSlots][4][3][32];
-  uint32_t swap[2][kDenseTile];                     // row maxima of the queries, between a row's two warps
+  uint16_t swap[4][kDenseTile];                     // largest magnitudes of the queries, between a row's four warps
+  int8_t q_shift[4][kDenseTile];                    // power of two each query row was scaled by, of four tiles in turn
   float ref[2][kDenseTile];                         // softmax reference, handed from block to block
 };
 
@@ -500,8 +502,72 @@ __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
                     mul_f16x2(e2m1_byte_f16x2<2>(w), sc2), mul_f16x2(e2m1_byte_f16x2<3>(w), sc2));
 }
 
+// The tile's queries, in the ring as two halves of 64 rows, into tensor memory as fp16
+// (latent channels) and bf16 (rope): lane quarter w % 4 has the row, its four warps the
+// channels.  Each row is scaled by the power of two that brings its largest value into
+// [2^14, 2^15): the 8 bits of bf16 are kept for all values down to 2^-28 of the largest,
+// smaller ones are off by 2^-39 of it; the softmax takes the power back.  The widening
+// warps do this, idle at that time, while the row warps finish the tile before.
+template <int G>
+__device__ inline bool queries_to_tmem(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int w, int lane, uint32_t tmem,
+                                       uint32_t k_item, int place) {
+  const int wq = w & 3, part4 = w >> 2, half = wq >> 1, r = wq * 32 + lane, st = (place + half) & 1;
+  // both halves: then the products that read the tile before are done, too (both stages were free)
+  if (!wait_warp(sm, &sm.q_place[0], k_item & 1, a.ws)) return false;
+  if (!wait_warp(sm, &sm.q_place[1], k_item & 1, a.ws)) return false;
+  tc::tc_fence_after_sync();
+  const uint32_t src = tc::smem_u32(base) + Lay<G>::kKvOff + st * kKBytes;
+  const uint32_t row = tc::sw128_offset(r & 63, 0), turn = (r & 7) << 4;       // chunk c of a row: row's base + (c << 4 ^ turn)
+  const uint32_t at = src + (row ^ turn);
+  uint32_t big[2] = {0, 0};
+#pragma unroll 1
+  for (int q = part4; q < 18; q += 4)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = ld_shared16(at + (q >> 1) * kReg + ((((q & 1) * 4 + i) << 4) ^ turn));
+      big[i & 1] = __vmaxu2(big[i & 1], __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+    }
+  const uint32_t b2 = __vmaxu2(big[0], big[1]);
+  sm.swap[part4][r] = uint16_t(max(b2 & 0xFFFFu, b2 >> 16));
+  some_sync(9 + half, 256);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, uint32_t(sm.swap[i][r]));
+  const int k = min(14 + 127 - int(top >> 7), 126);                            // top >> 7: biased exponent of the largest
+  const float up = __uint_as_float(uint32_t(127 + k) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);   // a negative scale negates the queries
+  const uint32_t up2 = (__float_as_uint(up) >> 16) * 0x10001u;
+  if (part4 == 0) sm.q_shift[k_item & 3][r] = int8_t(k);
+#pragma unroll 1
+  for (int q = part4; q < 18; q += 4) {
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = ld_shared16(at + (q >> 1) * kReg + ((((q & 1) * 4 + i) << 4) ^ turn));
+      v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+    }
+    if (q < 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = f16x2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], up2);
+    }
+    tmem_st16_nowait(tmem + (uint32_t(wq * 32) << 16) + q * 16, v);
+  }
+  tmem_wait_st();
+  tc::tc_fence_before_sync();
+  some_sync(9 + half, 256);
+  if (lane == 0) {
+    if ((wq & 1) == 0 && part4 == 0) arrive(&sm.kv_empty[st]);                 // the half has been read
+    arrive_leader<G>(&sm.q_full, 0);
+  }
+  __syncwarp();
+  return true;
+}
+
 template <int G, bool kScores>
-__device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int w, int lane) {
+__device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int w, int lane,
+                                  uint32_t tmem) {
   constexpr int kPieces = 2;
   constexpr int kLead = kScores ? 2 : 0;       // ring places of a tile's queries before its blocks
   constexpr int kLeader = kScores ? 0 : G;
@@ -527,13 +593,14 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
   const auto stage_of = [&]() { return G == 1 ? u % kKStages : uint32_t(g); };
   const auto parity_of = [&]() { return ((G == 1 ? u / kKStages : u) & 1) ^ 1; };
   int place = 0;                               // ring place (mod 2) of the item's start
-  while (walk.next(it)) {
-    // the tile's queries pass through the same ring: nothing to widen
+  for (uint32_t k_item = 0; walk.next(it); ++k_item) {
+    // the tile's queries come through the same ring
 #pragma unroll 1
     for (int k = 0; k < kLead / G; ++k, ++u) {
       if (!wait_warp(sm, &sm.kv_empty[stage_of()], parity_of(), a.ws)) return;
       if (lane == 0) arrive(&sm.q_turn[stage_of()]);
     }
+    if (kScores && !queries_to_tmem<G>(a, sm, base, w, lane, tmem, k_item, place)) return;
 #pragma unroll 1
     for (int i = G == 2 ? (g - place) & 1 : 0; i < it.n; i += G, ++u, ++v) {
       // raw stages: G 1: in turn; G 2: the warp's own
@@ -596,6 +663,16 @@ __device__ inline bool copy_queries(const DenseArgs& a, DenseSmall& sm, uint8_t*
   return true;
 }
 
+// Asks L2 for the rows of the next tile's queries (one piece of memory).
+__device__ inline void prefetch_queries(const DenseArgs& a, Walk walk, int part) {
+  Item it = {};
+  if (!walk.next(it)) return;
+  const int64_t row = int64_t(it.a.z) * a.d.heads + it.a.y + kDenseTile * part;
+  const int rows = min(kDenseTile, it.a.w * a.d.heads - it.a.y - kDenseTile * part);
+  if (rows > 0)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.q + row * kDqk), "r"(rows * kDqk * 2) : "memory");
+}
+
 // The copying and issuing warp; in the second CTA of a pair it only copies.
 template <int G>
 __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, uint32_t tmem,
@@ -611,6 +688,7 @@ __device__ inline void scores_mma_role(const DenseArgs& a, DenseSmall& sm, uint8
   const bool leader = elect_one();
   for (uint32_t k = 0; walk.next(it); ++k) {
     if (!copy_queries<G>(a, sm, base, it, part, n, k, leader, qmap)) return;      // two places a tile: place and block number have one parity
+    if (leader) prefetch_queries(a, walk, part);
     if (part != 0) {
       n += it.n;
       continue;
@@ -648,69 +726,12 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
   const int r = wq * 32 + lane;
   const float c2 = a.scale * 1.4426950408889634f;
-  uint32_t n = 0, m = 0;
+  uint32_t n = 0;
   uint32_t zeroed = 0;                               // slots in which this warp's rows of P are zeros
   Cursor cur(a.plan, cl, lane);
   for (uint32_t k_item = 0; cur.item(a); ++k_item) {
-    // The tile's queries into tensor memory (rows 0..63 in the first half, 64..127 in the
-    // second; a row's two warps take half of the channels each); the MMAs that read the
-    // previous tile's are done (its last scores have been read, by one of the two warps,
-    // and both meet at the barrier).  Each row is scaled by the power of two that brings
-    // its largest value into [2^14, 2^15), so that the 512 latent channels are fp16: the 8
-    // bits of bf16 are kept for all values down to 2^-28 of the largest, smaller ones are
-    // off by 2^-39 of it.
-    float c;
-    {
-      // both warps of a row are through the tile before: a wait for a parity must not
-      // start while the use before it is open
-      some_sync(11 + wq, 64);
-      const uint32_t mh = m + (wq >> 1), st = mh % kKStages;
-      if (!wait_warp(sm, &sm.q_place[st], k_item & 1, a.ws)) return;
-      const uint8_t* src = base + Lay<G>::kKvOff + st * kKBytes;
-      uint32_t big = 0;
-#pragma unroll 1
-      for (int q = 9 * half; q < 9 * half + 9; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + (q >> 1) * kReg + tc::sw128_offset(r & 63, (q & 1) * 4 + i));
-          big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-        }
-      sm.swap[half][r] = big;
-      some_sync(11 + wq, 64);
-      big = __vmaxu2(big, sm.swap[half ^ 1][r]);
-      const int ex = int(max(big & 0xFFFFu, big >> 16) >> 7);              // biased exponent of the largest
-      const int k = min(14 + 127 - ex, 126);
-      const float up = __uint_as_float(uint32_t(127 + k) << 23) * (c2 < 0.0f ? -1.0f : 1.0f);   // a negative scale negates the queries
-      c = fmaxf(fabsf(c2) * __uint_as_float(uint32_t(127 - k) << 23), 1.17549435e-38f);
-      const uint32_t up2 = (__float_as_uint(up) >> 16) * 0x10001u;
-#pragma unroll 1
-      for (int q = 9 * half; q < 9 * half + 9; ++q) {
-        uint32_t v[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + (q >> 1) * kReg + tc::sw128_offset(r & 63, (q & 1) * 4 + i));
-          v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
-        }
-        if (q < 16) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            v[i] = f16x2_rn(__uint_as_float(v[i] << 16) * up, __uint_as_float(v[i] & 0xFFFF0000u) * up);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], up2);
-        }
-        tmem_st16_nowait(lanes + q * 16, v);
-      }
-      tmem_wait_st();
-      tc::tc_fence_before_sync();
-      some_sync(9 + (wq >> 1), 128);
-      if (lane == 0) {
-        if ((wq & 1) == 0 && half == 0) arrive(&sm.kv_empty[st]);
-        arrive_leader<G>(&sm.q_full, 0);
-      }
-      __syncwarp();
-      m += 2 + cur.it.n;
-    }
+    some_sync(11 + wq, 64);                          // both warps of a row are through the tile before
+    float c = 0.0f;                                  // logits in base 2 per score; known with the first scores
     // positions this row sees: first .. last
     const int lr = cur.it.a.y + kDenseTile * part + r, tok = lr / a.d.heads;
     const bool live = __any_sync(0xFFFFFFFFu, tok < cur.it.a.w);     // some row of this warp (and of its other half) exists
@@ -719,6 +740,7 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       last = a.causal ? cur.it.b.x - cur.it.a.w + tok : cur.it.b.x - 1;
       if (a.window > 0) first = max(0, last - a.window + 1);
     }
+    bool own_first = true;
     float own = -INFINITY, sum = 0.0f;               // reference of this warp's last block, its sum under it
     const uint32_t n0 = n, n1 = n + cur.it.n;
     cur.i = int((half ^ n0) & 1);
@@ -756,6 +778,11 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       }
       zeroed &= ~(1u << slot);
       tc::tc_fence_after_sync();
+      if (own_first) {
+        // the scores' queries were scaled by 2^k (of four tiles in turn: there are never scores of more than three unread)
+        c = fmaxf(fabsf(c2) * __uint_as_float(uint32_t(127 - sm.q_shift[k_item & 3][r]) << 23), 1.17549435e-38f);
+        own_first = false;
+      }
       float x[64];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -894,7 +921,8 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
   const int wq = rw & 3, col0 = 256 * (rw >> 2);
   const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16) + uint32_t(col0);
   const int r = wq * 32 + lane;
-  uint8_t* stage = base + Lay<G>::kStageOff + rw * 2048;
+  constexpr int kCols = 32 * G;                      // columns staged at a time: 64 or 128 bytes of 32 rows
+  uint8_t* stage = base + Lay<G>::kStageOff + rw * (2048 * G);
   // channel of output column col0 + c: in order at G 1; at G 2 a product's 256 columns are 128 channels from each CTA's half
   const auto channel = [&](int c) { return G == 1 ? col0 + c : (col0 >> 1) + (c & 127) + ((c & 128) << 1); };
   Walk walk(a.plan, cl);
@@ -951,25 +979,32 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
       const int64_t g0 = int64_t(it.a.z) * a.d.heads + lr - lane;           // the warp's first row
       const int have = rows - (lr - lane);                                  // rows from it on that exist
       if (col0 == 0 && lr < rows) a.lse[g0 + lane] = lse;
-      uint16_t* dst = a.out + g0 * kLatent + 8 * (lane & 3);
+      constexpr int kChunks = kCols / 8;             // 16-byte chunks of a row
+      const auto chunk_at = [&](int row, int ch) {   // 64- or 128-byte swizzle
+        return G == 1 ? row * 64 + ((ch ^ ((row >> 1) & 3)) << 4) : row * 128 + ((ch ^ (row & 7)) << 4);
+      };
+      uint16_t* dst = a.out + g0 * kLatent + 8 * (lane % kChunks);
 #pragma unroll 1
-      for (int col = 0; col < 256; col += 32) {
-        float v[32];
-        tc::tmem_ld32(lanes + col, v);
+      for (int col = 0; col < 256; col += kCols) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(bf16x2_rn(v[8 * i] * inv, v[8 * i + 1] * inv), bf16x2_rn(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                         bf16x2_rn(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                         bf16x2_rn(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+        for (int h = 0; h < G; ++h) {
+          float v[32];
+          tc::tmem_ld32(lanes + col + 32 * h, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stage + chunk_at(lane, 4 * h + i)) =
+                make_uint4(bf16x2_rn(v[8 * i] * inv, v[8 * i + 1] * inv), bf16x2_rn(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                           bf16x2_rn(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                           bf16x2_rn(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+        }
         __syncwarp();
-        // eight rows of 64 bytes an instruction
+        // whole rows of 64 or 128 bytes an instruction
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * i + (lane >> 2);
+        for (int i = 0; i < kChunks; ++i) {
+          const int row = (32 / kChunks) * i + lane / kChunks;
           if (row < have)
             *reinterpret_cast<uint4*>(dst + int64_t(row) * kLatent + channel(col)) =
-                *reinterpret_cast<const uint4*>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                *reinterpret_cast<const uint4*>(stage + chunk_at(row, lane % kChunks));
         }
         __syncwarp();
       }
@@ -1006,7 +1041,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
       tc::mbar_init(&sm.s_full[i], 1);
       tc::mbar_init(&sm.s_empty[i], 4 * G);
     }
-    tc::mbar_init(&sm.q_full, kRowWarps * G);
+    tc::mbar_init(&sm.q_full, kConvWarps * G);
     for (int i = 0; i < Lay<G>::kPSlots; ++i) {
       tc::mbar_init(&sm.p_free[i], 1);
       tc::mbar_init(&sm.p_full[i], 1);
@@ -1035,7 +1070,7 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
       softmax_role<G>(a, sm, base, cl, part, wid, lane, tmem);
     } else if (wid < kMmaWarp) {
       regs_down<kConvRegs>();
-      widen_role<G, true>(a, sm, base, cl, part, wid - kConvWarp0, lane);
+      widen_role<G, true>(a, sm, base, cl, part, wid - kConvWarp0, lane, tmem);
     } else {
       regs_down<kMmaRegs>();
       if (wid == kMmaWarp) scores_mma_role<G>(a, sm, base, cl, part, tmem, qmap);
@@ -1044,10 +1079,11 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
     }
   } else {
     if (wid < kRowWarps) {
+      regs_up<kRowRegs>();
       output_role<G>(a, sm, base, cl, part, wid, lane, tmem);
     } else if (wid < kMmaWarp) {
       regs_down<kConvRegs>();
-      widen_role<G, false>(a, sm, base, cl, part, wid - kConvWarp0, lane);
+      widen_role<G, false>(a, sm, base, cl, part, wid - kConvWarp0, lane, tmem);
     } else {
       regs_down<kMmaRegs>();
       if (wid == kMmaWarp && part == 0) values_mma_role<G>(a, sm, base, cl, tmem);
