@@ -295,8 +295,11 @@ class Rope:
         object.__setattr__(self, "_c", CRope(self.rot, self.layout, self.scaling, self.mscale, self.theta, self.factor,
                                              self.orig_ctx, self.turns_lo, self.turns_hi))
 
-    def c(self) -> CRope:
-        return self._c
+        object.__setattr__(self, "_ref", ctypes.byref(self._c))
+
+    def ref(self):
+        """The C structure, by reference."""
+        return self._ref
 
 
 def _need(fn: str, ok: bool):
@@ -305,26 +308,22 @@ def _need(fn: str, ok: bool):
         raise Csa2Error(fn, 1)
 
 
-def _plane(t, dtype, rows, width, dev) -> bool:
-    """A contiguous [rows, width] (or more leading axes) tensor of dtype on dev."""
-    return t.dtype == dtype and t.device == dev and t.is_contiguous() and t.numel() == rows * width
+def _plane(t, dtype, n, dev) -> bool:
+    """A contiguous tensor of n elements of dtype on dev."""
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.device == dev
 
 
-class _On:
-    """The tensors' device made current for a call (a library call launches on the current device)."""
-
-    def __init__(self, dev):
-        self.dev = dev
-        self.other = dev.type == "cuda" and dev.index != torch.cuda.current_device()
-
-    def __enter__(self):
-        if self.other:
-            self.was = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.other:
-            torch.cuda.set_device(self.was)
+def _call(fn: str, dev, stream, args):
+    """Calls the library on dev (made current for the call: a library call launches on the
+    current device) and on its current stream, or on `stream`."""
+    f = getattr(_lib, fn)
+    if dev.type != "cuda":
+        _need(fn, False)
+    if stream is None and dev.index == torch.cuda.current_device():
+        _check(fn, f(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, f(*args, _stream(stream)))
 
 
 def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor | None = None, offset: int = 0,
@@ -333,16 +332,21 @@ def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tens
     (bf16 or fp32, any strides but the last axis's 1) into y (a new tensor; y=x: in
     place).  pos: int32 [tokens].  inverse=True is the gradient's turn."""
     fn = "csa2_rope_apply"
-    _need(fn, x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32) and (x.shape[2] <= 1 or x.stride(2) == 1))
+    dt = x.dtype
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _need(fn, y.shape == x.shape and y.dtype == x.dtype and y.device == x.device and (y.shape[2] <= 1 or y.stride(2) == 1))
-    _need(fn, pos.dtype == torch.int32 and pos.device == x.device and pos.is_contiguous() and pos.numel() == x.shape[0])
-    with _On(x.device):
-        _check(fn, _lib.csa2_rope_apply(
-            ctypes.byref(cfg.c()), 1 if x.dtype == torch.float32 else 0, _ptr(x), _ptr(y), _ptr(pos), x.shape[0],
-            x.shape[1], x.shape[2], int(offset), x.stride(0), x.stride(1), y.stride(0), y.stride(1), int(bool(inverse)),
-            _stream(stream)))
+        y = torch.empty(x.shape, dtype=dt, device=x.device)
+    _need(fn, x.dim() == 3 and (dt is torch.bfloat16 or dt is torch.float32))
+    tokens, heads, dim = x.shape
+    xt, xh, xc = x.stride()
+    if y is x:
+        yt, yh = xt, xh
+    else:
+        _need(fn, y.shape == x.shape and y.dtype is dt and y.device == x.device)
+        yt, yh, yc = y.stride()
+        _need(fn, yc == 1 or dim <= 1)
+    _need(fn, (xc == 1 or dim <= 1) and _plane(pos, torch.int32, tokens, x.device))
+    _call(fn, x.device, stream, (cfg.ref(), 1 if dt is torch.float32 else 0, x.data_ptr(), y.data_ptr(), pos.data_ptr(),
+                                 tokens, heads, dim, offset, xt, xh, yt, yh, 1 if inverse else 0))
     return y
 
 
@@ -354,17 +358,15 @@ def csa2_kv_append(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, dst_rows: torc
     [rows, 256], scales [rows, 32], rope [rows, 64]; entry (bf16 [n, 576]) also
     receives the row in bf16."""
     fn = "csa2_kv_append"
-    _need(fn, x.dim() == 2 and x.shape[1] == DQK and x.dtype == torch.bfloat16 and x.stride(1) == 1)
+    _need(fn, x.dim() == 2 and x.shape[1] == DQK and x.dtype is torch.bfloat16 and x.stride(1) == 1)
     n, dev, rows = x.shape[0], x.device, codes.numel() // (LATENT // 2)
-    _need(fn, _plane(pos, torch.int32, n, 1, dev) and _plane(dst_rows, torch.int64, n, 1, dev))
-    _need(fn, _plane(codes, torch.uint8, rows, LATENT // 2, dev) and _plane(scales, torch.uint8, rows, LATENT // 16, dev)
-          and _plane(rope, torch.bfloat16, rows, ROPE, dev))
-    _need(fn, norm_w is None or _plane(norm_w, torch.bfloat16, 1, LATENT, dev))
-    _need(fn, entry is None or _plane(entry, torch.bfloat16, n, DQK, dev))
-    with _On(dev):
-        _check(fn, _lib.csa2_kv_append(
-            ctypes.byref(cfg.c()), _ptr(x), n, x.stride(0), _ptr(norm_w), float(eps), _ptr(pos), _ptr(dst_rows),
-            _ptr(codes), _ptr(scales), _ptr(rope), rows, _ptr(entry), _stream(stream)))
+    _need(fn, _plane(pos, torch.int32, n, dev) and _plane(dst_rows, torch.int64, n, dev)
+          and _plane(codes, torch.uint8, rows * (LATENT // 2), dev) and _plane(scales, torch.uint8, rows * (LATENT // 16), dev)
+          and _plane(rope, torch.bfloat16, rows * ROPE, dev)
+          and (norm_w is None or _plane(norm_w, torch.bfloat16, LATENT, dev))
+          and (entry is None or _plane(entry, torch.bfloat16, n * DQK, dev)))
+    _call(fn, dev, stream, (cfg.ref(), x.data_ptr(), n, x.stride(0), _ptr(norm_w), eps, pos.data_ptr(), dst_rows.data_ptr(),
+                            codes.data_ptr(), scales.data_ptr(), rope.data_ptr(), rows, _ptr(entry)))
 
 
 def dense_attn_workspace_size(dims: Dims, batch: int, total_q: int) -> int:
@@ -388,21 +390,18 @@ def csa2_dense_attn_chunk(dims: Dims, batch: int, q, q_start, kv_codes, kv_scale
     DENSE_ALL_POSITIONS (no causal mask) or 0; window > 0: the last `window` positions."""
     fn = "csa2_dense_attn_chunk"
     total, h, dev = q.shape[0], dims.heads, q.device
-    _need(fn, _plane(q, torch.bfloat16, total, h * DQK, dev) and _plane(out, torch.bfloat16, total, h * LATENT, dev)
-          and _plane(lse, torch.float32, total, h, dev))
-    _need(fn, _plane(q_start, torch.int32, batch + 1, 1, dev) and _plane(ctx_len, torch.int32, batch, 1, dev))
-    if page_table is not None:
-        _need(fn, _plane(page_table, torch.int32, batch, dims.max_pages, dev))
     rows = batch * dims.max_ctx if page_table is None else dims.num_pages * PAGE
-    _need(fn, kv_codes.dtype == torch.uint8 and kv_scales.dtype == torch.uint8 and kv_rope.dtype == torch.bfloat16)
-    for t, width in ((kv_codes, LATENT // 2), (kv_scales, LATENT // 16), (kv_rope, ROPE)):
-        _need(fn, t.device == dev and t.is_contiguous() and t.numel() >= rows * width)
-    _need(fn, ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous())
-    with _On(dev):
-        _check(fn, _lib.csa2_dense_attn_chunk(
-            ctypes.byref(dims.c()), batch, total, _ptr(q), _ptr(q_start), _ptr(kv_codes), _ptr(kv_scales), _ptr(kv_rope),
-            _ptr(page_table), _ptr(ctx_len), float(scale), int(window), int(flags), _ptr(out), _ptr(lse), _ptr(ws),
-            ws.numel(), _stream(stream)))
+    _need(fn, _plane(q, torch.bfloat16, total * h * DQK, dev) and _plane(out, torch.bfloat16, total * h * LATENT, dev)
+          and _plane(lse, torch.float32, total * h, dev) and _plane(q_start, torch.int32, batch + 1, dev)
+          and _plane(ctx_len, torch.int32, batch, dev)
+          and (page_table is None or _plane(page_table, torch.int32, batch * dims.max_pages, dev)))
+    for t, dt, width in ((kv_codes, torch.uint8, LATENT // 2), (kv_scales, torch.uint8, LATENT // 16),
+                         (kv_rope, torch.bfloat16, ROPE)):
+        _need(fn, t.dtype is dt and t.numel() >= rows * width and t.is_contiguous() and t.device == dev)
+    _need(fn, ws.dtype is torch.uint8 and ws.is_contiguous() and ws.device == dev)
+    _call(fn, dev, stream, (ctypes.byref(dims.c()), batch, total, q.data_ptr(), q_start.data_ptr(), kv_codes.data_ptr(),
+                            kv_scales.data_ptr(), kv_rope.data_ptr(), _ptr(page_table), ctx_len.data_ptr(), scale, window,
+                            flags, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel()))
 
 
 def get_device_status(ws: torch.Tensor, stream=None) -> int:

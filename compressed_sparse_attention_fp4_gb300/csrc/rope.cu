@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 template <typename T>
 cudaError_t rope_typed(const RopeArgs& a, cudaStream_t st) {
   constexpr int V = Io<T>::kVec;
-  const RopeTable tab = make_rope_table(a.cfg);
+  const RopeTable tab = rope_table(a.cfg);
   const bool half = a.cfg.layout == CSA2_ROPE_HALF;
   const int rot = a.cfg.rot;
   const bool copy = a.x != a.y;
@@ -327,7 +327,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
-  const RopeTable tab = make_rope_table(a.cfg);
+  const RopeTable tab = rope_table(a.cfg);
   const int64_t want = (a.n + 7) / 8, cap = int64_t(device_sms()) * 8;
   const unsigned grid = unsigned(want < cap ? want : cap);
   auto kernel = a.cfg.layout == CSA2_ROPE_HALF ? append_kernel<true> : append_kernel<false>;

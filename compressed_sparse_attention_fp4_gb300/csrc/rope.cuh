@@ -16,6 +16,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "common.cuh"
 
@@ -53,6 +54,33 @@ inline RopeTable make_rope_table(const csa2_rope& r) {
     t.turn[i] = uint64_t(std::ldexp(f / kTwoPi, 64));   // f <= 1: below a sixth of a turn
   }
   return t;
+}
+
+// make_rope_table, remembered: a table is a pure function of its configuration, and the
+// powers of 32 to 128 frequencies take longer than a decode step's kernel.
+inline RopeTable rope_table(const csa2_rope& r) {
+  struct Entry {
+    bool used;
+    csa2_rope r;
+    RopeTable t;
+  };
+  constexpr int kEntries = 8;
+  static std::mutex mu;
+  static Entry cache[kEntries];
+  static int next = 0;
+  const auto same = [](const csa2_rope& a, const csa2_rope& b) {
+    return a.rot == b.rot && a.scaling == b.scaling && a.mscale == b.mscale && a.theta == b.theta && a.factor == b.factor &&
+           a.orig_ctx == b.orig_ctx && a.turns_lo == b.turns_lo && a.turns_hi == b.turns_hi;
+  };
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Entry& e : cache)
+    if (e.used && same(e.r, r)) return e.t;
+  Entry& e = cache[next];
+  next = (next + 1) % kEntries;
+  e.t = make_rope_table(r);
+  e.r = r;
+  e.used = true;
+  return e.t;
 }
 
 // Checks of a rotary configuration (host).
