@@ -16,9 +16,11 @@ namespace {
 // Rotary positions: y = m R(angle) x on channels [offset, offset + rot) of every
 // head, the other channels copied (or left, in place).
 //
-// A CTA takes kTok tokens and a range of heads: it forms the (cos, sin) of its
+// A CTA takes kRopeTok tokens and a range of heads: it forms the (cos, sin) of its
 // tokens once in shared memory (rot / 2 of them a token, against heads * rot
-// values to turn) and then walks 16-byte pieces.
+// values to turn) and then walks 16-byte pieces, four in flight a thread.  8,192 tokens
+// x 64 heads x 64 fp32 channels in place, 268 MB: 46.6 us (85 % of the copy rate; one
+// piece in flight and two divisions a piece: 68).
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTok = 8;
@@ -79,43 +81,68 @@ __global__ void __launch_bounds__(kRopeThreads)
   __syncthreads();
   if (vec) {
     constexpr int V = Io<T>::kVec;
-    // pieces of a head: turned (kHalf: two pieces rot / 2 apart at once), then copied
+    // pieces of a head: turned (kHalf: two pieces rot / 2 apart at once), then copied.  A
+    // thread keeps to one piece and walks the (token, head) rows, four in flight.
     const int nturn = kHalf ? pairs / V : 2 * pairs / V, ncopy = copy ? (dim - 2 * pairs) / V : 0;
-    const int per = nturn + ncopy, per_t = nh * per, all = nt * per_t;
-    for (int i = tid; i < all; i += kRopeThreads) {
-      const int t = i / per_t, r = i - t * per_t, h = r / per, c = r - h * per;
-      const T* xs = x + (t0 + t) * xt + int64_t(h0 + h) * xh;
-      T* ys = y + (t0 + t) * yt + int64_t(h0 + h) * yh;
-      const float2* a = cs + t * kMaxPairs;
-      if (c >= nturn) {
-        int at = (c - nturn) * V;
+    const int per = nturn + ncopy, rows = nt * nh;
+    for (int c0 = 0; c0 < per; c0 += kRopeThreads) {
+      const int here = min(per - c0, kRopeThreads), apart = kRopeThreads / here;
+      const int c = c0 + tid % here, r0 = tid / here;
+      if (r0 >= apart) continue;
+      const bool turn = c < nturn;
+      int at = offset + c * V;
+      if (!turn) {
+        at = (c - nturn) * V;
         if (at >= offset) at += 2 * pairs;
-        *reinterpret_cast<uint4*>(ys + at) = *reinterpret_cast<const uint4*>(xs + at);
-      } else if (kHalf) {
-        float u[V], v[V];
-        const int p = c * V;
-        Io<T>::unpack(*reinterpret_cast<const uint4*>(xs + offset + p), u);
-        Io<T>::unpack(*reinterpret_cast<const uint4*>(xs + offset + pairs + p), v);
+      }
+      const float inv = 1.0f / float(nh);            // rows < 2^20: (r + 1/2) / nh truncates to r / nh
+      for (int r = r0; r < rows; r += 4 * apart) {
+        uint4 u4[4], v4[4];
+        int tk[4];
+        int64_t yo[4];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float2 e = a[p + k];
-          const float w = u[k];
-          u[k] = w * e.x - v[k] * e.y;
-          v[k] = w * e.y + v[k] * e.x;
+        for (int b = 0; b < 4; ++b) {
+          const int rr = min(r + b * apart, rows - 1);
+          tk[b] = __float2int_rz((float(rr) + 0.5f) * inv);
+          const int h = h0 + rr - tk[b] * nh;
+          const T* xs = x + (t0 + tk[b]) * xt + int64_t(h) * xh + at;
+          yo[b] = (t0 + tk[b]) * yt + int64_t(h) * yh + at;
+          u4[b] = *reinterpret_cast<const uint4*>(xs);
+          if (kHalf && turn) v4[b] = *reinterpret_cast<const uint4*>(xs + pairs);
         }
-        *reinterpret_cast<uint4*>(ys + offset + p) = Io<T>::pack(u);
-        *reinterpret_cast<uint4*>(ys + offset + pairs + p) = Io<T>::pack(v);
-      } else {
-        float u[V];
-        Io<T>::unpack(*reinterpret_cast<const uint4*>(xs + offset + c * V), u);
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) {
-          const float2 e = a[c * (V / 2) + k];
-          const float w = u[2 * k];
-          u[2 * k] = w * e.x - u[2 * k + 1] * e.y;
-          u[2 * k + 1] = w * e.y + u[2 * k + 1] * e.x;
+        for (int b = 0; b < 4; ++b) {
+          if (r + b * apart >= rows) break;
+          T* ys = y + yo[b];
+          if (!turn) {
+            *reinterpret_cast<uint4*>(ys) = u4[b];
+            continue;
+          }
+          const float2* e2 = cs + tk[b] * kMaxPairs + (kHalf ? c * V : c * (V / 2));
+          float u[V];
+          Io<T>::unpack(u4[b], u);
+          if (kHalf) {
+            float v[V];
+            Io<T>::unpack(v4[b], v);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              const float2 e = e2[k];
+              const float w = u[k];
+              u[k] = w * e.x - v[k] * e.y;
+              v[k] = w * e.y + v[k] * e.x;
+            }
+            *reinterpret_cast<uint4*>(ys + pairs) = Io<T>::pack(v);
+          } else {
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) {
+              const float2 e = e2[k];
+              const float w = u[2 * k];
+              u[2 * k] = w * e.x - u[2 * k + 1] * e.y;
+              u[2 * k + 1] = w * e.y + u[2 * k + 1] * e.x;
+            }
+          }
+          *reinterpret_cast<uint4*>(ys) = Io<T>::pack(u);
         }
-        *reinterpret_cast<uint4*>(ys + offset + c * V) = Io<T>::pack(u);
       }
     }
   } else {
@@ -156,8 +183,11 @@ __global__ void __launch_bounds__(kRopeThreads)
 //   * 1/sqrt is rsqrtf and one Newton step kept as a second fp32 part;
 //   * x w is exact in fp32 (8 + 8 bits); only a product within 8 units of a
 //     bf16 midpoint (one in 4,000) needs the low parts.
+// Bound by its instructions (about 500 a row) a little above its bytes: 131,072 rows with
+// the bf16 rows written, 357 MB, in 90 us (3.9 TB/s; 53 us at the copy rate).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
+constexpr int kAppendBlocks = 3;                    // resident on an SM
 
 // xw * (r + rl) rounded once to bf16, for a product p = xw * r near a midpoint.
 __device__ __noinline__ float near_midpoint(float xw, float r, float rl, float p) {
@@ -169,27 +199,57 @@ __device__ __noinline__ float near_midpoint(float xw, float r, float rl, float p
   return q;
 }
 
-__device__ inline uint4 norm8(uint4 xv, uint4 wv, float up, float r, float rl) {
-  float x[8], w[8], y[8];
-  Io<uint16_t>::unpack(xv, x);
-  Io<uint16_t>::unpack(wv, w);
-  uint32_t near = 0xFFFFu;
+// 8 scaled inputs g and weights w: bf16(g w (r + rl)), rounded once.
+__device__ inline uint4 norm8(const float (&g)[8], const float (&w)[8], float r, float rl) {
+  float x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = (x[i] * up) * w[i];
+    x[i] = g[i] * w[i];
     y[i] = x[i] * r;
-    near = min(near, (__float_as_uint(y[i]) - 0x7FF8u) & 0xFFFFu);
   }
-  if (near <= 16u) {
+  // low halves within 8 of a midpoint, two values at a time (the carry between the two
+  // halves of the sum widens the test of the upper one by 1)
+  uint32_t near = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    near = __vminu2(near, __byte_perm(__float_as_uint(y[i]), __float_as_uint(y[i + 1]), 0x5410) + 0x80088008u);
+  if ((near & 0xFFFFu) <= 17u || (near >> 16) <= 17u) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (((__float_as_uint(y[i]) - 0x7FF8u) & 0xFFFFu) <= 16u) y[i] = near_midpoint(x[i], r, rl, y[i]);
+      if (((__float_as_uint(y[i]) + 0x8008u) & 0xFFFFu) <= 16u) y[i] = near_midpoint(x[i], r, rl, y[i]);
   }
   return Io<uint16_t>::pack(y);
 }
 
+// What a lane reads of a row.
+struct AppendRow {
+  uint4 v[2];
+  uint32_t p, p2;                                    // rotary pair: one word, or (kHalf) one value each
+  int32_t pos;
+  int64_t dst;
+};
 template <bool kHalf>
-__global__ void __launch_bounds__(kAppendThreads)
+__device__ inline AppendRow append_load(const uint16_t* x, int64_t stride, const int32_t* pos, const int64_t* dst, int64_t row,
+                                        int lane) {
+  AppendRow a;
+  const uint16_t* xr = x + row * stride;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) a.v[r] = __ldcs(reinterpret_cast<const uint4*>(xr) + r * 32 + lane);
+  if (kHalf) {                                       // not put together here: that would wait for them
+    a.p = __ldcs(xr + kLatent + lane);
+    a.p2 = __ldcs(xr + kLatent + 32 + lane);
+  } else {
+    a.p = __ldcs(reinterpret_cast<const uint32_t*>(xr + kLatent) + lane);
+    a.p2 = 0;
+  }
+  a.pos = __ldg(pos + row);
+  a.dst = __ldg(dst + row);
+  return a;
+}
+
+// The next row's loads are on their way while a row is worked on.
+template <bool kHalf, bool kNorm>
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     append_kernel(const __grid_constant__ RopeTable tab, const uint16_t* __restrict__ x, int64_t n, int64_t stride,
                   const uint16_t* __restrict__ norm_w, float eps, const int32_t* __restrict__ pos,
                   const int64_t* __restrict__ dst_rows, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
@@ -199,42 +259,34 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int64_t nwarps = (int64_t(gridDim.x) * blockDim.x) >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  uint4 w[2];
+  float w[2][8];
+  if (kNorm) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
-    w[r] = norm_w ? __ldg(reinterpret_cast<const uint4*>(norm_w) + r * 32 + lane) : make_uint4(0, 0, 0, 0);
+    for (int r = 0; r < 2; ++r) Io<uint16_t>::unpack(__ldg(reinterpret_cast<const uint4*>(norm_w) + r * 32 + lane), w[r]);
+  }
+  if (warp >= n) return;
+  AppendRow next = append_load<kHalf>(x, stride, pos, dst_rows, warp, lane);
   for (int64_t row = warp; row < n; row += nwarps) {
-    const uint16_t* xr = x + row * stride;
-    uint4 v[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) v[r] = __ldcs(reinterpret_cast<const uint4*>(xr) + r * 32 + lane);
-    float u0, u1;
-    if (kHalf) {
-      u0 = bf16_to_f32(__ldcs(xr + kLatent + lane));
-      u1 = bf16_to_f32(__ldcs(xr + kLatent + 32 + lane));
-    } else {
-      const uint32_t p = __ldcs(reinterpret_cast<const uint32_t*>(xr + kLatent) + lane);
-      u0 = __uint_as_float(p << 16);
-      u1 = __uint_as_float(p & 0xFFFF0000u);
-    }
-    const int32_t ps = __ldg(pos + row);
-    const int64_t dst = __ldg(dst_rows + row);
-    if (norm_w) {
+    uint4 v[2] = {next.v[0], next.v[1]};
+    const float u0 = __uint_as_float(next.p << 16), u1 = __uint_as_float(kHalf ? next.p2 << 16 : next.p & 0xFFFF0000u);
+    const int32_t ps = next.pos;
+    const int64_t dst = next.dst;
+    next = append_load<kHalf>(x, stride, pos, dst_rows, min64(row + nwarps, n - 1), lane);
+    if (kNorm) {
       const uint32_t a[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(bf16x8_amax(a), bf16x8_amax(b))));
       // exponent of the row's largest value, at least -40 (eps then outweighs the squares by far)
       const int ex = max(int(top >> 23) - 127, -40);
       const float up = __uint_as_float(uint32_t(127 - ex) << 23 | (ex == 127 ? 0x00400000u : 0u));
-      float s = 64.0f, e = 0.0f;
+      float g[2][8], s = 64.0f, e = 0.0f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float f[8];
-        Io<uint16_t>::unpack(v[r], f);
+        Io<uint16_t>::unpack(v[r], g[r]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float g = f[i] * up;
-          const float t = __fmaf_rn(g, g, s);
-          e += __fmaf_rn(g, g, s - t);
+          g[r][i] *= up;
+          const float t = __fmaf_rn(g[r][i], g[r][i], s);
+          e += __fmaf_rn(g[r][i], g[r][i], s - t);
           s = t;
         }
       }
@@ -253,7 +305,7 @@ __global__ void __launch_bounds__(kAppendThreads)
       const float d = __fmaf_rn(-mh, p, 1.0f) - __fmaf_rn(mh, pe, ml * p);
       const float rl = 0.5f * r0 * d;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) v[r] = norm8(v[r], w[r], up, r0, rl);
+      for (int r = 0; r < 2; ++r) v[r] = norm8(g[r], w[r], r0, rl);
     }
     const float2 cs = rope_cs(tab, lane, ps);
     const uint32_t turned = bf16x2_rn(u0 * cs.x - u1 * cs.y, u0 * cs.y + u1 * cs.x);
@@ -268,24 +320,19 @@ __global__ void __launch_bounds__(kAppendThreads)
         __stcs(reinterpret_cast<uint32_t*>(er + kLatent) + lane, turned);
       }
     }
-    const bool keep = dst >= 0 && dst < cache_rows;
+    if (dst < 0 || dst >= cache_rows) continue;       // the same for the whole warp
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       uint32_t sc;
-      const uint32_t packed = fp4_quantize_half_group(v[r], &sc);
-      if (keep) {
-        codes[dst * 64 + r * 32 + lane] = packed;
-        if ((lane & 1) == 0) scales[dst * 32 + r * 16 + (lane >> 1)] = uint8_t(sc);
-      }
+      codes[dst * 64 + r * 32 + lane] = fp4_quantize_half_group(v[r], &sc);
+      if ((lane & 1) == 0) scales[dst * 32 + r * 16 + (lane >> 1)] = uint8_t(sc);
     }
-    if (keep) {
-      uint16_t* rr = rope + dst * kRope;
-      if (kHalf) {
-        rr[lane] = uint16_t(turned);
-        rr[32 + lane] = uint16_t(turned >> 16);
-      } else {
-        reinterpret_cast<uint32_t*>(rr)[lane] = turned;
-      }
+    uint16_t* rr = rope + dst * kRope;
+    if (kHalf) {
+      rr[lane] = uint16_t(turned);
+      rr[32 + lane] = uint16_t(turned >> 16);
+    } else {
+      reinterpret_cast<uint32_t*>(rr)[lane] = turned;
     }
   }
 }
@@ -328,9 +375,12 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
   const RopeTable tab = rope_table(a.cfg);
-  const int64_t want = (a.n + 7) / 8, cap = int64_t(device_sms()) * 8;
+  // one row a warp up to what is resident at once (kAppendBlocks an SM), then rows in turn
+  const int64_t want = (a.n + 7) / 8, cap = int64_t(device_sms()) * kAppendBlocks;
   const unsigned grid = unsigned(want < cap ? want : cap);
-  auto kernel = a.cfg.layout == CSA2_ROPE_HALF ? append_kernel<true> : append_kernel<false>;
+  const bool half = a.cfg.layout == CSA2_ROPE_HALF;
+  auto kernel = a.norm_w ? (half ? append_kernel<true, true> : append_kernel<false, true>)
+                         : (half ? append_kernel<true, false> : append_kernel<false, false>);
   cudaError_t e;
   CSA2_PROFILED(st, "kv_append",
                 (e = launch_pdl(kernel, dim3(grid), dim3(kAppendThreads), 0, st, 1, tab, a.x, a.n, a.x_stride, a.norm_w,

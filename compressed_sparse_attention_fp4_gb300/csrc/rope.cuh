@@ -98,13 +98,20 @@ inline csa2_status check_rope(const csa2_rope* r) {
   return CSA2_OK;
 }
 
-// (cos, sin) * mscale of pair i at position pos.
+// (cos, sin) * mscale of pair i at position pos.  The angle, a 32-bit fraction of a turn,
+// is taken to within an eighth of a turn of a multiple of a quarter, where the Taylor
+// series about 0 to the 9th and 8th power are right to 2.5e-8 (the first terms left out,
+// (pi/4)^11 / 11! and (pi/4)^10 / 10!).
 __device__ inline float2 rope_cs(const RopeTable& t, int i, int32_t pos) {
-  const uint64_t a = uint64_t(int64_t(pos)) * t.turn[i];       // modulo one turn
-  const float half_turns = float(int32_t(a >> 32)) * 4.656612873077393e-10f;   // 2^-31: [-1, 1)
-  float s, c;
-  sincospif(half_turns, &s, &c);
-  return make_float2(c * t.mscale, s * t.mscale);
+  const uint32_t a = uint32_t((uint64_t(int64_t(pos)) * t.turn[i]) >> 32);      // modulo one turn
+  const uint32_t q = (a + 0x20000000u) >> 30;                                    // nearest quarter
+  const float x = float(int32_t(a - (q << 30))) * 1.4629180792671596e-9f;        // 2 pi / 2^32
+  const float z = x * x;
+  const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
+  const float u = (q & 1) ? s : c, v = (q & 1) ? c : s;
+  return make_float2(((q + 1) & 2) ? -u * t.mscale : u * t.mscale, (q & 2) ? -v * t.mscale : v * t.mscale);
 }
 
 }  // namespace csa2
