@@ -9,32 +9,49 @@
 // section 3.2: shared main KV), so the tokens and heads of a sequence are simply
 // rows of one matrix, cut into tiles of 128.
 //
-// Split over a pair of SMs.  128 rows x 512 fp32 outputs fill the tensor memory
-// of an SM, so scores and outputs cannot live on one SM.  A cluster of two CTAs
-// divides the work by kind instead:
-//   scores CTA (rank 0)   queries resident in tensor memory (288 columns); a block of
-//       64 positions is widened from FP4 to fp16 (exact: 6 significant bits, 2^-10 ..
-//       2688) in shared memory, its rope keys stay bf16; S[128 x 64] = Q . K^T (M 128,
-//       N 64, K 512 fp16 + 64 bf16 -> fp32); softmax, one thread a row; P as fp16 goes to
-//       the other CTA by an asynchronous shared-memory copy;
-//   values CTA (rank 1)   widens the same block's latents to fp16,
+// Scores and outputs on different SMs.  128 rows x 512 fp32 outputs fill the tensor memory
+// of an SM, so scores and outputs cannot live on one.  A cluster divides the work by
+// kind instead:
+//   scores CTA   queries resident in tensor memory (288 columns); a block of 64 positions
+//       is widened from FP4 to fp16 (exact: 6 significant bits, 2^-10 .. 2688) in shared
+//       memory, its rope keys stay bf16; S[128 x 64] = Q . K^T (M 128, N 64, K 512 fp16 +
+//       64 bf16 -> fp32); softmax, one thread a row; P as fp16 goes to the values CTA by
+//       an asynchronous copy between their shared memories;
+//   values CTA   widens the same block's latents to fp16,
 //       O[128 x 512] += P . V (M 128, N 2 x 256, K 64).
-// Data flow one way only, so each side runs ahead through its rings (2 blocks of
-// keys, 2 score buffers, 3 blocks of P, 2 blocks of values).  Tensor work a block:
-// 1,152 and 1,024 cycles; the halves are balanced and nothing is computed twice but
-// the widening.
+// Data flow one way only, so each side runs ahead through its rings (raw bytes of the
+// next blocks, 2 blocks of keys or values, 3 score buffers, 3 blocks of P).  Tensor work
+// a block: 1,152 and 1,024 cycles; nothing is computed twice but the widening.
+//   G = 1: clusters of 2 CTAs, tiles of 128 rows;
+//   G = 2: clusters of 4, tiles of 256 rows: two scores and two values CTAs, each pair one
+//       product (cta_group::2: own rows, shared keys or values, of which each CTA widens and
+//       holds half).  Half of the widening per row, and half of the shared-memory reads for
+//       the shared operand.
 //
 // Softmax reference: kept per row as an integer (base-2) and raised only when a
 // block's maximum passes it by more than 8, so the outputs are rarely rescaled, and
-// then by an exact power of two.  P = 2^(x - ref + 7) <= 2^15 fits fp16; terms
-// 2^-31 below the reference are the first to be lost.  Sums are fp32, of the
-// unrounded P.
+// then by a power of two.  P = 2^(x - ref + 7) <= 2^15 fits fp16 (rounded to 11 bits where
+// bf16 has 8); terms 2^-31 below the reference are the first to be lost.  Sums are
+// fp32, of the unrounded P.
 //
 // Work division: the (tile, block) pairs of the call are counted by a plan kernel
 // and cut into equal runs, one per cluster, whatever the shape: a decode batch splits
 // its long contexts, a prompt gives each cluster whole tiles.  A tile cut by a
 // boundary leaves partial outputs (fp32, at most two per cluster) that a merge kernel
 // joins in a fixed order: results are the same from call to call.
+//
+// Roles of a CTA's 28 warps: 8 row warps (softmax / outputs), 16 widening warps (which also
+// bring the queries into tensor memory), one that issues the MMAs, one that copies blocks
+// from the cache, one for rope keys (scores CTA, G 1) or for handing slots of P back
+// (values CTA).
+//
+// Measured (GB300; 1,933 TFLOP/s measured bf16 rate, 2 * 1088 flop a visible (row, position)):
+// 2,048 tokens x 64 heads on 32,768 positions 5.6 ms, 1.61 PFLOP/s (83 %); bound by the
+// tensor pipe and the shared-memory bandwidth that feeds it.  8 contexts of 131,072 with
+// one token 0.33 ms, 0.45 PFLOP/s (64 of 128 rows of each product are used; 0.235 ms
+// with the copies from the cache left out: one block on its way at a time).  Short
+// prompts (tiles of one or two blocks) 0.5 PFLOP/s: a tile's queries, 147 KB a CTA, cannot
+// come before the last product of the tile before it.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>

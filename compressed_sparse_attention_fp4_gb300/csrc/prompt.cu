@@ -35,7 +35,8 @@ csa2_status check_dense_dims(const csa2_dims* d, int32_t batch, int64_t total_q)
   if (!d || batch < 0 || total_q < 0) return CSA2_ERR_INVALID_ARG;
   if (d->heads < 1 || d->heads > kMaxHeads) return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (d->max_ctx < 1 || d->max_ctx > kMaxCtx) return CSA2_ERR_UNSUPPORTED_SHAPE;
-  if (batch > (1 << 20) || total_q > INT32_MAX / d->heads) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  // rows (and positions less a window) are counted in 32 bits with room to spare
+  if (batch > (1 << 20) || total_q > (1 << 30) / d->heads) return CSA2_ERR_UNSUPPORTED_SHAPE;
   return CSA2_OK;
 }
 
@@ -151,7 +152,7 @@ csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t tot
   a.batch = batch;
   a.total_q = int(total_q);
   a.causal = causal ? 1 : 0;
-  a.window = window;
+  a.window = int(min64(window, kMaxCtx));          // a longer one is no window at all
   a.q = q;
   a.q_start = q_start;
   a.codes = kv_codes;

@@ -451,8 +451,9 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
  *             first 256 the error word as elsewhere.  Calls that may run at the same
  *             time need a workspace each.
  *   P is rounded to fp16 (2^-11) and the output to bf16; everything between is fp32.
- * Limits: total_q * H < 2^31, batch <= 2^20, cache rows (batch * max_ctx, or num_pages *
+ * Limits: total_q * H <= 2^30, batch <= 2^20, cache rows (batch * max_ctx, or num_pages *
  * 64) < 2^31.
+ * Make the first call on a device before any stream capture.
  * Errors: CSA2_ERR_INVALID_ARG (window < 0, window with CSA2_DENSE_ALL_POSITIONS,
  *         unknown flags, pointers, NaN scale), CSA2_ERR_UNSUPPORTED_SHAPE,
  *         CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
