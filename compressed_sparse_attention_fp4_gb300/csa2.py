@@ -344,7 +344,7 @@ def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tens
         _need(fn, y.shape == x.shape and y.dtype is dt and y.device == x.device)
         yt, yh, yc = y.stride()
         _need(fn, yc == 1 or dim <= 1)
-    _need(fn, (xc == 1 or dim <= 1) and _plane(pos, torch.int32, tokens, x.device))
+    _need(fn, (xc == 1 or dim <= 1) and 0 <= offset <= dim and _plane(pos, torch.int32, tokens, x.device))
     _call(fn, x.device, stream, (cfg.ref(), 1 if dt is torch.float32 else 0, x.data_ptr(), y.data_ptr(), pos.data_ptr(),
                                  tokens, heads, dim, offset, xt, xh, yt, yh, 1 if inverse else 0))
     return y
@@ -398,7 +398,9 @@ def csa2_dense_attn_chunk(dims: Dims, batch: int, q, q_start, kv_codes, kv_scale
     for t, dt, width in ((kv_codes, torch.uint8, LATENT // 2), (kv_scales, torch.uint8, LATENT // 16),
                          (kv_rope, torch.bfloat16, ROPE)):
         _need(fn, t.dtype is dt and t.numel() >= rows * width and t.is_contiguous() and t.device == dev)
-    _need(fn, ws.dtype is torch.uint8 and ws.is_contiguous() and ws.device == dev)
+    # whole numbers that ctypes would cut to 32 bits
+    _need(fn, ws.dtype is torch.uint8 and ws.is_contiguous() and ws.device == dev and 0 <= window < 1 << 31
+          and 0 <= flags < 1 << 31)
     _call(fn, dev, stream, (ctypes.byref(dims.c()), batch, total, q.data_ptr(), q_start.data_ptr(), kv_codes.data_ptr(),
                             kv_scales.data_ptr(), kv_rope.data_ptr(), _ptr(page_table), ctx_len.data_ptr(), scale, window,
                             flags, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel()))

@@ -640,7 +640,11 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         // rows behind the context hold anything: their scale is taken as 0 (0 * P stays 0; their scores are masked)
-        const uint32_t two = e4m3x2_to_f16x2(uint16_t(have ? sc[j] : 0u));
+        uint32_t code = have ? sc[j] : 0u;
+        // a NaN scale makes NaN of the scores of the rows that see its position, by the keys; taken
+        // as 0 among the values it leaves the others alone (0 * P)
+        if (!kScores) code &= ~((((code & 0x7F7Fu) + 0x0101u) >> 7 & 0x0101u) * 0xFFu);
+        const uint32_t two = e4m3x2_to_f16x2(uint16_t(code));
         const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
         st_shared16(d + 2 * j * kRegion + o0, widen8(cw[j].x, s0));
         st_shared16(d + 2 * j * kRegion + (o0 ^ 16), widen8(cw[j].y, s0));
@@ -838,7 +842,7 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
         sm.ref[half][r] = ref;
         some_arrive(1 + 4 * half + wq, 64);
       }
-      if (own != ref) sum = own == -INFINITY ? 0.0f : sum * ex2(own - ref);
+      if (own != ref && own != -INFINITY) sum *= ex2(own - ref);     // (no reference yet: 0, or NaN)
       own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
       if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) return;
@@ -977,9 +981,9 @@ __device__ inline void output_role(const DenseArgs& a, DenseSmall& sm, uint8_t* 
     const uint32_t m = n - 1;
     if (!wait_warp(sm, &sm.pv_done[m % Lay<G>::kPSlots], (m / Lay<G>::kPSlots) & 1, a.ws)) return;
     tc::tc_fence_after_sync();
-    if (sum_b > 0.0f) sum += sum_b * ex2(sub_b - sub);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const float lse = sum > 0.0f ? (sub + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (sum_b != 0.0f) sum += sum_b * ex2(sub_b - sub);
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;                 // NaN stays NaN
+    const float lse = sum != 0.0f ? (sub + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     const int lr = it.a.y + kDenseTile * part + r, rows = it.a.w * a.d.heads;
     if (it.head || it.tail) {
       const int slot = (2 * cl + (it.head ? 0 : 1)) * G + part;
@@ -1375,7 +1379,7 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
 #pragma unroll
         for (int k = 0; k < kMergeCh; ++k) o[k] = fmaf(w, __ldg(po + k * kDenseTile), o[k]);
       }
-      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      const float inv = total != 0.0f ? 1.0f / total : 0.0f;
       const int64_t row = int64_t(ta.z) * a.d.heads + lr;
       uint4* dst = reinterpret_cast<uint4*>(a.out + row * kLatent + g * kMergeCh);
 #pragma unroll
@@ -1383,7 +1387,7 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
         dst[k] = make_uint4(bf16x2_rn(o[8 * k] * inv, o[8 * k + 1] * inv), bf16x2_rn(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
                             bf16x2_rn(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
                             bf16x2_rn(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-      if (g == 0) a.lse[row] = total > 0.0f ? top + logf(total) : -INFINITY;
+      if (g == 0) a.lse[row] = total != 0.0f ? top + logf(total) : -INFINITY;
     }
   }
   // tiles that see nothing

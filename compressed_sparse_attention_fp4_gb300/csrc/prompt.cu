@@ -91,7 +91,7 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
   csa2_status st = check_rope(r);
   if (st != CSA2_OK) return st;
   if (r->rot != kRope) return CSA2_ERR_UNSUPPORTED_SHAPE;
-  if (n < 0 || cache_rows < 0 || (norm_w && (!(eps > 0.0f) || !std::isfinite(eps)))) return CSA2_ERR_INVALID_ARG;
+  if (n < 0 || cache_rows < 0 || (norm_w && !(eps > 0.0f && eps <= 1.0f))) return CSA2_ERR_INVALID_ARG;
   if (n == 0) return CSA2_OK;
   if (!x || !pos || !dst_rows || !codes || !scales || !rope) return CSA2_ERR_INVALID_ARG;
   if (!is_aligned(x, 16) || !is_aligned(codes, 16) || !is_aligned(scales, 2) || !is_aligned(rope, 16) ||
@@ -99,6 +99,12 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
       (entry && !is_aligned(entry, 16)))
     return CSA2_ERR_INVALID_ARG;
   if (n > 1 && (x_stride < kDqk || x_stride % 8 != 0)) return CSA2_ERR_INVALID_ARG;
+  if (entry) {
+    const __int128 last = __int128(n - 1) * (n > 1 ? x_stride : 0) + kDqk;
+    if (last > (__int128(1) << 59) || n > (int64_t(1) << 49)) return CSA2_ERR_UNSUPPORTED_SHAPE;
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ea = reinterpret_cast<uintptr_t>(entry);
+    if (xa < ea + uintptr_t(n) * kDqk * 2 && ea < xa + uintptr_t(last) * 2) return CSA2_ERR_INVALID_ARG;
+  }
   AppendArgs a = {};
   a.cfg = *r;
   a.x = x;

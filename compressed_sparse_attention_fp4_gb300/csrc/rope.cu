@@ -199,6 +199,12 @@ __device__ __noinline__ float near_midpoint(float xw, float r, float rl, float p
   return q;
 }
 
+// Largest magnitude bits of 8 bf16 values, two candidates in one word.
+__device__ inline uint32_t bf16x8_top(uint4 v) {
+  constexpr uint32_t m = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+}
+
 // 8 scaled inputs g and weights w: bf16(g w (r + rl)), rounded once.
 __device__ inline uint4 norm8(const float (&g)[8], const float (&w)[8], float r, float rl) {
   float x[8], y[8];
@@ -273,11 +279,13 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     const int64_t dst = next.dst;
     next = append_load<kHalf>(x, stride, pos, dst_rows, min64(row + nwarps, n - 1), lane);
     if (kNorm) {
-      const uint32_t a[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(bf16x8_amax(a), bf16x8_amax(b))));
+      const uint32_t b2 = __vmaxu2(bf16x8_top(v[0]), bf16x8_top(v[1]));
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(b2 & 0xFFFFu, b2 >> 16));
+      // an infinity or a NaN in the row: its values as they are times 0 or NaN (below)
+      const bool whole = top < 0x7F80u;
       // exponent of the row's largest value, at least -40 (eps then outweighs the squares by far)
-      const int ex = max(int(top >> 23) - 127, -40);
-      const float up = __uint_as_float(uint32_t(127 - ex) << 23 | (ex == 127 ? 0x00400000u : 0u));
+      const int ex = max(int(top >> 7) - 127, -40);
+      const float up = whole ? __uint_as_float(uint32_t(127 - ex) << 23 | (ex == 127 ? 0x00400000u : 0u)) : 1.0f;
       float g[2][8], s = 64.0f, e = 0.0f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -300,7 +308,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
       const float ms = m0 + es, back = ms - m0;
       const float ml0 = (m0 - (ms - back)) + (es - back) + m1;
       const float mh = ms + ml0, ml = (ms - mh) + ml0;
-      const float r0 = rsqrtf(mh);
+      const float r0 = whole ? rsqrtf(mh) : top > 0x7F80u ? __uint_as_float(0x7FC00000u) : 0.0f;
       const float p = r0 * r0, pe = __fmaf_rn(r0, r0, -p);
       const float d = __fmaf_rn(-mh, p, 1.0f) - __fmaf_rn(mh, pe, ml * p);
       const float rl = 0.5f * r0 * d;

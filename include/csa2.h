@@ -408,17 +408,19 @@ csa2_status csa2_rope_apply(const csa2_rope* r, int32_t dtype, const void* x, vo
  * channels: 512 latent, then 64 rotary) is normed, rotated, quantized and written
  * to cache row dst_rows[i] in one pass:
  *   latent = bf16(x w / sqrt(mean(x^2) + eps)), rounded once from the exact value
- *            (x itself when norm_w is NULL);
+ *            (x itself when norm_w is NULL); in a row that holds an infinity or a NaN
+ *            the square root is infinite or NaN: 0 or NaN throughout;
  *   codes, scales of the latent exactly as fp4_kv_quantize forms them;
  *   rope   = bf16(rotary(x[512..575], pos[i])) with r (r->rot must be 64).
  * A row whose destination is negative or not below cache_rows writes no cache row.
  * Destinations must differ from each other (of two rows with the same one, which
  * bytes of which row remain is not specified).
- *   norm_w:   device bf16 [512], or NULL;  eps > 0, finite
+ *   norm_w:   device bf16 [512], or NULL;  0 < eps <= 1
  *   pos:      device int32 [n];  dst_rows: device int64 [n]
  *   codes, scales, rope: the cache planes (layout above; 16-, 2- and 16-byte aligned)
  *   entry:    device bf16 [n][576], or NULL: also receives every row i as
- *             [latent ; rope] in bf16 (an SWA window row), whatever dst_rows[i] is
+ *             [latent ; rope] in bf16 (an SWA window row), whatever dst_rows[i] is;
+ *             no part of it within x
  *   x: 16-byte aligned, x_stride a multiple of 8, at least 576 for n > 1
  * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (rot != 64), CSA2_ERR_CUDA. */
 csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int64_t x_stride,
@@ -439,6 +441,8 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
  * Any number of tokens per sequence, none included: one (a decode step), a few
  * (drafts), a prompt's chunk, a whole prompt.  Tokens of q before q_start[0] or
  * from q_start[batch] on are not touched.  Results do not change from call to call.
+ * An infinity or a NaN at a position (rope keys, a NaN scale) or in a query reaches only
+ * the outputs of the tokens that see that position, or of that token and head.
  *   Dimensions read: heads, max_ctx, max_pages, num_pages (the others must be valid
  *   only for the calls that use them).
  *   q:        device bf16 [total_q][H][576], 16-byte aligned

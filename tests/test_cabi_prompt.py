@@ -113,3 +113,12 @@ def test_binding_refuses_wrong_tensors(mod):
         with pytest.raises(mod.Csa2Error) as e:
             bad()
         assert e.value.code == 1
+
+
+def test_append_limits_of_eps_and_overlap(mod):
+    for eps in (1.5, 1e30):
+        assert append(mod, eps=eps) == 1
+    assert append(mod, n=4, entry=FAKE) == 1                      # over x itself
+    assert append(mod, n=4, entry=P(FAKE.value + 3 * 1152)) == 1  # within its last row
+    assert append(mod, n=4, entry=P(FAKE.value - 16 if FAKE.value > 16 else 16)) == 1
+    assert append(mod, n=1 << 50, entry=P(1 << 40)) in (1, 2)

@@ -129,3 +129,51 @@ def test_same_bytes_as_the_codec_write():
     codes, scales, _, ent = run(x, w, pos, dst, 320, cfg)
     c2, s2 = csa2.fp4_kv_quantize(ent[:, :512].contiguous())
     assert torch.equal(codes[dst], c2) and torch.equal(scales[dst], s2)
+
+
+def test_rows_with_infinities_and_nan():
+    """As the formula has it: the root is infinite or NaN, so the row is 0 where finite, NaN else; other rows are alone."""
+    x, w, pos, dst = inputs(9, 64, 31)
+    cfg = csa2.Rope()
+    clean = run(x, w, pos, dst, 64, cfg)
+    x[1, 7] = float("inf")
+    x[2, 100] = float("nan")
+    x[3, 3], x[3, 500] = -float("inf"), float("nan")
+    codes, scales, rope, ent = run(x, w, pos, dst, 64, cfg)
+    e = ent[:, :512].float()
+    assert torch.isnan(e[1, 7]) and torch.all(e[1, torch.arange(512) != 7] == 0)
+    assert torch.isnan(e[2]).all() and torch.isnan(e[3]).all()
+    rest = [0, 4, 5, 6, 7, 8]
+    assert torch.equal(ent[rest], clean[3][rest])
+    for got, want in ((codes, clean[0]), (scales, clean[1]), (rope, clean[2])):
+        assert torch.equal(got[dst[rest]], want[dst[rest]])
+    assert torch.equal(rope[dst], clean[2][dst])
+    c2, s2 = csa2.fp4_kv_quantize(ent[:, :512].contiguous())
+    assert torch.equal(codes[dst], c2) and torch.equal(scales[dst], s2)
+
+
+def test_graph_replay_and_other_stream():
+    x, w, pos, dst = inputs(20, 64, 32)
+    cfg = csa2.Rope()
+    want = run(x, w, pos, dst, 64, cfg)
+    planes = [torch.full_like(t, 1) for t in want]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        csa2.csa2_kv_append(cfg, x, pos, dst, *planes[:3], norm_w=w, entry=planes[3])
+    s.synchronize()
+    for a, b in zip(planes[:3], want[:3]):
+        assert torch.equal(a[dst], b[dst])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        csa2.csa2_kv_append(cfg, x, pos, dst, *planes[:3], norm_w=w, entry=planes[3])
+    x2, _, pos2, dst2 = inputs(20, 64, 33)
+    x.copy_(x2), pos.copy_(pos2), dst.copy_(dst2)
+    g.replay()
+    check(x2, w, pos2, dst2, 64, cfg, 1e-6, (*run(x2, w, pos2, dst2, 64, cfg)[:3], planes[3]))
+    torch.cuda.synchronize()
+    want = run(x2, w, pos2, dst2, 64, cfg)
+    for a, b in zip(planes[:3], want[:3]):
+        assert torch.equal(a[dst2], b[dst2])
+    with pytest.raises(csa2.Csa2Error):                      # the bf16 rows over their own input
+        csa2.csa2_kv_append(cfg, x, pos, dst, *planes[:3], norm_w=w, entry=x)

@@ -242,3 +242,91 @@ def test_bad_lengths_are_reported():
         torch.cuda.synchronize()
         assert csa2.get_device_status(p.ws) == 0x40, bad
         assert torch.isfinite(p.out.float()).all()
+
+
+@pytest.mark.parametrize("q_lens,ctx,heads", [([6, 2], [200, 90], 64), ([1, 1], [200, 90], 16), ([40, 1], [130, 64], 16)])
+def test_nan_reaches_only_the_tokens_that_see_it(q_lens, ctx, heads):
+    p = Problem(q_lens, ctx, heads=heads, seed=30).run()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    at = int(p.row[0][-1])                                 # seen by the last token of the first sequence only
+    for scale_code, rope in ((0x7F, None), (0xFF, None), (None, float("nan"))):
+        s, k = p.scales[at].clone(), p.kr[at].clone()
+        if scale_code is not None:
+            p.scales[at, 5] = scale_code
+        if rope is not None:
+            p.kr[at, 3] = rope
+        p.run()
+        torch.cuda.synchronize()
+        t = q_lens[0] - 1
+        assert torch.isnan(p.out[t].float()).all() and torch.isnan(p.lse[t]).all()
+        others = [i for i in range(p.total) if i != t]
+        assert torch.equal(p.out[others], clean[others]) and torch.equal(p.lse[others], clean_lse[others])
+        p.scales[at], p.kr[at] = s, k
+    assert torch.equal(p.run().out, clean)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_nan_behind_the_window(heads):
+    p = Problem([5, 1], [300, 200], heads=heads, seed=31).run(window=64)
+    clean = p.out.clone()
+    for b, n in ((0, 5), (1, 1)):
+        gone = torch.from_numpy(p.row[b][:p.ctx[b] - n - 63]).cuda()         # the first token sees 64 from there on
+        p.scales[gone] = 0x7F
+        p.kr[gone] = float("nan")
+    assert torch.equal(p.run(window=64).out, clean)
+    p.check(window=64)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_query_rows_stay_alone(bad):
+    p = Problem([3, 1], [200, 90], heads=16, seed=32).run()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    p.q[1, 3, 17] = bad
+    p.q[3, 15, 570] = bad
+    p.run()
+    torch.cuda.synchronize()
+    rows = torch.ones(4, 16, dtype=torch.bool)
+    rows[1, 3] = rows[3, 15] = False
+    rows = rows.cuda()
+    assert torch.equal(p.out[rows], clean[rows]) and torch.equal(p.lse[rows], clean_lse[rows])
+    assert not torch.isfinite(p.out[~rows].float()).any()
+
+
+def test_thousands_of_sequences():
+    """More sequences and tiles than the plan's threads; empty queries and empty contexts among them."""
+    r = np.random.default_rng(33)
+    q = r.integers(0, 3, 1500)
+    c = np.maximum(r.integers(0, 70, 1500), q - 1)
+    Problem([int(x) for x in q], [int(x) for x in c], heads=3, seed=33, gap=(2, 1)).run().check()
+
+
+def test_more_tiles_than_plan_threads():
+    Problem([2800], [2900], heads=64, seed=34).run(window=70).check(window=70, some=6)
+    Problem([60] * 600, [61] * 600, heads=5, seed=35).run().check(some=2)
+
+
+def test_longest_window_and_more_queries_than_context():
+    w = 2 ** 31 - 1
+    p = Problem([70, 3, 5], [50, 2, 0], heads=16, seed=36).run(window=w)
+    p.check(window=w)
+    for bad in (2 ** 31, 2 ** 32 + 5, -1):
+        with pytest.raises(csa2.Csa2Error):
+            p.run(window=bad)
+
+
+@pytest.mark.parametrize("heads,q_lens", [(16, [1, 1]), (64, [5, 100])])
+def test_contiguous_cache_that_ends_inside_a_block(heads, q_lens):
+    p = Problem(q_lens, [100, 100], heads=heads, paged=False, seed=37)
+    short = lambda t: t.view(2, 128, -1)[:, :100].reshape(200, -1).contiguous()
+    p.codes, p.scales, p.kr = short(p.codes), short(p.scales), short(p.kr)
+    p.dims = csa2.Dims(heads=heads, max_ctx=100)
+    p.run().check()
+
+
+def test_other_stream_than_the_inputs():
+    p = Problem([3], [400], heads=16, seed=38)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        p.run()
+    p.check()
