@@ -42,14 +42,13 @@
 //
 // Roles of a CTA's 28 warps: 8 row warps (softmax / outputs), 16 widening warps (which also
 // bring the queries into tensor memory), one that issues the MMAs, one that copies blocks
-// from the cache, one for rope keys (scores CTA, G 1) or for handing slots of P back
-// (values CTA).
+// from the cache, and in a values CTA one that hands slots of P back.
 //
 // Measured (GB300; 1,933 TFLOP/s measured bf16 rate, 2 * 1088 flop a visible (row, position)):
 // 2,048 tokens x 64 heads on 32,768 positions 5.6 ms, 1.61 PFLOP/s (83 %); bound by the
 // tensor pipe and the shared-memory bandwidth that feeds it.  8 contexts of 131,072 with
-// one token 0.33 ms, 0.45 PFLOP/s (64 of 128 rows of each product are used; 0.235 ms
-// with the copies from the cache left out: one block on its way at a time).  Short
+// one token 0.32 ms, 0.45 PFLOP/s (64 of 128 rows of each product are used, and both CTAs
+// widen every block: a block every 2,800 cycles, of which its product takes 1,152).  Short
 // prompts (tiles of one or two blocks) 0.5 PFLOP/s: a tile's queries, 147 KB a CTA, cannot
 // come before the last product of the tile before it.
 #include <cooperative_groups.h>
@@ -86,24 +85,24 @@ constexpr int kKBytes = 9 * kReg;                   // 576 channels of a block's
 constexpr int kVBytes = 8 * kReg;                   // 512 channels
 
 // Shared memory of a CTA: slots of P, the ring of keys or values, raw bytes of the
-// blocks to widen as they come from the cache (64 / G rows in a scores CTA, 1 / G of the
-// codes in a values CTA).  At G 1, where a block is twice the bytes, the rope keys go
-// straight into the ring.
+// blocks to widen as they come from the cache, in two stages (G 1: 32 rows, half a block;
+// G 2: a block's 32 rows in a scores CTA, half of its codes in a values CTA).
 template <int G>
 struct Lay {
   static constexpr int kPSlots = 3;
-  static constexpr int kRawStages = G;
+  static constexpr int kRawStages = 2;
   static constexpr int kKvOff = kPSlots * kPBytes;
   static constexpr int kRawOff = kKvOff + kKStages * kKBytes;
-  static constexpr int kRawRope = G == 1 ? 0 : kDenseBlk * kRope * 2 / G;       // scores CTA only
-  static constexpr int kRawCodes = kDenseBlk * kCodesPerRow / G;
-  static constexpr int kRawStage = kRawRope + kRawCodes + kDenseBlk * kScalesPerRow / G;   // (a values CTA at G 2: all scales, no rope)
+  static constexpr int kRawRope = 32 * kRope * 2;                     // scores CTA only
+  static constexpr int kRawCodes = 32 * kCodesPerRow;                 // (a values CTA at G 2: 64 rows x 128 bytes)
+  static constexpr int kRawStage = kRawRope + kRawCodes + 32 * kScalesPerRow;   // (a values CTA at G 2: 64 rows of scales, no rope)
   // values CTA: output staging, 2 G KB a warp, behind the values (at G 2 they are half of a stage)
   static constexpr int kStageOff = G == 1 ? kKvOff + kKStages * kVBytes : kKvOff + (kKStages - 1) * kVBytes + kVBytes / 2;
   static constexpr int kSmem = kRawOff + kRawStages * kRawStage;
   static_assert(kStageOff + kRowWarps * 2048 * G <= kRawOff, "output staging of the values CTA");
-  static_assert(kRawCodes + kDenseBlk * kScalesPerRow <= kRawStage, "raw bytes of a values CTA");
-  static_assert(kRawStage % 1024 == 0 && kSmem + 1024 + 8192 <= 232448, "alignment and size of shared memory");
+  static_assert(G == 1 || kRawCodes + kDenseBlk * kScalesPerRow <= kRawStage, "raw bytes of a values CTA");
+  // beside at most 8 KB of named variables; the dynamic part starts on a multiple of its alignment
+  static_assert(kRawStage % 1024 == 0 && kSmem + 8192 <= 232448, "alignment and size of shared memory");
 };
 
 constexpr uint32_t kSCol = 320;                     // score buffers behind the 288 query columns
@@ -111,7 +110,7 @@ constexpr int kSBufs = 3;
 constexpr int kMetaWarp = 3 * 32 * 4;               // alpha, sum, reference of a warp's rows
 
 struct DenseSmall {
-  uint64_t raw_full[2], raw_empty[2];
+  uint64_t raw_full[3], raw_empty[3];
   uint64_t kv_full[kKStages], kv_empty[kKStages];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t q_turn[kKStages], q_place[kKStages];     // a ring stage free for queries; holding them
@@ -124,7 +123,7 @@ struct DenseSmall {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
-  int raw_rows[2];                                  // rows of the raw block before the context's end (0: bad page)
+  int raw_rows[3];                                  // rows of the raw bytes before the context's end (0: bad page)
   __align__(16) float meta[kMaxPSlots][4][3][32];
   uint16_t swap[4][kDenseTile];                     // largest magnitudes of the queries, between a row's four warps
   int8_t q_shift[4][kDenseTile];                    // power of two each query row was scaled by, of four tiles in turn
@@ -440,78 +439,68 @@ struct Cursor {
 // Widening warps (every CTA): E2M1 x E4M3 -> fp16, exact (6 significant bits, 2^-10 ..
 // 2688).  A lane takes 16 bytes of codes (32 channels) of one row at a time, lane = 8 *
 // piece + row: a quarter-warp reads and stores one 16-byte chunk of 8 rows (all 32 banks,
-// 128-byte swizzle).  Two such pieces a lane and block:
-//   G 1: the 16 warps take every block together, 64 rows x 512 channels;
-//   G 2: 8 warps take every other block (those of one ring stage); a scores CTA has 32
-//        of the 64 rows, a values CTA its half of the 512 channels.
+// 128-byte swizzle).  The rope keys are copied along:
+//   G 1: the 16 warps take half a block, 32 rows x 512 channels, together, one piece each;
+//   G 2: 8 warps take every other block (those of one ring stage), two pieces each; a
+//        scores CTA has 32 of the 64 rows, a values CTA its half of the 512 channels.
+// (128K decode batch, kernel alone: 303 us.  Whole blocks in one raw stage, the rope keys
+// copied straight into the ring and awaited there: 323; halves, but the rope keys so: 314;
+// rows as they lie in the cache by untiled copies: 307; 8 warps on every other block at G 1,
+// too: 332.)
 // ---------------------------------------------------------------------------
 // Copies the run's blocks into the raw stages: boxes of 128 bytes x 32 rows (64-byte boxes
 // take the copy engine nearly twice as long), scales in one piece.
 template <int G, bool kScores>
 __device__ inline void raw_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int lane,
                                 const CUtensorMap* codes, const CUtensorMap* rope) {
-  constexpr int kRows = G == 2 && kScores ? 32 : 64;
+  constexpr bool kColumns = G == 2 && !kScores;
+  constexpr int kRows = kColumns ? 64 : 32;                           // of a raw stage
+  constexpr int kStages = Lay<G>::kRawStages;
   constexpr int kCodesAt = kScores ? Lay<G>::kRawRope : 0, kScalesAt = kCodesAt + Lay<G>::kRawCodes;
   constexpr uint32_t kBytes = kScalesAt;
   Cursor cur(a.plan, cl, lane);
-  uint32_t n = 0;
-  for (bool more = cur.item(a); more; more = cur.step(a, 1) || cur.item(a), ++n) {
-    const uint32_t st = n % Lay<G>::kRawStages;
-    int64_t row0 = cur.row0(a);
-    if (kScores && part == 0 && row0 < 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
-    const int first = G == 2 && kScores ? 32 * part : 0;              // first of this CTA's rows in the block
-    const int rows = row0 < 0 ? 0 : max(0, min(kRows, cur.it.b.x - (cur.it.blk + cur.i) * kDenseBlk - first));
-    row0 = (row0 < 0 ? 0 : row0) + first;
-    if (!wait_warp(sm, &sm.raw_empty[st], ((n / Lay<G>::kRawStages) & 1) ^ 1, a.ws)) return;
-    if (lane == 0) {
-      uint8_t* raw = base + Lay<G>::kRawOff + st * Lay<G>::kRawStage;
-      uint64_t* bar = &sm.raw_full[st];
-      sm.raw_rows[st] = rows;
-      tc::mbar_expect_tx(bar, kBytes + uint32_t(rows * kScalesPerRow));
-#pragma unroll 1
-      for (int h = 0; h < kRows / 32; ++h) {
-        uint8_t* c = raw + kCodesAt + h * 4096;
-        if (G == 2 && !kScores) {
-          tc::tma_load_2d(codes, c, 128 * part, int(row0) + 32 * h, bar);
-        } else {
-          tc::tma_load_2d(codes, c, 0, int(row0) + 32 * h, bar);
-          tc::tma_load_2d(codes, c + kRows * 128, 128, int(row0) + 32 * h, bar);
-        }
-        if (kScores && G == 2) tc::tma_load_2d(rope, raw + h * 4096, 0, int(row0) + 32 * h, bar);
-      }
-      // valid rows only: the plane may end behind them
-      if (rows > 0)
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                     ::"r"(tc::smem_u32(raw + kScalesAt)), "l"(a.scales + row0 * kScalesPerRow),
-                       "r"(rows * kScalesPerRow), "r"(tc::smem_u32(bar))
-                     : "memory");
-    }
-    __syncwarp();
-  }
-}
-
-// G 1: the rope keys of each block, straight into the ring (they need no widening; rows
-// behind the context are masked scores, whatever they hold).  Follows the ring place by place.
-__device__ inline void rope_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int lane, const CUtensorMap* rope) {
-  Cursor cur(a.plan, cl, lane);
-  uint32_t m = 0;
+  uint32_t n = 0;                                                     // raw stages filled
   for (bool more = cur.item(a); more; more = cur.step(a, 1) || cur.item(a)) {
     const int64_t row0 = cur.row0(a);
-    for (int k = cur.i == 0 ? 2 : 0; k >= 0; --k, ++m) {              // the tile's two query places, then the block's
-      const uint32_t st = m % kKStages;
-      if (!wait_warp(sm, &sm.kv_empty[st], ((m / kKStages) & 1) ^ 1, a.ws)) return;
-      if (k > 0) {
-        if (lane == 0) arrive(&sm.q_turn[st]);
-      } else if (lane == 0) {
-        uint8_t* dst = base + Lay<1>::kKvOff + st * kKBytes + 8 * kReg;
-        tc::mbar_expect_tx(&sm.kv_full[st], kReg);
-        tc::tma_load_2d(rope, dst, 0, row0 < 0 ? 0 : int(row0), &sm.kv_full[st]);
-        tc::tma_load_2d(rope, dst + kReg / 2, 0, row0 < 0 ? 32 : int(row0) + 32, &sm.kv_full[st]);
+    if (kScores && part == 0 && row0 < 0 && lane == 0) raise_err(a.ws, CSA2_DEV_PAGE_ID);
+    const int valid = row0 < 0 ? 0 : cur.it.b.x - (cur.it.blk + cur.i) * kDenseBlk;   // of the block
+#pragma unroll 1
+    for (int half = 0; half < (G == 1 ? 2 : 1); ++half, ++n) {
+      const uint32_t st = n % kStages;
+      const int first = G == 1 ? 32 * half : kScores ? 32 * part : 0;   // first of the stage's rows in the block
+      const int rows = max(0, min(kRows, valid - first));
+      const int64_t row = (row0 < 0 ? 0 : row0) + first;
+      if (!wait_warp(sm, &sm.raw_empty[st], ((n / kStages) & 1) ^ 1, a.ws)) return;
+      if (lane == 0) {
+        uint8_t* raw = base + Lay<G>::kRawOff + st * Lay<G>::kRawStage;
+        uint64_t* bar = &sm.raw_full[st];
+        sm.raw_rows[st] = rows;
+        tc::mbar_expect_tx(bar, kBytes + uint32_t(rows * kScalesPerRow));
+        uint8_t* c = raw + kCodesAt;
+        if (kColumns) {
+          tc::tma_load_2d(codes, c, 128 * part, int(row), bar);
+          tc::tma_load_2d(codes, c + 4096, 128 * part, int(row) + 32, bar);
+        } else {
+          tc::tma_load_2d(codes, c, 0, int(row), bar);
+          tc::tma_load_2d(codes, c + 4096, 128, int(row), bar);
+        }
+        if (kScores) tc::tma_load_2d(rope, raw, 0, int(row), bar);
+        // valid rows only: the plane may end behind them
+        if (rows > 0)
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                       ::"r"(tc::smem_u32(raw + kScalesAt)), "l"(a.scales + row * kScalesPerRow), "r"(rows * kScalesPerRow),
+                         "r"(tc::smem_u32(bar))
+                       : "memory");
       }
       __syncwarp();
     }
   }
 }
+
+// 0xFF in each of two scale codes that is a NaN.  Such a scale makes NaN of the scores of the
+// rows that see its position, by the keys; taken as 0 among the values it leaves the others
+// alone (0 * P).
+__device__ inline uint32_t nan_scales(uint32_t two) { return (((two & 0x7F7Fu) + 0x0101u) >> 7 & 0x0101u) * 0xFFu; }
 
 // One 4-byte word of codes: 8 channels under one scale (twice in sc2).
 __device__ inline uint4 widen8(uint32_t w, uint32_t sc2) {
@@ -585,78 +574,124 @@ __device__ inline bool queries_to_tmem(const DenseArgs& a, DenseSmall& sm, uint8
 template <int G, bool kScores>
 __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* base, int cl, int part, int w, int lane,
                                   uint32_t tmem) {
-  constexpr int kPieces = 2;
   constexpr int kLead = kScores ? 2 : 0;       // ring places of a tile's queries before its blocks
-  constexpr int kLeader = kScores ? 0 : G;
-  constexpr bool kColumns = G == 2 && !kScores;
-  constexpr int kRows = G == 2 && kScores ? 32 : 64;
-  constexpr int kRegion = kRows * 128;
   constexpr uint32_t kStageBytes = kScores ? kKBytes : kVBytes;
-  const int g = G == 2 ? w >> 3 : 0;           // G 2: the warp's ring and raw stage
-  const int w8 = w & 7, p = lane >> 3;
-  const int hi = G == 1 ? w >> 3 : kScores ? w8 >> 2 : 0;             // half of the channels (256) this warp takes
-  const int row = 8 * (G == 2 && kScores ? w8 & 3 : w8) + (lane & 7);  // in the stage
-  // raw codes (128 bytes of a row; the second piece is 64 bytes on), its scales, first region (the next is two on)
-  const uint32_t raw0 = tc::smem_u32(base) + Lay<G>::kRawOff;
-  constexpr uint32_t kCodesAt = kScores ? Lay<G>::kRawRope : 0;
-  const uint32_t src = kCodesAt + hi * kRows * 128 + tc::sw128_offset(row, p);
-  const uint32_t ssrc = kCodesAt + Lay<G>::kRawCodes + row * kScalesPerRow + 2 * (8 * (kColumns ? part : hi) + p);
-  const uint32_t o_rope = tc::sw128_offset(row, hi * 4 + p);          // rope: one 16-byte chunk a lane
-  const uint32_t dst = tc::smem_u32(base) + Lay<G>::kKvOff + (4 * hi + (p >> 1)) * kRegion;
-  const uint32_t o0 = tc::sw128_offset(row, (p & 1) * 4);             // chunk i of a piece's four: o0 ^ 16 i
+  const uint32_t raw0 = tc::smem_u32(base) + Lay<G>::kRawOff, ring = tc::smem_u32(base) + Lay<G>::kKvOff;
+  const int p = lane >> 3;
   Walk walk(a.plan, cl);
   Item it = {};
-  uint32_t u = 0, v = 0;                       // uses of the ring (G 1: places, G 2: of the stage) and of the raw stage
-  const auto stage_of = [&]() { return G == 1 ? u % kKStages : uint32_t(g); };
-  const auto parity_of = [&]() { return ((G == 1 ? u / kKStages : u) & 1) ^ 1; };
   int place = 0;                               // ring place (mod 2) of the item's start
-  for (uint32_t k_item = 0; walk.next(it); ++k_item) {
-    // the tile's queries come through the same ring
+  if constexpr (G == 1) {
+    // a raw stage is 32 rows: one piece a lane, a block in two turns
+    const int row = 8 * (w & 3) + (lane & 7), group = w >> 2;         // in the stage; 64 of a row's 256 code bytes
+    constexpr uint32_t kCodesAt = kScores ? Lay<1>::kRawRope : 0;
+    const bool with_rope = kScores && w < 8;
+    const uint32_t o_rope = tc::sw128_offset(row, (w >> 2) * 4 + p);
+    const uint32_t src = kCodesAt + (group >> 1) * 4096 + tc::sw128_offset(row, (group & 1) * 4 + p);
+    const uint32_t ssrc = kCodesAt + Lay<1>::kRawCodes + row * kScalesPerRow + 2 * (4 * group + p);
+    const uint32_t dst = ring + (2 * group + (p >> 1)) * kReg + tc::sw128_offset(row, (p & 1) * 4);
+    uint32_t u = 0, v = 0;                     // ring places passed, raw stages used
+    for (uint32_t k_item = 0; walk.next(it); ++k_item) {
+      // the tile's queries come through the same ring
 #pragma unroll 1
-    for (int k = 0; k < kLead / G; ++k, ++u) {
-      if (!wait_warp(sm, &sm.kv_empty[stage_of()], parity_of(), a.ws)) return;
-      if (lane == 0) arrive(&sm.q_turn[stage_of()]);
-    }
-    if (kScores && !queries_to_tmem<G>(a, sm, base, w, lane, tmem, k_item, place)) return;
+      for (int k = 0; k < kLead; ++k, ++u) {
+        if (!wait_warp(sm, &sm.kv_empty[u % kKStages], ((u / kKStages) & 1) ^ 1, a.ws)) return;
+        if (lane == 0) arrive(&sm.q_turn[u % kKStages]);
+      }
+      if (kScores && !queries_to_tmem<1>(a, sm, base, w, lane, tmem, k_item, place)) return;
 #pragma unroll 1
-    for (int i = G == 2 ? (g - place) & 1 : 0; i < it.n; i += G, ++u, ++v) {
-      // raw stages: G 1: in turn; G 2: the warp's own
-      const uint32_t rs = G == 1 ? v % Lay<G>::kRawStages : uint32_t(g), raw = raw0 + rs * Lay<G>::kRawStage;
-      if (!wait_warp(sm, &sm.raw_full[rs], (G == 1 ? v / Lay<G>::kRawStages : v) & 1, a.ws)) return;
-      uint4 cw[kPieces], rp;
-      uint32_t sc[kPieces];
-      const bool have = row < sm.raw_rows[rs];
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        cw[j] = ld_shared16((raw + src) ^ (64 * j));
-        sc[j] = ld_shared_u16(raw + ssrc + 8 * j);
+      for (int i = 0; i < it.n; ++i, ++u) {
+        const uint32_t st = u % kKStages;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half, ++v) {
+          const uint32_t rs = v % Lay<1>::kRawStages, raw = raw0 + rs * Lay<1>::kRawStage;
+          if (!wait_warp(sm, &sm.raw_full[rs], (v / Lay<1>::kRawStages) & 1, a.ws)) return;
+          const bool have = row < sm.raw_rows[rs];
+          const uint4 cw = ld_shared16(raw + src);
+          const uint32_t sc = ld_shared_u16(raw + ssrc);
+          uint4 rp;
+          if (with_rope) rp = ld_shared16(raw + o_rope);
+          __syncwarp();
+          if (lane == 0) arrive(&sm.raw_empty[rs]);
+          // rows behind the context hold anything: their scale is taken as 0 (0 * P stays 0; their scores are masked)
+          uint32_t code = have ? sc : 0u;
+          if (!kScores) code &= ~nan_scales(code);
+          const uint32_t two = e4m3x2_to_f16x2(uint16_t(code));
+          const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+          const uint4 w0 = widen8(cw.x, s0), w1 = widen8(cw.y, s0), w2 = widen8(cw.z, s1), w3 = widen8(cw.w, s1);
+          if (half == 0 && !wait_warp(sm, &sm.kv_empty[st], ((u / kKStages) & 1) ^ 1, a.ws)) return;
+          const uint32_t d = dst + st * kStageBytes + half * 4096;    // 32 rows on; a row's swizzle repeats every 8
+          st_shared16(d, w0);
+          st_shared16(d ^ 16, w1);
+          st_shared16(d ^ 32, w2);
+          st_shared16(d ^ 48, w3);
+          if (with_rope) st_shared16(ring + st * kStageBytes + 8 * kReg + half * 4096 + o_rope, rp);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive(&sm.kv_full[st]);
       }
-      if (kScores && G == 2) rp = ld_shared16(raw + o_rope);
-      __syncwarp();
-      if (lane == 0) arrive(&sm.raw_empty[rs]);
-      const uint32_t st = stage_of();
-      if (!wait_warp(sm, &sm.kv_empty[st], parity_of(), a.ws)) return;
-      const uint32_t d = dst + st * kStageBytes;
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        // rows behind the context hold anything: their scale is taken as 0 (0 * P stays 0; their scores are masked)
-        uint32_t code = have ? sc[j] : 0u;
-        // a NaN scale makes NaN of the scores of the rows that see its position, by the keys; taken
-        // as 0 among the values it leaves the others alone (0 * P)
-        if (!kScores) code &= ~((((code & 0x7F7Fu) + 0x0101u) >> 7 & 0x0101u) * 0xFFu);
-        const uint32_t two = e4m3x2_to_f16x2(uint16_t(code));
-        const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-        st_shared16(d + 2 * j * kRegion + o0, widen8(cw[j].x, s0));
-        st_shared16(d + 2 * j * kRegion + (o0 ^ 16), widen8(cw[j].y, s0));
-        st_shared16(d + 2 * j * kRegion + (o0 ^ 32), widen8(cw[j].z, s1));
-        st_shared16(d + 2 * j * kRegion + (o0 ^ 48), widen8(cw[j].w, s1));
-      }
-      if (kScores && G == 2) st_shared16(tc::smem_u32(base) + Lay<G>::kKvOff + st * kStageBytes + 8 * kRegion + o_rope, rp);
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_leader<G>(&sm.kv_full[st], kLeader);
+      place = (place + kLead + it.n) & 1;
     }
-    place = (place + kLead + it.n) & 1;
+  } else {
+    constexpr int kPieces = 2;
+    constexpr int kLeader = kScores ? 0 : G;
+    constexpr bool kColumns = !kScores;
+    constexpr int kRows = kScores ? 32 : 64;
+    constexpr int kRegion = kRows * 128;
+    const int g = w >> 3, w8 = w & 7;          // the warp's ring and raw stage
+    const int hi = kScores ? w8 >> 2 : 0;      // half of the channels (256) this warp takes
+    const int row = 8 * (kScores ? w8 & 3 : w8) + (lane & 7);          // in the stage
+    // raw codes (128 bytes of a row; the second piece is 64 bytes on), its scales, first region (the next is two on)
+    constexpr uint32_t kCodesAt = kScores ? Lay<G>::kRawRope : 0;
+    const uint32_t raw = raw0 + g * Lay<G>::kRawStage;
+    const uint32_t src = raw + kCodesAt + hi * kRows * 128 + tc::sw128_offset(row, p);
+    const uint32_t ssrc = raw + kCodesAt + Lay<G>::kRawCodes + row * kScalesPerRow + 2 * (8 * (kColumns ? part : hi) + p);
+    const uint32_t o_rope = tc::sw128_offset(row, hi * 4 + p);        // rope: one 16-byte chunk a lane
+    const uint32_t dst = ring + g * kStageBytes + (4 * hi + (p >> 1)) * kRegion + tc::sw128_offset(row, (p & 1) * 4);
+    uint32_t u = 0, v = 0;                     // uses of the ring stage and of the raw stage
+    for (uint32_t k_item = 0; walk.next(it); ++k_item) {
+      // the tile's queries come through the same ring
+      if (kScores) {
+        if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
+        if (lane == 0) arrive(&sm.q_turn[g]);
+        ++u;
+        if (!queries_to_tmem<G>(a, sm, base, w, lane, tmem, k_item, place)) return;
+      }
+#pragma unroll 1
+      for (int i = (g - place) & 1; i < it.n; i += 2, ++u, ++v) {
+        if (!wait_warp(sm, &sm.raw_full[g], v & 1, a.ws)) return;
+        uint4 cw[kPieces], rp;
+        uint32_t sc[kPieces];
+        const bool have = row < sm.raw_rows[g];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          cw[j] = ld_shared16(src ^ (64 * j));
+          sc[j] = ld_shared_u16(ssrc + 8 * j);
+        }
+        if (kScores) rp = ld_shared16(raw + o_rope);
+        __syncwarp();
+        if (lane == 0) arrive(&sm.raw_empty[g]);
+        if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          uint32_t code = have ? sc[j] : 0u;
+          if (!kScores) code &= ~nan_scales(code);
+          const uint32_t two = e4m3x2_to_f16x2(uint16_t(code));
+          const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+          const uint32_t d = dst + 2 * j * kRegion;
+          st_shared16(d, widen8(cw[j].x, s0));
+          st_shared16(d ^ 16, widen8(cw[j].y, s0));
+          st_shared16(d ^ 32, widen8(cw[j].z, s1));
+          st_shared16(d ^ 48, widen8(cw[j].w, s1));
+        }
+        if (kScores) st_shared16(ring + g * kStageBytes + 8 * kRegion + o_rope, rp);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_leader<G>(&sm.kv_full[g], kLeader);
+      }
+      place = (place + kLead + it.n) & 1;
+    }
   }
 }
 
@@ -1040,11 +1075,16 @@ template <int G>
 __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, const CUtensorMap* codes,
                                   const CUtensorMap* rope) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* base = smem_raw;                          // 1024-byte aligned: checked below
   __shared__ DenseSmall sm;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = blockIdx.x % (2 * G), cl = blockIdx.x / (2 * G), part = rank % G;
   const bool scores = rank < G;
+  if (tc::smem_u32(base) & 1023u) {                  // never, as laid out; the same in every CTA
+    pdl_wait();
+    if (tid == 0) raise_err(a.ws, CSA2_DEV_TIMEOUT);
+    return;
+  }
   if (wid == 0) tmem_alloc_all<G>(&sm.tmem_slot);
   if (tid == 0) {
     for (int i = 0; i < Lay<G>::kRawStages; ++i) {
@@ -1053,9 +1093,9 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
     }
     for (int i = 0; i < kKStages; ++i) {
       // G 1: all widening warps, and the rope keys' thread; G 2: 8 in each CTA of the pair
-      tc::mbar_init(&sm.kv_full[i], G == 1 && scores ? kConvWarps + 1 : kConvWarps);
+      tc::mbar_init(&sm.kv_full[i], kConvWarps);
       tc::mbar_init(&sm.kv_empty[i], 1);
-      tc::mbar_init(&sm.q_turn[i], G == 1 ? kConvWarps + 1 : kConvWarps / 2);
+      tc::mbar_init(&sm.q_turn[i], kConvWarps / G);
       tc::mbar_init(&sm.q_place[i], 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
@@ -1096,7 +1136,6 @@ __device__ inline void dense_body(const DenseArgs& a, const CUtensorMap* qmap, c
       regs_down<kMmaRegs>();
       if (wid == kMmaWarp) scores_mma_role<G>(a, sm, base, cl, part, tmem, qmap);
       else if (wid == kMmaWarp + 1) raw_role<G, true>(a, sm, base, cl, part, lane, codes, rope);
-      else if (G == 1 && wid == kMmaWarp + 2) rope_role(a, sm, base, cl, lane, rope);
     }
   } else {
     if (wid < kRowWarps) {
@@ -1339,7 +1378,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a
 // ---------------------------------------------------------------------------
 // Merge: CTA (g, c) joins 8 channels of the tile that the boundary before run c
 // cuts, if c is the first boundary inside it.  Thread = row.  It also writes the
-// rows of tiles that see nothing.
+// rows of tiles that see nothing.  Bound by the latency of its loads: 48 in flight (16.3 us
+// with 16 on the 128K decode batch, where a tile has about ten pieces; 14.2).
 // ---------------------------------------------------------------------------
 constexpr int kMergeCh = 8;
 
@@ -1369,7 +1409,7 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
       float o[kMergeCh], total = 0.0f;
 #pragma unroll
       for (int k = 0; k < kMergeCh; ++k) o[k] = 0.0f;
-#pragma unroll 2
+#pragma unroll 6
       for (int i = 0; i < n; ++i) {
         const int s = slot(i);
         const float l = __ldg(a.part_lse + s * kDenseTile + r);
@@ -1470,7 +1510,7 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
   static KernelAttrs attrs[2];
-  const size_t smem = size_t(G == 2 ? Lay<2>::kSmem : Lay<1>::kSmem) + 1024;
+  const size_t smem = size_t(G == 2 ? Lay<2>::kSmem : Lay<1>::kSmem);
   auto kernel = G == 2 ? dense_pair_kernel : dense_kernel;
   cudaError_t e = prepare_kernel(kernel, smem, false, attrs[G - 1]);
   if (e != cudaSuccess) return e;

@@ -62,7 +62,7 @@ inline DenseLayout make_dense_layout(const csa2_dims& d, int64_t batch, int64_t 
 
 // Whether a call takes tiles of 256 rows on 4 SMs instead of 128 on 2: from 128 rows a
 // sequence on (mean).  Measured, 64 heads, 128- against 256-row tiles: 1 token (64 rows),
-// 8 contexts of 128K 327 / 349 us; 2 tokens on 8,000 positions 46.9 / 45.3; 1 to 5 tokens on
+// 8 contexts of 128K 311 / 349 us; 2 tokens on 8,000 positions 46.9 / 45.3; 1 to 5 tokens on
 // up to 16,384 (16 sequences) 101 / 88; 8 tokens on 16,000 (8 sequences) 164 / 113;
 // prompts of 301 to 2,000 tokens 546 / 426.  The larger tile widens each block once for
 // twice the rows.
