@@ -16,24 +16,24 @@ namespace {
 // Rotary positions: y = m R(angle) x on channels [offset, offset + rot) of every
 // head, the other channels copied (or left, in place).
 //
-// A CTA takes kRopeTok tokens and a range of heads: it forms the (cos, sin) of its
-// tokens once in shared memory (rot / 2 of them a token, against heads * rot
-// values to turn) and then walks 16-byte pieces, four in flight a thread.  8,192 tokens
-// x 64 heads x 64 fp32 channels in place, 268 MB: 46.6 us (85 % of the copy rate; one
-// piece in flight and two divisions a piece: 68).
+// A CTA takes kRopeTok tokens and a range of heads: it asks for its first 16-byte pieces,
+// four a thread, forms the (cos, sin) of its tokens in shared memory meanwhile (rot / 2 of
+// them a token, against heads * rot values to turn) and then walks the pieces, four in
+// flight.  Measured (kernel in a graph): 8,192 tokens x 64 heads x 64 fp32 channels in place,
+// 268 MB, 44.0 us (90 % of the copy rate); 4,099 x 16 heads x 128 bf16 channels into another
+// buffer, half layout, 34 MB, 7.4 us.  Loads behind the angles: 45.5 and 12; tiles of 8 tokens:
+// 43.9 and 8.1; 2: 43.1 and 10.0; three CTAs an SM instead of four: 44.0 and 7.9, five: 44.2
+// and 12.3; one piece in flight and two divisions a piece: 68 for the first.
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTok = 8;
+constexpr int kRopeTok = 4;
 
 template <typename T> struct Io;
 template <> struct Io<float> {
   static constexpr int kVec = 4;
-  __device__ static void unpack(uint4 v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
-  }
-  __device__ static uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
+  // the values of a word (fp32: one, twice) and back
+  __device__ static float2 word(uint32_t w) { return make_float2(__uint_as_float(w), __uint_as_float(w)); }
+  __device__ static uint32_t unword(float a, float) { return __float_as_uint(a); }
   __device__ static float get(float v) { return v; }
   __device__ static float put(float v) { return v; }
 };
@@ -52,6 +52,8 @@ template <> struct Io<uint16_t> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
+  __device__ static float2 word(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+  __device__ static uint32_t unword(float a, float b) { return bf16x2_rn(a, b); }
   __device__ static uint4 pack(const float (&f)[8]) {
     return make_uint4(bf16x2_rn(f[0], f[1]), bf16x2_rn(f[2], f[3]), bf16x2_rn(f[4], f[5]), bf16x2_rn(f[6], f[7]));
   }
@@ -61,7 +63,7 @@ template <> struct Io<uint16_t> {
 
 // x, y and the strides count elements of T; sign is -1 for the inverse.
 template <typename T, bool kHalf>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
     rope_kernel(const __grid_constant__ RopeTable tab, const T* x, T* y, const int32_t* __restrict__ pos, int64_t tokens,
                 int heads, int dim, int offset, int64_t xt, int64_t xh, int64_t yt, int64_t yh, int heads_per, int copy,
                 int vec, float sign) {
@@ -72,6 +74,41 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int64_t t0 = int64_t(blockIdx.x) * kRopeTok;
   const int nt = int(min64(kRopeTok, tokens - t0));
   const int h0 = blockIdx.y * heads_per, nh = min(heads_per, heads - h0);
+  // pieces of a head: turned (kHalf: two pieces rot / 2 apart at once), then copied.  A
+  // thread keeps to one piece and walks the (token, head) rows, four in flight.
+  constexpr int V = Io<T>::kVec;
+  const int nturn = kHalf ? pairs / V : 2 * pairs / V, per = nturn + (copy ? (dim - 2 * pairs) / V : 0);
+  const int rows = nt * nh;
+  const float inv = 1.0f / float(nh);                // rows < 2^20: (r + 1/2) / nh truncates to r / nh
+  uint4 u4[4], v4[4];
+  int tk[4];
+  int64_t yo[4];
+  int c, at, r, apart;
+  const auto place = [&](int c0) {                   // the thread's piece and first row among those from c0 on
+    const int here = min(per - c0, kRopeThreads);
+    apart = kRopeThreads / here;
+    c = c0 + tid % here;
+    r = tid / here < apart ? tid / here : rows;      // threads left over: none
+    at = c < nturn ? offset + c * V : (c - nturn) * V;
+    if (c >= nturn && at >= offset) at += 2 * pairs;
+  };
+  const auto load = [&]() {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int rr = min(r + b * apart, rows - 1);
+      tk[b] = __float2int_rz((float(rr) + 0.5f) * inv);
+      const int h = h0 + rr - tk[b] * nh;
+      const T* xs = x + (t0 + tk[b]) * xt + int64_t(h) * xh + at;
+      yo[b] = (t0 + tk[b]) * yt + int64_t(h) * yh + at;
+      u4[b] = *reinterpret_cast<const uint4*>(xs);
+      if (kHalf && c < nturn) v4[b] = *reinterpret_cast<const uint4*>(xs + pairs);
+    }
+  };
+  // the first rows are on their way while the angles are formed
+  if (vec) {
+    place(0);
+    if (r < rows) load();
+  }
   for (int i = tid; i < nt * pairs; i += kRopeThreads) {
     const int t = i / pairs, p = i - t * pairs;
     float2 v = rope_cs(tab, p, __ldg(pos + t0 + t));
@@ -80,36 +117,13 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
   __syncthreads();
   if (vec) {
-    constexpr int V = Io<T>::kVec;
-    // pieces of a head: turned (kHalf: two pieces rot / 2 apart at once), then copied.  A
-    // thread keeps to one piece and walks the (token, head) rows, four in flight.
-    const int nturn = kHalf ? pairs / V : 2 * pairs / V, ncopy = copy ? (dim - 2 * pairs) / V : 0;
-    const int per = nturn + ncopy, rows = nt * nh;
     for (int c0 = 0; c0 < per; c0 += kRopeThreads) {
-      const int here = min(per - c0, kRopeThreads), apart = kRopeThreads / here;
-      const int c = c0 + tid % here, r0 = tid / here;
-      if (r0 >= apart) continue;
-      const bool turn = c < nturn;
-      int at = offset + c * V;
-      if (!turn) {
-        at = (c - nturn) * V;
-        if (at >= offset) at += 2 * pairs;
+      if (c0 > 0) {
+        place(c0);
+        if (r < rows) load();
       }
-      const float inv = 1.0f / float(nh);            // rows < 2^20: (r + 1/2) / nh truncates to r / nh
-      for (int r = r0; r < rows; r += 4 * apart) {
-        uint4 u4[4], v4[4];
-        int tk[4];
-        int64_t yo[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int rr = min(r + b * apart, rows - 1);
-          tk[b] = __float2int_rz((float(rr) + 0.5f) * inv);
-          const int h = h0 + rr - tk[b] * nh;
-          const T* xs = x + (t0 + tk[b]) * xt + int64_t(h) * xh + at;
-          yo[b] = (t0 + tk[b]) * yt + int64_t(h) * yh + at;
-          u4[b] = *reinterpret_cast<const uint4*>(xs);
-          if (kHalf && turn) v4[b] = *reinterpret_cast<const uint4*>(xs + pairs);
-        }
+      const bool turn = c < nturn;
+      while (r < rows) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           if (r + b * apart >= rows) break;
@@ -118,31 +132,38 @@ __global__ void __launch_bounds__(kRopeThreads)
             *reinterpret_cast<uint4*>(ys) = u4[b];
             continue;
           }
+          // word by word: few values are held widened at a time
           const float2* e2 = cs + tk[b] * kMaxPairs + (kHalf ? c * V : c * (V / 2));
-          float u[V];
-          Io<T>::unpack(u4[b], u);
+          uint32_t uw[4] = {u4[b].x, u4[b].y, u4[b].z, u4[b].w};
           if (kHalf) {
-            float v[V];
-            Io<T>::unpack(v4[b], v);
+            uint32_t vw[4] = {v4[b].x, v4[b].y, v4[b].z, v4[b].w};
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-              const float2 e = e2[k];
-              const float w = u[k];
-              u[k] = w * e.x - v[k] * e.y;
-              v[k] = w * e.y + v[k] * e.x;
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = Io<T>::word(uw[k]), v = Io<T>::word(vw[k]);
+              const float2 e = e2[k * (V / 4)], f = V == 8 ? e2[2 * k + 1] : e;
+              uw[k] = Io<T>::unword(u.x * e.x - v.x * e.y, u.y * f.x - v.y * f.y);
+              vw[k] = Io<T>::unword(u.x * e.y + v.x * e.x, u.y * f.y + v.y * f.x);
             }
-            *reinterpret_cast<uint4*>(ys + pairs) = Io<T>::pack(v);
+            *reinterpret_cast<uint4*>(ys + pairs) = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+          } else if (V == 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = Io<T>::word(uw[k]), e = e2[k];
+              uw[k] = Io<T>::unword(u.x * e.x - u.y * e.y, u.x * e.y + u.y * e.x);
+            }
           } else {
 #pragma unroll
-            for (int k = 0; k < V / 2; ++k) {
-              const float2 e = e2[k];
-              const float w = u[2 * k];
-              u[2 * k] = w * e.x - u[2 * k + 1] * e.y;
-              u[2 * k + 1] = w * e.y + u[2 * k + 1] * e.x;
+            for (int k = 0; k < 4; k += 2) {
+              const float u = __uint_as_float(uw[k]), v = __uint_as_float(uw[k + 1]);
+              const float2 e = e2[k / 2];
+              uw[k] = __float_as_uint(u * e.x - v * e.y);
+              uw[k + 1] = __float_as_uint(u * e.y + v * e.x);
             }
           }
-          *reinterpret_cast<uint4*>(ys) = Io<T>::pack(u);
+          *reinterpret_cast<uint4*>(ys) = make_uint4(uw[0], uw[1], uw[2], uw[3]);
         }
+        r += 4 * apart;
+        if (r < rows) load();
       }
     }
   } else {
