@@ -334,7 +334,7 @@ def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tens
     fn = "csa2_rope_apply"
     dt = x.dtype
     if y is None:
-        y = torch.empty(x.shape, dtype=dt, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     _need(fn, x.dim() == 3 and (dt is torch.bfloat16 or dt is torch.float32))
     tokens, heads, dim = x.shape
     xt, xh, xc = x.stride()

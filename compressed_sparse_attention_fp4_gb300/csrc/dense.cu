@@ -1516,8 +1516,13 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.clusters = resident_clusters(kernel, G, smem);
   if (a.clusters < 1) return cudaErrorInvalidConfiguration;
-  // as many threads as there can be sequences or tiles, up to the most
   a.max_tiles = int(min64((int64_t(a.total_q) * a.d.heads + a.tile - 1) / a.tile + a.batch, INT32_MAX));
+  // no more clusters than there can be runs (one token over at most 256 positions: 16.3
+  // instead of 20.7 us)
+  const int64_t ctx = a.page_table ? min64(a.d.max_ctx, int64_t(a.d.max_pages) * kPage) : a.d.max_ctx;
+  const int64_t most = (a.max_tiles * ((ctx + kDenseBlk - 1) / kDenseBlk) + kDenseMinBlocks - 1) / kDenseMinBlocks;
+  a.clusters = int(min64(a.clusters, most));
+  // as many threads as there can be sequences or tiles, up to the most
   const int64_t want = max64(max64(a.max_tiles, a.batch), 128);
   const unsigned threads = want >= kPlanThreads ? kPlanThreads : unsigned((want + 31) / 32 * 32);
   CSA2_PROFILED(st, "dense_plan", (e = launch_pdl(dense_plan_kernel, dim3(1), dim3(threads), 0, st, 1, a)));
