@@ -309,18 +309,18 @@ def _need(fn: str, ok: bool):
 
 
 def _plane(t, dtype, n, dev) -> bool:
-    """A contiguous tensor of n elements of dtype on dev."""
-    return t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.device == dev
+    """A contiguous tensor of n elements of dtype on CUDA device number dev (-1: the host)."""
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev
 
 
-def _call(fn: str, dev, stream, args):
-    """Calls the library on dev (made current for the call: a library call launches on the
-    current device) and on its current stream, or on `stream`."""
+def _call(fn: str, dev: int, stream, args):
+    """Calls the library on CUDA device number dev (made current for the call: a library call
+    launches on the current device) and on its current stream, or on `stream`."""
     f = getattr(_lib, fn)
-    if dev.type != "cuda":
+    if dev < 0:
         _need(fn, False)
-    if stream is None and dev.index == torch.cuda.current_device():
-        _check(fn, f(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+    if stream is None and dev == torch._C._cuda_getDevice():
+        _check(fn, f(*args, torch._C._cuda_getCurrentRawStream(dev)))
         return
     with torch.cuda.device(dev):
         _check(fn, f(*args, _stream(stream)))
@@ -332,7 +332,7 @@ def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tens
     (bf16 or fp32, any strides but the last axis's 1) into y (a new tensor; y=x: in
     place).  pos: int32 [tokens].  inverse=True is the gradient's turn."""
     fn = "csa2_rope_apply"
-    dt = x.dtype
+    dt, dev = x.dtype, x.get_device()
     if y is None:
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
     _need(fn, x.dim() == 3 and (dt is torch.bfloat16 or dt is torch.float32))
@@ -341,12 +341,12 @@ def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tens
     if y is x:
         yt, yh = xt, xh
     else:
-        _need(fn, y.shape == x.shape and y.dtype is dt and y.device == x.device)
+        _need(fn, y.shape == x.shape and y.dtype is dt and y.get_device() == dev)
         yt, yh, yc = y.stride()
         _need(fn, yc == 1 or dim <= 1)
-    _need(fn, (xc == 1 or dim <= 1) and 0 <= offset <= dim and _plane(pos, torch.int32, tokens, x.device))
-    _call(fn, x.device, stream, (cfg.ref(), 1 if dt is torch.float32 else 0, x.data_ptr(), y.data_ptr(), pos.data_ptr(),
-                                 tokens, heads, dim, offset, xt, xh, yt, yh, 1 if inverse else 0))
+    _need(fn, (xc == 1 or dim <= 1) and 0 <= offset <= dim and _plane(pos, torch.int32, tokens, dev))
+    _call(fn, dev, stream, (cfg.ref(), 1 if dt is torch.float32 else 0, x.data_ptr(), y.data_ptr(), pos.data_ptr(),
+                            tokens, heads, dim, offset, xt, xh, yt, yh, 1 if inverse else 0))
     return y
 
 
@@ -359,7 +359,7 @@ def csa2_kv_append(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, dst_rows: torc
     receives the row in bf16."""
     fn = "csa2_kv_append"
     _need(fn, x.dim() == 2 and x.shape[1] == DQK and x.dtype is torch.bfloat16 and x.stride(1) == 1)
-    n, dev, rows = x.shape[0], x.device, codes.numel() // (LATENT // 2)
+    n, dev, rows = x.shape[0], x.get_device(), codes.numel() // (LATENT // 2)
     _need(fn, _plane(pos, torch.int32, n, dev) and _plane(dst_rows, torch.int64, n, dev)
           and _plane(codes, torch.uint8, rows * (LATENT // 2), dev) and _plane(scales, torch.uint8, rows * (LATENT // 16), dev)
           and _plane(rope, torch.bfloat16, rows * ROPE, dev)
@@ -389,7 +389,7 @@ def csa2_dense_attn_chunk(dims: Dims, batch: int, q, q_start, kv_codes, kv_scale
     cache position: out bf16 [total_q, H, 512], lse fp32 [total_q, H].  flags:
     DENSE_ALL_POSITIONS (no causal mask) or 0; window > 0: the last `window` positions."""
     fn = "csa2_dense_attn_chunk"
-    total, h, dev = q.shape[0], dims.heads, q.device
+    total, h, dev = q.shape[0], dims.heads, q.get_device()
     rows = batch * dims.max_ctx if page_table is None else dims.num_pages * PAGE
     _need(fn, _plane(q, torch.bfloat16, total * h * DQK, dev) and _plane(out, torch.bfloat16, total * h * LATENT, dev)
           and _plane(lse, torch.float32, total * h, dev) and _plane(q_start, torch.int32, batch + 1, dev)
@@ -397,9 +397,9 @@ def csa2_dense_attn_chunk(dims: Dims, batch: int, q, q_start, kv_codes, kv_scale
           and (page_table is None or _plane(page_table, torch.int32, batch * dims.max_pages, dev)))
     for t, dt, width in ((kv_codes, torch.uint8, LATENT // 2), (kv_scales, torch.uint8, LATENT // 16),
                          (kv_rope, torch.bfloat16, ROPE)):
-        _need(fn, t.dtype is dt and t.numel() >= rows * width and t.is_contiguous() and t.device == dev)
+        _need(fn, t.dtype is dt and t.numel() >= rows * width and t.is_contiguous() and t.get_device() == dev)
     # whole numbers that ctypes would cut to 32 bits
-    _need(fn, ws.dtype is torch.uint8 and ws.is_contiguous() and ws.device == dev and 0 <= window < 1 << 31
+    _need(fn, ws.dtype is torch.uint8 and ws.is_contiguous() and ws.get_device() == dev and 0 <= window < 1 << 31
           and 0 <= flags < 1 << 31)
     _call(fn, dev, stream, (ctypes.byref(dims.c()), batch, total, q.data_ptr(), q_start.data_ptr(), kv_codes.data_ptr(),
                             kv_scales.data_ptr(), kv_rope.data_ptr(), _ptr(page_table), ctx_len.data_ptr(), scale, window,
