@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -294,8 +294,11 @@ class Rope:
     def __post_init__(self):
         object.__setattr__(self, "_c", CRope(self.rot, self.layout, self.scaling, self.mscale, self.theta, self.factor,
                                              self.orig_ctx, self.turns_lo, self.turns_hi))
-
         object.__setattr__(self, "_ref", ctypes.byref(self._c))
+
+    def __reduce__(self):
+        # copies and pickles carry the fields; a reference to a C structure cannot be copied
+        return Rope, tuple(getattr(self, f.name) for f in fields(self))
 
     def ref(self):
         """The C structure, by reference."""

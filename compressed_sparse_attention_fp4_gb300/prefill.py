@@ -32,7 +32,7 @@ class ChunkBuffers:
     q: torch.Tensor                 # bf16 [total, H, 576]; its last 64 channels are rotated in place
     x: torch.Tensor                 # bf16 [total, 576] projections (latent | rotary part) of the new tokens
     pos: torch.Tensor               # int32 [total] positions
-    dst_rows: torch.Tensor          # int64 [total] cache rows (negative: none, a padding token)
+    dst_rows: torch.Tensor          # int64 [total] cache rows (negative: none, a padding token; see cache_rows)
     scale: float
     norm_w: torch.Tensor | None = None   # bf16 [512]
     eps: float = 1e-6
@@ -51,23 +51,24 @@ class ChunkBuffers:
         return self
 
 
-def cache_rows(ctx_len, q_start, page_table=None, max_ctx: int = 0):
+def cache_rows(ctx_len, q_start, page_table=None, max_ctx: int = 0, total: int | None = None):
     """Positions (int32 [total]) and cache rows (int64 [total]) of a chunk's tokens.
 
-    ctx_len: contexts with the chunk included; q_start: as in ChunkBuffers.  Token i of
-    sequence b, of n, stands at position ctx_len[b] - n + i; a position below 0 (more
-    tokens than context) has no row."""
+    ctx_len: contexts with the chunk included; q_start: as in ChunkBuffers; total: packed
+    tokens, padding included (None: q_start[-1]).  Token i of sequence b, of n, stands at
+    position ctx_len[b] - n + i; a position below 0 (more tokens than context) has no row,
+    nor has a padding token, before q_start[0] or from q_start[-1] on (its position is 0)."""
     starts = q_start.long()
-    total = int(starts[-1])
-    t = torch.arange(total, device=starts.device)
-    b = torch.searchsorted(starts[1:].contiguous(), t, right=True)
-    pos = ctx_len.long()[b] - (starts[b + 1] - t)
+    t = torch.arange(int(starts[-1]) if total is None else total, device=starts.device)
+    own = (t >= starts[0]) & (t < starts[-1])
+    b = torch.searchsorted(starts[1:].contiguous(), t, right=True).clamp(max=max(0, ctx_len.numel() - 1))
+    pos = torch.where(own, ctx_len.long()[b] - (starts[b + 1] - t), torch.zeros_like(t))
     at = pos.clamp(min=0)
     if page_table is None:
         rows = b * max_ctx + at
     else:
         rows = page_table.long()[b, at // csa2.PAGE] * csa2.PAGE + at % csa2.PAGE
-    return pos.to(torch.int32), torch.where(pos >= 0, rows, torch.full_like(rows, -1))
+    return pos.to(torch.int32), torch.where(own & (pos >= 0), rows, torch.full_like(rows, -1))
 
 
 def run_chunk(cb: ChunkBuffers, stream=None):

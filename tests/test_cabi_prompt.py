@@ -122,3 +122,33 @@ def test_append_limits_of_eps_and_overlap(mod):
     assert append(mod, n=4, entry=P(FAKE.value + 3 * 1152)) == 1  # within its last row
     assert append(mod, n=4, entry=P(FAKE.value - 16 if FAKE.value > 16 else 16)) == 1
     assert append(mod, n=1 << 50, entry=P(1 << 40)) in (1, 2)
+
+
+def test_rope_configurations_copy_and_pickle(mod):
+    import copy
+    import pickle
+    r = mod.Rope(rot=32, scaling=mod.ROPE_PARTS, factor=4.0, orig_ctx=4096.0, layout=mod.ROPE_HALF)
+    for c in (copy.deepcopy(r), pickle.loads(pickle.dumps(r)), copy.copy(r)):
+        assert c == r and c._c.rot == 32 and c._c.orig_ctx == 4096.0 and c.ref() is not None
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_cache_rows_of_padded_batches(mod, paged):
+    """Every token's row by counting, with padding before, behind and empty sequences."""
+    from compressed_sparse_attention_fp4_gb300 import prefill
+    ctx = torch.tensor([5, 130, 0, 2, 64], dtype=torch.int32)
+    start = torch.tensor([2, 5, 9, 9, 13, 14], dtype=torch.int32)      # the fourth has 4 tokens, 2 positions
+    table = torch.tensor([[7, 0, 0], [3, 9, 1], [0, 0, 0], [4, 0, 0], [2, 0, 0]], dtype=torch.int32) if paged else None
+    pos, rows = prefill.cache_rows(ctx, start, table, max_ctx=192, total=17)
+    assert pos.dtype == torch.int32 and rows.dtype == torch.int64 and len(pos) == len(rows) == 17
+    want = [-1] * 17
+    for b in range(5):
+        n = int(start[b + 1] - start[b])
+        for i in range(n):
+            p = int(ctx[b]) - n + i
+            if p >= 0:
+                want[int(start[b]) + i] = int(table[b, p // 64]) * 64 + p % 64 if paged else b * 192 + p
+                assert int(pos[int(start[b]) + i]) == p
+    assert rows.tolist() == want
+    short = prefill.cache_rows(ctx, start, table, max_ctx=192)
+    assert len(short[0]) == 14 and short[1].tolist() == want[:14]
