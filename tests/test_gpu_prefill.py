@@ -147,3 +147,51 @@ def test_same_logits_as_the_sparse_decode_over_the_same_positions():
     big = out.abs().amax(-1, keepdim=True)
     assert ((cb.out.float() - out).abs() <= 2.0 ** -8 * out.abs() + 4e-3 * big).all()
     assert ((cb.lse - lse).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("H,take", [(16, [1, 1, 0]), (64, [70, 3, 20])])
+def test_padded_batch(H, take):
+    """Padding tokens that hold NaN, before and behind the sequences: no cache row, no output, the same results."""
+    lens = [150, 65, 40]
+    rope = csa2.Rope()
+    done = [n - t for n, t in zip(lens, take)]
+    got = []
+    for pad in (False, True):
+        dims, planes, x, q, w, table = make(lens, H, 40)
+        prefill.run_chunk(chunk(dims, planes, x, q, w, [0, 0, 0], done, rope))
+        cb = chunk(dims, planes, x, q, w, done, take, rope)
+        n = cb.q.shape[0]
+        if pad:
+            wide = lambda t: torch.cat([torch.full_like(t[:1], float("nan")).expand(2, *t.shape[1:]), t,
+                                        torch.full_like(t[:1], float("nan")).expand(3, *t.shape[1:])]).contiguous()
+            cb.q, cb.x, cb.entry = wide(cb.q), wide(cb.x), wide(cb.entry)
+            cb.q_start = cb.q_start + 2
+            cb.pos, cb.dst_rows = prefill.cache_rows(cb.ctx_len, cb.q_start, planes["page_table"], total=n + 5)
+            cb.allocate_outputs()
+            cb.out.fill_(9.0)
+            cb.lse.fill_(9.0)
+        prefill.run_chunk(cb)
+        torch.cuda.synchronize()
+        assert csa2.get_device_status(cb.ws) == 0
+        if pad:
+            for t in (cb.out, cb.lse):
+                assert torch.all(t[:2] == 9.0) and torch.all(t[n + 2:] == 9.0)
+        s = slice(2, n + 2) if pad else slice(0, n)
+        got.append((cb.out[s], cb.lse[s], cb.entry[s], *(planes[k].view(torch.uint8) for k in ("kv_codes", "kv_scales", "kv_rope"))))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_chunks_of_two_layers_on_two_streams():
+    lens = [200, 90]
+    rope = csa2.Rope()
+    work = []
+    for seed in (50, 51):
+        dims, planes, x, q, w, table = make(lens, 64, seed)
+        work.append((chunk(dims, planes, x, q, w, [0, 0], lens, rope), planes, x, w, table))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for (cb, *_), s in zip(work, streams):
+        prefill.run_chunk(cb, stream=s)
+    for cb, planes, x, w, table in work:
+        check(cb, planes, x, w, table, [0, 0], lens, 64)
