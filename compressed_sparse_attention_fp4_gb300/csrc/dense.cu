@@ -45,9 +45,9 @@
 // from the cache, and in a values CTA one that hands slots of P back.
 //
 // Measured (GB300; 1,933 TFLOP/s measured bf16 rate, 2 * 1088 flop a visible (row, position)):
-// 2,048 tokens x 64 heads on 32,768 positions 5.6 ms, 1.61 PFLOP/s (83 %); bound by the
+// 2,048 tokens x 64 heads on 32,768 positions 5.4-5.6 ms, 1.62-1.68 PFLOP/s (84-87 %); bound by the
 // tensor pipe and the shared-memory bandwidth that feeds it.  8 contexts of 131,072 with
-// one token 0.32 ms, 0.45 PFLOP/s (64 of 128 rows of each product are used, and both CTAs
+// one token 0.31 ms, 0.47 PFLOP/s (64 of 128 rows of each product are used, and both CTAs
 // widen every block: a block every 2,800 cycles, of which its product takes 1,152).  Short
 // prompts (tiles of one or two blocks) 0.5 PFLOP/s: a tile's queries, 147 KB a CTA, cannot
 // come before the last product of the tile before it.
@@ -110,7 +110,7 @@ constexpr int kSBufs = 3;
 constexpr int kMetaWarp = 3 * 32 * 4;               // alpha, sum, reference of a warp's rows
 
 struct DenseSmall {
-  uint64_t raw_full[3], raw_empty[3];
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t kv_full[kKStages], kv_empty[kKStages];
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t q_turn[kKStages], q_place[kKStages];     // a ring stage free for queries; holding them
@@ -123,7 +123,7 @@ struct DenseSmall {
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
-  int raw_rows[3];                                  // rows of the raw bytes before the context's end (0: bad page)
+  int raw_rows[2];                                  // rows of the raw bytes before the context's end (0: bad page)
   __align__(16) float meta[kMaxPSlots][4][3][32];
   uint16_t swap[4][kDenseTile];                     // largest magnitudes of the queries, between a row's four warps
   int8_t q_shift[4][kDenseTile];                    // power of two each query row was scaled by, of four tiles in turn
@@ -196,7 +196,9 @@ __device__ __forceinline__ bool wait_slow(DenseSmall& sm, uint64_t* bar, uint32_
     }
   }
 }
-// for a converged warp: one answer for all lanes
+// For a converged warp: one answer for all lanes.  (128K decode batch, 310 us: one lane asking
+// for the others 645; a time hint on the wait, of whatever length, 322; some tests without
+// suspending before it 333.)
 template <bool kCluster = false>
 __device__ inline bool wait_warp(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
   return __all_sync(0xFFFFFFFFu, try_wait<kCluster>(bar, parity) || wait_slow<kCluster>(sm, bar, parity, ws));
@@ -812,7 +814,10 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       if (!live) {
         // no row at all (a decode tile of few heads): P stays zero
         if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) return;
-        if (!(zeroed >> slot & 1)) {
+        // Zeros once sent stand in the values CTA's slot as well: the bytes are only counted from
+        // then on.  (What a later tile leaves there meets only rows that do not exist.)
+        const bool sent = zeroed >> slot & 1;
+        if (!sent) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(ps + wq * 4096 + i * 512 + lane * 16) = make_uint4(0, 0, 0, 0);
           sm.meta[slot][wq][0][lane] = 1.0f;
@@ -825,8 +830,12 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
         if (lane == 0) {
           arrive_leader<G>(&sm.s_empty[buf], 0);
           const uint32_t bar = peer_addr(&sm.p_full[slot], uint32_t(G + part));
-          copy_to_peer(peer_addr(ps + wq * 4096, uint32_t(G + part)), ps + wq * 4096, 4096, bar);
-          copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], uint32_t(G + part)), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
+          if (sent) {
+            asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(4096 + kMetaWarp) : "memory");
+          } else {
+            copy_to_peer(peer_addr(ps + wq * 4096, uint32_t(G + part)), ps + wq * 4096, 4096, bar);
+            copy_to_peer(peer_addr(&sm.meta[slot][wq][0][0], uint32_t(G + part)), &sm.meta[slot][wq][0][0], kMetaWarp, bar);
+          }
         }
         __syncwarp();
         cur.step(a, 2);
