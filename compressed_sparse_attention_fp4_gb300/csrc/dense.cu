@@ -1385,49 +1385,99 @@ __global__ void __launch_bounds__(kPlanThreads, 1) dense_plan_kernel(DenseArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Merge: CTA (g, c) joins 8 channels of the tile that the boundary before run c
-// cuts, if c is the first boundary inside it.  Thread = row.  It also writes the
-// rows of tiles that see nothing.  Bound by the latency of its loads: 48 in flight (16.3 us
-// with 16 on the 128K decode batch, where a tile has about ten pieces; 14.2).
+// Merge: a CTA joins 8 channels of a tile that was cut between runs.  Thread = row.  It
+// also writes the rows of tiles that see nothing.  Bound by the latency of its loads, so
+// as many as may be are in flight (48 a thread; 16.3 us with 16 on the 128K decode batch,
+// where a tile has about ten pieces; 14.2).
+//   kFew, where there are few tiles, of many pieces each: CTA (g, t) is for tile t, and a
+//     row has four threads, which take a quarter of the pieces each;
+//   else CTA (g, c) is for the tile that the boundary before run c cuts, if c is the first
+//     boundary inside it.
 // ---------------------------------------------------------------------------
 constexpr int kMergeCh = 8;
+constexpr int kMergeFew = 4;                        // threads a row where there are few tiles
 
-__global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
+template <bool kFew>
+__global__ void __launch_bounds__(kDenseTile * (kFew ? kMergeFew : 1)) dense_merge_kernel(DenseArgs a) {
+  constexpr int Y = kFew ? kMergeFew : 1;
+  __shared__ float s_top[kFew ? Y : 1][kDenseTile], s_total[kFew ? Y : 1][kDenseTile];
+  __shared__ float s_o[kFew ? Y : 1][kFew ? kMergeCh : 1][kDenseTile];
   pdl_wait();
   pdl_launch_dependents();
-  const int r = threadIdx.x, g = blockIdx.x, c = blockIdx.y;
+  const int r = threadIdx.x, y = kFew ? threadIdx.y : 0, g = blockIdx.x;
   const int G = a.tile / kDenseTile, part = blockIdx.z;
-  // independent loads first: each level of dependent ones is most of a microsecond
-  const int4 head = __ldg(a.plan.head), run = __ldg(a.plan.runs + c), prev = __ldg(a.plan.runs + max(c - 1, 0));
   const int ctas = gridDim.x * gridDim.y * gridDim.z;
   const int t0 = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-  // a boundary inside a tile, the first there: the run before starts at or before the tile's first block
-  if (c < head.y && run.y > 0 && (prev.x != run.x || prev.y == 0)) {
-    const int4 ta = __ldg(a.plan.tiles + 2 * run.x), tb = __ldg(a.plan.tiles + 2 * run.x + 1);
-    const int64_t last = __ldg(a.plan.before + run.x) + tb.z - 1;               // the tile's last block
-    const int64_t blocks = int64_t(uint32_t(head.z)) | int64_t(head.w) << 32;
+  // the tile and its pieces: runs first .. first + n - 1 (see make_run); n 0: none, or one
+  const int4 head = __ldg(a.plan.head);
+  const int64_t blocks = int64_t(uint32_t(head.z)) | int64_t(head.w) << 32;
+  const auto run_of = [&](int64_t block) { return int(((block + 1) * head.y - 1) / blocks); };
+  int4 ta = {};
+  int first = 0, n = 0;
+  if constexpr (kFew) {
+    const int t = blockIdx.y;
+    ta = __ldg(a.plan.tiles + 2 * t);
+    const int4 tb = __ldg(a.plan.tiles + 2 * t + 1);
+    const int64_t b0 = __ldg(a.plan.before + t);
+    if (t < head.x && tb.z > 0) {
+      first = run_of(b0);
+      n = run_of(b0 + tb.z - 1) - first + 1;
+    }
+  } else {
+    // independent loads first: each level of dependent ones is most of a microsecond
+    const int c = blockIdx.y;
+    const int4 run = __ldg(a.plan.runs + c), prev = __ldg(a.plan.runs + max(c - 1, 0));
+    // a boundary inside a tile, the first there: the run before starts at or before the tile's first block
+    if (c < head.y && run.y > 0 && (prev.x != run.x || prev.y == 0)) {
+      ta = __ldg(a.plan.tiles + 2 * run.x);
+      const int4 tb = __ldg(a.plan.tiles + 2 * run.x + 1);
+      first = c - 1;
+      n = run_of(__ldg(a.plan.before + run.x) + tb.z - 1) - first + 1;
+    }
+  }
+  if (n > 1) {
     const int lr = ta.y + kDenseTile * part + r;
-    if (lr < ta.w * a.d.heads) {
-      const int c1 = int(((last + 1) * head.y - 1) / blocks);                  // the run it is in (see make_run)
-      const int n = c1 - c + 2;                      // pieces: runs c - 1 .. c1
-      // the first piece ends the run before (its tail); the others start theirs
-      const auto slot = [&](int i) { return (i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * G + part; };
-      float top = -INFINITY;
+    const bool in = lr < ta.w * a.d.heads;
+    const int mine = in ? n : 0;
+    // the first piece ends its run (its tail); the others start theirs
+    const auto slot = [&](int i) { return (i == 0 ? 2 * first + 1 : 2 * (first + i)) * G + part; };
+    float top = -INFINITY;
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) top = fmaxf(top, __ldg(a.part_lse + slot(i) * kDenseTile + r));
-      float o[kMergeCh], total = 0.0f;
+    for (int i = y; i < mine; i += Y) top = fmaxf(top, __ldg(a.part_lse + slot(i) * kDenseTile + r));
+    if (kFew) {
+      s_top[y][r] = top;
+      __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kMergeCh; ++k) o[k] = 0.0f;
+      for (int j = 0; j < Y; ++j) top = fmaxf(top, s_top[j][r]);
+    }
+    float o[kMergeCh], total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMergeCh; ++k) o[k] = 0.0f;
 #pragma unroll 6
-      for (int i = 0; i < n; ++i) {
-        const int s = slot(i);
-        const float l = __ldg(a.part_lse + s * kDenseTile + r);
-        const float w = l == -INFINITY ? 0.0f : exp2f((l - top) * 1.4426950408889634f);
-        total += w;
-        const float* po = a.part_o + (int64_t(s) * kLatent + g * kMergeCh) * kDenseTile + r;
+    for (int i = y; i < mine; i += Y) {
+      const int s = slot(i);
+      const float l = __ldg(a.part_lse + s * kDenseTile + r);
+      const float w = l == -INFINITY ? 0.0f : exp2f((l - top) * 1.4426950408889634f);
+      total += w;
+      const float* po = a.part_o + (int64_t(s) * kLatent + g * kMergeCh) * kDenseTile + r;
 #pragma unroll
-        for (int k = 0; k < kMergeCh; ++k) o[k] = fmaf(w, __ldg(po + k * kDenseTile), o[k]);
+      for (int k = 0; k < kMergeCh; ++k) o[k] = fmaf(w, __ldg(po + k * kDenseTile), o[k]);
+    }
+    if (kFew) {
+      s_total[y][r] = total;
+#pragma unroll
+      for (int k = 0; k < kMergeCh; ++k) s_o[y][kFew ? k : 0][r] = o[k];
+      __syncthreads();
+      if (y == 0) {
+#pragma unroll
+        for (int j = 1; j < Y; ++j) {
+          total += s_total[j][r];
+#pragma unroll
+          for (int k = 0; k < kMergeCh; ++k) o[k] += s_o[j][kFew ? k : 0][r];
+        }
       }
+    }
+    if (in && y == 0) {
       const float inv = total != 0.0f ? 1.0f / total : 0.0f;
       const int64_t row = int64_t(ta.z) * a.d.heads + lr;
       uint4* dst = reinterpret_cast<uint4*>(a.out + row * kLatent + g * kMergeCh);
@@ -1445,9 +1495,9 @@ __global__ void __launch_bounds__(kDenseTile) dense_merge_kernel(DenseArgs a) {
     const int4 ta = __ldg(a.plan.tiles + 2 * t);
     const int rows = min(a.tile, ta.w * a.d.heads - ta.y);
     const int64_t row = int64_t(ta.z) * a.d.heads + ta.y;
-    for (int i = r; i < rows * (kLatent / 8); i += kDenseTile)
+    for (int i = y * kDenseTile + r; i < rows * (kLatent / 8); i += Y * kDenseTile)
       reinterpret_cast<uint4*>(a.out + row * kLatent)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = r; i < rows; i += kDenseTile) a.lse[row + i] = -INFINITY;
+    for (int i = y * kDenseTile + r; i < rows; i += Y * kDenseTile) a.lse[row + i] = -INFINITY;
   }
 }
 
@@ -1539,9 +1589,16 @@ cudaError_t launch_dense(DenseArgs a, cudaStream_t st) {
   CSA2_PROFILED(st, "dense_attn",
                 (e = launch_pdl(kernel, dim3(unsigned(2 * G * a.clusters)), dim3(kDenseThreads), smem, st, 1, a, m)));
   if (e != cudaSuccess) return e;
+  // Few tiles, up to one for four clusters: four threads a row in the merge.  Measured, with and
+  // without (graph): one token on 131,072 positions 60 / 88 us, on 16,000 28 / 51; 8 on 4,000
+  // 35.5 / 38.1; 4 x 4 tokens on 2,000 25.1 / 26.9.  With up to one for two clusters: 16 tokens on
+  // 1,000 (32 heads) 28.1 instead of 25.5.
+  const bool few = int64_t(a.max_tiles) * 4 <= a.clusters;
   CSA2_PROFILED(st, "dense_merge",
-                (e = launch_pdl(dense_merge_kernel, dim3(kLatent / kMergeCh, unsigned(a.clusters), unsigned(G)),
-                                dim3(kDenseTile), 0, st, 1, a)));
+                (e = few ? launch_pdl(dense_merge_kernel<true>, dim3(kLatent / kMergeCh, unsigned(a.max_tiles), unsigned(G)),
+                                      dim3(kDenseTile, kMergeFew), 0, st, 1, a)
+                         : launch_pdl(dense_merge_kernel<false>, dim3(kLatent / kMergeCh, unsigned(a.clusters), unsigned(G)),
+                                      dim3(kDenseTile), 0, st, 1, a)));
   return e;
 }
 
