@@ -178,7 +178,11 @@ __device__ inline bool try_wait(uint64_t* bar, uint32_t parity) {
 
 // Every wait of the kernel: bounded (200 ms against microseconds; the clock is only read
 // after some tries, it takes longer than most waits), and cut short once another role
-// of the CTA has given up.  False: the caller's role ends.
+// of the CTA has given up.  False: the caller's role ends.  The hardware barriers between
+// warps have no limit, so a role that ends early still takes part in all those left to it
+// (labels `leave`): none of its partners waits there for ever.  (mbarriers in their place
+// cost 4 to 12 % of a call: 128K decode batch 306 -> 342 us, prompts 422 -> 445; for the
+// queries' barriers alone 1 to 7 %.)
 template <bool kCluster>
 __device__ __forceinline__ bool wait_slow(DenseSmall& sm, uint64_t* bar, uint32_t parity, uint8_t* ws) {
   uint64_t t0 = 0;
@@ -270,6 +274,10 @@ __device__ inline bool elect_one() {
   return p != 0;
 }
 
+// Hardware barriers, each for one lane quarter of the softmax warps: the hand-off of the
+// reference from the even blocks' warp, from the odd blocks' warp, the start of a tile; and
+// for one half of the queries, of the widening warps.
+constexpr int kRefBar = 1, kTurnBar = 9, kQueryBar = 13;
 __device__ inline void some_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ inline void some_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
@@ -523,6 +531,7 @@ __device__ inline bool queries_to_tmem(const DenseArgs& a, DenseSmall& sm, uint8
   // both halves: then the products that read the tile before are done, too (both stages were free)
   if (!wait_warp(sm, &sm.q_place[0], k_item & 1, a.ws)) return false;
   if (!wait_warp(sm, &sm.q_place[1], k_item & 1, a.ws)) return false;
+  // from here on no way out: a warp takes part in both hardware barriers, or has left before them
   tc::tc_fence_after_sync();
   const uint32_t src = tc::smem_u32(base) + Lay<G>::kKvOff + st * kKBytes;
   const uint32_t row = tc::sw128_offset(r & 63, 0), turn = (r & 7) << 4;       // chunk c of a row: row's base + (c << 4 ^ turn)
@@ -537,7 +546,7 @@ __device__ inline bool queries_to_tmem(const DenseArgs& a, DenseSmall& sm, uint8
     }
   const uint32_t b2 = __vmaxu2(big[0], big[1]);
   sm.swap[part4][r] = uint16_t(max(b2 & 0xFFFFu, b2 >> 16));
-  some_sync(9 + half, 256);
+  some_sync(kQueryBar + half, 256);
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) top = max(top, uint32_t(sm.swap[i][r]));
@@ -564,7 +573,7 @@ __device__ inline bool queries_to_tmem(const DenseArgs& a, DenseSmall& sm, uint8
   }
   tmem_wait_st();
   tc::tc_fence_before_sync();
-  some_sync(9 + half, 256);
+  some_sync(kQueryBar + half, 256);
   if (lane == 0) {
     if ((wq & 1) == 0 && part4 == 0) arrive(&sm.kv_empty[st]);                 // the half has been read
     arrive_leader<G>(&sm.q_full, 0);
@@ -597,17 +606,17 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
       // the tile's queries come through the same ring
 #pragma unroll 1
       for (int k = 0; k < kLead; ++k, ++u) {
-        if (!wait_warp(sm, &sm.kv_empty[u % kKStages], ((u / kKStages) & 1) ^ 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.kv_empty[u % kKStages], ((u / kKStages) & 1) ^ 1, a.ws)) goto leave_queries;
         if (lane == 0) arrive(&sm.q_turn[u % kKStages]);
       }
-      if (kScores && !queries_to_tmem<1>(a, sm, base, w, lane, tmem, k_item, place)) return;
+      if (kScores && !queries_to_tmem<1>(a, sm, base, w, lane, tmem, k_item, place)) goto leave_queries;
 #pragma unroll 1
       for (int i = 0; i < it.n; ++i, ++u) {
         const uint32_t st = u % kKStages;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half, ++v) {
           const uint32_t rs = v % Lay<1>::kRawStages, raw = raw0 + rs * Lay<1>::kRawStage;
-          if (!wait_warp(sm, &sm.raw_full[rs], (v / Lay<1>::kRawStages) & 1, a.ws)) return;
+          if (!wait_warp(sm, &sm.raw_full[rs], (v / Lay<1>::kRawStages) & 1, a.ws)) goto leave;
           const bool have = row < sm.raw_rows[rs];
           const uint4 cw = ld_shared16(raw + src);
           const uint32_t sc = ld_shared_u16(raw + ssrc);
@@ -621,7 +630,7 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
           const uint32_t two = e4m3x2_to_f16x2(uint16_t(code));
           const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
           const uint4 w0 = widen8(cw.x, s0), w1 = widen8(cw.y, s0), w2 = widen8(cw.z, s1), w3 = widen8(cw.w, s1);
-          if (half == 0 && !wait_warp(sm, &sm.kv_empty[st], ((u / kKStages) & 1) ^ 1, a.ws)) return;
+          if (half == 0 && !wait_warp(sm, &sm.kv_empty[st], ((u / kKStages) & 1) ^ 1, a.ws)) goto leave;
           const uint32_t d = dst + st * kStageBytes + half * 4096;    // 32 rows on; a row's swizzle repeats every 8
           st_shared16(d, w0);
           st_shared16(d ^ 16, w1);
@@ -655,14 +664,14 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
     for (uint32_t k_item = 0; walk.next(it); ++k_item) {
       // the tile's queries come through the same ring
       if (kScores) {
-        if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) goto leave_queries;
         if (lane == 0) arrive(&sm.q_turn[g]);
         ++u;
-        if (!queries_to_tmem<G>(a, sm, base, w, lane, tmem, k_item, place)) return;
+        if (!queries_to_tmem<G>(a, sm, base, w, lane, tmem, k_item, place)) goto leave_queries;
       }
 #pragma unroll 1
       for (int i = (g - place) & 1; i < it.n; i += 2, ++u, ++v) {
-        if (!wait_warp(sm, &sm.raw_full[g], v & 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.raw_full[g], v & 1, a.ws)) goto leave;
         uint4 cw[kPieces], rp;
         uint32_t sc[kPieces];
         const bool have = row < sm.raw_rows[g];
@@ -674,7 +683,7 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
         if (kScores) rp = ld_shared16(raw + o_rope);
         __syncwarp();
         if (lane == 0) arrive(&sm.raw_empty[g]);
-        if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.kv_empty[g], (u & 1) ^ 1, a.ws)) goto leave;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
           uint32_t code = have ? sc[j] : 0u;
@@ -694,6 +703,20 @@ __device__ inline void widen_role(const DenseArgs& a, DenseSmall& sm, uint8_t* b
       }
       place = (place + kLead + it.n) & 1;
     }
+  }
+  return;
+  // a wait has given up: the hardware barriers of this tile's queries, unless they are through, and of the tiles to come
+leave_queries:
+  __syncwarp();
+  if (kScores) {
+    some_sync(kQueryBar + ((w & 3) >> 1), 256);
+    some_sync(kQueryBar + ((w & 3) >> 1), 256);
+  }
+leave:
+  __syncwarp();
+  while (kScores && walk.next(it)) {
+    some_sync(kQueryBar + ((w & 3) >> 1), 256);
+    some_sync(kQueryBar + ((w & 3) >> 1), 256);
   }
 }
 
@@ -786,13 +809,15 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
   const float c2 = a.scale * 1.4426950408889634f;
   uint32_t n = 0;
   uint32_t zeroed = 0;                               // slots in which this warp's rows of P are zeros
+  uint32_t n0 = 0, n1 = 0;                           // blocks of the item
+  bool live = false;                                 // some row of this warp (and of its other half) exists
   Cursor cur(a.plan, cl, lane);
   for (uint32_t k_item = 0; cur.item(a); ++k_item) {
-    some_sync(11 + wq, 64);                          // both warps of a row are through the tile before
+    some_sync(kTurnBar + wq, 64);                    // both warps of a row are through the tile before
     float c = 0.0f;                                  // logits in base 2 per score; known with the first scores
     // positions this row sees: first .. last
     const int lr = cur.it.a.y + kDenseTile * part + r, tok = lr / a.d.heads;
-    const bool live = __any_sync(0xFFFFFFFFu, tok < cur.it.a.w);     // some row of this warp (and of its other half) exists
+    live = __any_sync(0xFFFFFFFFu, tok < cur.it.a.w);
     int last = -1, first = 0;
     if (tok < cur.it.a.w) {
       last = a.causal ? cur.it.b.x - cur.it.a.w + tok : cur.it.b.x - 1;
@@ -800,7 +825,8 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
     }
     bool own_first = true;
     float own = -INFINITY, sum = 0.0f;               // reference of this warp's last block, its sum under it
-    const uint32_t n0 = n, n1 = n + cur.it.n;
+    n0 = n;
+    n1 = n + cur.it.n;
     cur.i = int((half ^ n0) & 1);
     n += uint32_t(cur.i);
 #pragma unroll 1
@@ -810,10 +836,10 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       const int lo = first - t0, hi = cur.row0(a) < 0 ? -1 : last - t0;
       const bool edge = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kDenseBlk - 1);
       uint8_t* ps = base + slot * kPBytes;
-      if (!wait_warp(sm, &sm.s_full[buf], (n / kSBufs) & 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.s_full[buf], (n / kSBufs) & 1, a.ws)) goto leave;
       if (!live) {
         // no row at all (a decode tile of few heads): P stays zero
-        if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) return;
+        if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) goto leave;
         // Zeros once sent stand in the values CTA's slot as well: the bytes are only counted from
         // then on.  (What a later tile leaves there meets only rows that do not exist.)
         const bool sent = zeroed >> slot & 1;
@@ -870,11 +896,11 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
         for (int k = 0; k < 4; ++k) t4[k] = i + 4 + k < 64 ? fmaxf(fmaxf(t4[k], x[i + k]), x[i + 4 + k]) : fmaxf(t4[k], x[i + k]);
       }
       const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
-      // the reference so far, from the other warp (barriers 1..4 to the odd blocks' warps,
-      // 5..8 back; each arrival is awaited before the next on the same barrier)
+      // the reference so far, from the other warp (each arrival is awaited before the next on
+      // the same barrier)
       float before = -INFINITY;
       if (n != n0) {
-        some_sync(1 + 4 * (half ^ 1) + wq, 64);
+        some_sync(kRefBar + 4 * (half ^ 1) + wq, 64);
         before = sm.ref[half ^ 1][r];
       }
       float ref = before, alpha = 1.0f;
@@ -884,12 +910,15 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       }
       if (n + 1 != n1) {
         sm.ref[half][r] = ref;
-        some_arrive(1 + 4 * half + wq, 64);
+        some_arrive(kRefBar + 4 * half + wq, 64);
       }
       if (own != ref && own != -INFINITY) sum *= ex2(own - ref);     // (no reference yet: 0, or NaN)
       own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref - 7.0f;
-      if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) return;
+      if (!wait_warp(sm, &sm.p_free[slot], ((n / Lay<G>::kPSlots) & 1) ^ 1, a.ws)) {
+        n += 2;                                      // this block's hand-offs are done
+        goto leave;
+      }
       const uint64_t cc = pack2(c, c), ss = pack2(-sub, -sub);
       uint64_t acc[2] = {0, 0};                      // +0, +0
 #pragma unroll
@@ -925,6 +954,22 @@ __device__ inline void softmax_role(const DenseArgs& a, DenseSmall& sm, uint8_t*
       cur.step(a, 2);
     }
     n = n1;
+  }
+  return;
+  // a wait has given up: the hand-offs of the tile's blocks from n on, and of the tiles to come
+leave:
+  __syncwarp();
+  for (;;) {
+    for (; live && n < n1; n += 2) {
+      if (n != n0) some_sync(kRefBar + 4 * (half ^ 1) + wq, 64);
+      if (n + 1 != n1) some_arrive(kRefBar + 4 * half + wq, 64);
+    }
+    if (!cur.walk.next(cur.it)) return;
+    some_sync(kTurnBar + wq, 64);
+    live = __any_sync(0xFFFFFFFFu, (cur.it.a.y + kDenseTile * part + r) / a.d.heads < cur.it.a.w);
+    n0 = n1;
+    n1 += cur.it.n;
+    n = n0 + ((half ^ n0) & 1);
   }
 }
 
