@@ -125,6 +125,16 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A new output of a call on `stream`, from the memory of that stream: a block of the current
+    stream's may still be in use by work queued there, and would go back there while `stream` writes it.
+    To use the output on a third stream, wait and ``record_stream`` as for any tensor."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 @dataclass
 class Dims:
     """Python view of ``csa2_dims`` (see include/csa2.h)."""
@@ -165,9 +175,9 @@ def fp4_kv_quantize(x: torch.Tensor, codes: torch.Tensor | None = None,
     """bf16 [n, 512] -> (codes uint8 [n, 256], scales uint8 [n, 32])."""
     n = x.shape[0]
     if codes is None:
-        codes = torch.empty((n, LATENT // 2), dtype=torch.uint8, device=x.device)
+        codes = _new((n, LATENT // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((n, LATENT // 16), dtype=torch.uint8, device=x.device)
+        scales = _new((n, LATENT // 16), torch.uint8, x.device, stream)
     _check("fp4_kv_quantize", _lib.fp4_kv_quantize(_ptr(x), n, _ptr(codes), _ptr(scales), _stream(stream)))
     return codes, scales
 
@@ -208,7 +218,7 @@ def fp4_kv_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor
     """(codes, scales) -> bf16 [n, 512]."""
     n = codes.shape[0]
     if y is None:
-        y = torch.empty((n, LATENT), dtype=torch.bfloat16, device=codes.device)
+        y = _new((n, LATENT), torch.bfloat16, codes.device, stream)
     _check("fp4_kv_dequantize", _lib.fp4_kv_dequantize(_ptr(codes), _ptr(scales), n, _ptr(y), _stream(stream)))
     return y
 
@@ -332,12 +342,12 @@ def _call(fn: str, dev: int, stream, args):
 def csa2_rope_apply(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor | None = None, offset: int = 0,
                     inverse: bool = False, stream=None) -> torch.Tensor:
     """Rotary positions on channels [offset, offset + cfg.rot) of x [tokens, heads, dim]
-    (bf16 or fp32, any strides but the last axis's 1) into y (a new tensor; y=x: in
-    place).  pos: int32 [tokens].  inverse=True is the gradient's turn."""
+    (bf16 or fp32, any strides but the last axis's 1) into y (None: a new tensor, of the
+    memory of `stream`; y=x: in place).  pos: int32 [tokens].  inverse=True is the gradient's turn."""
     fn = "csa2_rope_apply"
     dt, dev = x.dtype, x.get_device()
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = _new(x.shape, dt, x.device, stream)
     _need(fn, x.dim() == 3 and (dt is torch.bfloat16 or dt is torch.float32))
     tokens, heads, dim = x.shape
     xt, xh, xc = x.stride()
