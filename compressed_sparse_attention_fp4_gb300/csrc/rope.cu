@@ -3,6 +3,8 @@
 //
 // Both kernels are bound by memory: every value is read once and written once,
 // and the arithmetic between is kept under the time of the bytes.
+#include <cmath>
+
 #include "fp4.cuh"
 #include "kernels.cuh"
 #include "profile.cuh"
@@ -198,9 +200,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 // codec's do.  fp32 arithmetic alone would round some thousandths of a percent
 // of the values the other way, so
 //   * x is scaled by the power of two that brings the row's largest value into
-//     [1, 2); a lane adds its 16 squares to 64 (each step's rounding error is
-//     then exact in fp32 and summed beside it), and both sums are added over
-//     the warp as integers;
+//     [1, 2), or, where the row is so small that eps outweighs its squares, eps to
+//     1 or more (the squares' sums are right to 2^-40 of that); a lane adds its
+//     16 squares to 64 (each step's rounding error is then exact in fp32 and summed
+//     beside it), and both sums are added over the warp as integers;
 //   * 1/sqrt is rsqrtf and one Newton step kept as a second fp32 part;
 //   * x w is exact in fp32 (8 + 8 bits); only a product within 8 units of a
 //     bf16 midpoint (one in 4,000) needs the low parts.
@@ -278,7 +281,7 @@ __device__ inline AppendRow append_load(const uint16_t* x, int64_t stride, const
 template <bool kHalf, bool kNorm>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     append_kernel(const __grid_constant__ RopeTable tab, const uint16_t* __restrict__ x, int64_t n, int64_t stride,
-                  const uint16_t* __restrict__ norm_w, float eps, const int32_t* __restrict__ pos,
+                  const uint16_t* __restrict__ norm_w, float eps, int least_ex, const int32_t* __restrict__ pos,
                   const int64_t* __restrict__ dst_rows, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                   uint16_t* __restrict__ rope, int64_t cache_rows, uint16_t* __restrict__ entry) {
   const int lane = threadIdx.x & 31;
@@ -304,8 +307,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(b2 & 0xFFFFu, b2 >> 16));
       // an infinity or a NaN in the row: its values as they are times 0 or NaN (below)
       const bool whole = top < 0x7F80u;
-      // exponent of the row's largest value, at least -40 (eps then outweighs the squares by far)
-      const int ex = max(int(top >> 7) - 127, -40);
+      // exponent of the row's largest value, at least least_ex (launch_append)
+      const int ex = max(int(top >> 7) - 127, least_ex);
       const float up = whole ? __uint_as_float(uint32_t(127 - ex) << 23 | (ex == 127 ? 0x00400000u : 0u)) : 1.0f;
       float g[2][8], s = 64.0f, e = 0.0f;
 #pragma unroll
@@ -410,10 +413,13 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
   const bool half = a.cfg.layout == CSA2_ROPE_HALF;
   auto kernel = a.norm_w ? (half ? append_kernel<true, true> : append_kernel<false, true>)
                          : (half ? append_kernel<true, false> : append_kernel<false, false>);
+  // least power of two that rows are scaled by, as the exponent that it takes to 0: where it acts,
+  // eps / 2^(2 ex) is 1 or more (eps 2^-149, the least, and ex -75: 2)
+  const int least_ex = a.norm_w ? int(min64(-40, std::ilogb(a.eps) >> 1)) : 0;
   cudaError_t e;
   CSA2_PROFILED(st, "kv_append",
                 (e = launch_pdl(kernel, dim3(grid), dim3(kAppendThreads), 0, st, 1, tab, a.x, a.n, a.x_stride, a.norm_w,
-                                a.eps, a.pos, a.dst_rows, reinterpret_cast<uint32_t*>(a.codes), a.scales, a.rope,
+                                a.eps, least_ex, a.pos, a.dst_rows, reinterpret_cast<uint32_t*>(a.codes), a.scales, a.rope,
                                 a.cache_rows, a.entry)));
   return e;
 }

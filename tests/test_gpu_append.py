@@ -177,3 +177,15 @@ def test_graph_replay_and_other_stream():
         assert torch.equal(a[dst2], b[dst2])
     with pytest.raises(csa2.Csa2Error):                      # the bf16 rows over their own input
         csa2.csa2_kv_append(cfg, x, pos, dst, *planes[:3], norm_w=w, entry=x)
+
+
+@pytest.mark.parametrize("eps", [1e-24, 2e-27, 1e-30, 1e-33, 1e-36, 1.2e-38, 1e-41, 1.4e-45])
+def test_smallest_eps(eps):
+    """Rows about as small as sqrt(eps), far above it and far below: every eps above 0, subnormal ones too."""
+    x, w, pos, dst = inputs(400, 448, 51)
+    middle = np.log2(np.float64(np.float32(eps))) / 2
+    lowest = max(middle - 45, -120)                        # the results stay normal bf16 values
+    s = torch.exp2(torch.linspace(lowest, middle + 40, 400)).cuda()[:, None]
+    x[:, :512] = (x[:, :512].float() * s).to(torch.bfloat16)
+    cfg = csa2.Rope()
+    check(x, w, pos, dst, 448, cfg, eps, run(x, w, pos, dst, 448, cfg, eps=eps))
