@@ -1,4 +1,4 @@
-// rope.cuh -- rotary positions: per-pair frequencies (host) and angles (device).
+// rope.cuh -- rotary positions: configurations (host) and angles (device).
 //
 // Pair i of a rotated part of `rot` channels turns by the angle pos * f_i.  The
 // pages apply rotary positions to the 64 bf16 key channels and the matching
@@ -10,8 +10,9 @@
 // hundredths of a radian.  f_i / 2 pi is therefore held as a 64-bit fraction of
 // a turn, and pos * F_i modulo 2^64 is the angle modulo one turn, exactly: one
 // integer multiply in place of 64-bit floating point, which this GPU runs at a
-// small part of its fp32 rate.  The top 32 bits give the angle to 2^-32 turns;
-// the sine and cosine are fp32.
+// small part of its fp32 rate.  The top 32 bits give the angle: to 2^-32 turns, and
+// 2^-34 for the fraction's own rounding at the farthest positions (rope_table.cuh).
+// The sine and cosine are fp32.
 #pragma once
 
 #include <cmath>
@@ -19,42 +20,9 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "rope_table.cuh"
 
 namespace csa2 {
-
-constexpr int kMaxRot = 256;
-constexpr int kMaxPairs = kMaxRot / 2;
-
-// By value into the kernels (constant bank): the turn fraction of every pair.
-struct RopeTable {
-  uint64_t turn[kMaxPairs];    // f_i / (2 pi) * 2^64
-  float mscale;                // multiplies cosine and sine
-  int pairs;
-};
-
-// The frequencies of `r` (host, 64 bits).  The caller has checked `r`.
-inline RopeTable make_rope_table(const csa2_rope& r) {
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
-  RopeTable t;
-  t.mscale = r.mscale;
-  t.pairs = r.rot / 2;
-  double theta = r.theta;
-  if (r.scaling == CSA2_ROPE_BASE && r.rot > 2) theta *= std::pow(r.factor, double(r.rot) / double(r.rot - 2));
-  for (int i = 0; i < t.pairs; ++i) {
-    double f = std::pow(theta, -2.0 * i / r.rot);
-    if (r.scaling == CSA2_ROPE_LINEAR) f /= r.factor;
-    if (r.scaling == CSA2_ROPE_PARTS) {
-      // turns the pair makes over the original context: above turns_hi the
-      // frequency stays, below turns_lo it is divided, linear between
-      const double turns = r.orig_ctx * f / kTwoPi;
-      double keep = (turns - r.turns_lo) / (r.turns_hi - r.turns_lo);
-      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-      f = f * keep + f / r.factor * (1.0 - keep);
-    }
-    t.turn[i] = uint64_t(std::ldexp(f / kTwoPi, 64));   // f <= 1: below a sixth of a turn
-  }
-  return t;
-}
 
 // make_rope_table, remembered: a table is a pure function of its configuration, and the
 // powers of 32 to 128 frequencies take longer than a decode step's kernel.

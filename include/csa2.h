@@ -365,7 +365,7 @@ csa2_status csa2_sparse_attn_decode_noalloc(const csa2_dims* d, int32_t batch, i
  *     over the original context (the by-parts rule of YaRN): with k = (n_i - turns_lo)
  *     / (turns_hi - turns_lo) limited to [0, 1], f_i * k + f_i / factor * (1 - k);
  *   CSA2_ROPE_BASE:   theta replaced by theta * factor^(rot / (rot - 2)) (rot > 2).
- * Angles are exact modulo one turn for every int32 position (to 2^-32 turns). */
+ * Angles are right modulo one turn for every int32 position, to 2^-31 turns. */
 typedef enum { CSA2_ROPE_INTERLEAVED = 0, CSA2_ROPE_HALF = 1 } csa2_rope_layout;
 typedef enum {
   CSA2_ROPE_PLAIN = 0,
