@@ -55,20 +55,26 @@ def cache_rows(ctx_len, q_start, page_table=None, max_ctx: int = 0, total: int |
     """Positions (int32 [total]) and cache rows (int64 [total]) of a chunk's tokens.
 
     ctx_len: contexts with the chunk included; q_start: as in ChunkBuffers; total: packed
-    tokens, padding included (None: q_start[-1]).  Token i of sequence b, of n, stands at
-    position ctx_len[b] - n + i; a position below 0 (more tokens than context) has no row,
-    nor has a padding token, before q_start[0] or from q_start[-1] on (its position is 0)."""
-    starts = q_start.long()
-    t = torch.arange(int(starts[-1]) if total is None else total, device=starts.device)
-    own = (t >= starts[0]) & (t < starts[-1])
-    b = torch.searchsorted(starts[1:].contiguous(), t, right=True).clamp(max=max(0, ctx_len.numel() - 1))
+    tokens, padding included (None: q_start[-1]); max_ctx: rows of a sequence in a cache
+    without a page table (needed for more than one).  Token i of sequence b, of n, stands at
+    position ctx_len[b] - n + i; a position below 0 (more tokens than context) or behind the
+    sequence's rows (its pages, max_ctx) has no row, nor has a padding token, before q_start[0]
+    or from q_start[-1] on (its position is 0)."""
+    starts, batch, dev = q_start.long(), ctx_len.numel(), q_start.device
+    csa2._need("cache_rows", starts.numel() == batch + 1 and (page_table is not None or batch <= 1 or max_ctx > 0))
+    t = torch.arange(int(starts[-1]) if total is None else total, device=dev)
+    room = page_table.shape[1] * csa2.PAGE if page_table is not None else max_ctx if max_ctx > 0 else 1 << 31
+    if batch == 0 or room == 0:
+        return torch.zeros_like(t, dtype=torch.int32), torch.full_like(t, -1)
+    b = torch.searchsorted(starts[1:].contiguous(), t, right=True).clamp(max=batch - 1)
+    own = (t >= starts[b]) & (t < starts[b + 1])
     pos = torch.where(own, ctx_len.long()[b] - (starts[b + 1] - t), torch.zeros_like(t))
-    at = pos.clamp(min=0)
+    at = pos.clamp(min=0, max=room - 1)
     if page_table is None:
         rows = b * max_ctx + at
     else:
         rows = page_table.long()[b, at // csa2.PAGE] * csa2.PAGE + at % csa2.PAGE
-    return pos.to(torch.int32), torch.where(own & (pos >= 0), rows, torch.full_like(rows, -1))
+    return pos.to(torch.int32), torch.where(own & (pos == at), rows, torch.full_like(rows, -1))
 
 
 def run_chunk(cb: ChunkBuffers, stream=None):
