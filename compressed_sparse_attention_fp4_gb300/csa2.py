@@ -302,6 +302,8 @@ class Rope:
     mscale: float = 1.0
 
     def __post_init__(self):
+        # whole numbers that ctypes would cut to 32 bits; what they mean is checked by the calls
+        _need("csa2_rope", all(-1 << 31 <= v < 1 << 31 for v in (self.rot, self.layout, self.scaling)))
         object.__setattr__(self, "_c", CRope(self.rot, self.layout, self.scaling, self.mscale, self.theta, self.factor,
                                              self.orig_ctx, self.turns_lo, self.turns_hi))
         object.__setattr__(self, "_ref", ctypes.byref(self._c))
@@ -384,6 +386,7 @@ def csa2_kv_append(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, dst_rows: torc
 
 def dense_attn_workspace_size(dims: Dims, batch: int, total_q: int) -> int:
     out = ctypes.c_size_t(0)
+    _need("csa2_dense_attn_workspace_size", -1 << 31 <= batch < 1 << 31)
     _check("csa2_dense_attn_workspace_size",
            _lib.csa2_dense_attn_workspace_size(ctypes.byref(dims.c()), batch, total_q, ctypes.byref(out)))
     return out.value

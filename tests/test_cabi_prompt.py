@@ -152,3 +152,13 @@ def test_cache_rows_of_padded_batches(mod, paged):
     assert rows.tolist() == want
     short = prefill.cache_rows(ctx, start, table, max_ctx=192)
     assert len(short[0]) == 14 and short[1].tolist() == want[:14]
+
+
+def test_numbers_past_32_bits_are_refused(mod):
+    """Not cut to another number that the call would take."""
+    for kw in (dict(rot=2 ** 32 + 64), dict(layout=2 ** 32), dict(scaling=2 ** 32 + 1), dict(rot=-2 ** 32 + 64)):
+        with pytest.raises(mod.Csa2Error):
+            mod.Rope(**kw)
+    for batch in (2 ** 32 + 1, -2 ** 32 + 1):
+        with pytest.raises(mod.Csa2Error):
+            mod.dense_attn_workspace_size(mod.Dims(max_ctx=1024), batch, 8)
