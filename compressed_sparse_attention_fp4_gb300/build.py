@@ -7,6 +7,7 @@ skipped while the library is newer than every source and header.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -49,6 +50,16 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def check_registers(source: str, ptxas: str):
+    """Raises where ptxas gave a dense attention kernel another number of registers than the split
+    among its roles counts on (kLaunchRegs): the library would refuse every call, without this reason."""
+    want = int(re.search(r"kLaunchRegs = (\d+)", source).group(1))
+    for name, got in re.findall(r"entry function '\w*?(dense_kernel|dense_pair_kernel)E\w*'.*?Used (\d+) registers", ptxas, re.S):
+        if int(got) != want:
+            raise RuntimeError(f"{name}: {got} registers a thread, but its role split (csrc/dense.cu) is for {want}: "
+                               "build with the CUDA toolkit it was written for, or change kLaunchRegs and the split")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; returns the library path."""
     if not force and up_to_date():
@@ -59,14 +70,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *FLAGS, "-c", src, "-o", obj]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
+        cmd = [cc, "-Xptxas=-v", *ARCH, *FLAGS, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         if verbose:
             sys.stderr.write(r.stderr)
+        if os.path.basename(src) == "dense.cu":
+            with open(src) as f:
+                check_registers(f.read(), r.stderr)
         return obj
 
     srcs = sources()
