@@ -63,6 +63,13 @@ template <> struct Io<uint16_t> {
   __device__ static uint16_t put(float v) { return uint16_t(bf16x2_rn(v, 0.0f)); }
 };
 
+// A turned pair, (u c - v s, u s + v c), in the same operations wherever it is formed: a result
+// depends neither on strides and alignment nor on the kernel (left to the compiler, the product
+// that is rounded first differed between the paths).
+__device__ inline float2 turn_pair(float u, float v, float2 cs) {
+  return make_float2(__fmaf_rn(u, cs.x, -__fmul_rn(v, cs.y)), __fmaf_rn(v, cs.x, __fmul_rn(u, cs.y)));
+}
+
 // x, y and the strides count elements of T; sign is -1 for the inverse.
 template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, 4)
@@ -143,23 +150,25 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
             for (int k = 0; k < 4; ++k) {
               const float2 u = Io<T>::word(uw[k]), v = Io<T>::word(vw[k]);
               const float2 e = e2[k * (V / 4)], f = V == 8 ? e2[2 * k + 1] : e;
-              uw[k] = Io<T>::unword(u.x * e.x - v.x * e.y, u.y * f.x - v.y * f.y);
-              vw[k] = Io<T>::unword(u.x * e.y + v.x * e.x, u.y * f.y + v.y * f.x);
+              const float2 a = turn_pair(u.x, v.x, e), b = turn_pair(u.y, v.y, f);
+              uw[k] = Io<T>::unword(a.x, b.x);
+              vw[k] = Io<T>::unword(a.y, b.y);
             }
             *reinterpret_cast<uint4*>(ys + pairs) = make_uint4(vw[0], vw[1], vw[2], vw[3]);
           } else if (V == 8) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float2 u = Io<T>::word(uw[k]), e = e2[k];
-              uw[k] = Io<T>::unword(u.x * e.x - u.y * e.y, u.x * e.y + u.y * e.x);
+              const float2 a = turn_pair(u.x, u.y, e);
+              uw[k] = Io<T>::unword(a.x, a.y);
             }
           } else {
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
               const float u = __uint_as_float(uw[k]), v = __uint_as_float(uw[k + 1]);
-              const float2 e = e2[k / 2];
-              uw[k] = __float_as_uint(u * e.x - v * e.y);
-              uw[k + 1] = __float_as_uint(u * e.y + v * e.x);
+              const float2 a = turn_pair(u, v, e2[k / 2]);
+              uw[k] = __float_as_uint(a.x);
+              uw[k + 1] = __float_as_uint(a.y);
             }
           }
           *reinterpret_cast<uint4*>(ys) = make_uint4(uw[0], uw[1], uw[2], uw[3]);
@@ -184,8 +193,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
         const float2 e = cs[t * kMaxPairs + c];
         const int iu = offset + (kHalf ? c : 2 * c), iv = offset + (kHalf ? c + pairs : 2 * c + 1);
         const float u = Io<T>::get(xs[iu]), v = Io<T>::get(xs[iv]);
-        ys[iu] = Io<T>::put(u * e.x - v * e.y);
-        ys[iv] = Io<T>::put(u * e.y + v * e.x);
+        const float2 a = turn_pair(u, v, e);
+        ys[iu] = Io<T>::put(a.x);
+        ys[iv] = Io<T>::put(a.y);
       }
     }
   }
@@ -340,7 +350,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
       for (int r = 0; r < 2; ++r) v[r] = norm8(g[r], w[r], r0, rl);
     }
     const float2 cs = rope_cs(tab, lane, ps);
-    const uint32_t turned = bf16x2_rn(u0 * cs.x - u1 * cs.y, u0 * cs.y + u1 * cs.x);
+    const float2 uv = turn_pair(u0, u1, cs);
+    const uint32_t turned = bf16x2_rn(uv.x, uv.y);
     if (entry) {
       uint16_t* er = entry + row * kDqk;
 #pragma unroll

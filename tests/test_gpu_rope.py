@@ -129,3 +129,32 @@ def test_replayed_graph_and_other_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want * 2)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_same_bits_whatever_the_strides(dtype, half):
+    """Rows of odd strides and addresses, in place, and the append's rotary part: the bits of the aligned call."""
+    cfg = csa2.Rope(layout=csa2.ROPE_HALF if half else csa2.ROPE_INTERLEAVED, **SCALINGS["parts"])
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(3000, 16, 64, generator=g).to(dtype).cuda()
+    pos = torch.randint(0, 1 << 20, (3000,), generator=g, dtype=torch.int32).cuda()
+    for inverse in (False, True):
+        want = csa2.csa2_rope_apply(cfg, x, pos, inverse=inverse)
+        odd = torch.empty(3000, 16, 67, dtype=dtype, device="cuda")[..., 1:65]
+        odd.copy_(x)
+        assert torch.equal(csa2.csa2_rope_apply(cfg, odd, pos, inverse=inverse), want)
+        csa2.csa2_rope_apply(cfg, odd, pos, y=odd, inverse=inverse)
+        assert torch.equal(odd, want)
+        z = x.clone()
+        csa2.csa2_rope_apply(cfg, z, pos, y=z, inverse=inverse)
+        assert torch.equal(z, want)
+    if dtype is torch.bfloat16:
+        n = 3000 * 16
+        rows = torch.zeros(n, 576, dtype=dtype, device="cuda")
+        rows[:, 512:] = x.view(n, 64)
+        dst = torch.arange(n, device="cuda")
+        codes, scales = (torch.empty(n, k, dtype=torch.uint8, device="cuda") for k in (256, 32))
+        kr = torch.empty(n, 64, dtype=dtype, device="cuda")
+        csa2.csa2_kv_append(cfg, rows, pos.repeat_interleave(16), dst, codes, scales, kr)
+        assert torch.equal(kr.view(3000, 16, 64), csa2.csa2_rope_apply(cfg, x, pos))
