@@ -32,7 +32,10 @@
 // block's maximum passes it by more than 8, so the outputs are rarely rescaled, and
 // then by a power of two.  P = 2^(x - ref + 7) <= 2^15 fits fp16 (rounded to 11 bits where
 // bf16 has 8); terms 2^-31 below the reference are the first to be lost.  Sums are
-// fp32, of the unrounded P.
+// fp32, of the unrounded P.  The rounding of P moves an output by at most 2^-11 of
+// sum p |v|, its bf16 form by 2^-8 of itself: against 64 bits the error is that of
+// unrounded P to two digits (1.7e-3 relative; 1e-5 more with few positions).  P in two
+// parts would double the values product, 1,024 of a block's tensor cycles.
 //
 // Work division: the (tile, block) pairs of the call are counted by a plan kernel
 // and cut into equal runs, one per cluster, whatever the shape: a decode batch splits
@@ -48,9 +51,11 @@
 // 2,048 tokens x 64 heads on 32,768 positions 5.4-5.6 ms, 1.62-1.68 PFLOP/s (84-87 %); bound by the
 // tensor pipe and the shared-memory bandwidth that feeds it.  8 contexts of 131,072 with
 // one token 0.31 ms, 0.47 PFLOP/s (64 of 128 rows of each product are used, and both CTAs
-// widen every block: a block every 2,800 cycles, of which its product takes 1,152).  Short
-// prompts (tiles of one or two blocks) 0.5 PFLOP/s: a tile's queries, 147 KB a CTA, cannot
-// come before the last product of the tile before it.
+// widen every block: a block every 2,800 cycles, of which its product takes 1,152).  Whole
+// prompts of 509 to 1,310 tokens 0.42 ms, 0.5 PFLOP/s: a tile costs about 8,000 cycles
+// before its first block (its queries, 147 KB a CTA, cannot come before the last product of
+// the tile before it), and runs of equal blocks hold 9 to 67 tiles, so the call waits for the
+// clusters that have the first, short tiles of the prompts.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -53,7 +53,7 @@ csa2_status csa2_rope_apply(const csa2_rope* r, int32_t dtype, const void* x, vo
   if (tokens < 0 || tokens > (int64_t(1) << 31) || heads < 0 || heads > 65535 || dim < 1 || offset < 0 ||
       int64_t(offset) + r->rot > dim)
     return CSA2_ERR_UNSUPPORTED_SHAPE;
-  // pieces of one CTA (8 tokens, all heads) are counted in 32 bits
+  // pieces of one CTA (kRopeTok tokens, all heads) are counted in 32 bits
   if (int64_t(heads) * dim > (int64_t(1) << 27)) return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (tokens == 0 || heads == 0) return CSA2_OK;
   const uintptr_t size = dtype == CSA2_ROPE_F32 ? 4 : 2;

@@ -25,7 +25,8 @@ namespace {
 // 268 MB, 44.0 us (90 % of the copy rate); 4,099 x 16 heads x 128 bf16 channels into another
 // buffer, half layout, 34 MB, 7.4 us.  Loads behind the angles: 45.5 and 12; tiles of 8 tokens:
 // 43.9 and 8.1; 2: 43.1 and 10.0; three CTAs an SM instead of four: 44.0 and 7.9, five: 44.2
-// and 12.3; one piece in flight and two divisions a piece: 68 for the first.
+// and 12.3; one piece in flight and two divisions a piece: 68 for the first.  (At four CTAs an
+// SM, 64 registers, the half layouts spill 44 (fp32) and 68 bytes a thread.)
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTok = 4;
@@ -217,8 +218,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 //   * 1/sqrt is rsqrtf and one Newton step kept as a second fp32 part;
 //   * x w is exact in fp32 (8 + 8 bits); only a product within 8 units of a
 //     bf16 midpoint (one in 4,000) needs the low parts.
-// Bound by its instructions (about 500 a row) a little above its bytes: 131,072 rows with
-// the bf16 rows written, 357 MB, in 90 us (3.9 TB/s; 53 us at the copy rate).
+// Bound by its instructions, 584 a warp and row, and by the latencies between them: issue
+// slots are 69 % busy with the 24 warps an SM that 79 registers leave.  131,072 rows with
+// the bf16 rows written, 357 MB, in 89 us (4.0 TB/s; 53 us at the copy rate).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendBlocks = 3;                    // resident on an SM

@@ -1,10 +1,14 @@
 """Prompt-side runner: a chunk of new tokens of a ragged batch through one layer.
 
-What the decode step (``step.py``) does for one token per sequence, in the dense
-form that a prompt, a context no longer than the Top-K, or a verification of
-draft tokens takes: rotary positions on the queries, the new tokens' rows normed,
+The dense form, for a prompt, a context no longer than the Top-K, or a verification
+of draft tokens: rotary positions on the queries, the new tokens' rows normed,
 rotated, quantized and appended to the FP4 cache, then attention of the chunk
 over every visible position of it.  Three library calls; no arithmetic here.
+
+Attention reads FP4 rows alone.  The decode step (``step.py``) joins them with the
+exact bf16 rows of the newest tokens where its layer has a window (``swa`` > 0): the
+two are the same function only for a layer without one (``swa`` 0) whose Top-K set
+holds every position.  ``entry`` keeps the exact rows for a decode step's window.
 """
 from __future__ import annotations
 
@@ -37,7 +41,7 @@ class ChunkBuffers:
     norm_w: torch.Tensor | None = None   # bf16 [512]
     eps: float = 1e-6
     window: int = 0
-    entry: torch.Tensor | None = None    # bf16 [total, 576]: also receives the exact rows (SWA window)
+    entry: torch.Tensor | None = None    # bf16 [total, 576]: also receives the exact rows, for a later decode step's window
     # outputs
     out: torch.Tensor = None        # bf16 [total, H, 512]
     lse: torch.Tensor = None        # fp32 [total, H]

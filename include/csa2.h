@@ -397,7 +397,8 @@ typedef struct {
  * element) that do not overlap.
  * Errors: CSA2_ERR_INVALID_ARG (also: y's rows overlap), CSA2_ERR_UNSUPPORTED_SHAPE
  * (rot outside 2..256 or odd, offset + rot > dim, sizes below 0, more than 2^31
- * positions, heads > 65535), CSA2_ERR_CUDA. */
+ * positions, heads > 65535, heads * dim > 2^27), CSA2_ERR_CUDA.  The same values give
+ * the same bits whatever the strides and the alignment. */
 #define CSA2_ROPE_BF16 0
 #define CSA2_ROPE_F32 1
 csa2_status csa2_rope_apply(const csa2_rope* r, int32_t dtype, const void* x, void* y, const int32_t* pos,
@@ -415,7 +416,7 @@ csa2_status csa2_rope_apply(const csa2_rope* r, int32_t dtype, const void* x, vo
  * A row whose destination is negative or not below cache_rows writes no cache row.
  * Destinations must differ from each other (of two rows with the same one, which
  * bytes of which row remain is not specified).
- *   norm_w:   device bf16 [512], or NULL;  0 < eps <= 1
+ *   norm_w:   device bf16 [512] of magnitudes below 2^127, or NULL;  0 < eps <= 1
  *   pos:      device int32 [n];  dst_rows: device int64 [n]
  *   codes, scales, rope: the cache planes (layout above; 16-, 2- and 16-byte aligned)
  *   entry:    device bf16 [n][576], or NULL: also receives every row i as
@@ -455,11 +456,16 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
  *             first 256 the error word as elsewhere.  Calls that may run at the same
  *             time need a workspace each.
  *   P is rounded to fp16 (2^-11) and the output to bf16; everything between is fp32.
+ *   The product of a row of q, scaled by the power of two that brings its largest value
+ *   to 2^14, with a key has to stay within fp32 (rope keys below 2^100 do).
+ * A CSA2 layer with a window (dims.swa > 0) joins the FP4 entries with exact bf16 rows in
+ * one softmax (csa2_sparse_attn_decode); this call has no such operand and reads FP4 rows
+ * alone, as that one does with swa 0 and every position in its Top-K set.
  * Limits: total_q * H <= 2^30, batch <= 2^20, cache rows (batch * max_ctx, or num_pages *
  * 64) < 2^31.
  * Make the first call on a device before any stream capture.
  * Errors: CSA2_ERR_INVALID_ARG (window < 0, window with CSA2_DENSE_ALL_POSITIONS,
- *         unknown flags, pointers, NaN scale), CSA2_ERR_UNSUPPORTED_SHAPE,
+ *         unknown flags, pointers, a scale that is not finite), CSA2_ERR_UNSUPPORTED_SHAPE,
  *         CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
 #define CSA2_DENSE_ALL_POSITIONS 1
 csa2_status csa2_dense_attn_workspace_size(const csa2_dims* d, int32_t batch, int64_t total_q, size_t* bytes);
