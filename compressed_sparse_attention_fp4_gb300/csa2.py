@@ -26,6 +26,7 @@ KV_EARLY_INPUTS = 1
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_PARTS, ROPE_BASE = 0, 1, 2, 3
 DENSE_ALL_POSITIONS = 1
+IDX_NORM_NONE, IDX_NORM_RMS, IDX_NORM_LAYER = 0, 1, 2
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED_SHAPE",
           3: "CSA2_ERR_WORKSPACE_TOO_SMALL", 4: "CSA2_ERR_CUDA",
@@ -82,6 +83,11 @@ SIGNATURES = {
     "csa2_dense_attn_workspace_size": (_I32, [ctypes.POINTER(CDims), _I32, _I64, ctypes.POINTER(_SZ)]),
     "csa2_dense_attn_chunk": (_I32, [ctypes.POINTER(CDims), _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _F, _I32, _I32,
                                      _P, _P, _P, _SZ, _P]),
+    "csa2_window_append": (_I32, [ctypes.POINTER(CRope), _P, _I64, _I64, _P, _F, _P, _P, _P, _I64, _P]),
+    "csa2_idx_k_append": (_I32, [ctypes.POINTER(CRope), _I32, _P, _I64, _I64, _I32, _I32, _P, _P, _F, _P, _P, _P, _I64, _P]),
+    "csa2_window_attn_workspace_size": (_I32, [ctypes.POINTER(CDims), _I32, _I64, ctypes.POINTER(_SZ)]),
+    "csa2_window_attn_chunk": (_I32, [ctypes.POINTER(CDims), _I32, _I64, _P, _P, _P, _P, _P, _F, _I32, _I32, _P, _P, _P, _P,
+                                      _P, _SZ, _P]),
     "csa2_get_device_status": (_I32, [_P, _P, ctypes.POINTER(_I32)]),
     "csa2_profile_enable": (_I32, [_I32]),
     "csa2_profile_read": (_I32, [ctypes.POINTER(CKernelTime), _I32, ctypes.POINTER(_I32)]),
@@ -420,6 +426,83 @@ def csa2_dense_attn_chunk(dims: Dims, batch: int, q, q_start, kv_codes, kv_scale
     _call(fn, dev, stream, (ctypes.byref(dims.c()), batch, total, q.data_ptr(), q_start.data_ptr(), kv_codes.data_ptr(),
                             kv_scales.data_ptr(), kv_rope.data_ptr(), _ptr(page_table), ctx_len.data_ptr(), scale, window,
                             flags, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel()))
+
+
+def csa2_window_append(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, dst_rows: torch.Tensor, kv: torch.Tensor,
+                       norm_w: torch.Tensor | None = None, eps: float = 1e-6, stream=None):
+    """Norm, rotate and write row i of x (bf16 [n, 576], rows strided) in bf16 to row
+    dst_rows[i] (int64; outside the cache: skipped) of the window cache kv [rows, 576]."""
+    fn = "csa2_window_append"
+    _need(fn, x.dim() == 2 and x.shape[1] == DQK and x.dtype is torch.bfloat16 and x.stride(1) == 1)
+    n, dev, rows = x.shape[0], x.get_device(), kv.numel() // DQK
+    _need(fn, _plane(pos, torch.int32, n, dev) and _plane(dst_rows, torch.int64, n, dev)
+          and _plane(kv, torch.bfloat16, rows * DQK, dev)
+          and (norm_w is None or _plane(norm_w, torch.bfloat16, LATENT, dev)))
+    _call(fn, dev, stream, (cfg.ref(), x.data_ptr(), n, x.stride(0), _ptr(norm_w), eps, pos.data_ptr(), dst_rows.data_ptr(),
+                            kv.data_ptr(), rows))
+
+
+_KEY_ROW = {IDXK_E4M3: (torch.bfloat16, 128, 128), IDXK_F32: (torch.float32, 64, 256), IDXK_FP4: (torch.bfloat16, 128, 72)}
+
+
+def csa2_idx_k_append(cfg: Rope | None, kind: int, x: torch.Tensor, pos: torch.Tensor | None, dst_rows: torch.Tensor,
+                      idx_k: torch.Tensor, cache_rows: int, offset: int = 0, norm: int = IDX_NORM_NONE,
+                      norm_w: torch.Tensor | None = None, norm_b: torch.Tensor | None = None, eps: float = 1e-6, stream=None):
+    """Norm, rotate (cfg on channels [offset, offset + cfg.rot); None: not) and write row i
+    of x (bf16 [n, 128], fp32 [n, 64] for IDXK_F32; rows strided) to row dst_rows[i] (int64;
+    outside the cache: skipped) of the indexer keys idx_k of `kind` (IDXK_E4M3, IDXK_FP4,
+    IDXK_F32; cache_rows rows).  norm: IDX_NORM_*, norm_w and norm_b of x's type."""
+    fn = "csa2_idx_k_append"
+    _need(fn, kind in _KEY_ROW)
+    dt, dim, size = _KEY_ROW[kind]
+    _need(fn, x.dim() == 2 and x.shape[1] == dim and x.dtype is dt and x.stride(1) == 1)
+    n, dev = x.shape[0], x.get_device()
+    # whole numbers that ctypes would cut to 32 bits
+    _need(fn, 0 <= offset < 1 << 31 and 0 <= norm < 1 << 31 and _plane(dst_rows, torch.int64, n, dev)
+          and (pos is None or _plane(pos, torch.int32, n, dev)) and (norm_w is None or _plane(norm_w, dt, dim, dev))
+          and (norm_b is None or _plane(norm_b, dt, dim, dev)) and idx_k.is_contiguous() and idx_k.get_device() == dev
+          and idx_k.numel() * idx_k.element_size() == cache_rows * size)
+    _call(fn, dev, stream, (None if cfg is None else cfg.ref(), kind, x.data_ptr(), n, x.stride(0), offset, norm, _ptr(norm_w),
+                            _ptr(norm_b), eps, _ptr(pos), dst_rows.data_ptr(), idx_k.data_ptr(), cache_rows))
+
+
+def window_attn_workspace_size(dims: Dims, batch: int, total_q: int) -> int:
+    out = ctypes.c_size_t(0)
+    _need("csa2_window_attn_workspace_size", -1 << 31 <= batch < 1 << 31)
+    _check("csa2_window_attn_workspace_size",
+           _lib.csa2_window_attn_workspace_size(ctypes.byref(dims.c()), batch, total_q, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_window_attn_workspace(dims: Dims, batch: int, total_q: int, device="cuda") -> torch.Tensor:
+    """Workspace of csa2_window_attn_chunk (uint8; its error word zeroed)."""
+    ws = torch.empty(window_attn_workspace_size(dims, batch, total_q), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def csa2_window_attn_chunk(dims: Dims, batch: int, q, q_start, kv, page_table, ctx_len, scale: float, window: int, out, lse,
+                           ws, sinks: int = 0, prev_out=None, prev_lse=None, stream=None):
+    """Attention of packed query tokens q bf16 [total_q, H, 576] over exact rows kv bf16
+    [rows, 576]: the last `window` positions of each and the first `sinks`; joined in one softmax
+    with prev_out / prev_lse (another attention's results for these queries; may be out / lse).
+    out bf16 [total_q, H, 512], lse fp32 [total_q, H]."""
+    fn = "csa2_window_attn_chunk"
+    total, h, dev = q.shape[0], dims.heads, q.get_device()
+    rows = batch * dims.max_ctx if page_table is None else dims.num_pages * PAGE
+    _need(fn, _plane(q, torch.bfloat16, total * h * DQK, dev) and _plane(out, torch.bfloat16, total * h * LATENT, dev)
+          and _plane(lse, torch.float32, total * h, dev) and _plane(q_start, torch.int32, batch + 1, dev)
+          and _plane(ctx_len, torch.int32, batch, dev)
+          and (page_table is None or _plane(page_table, torch.int32, batch * dims.max_pages, dev))
+          and (prev_out is None or _plane(prev_out, torch.bfloat16, total * h * LATENT, dev))
+          and (prev_lse is None or _plane(prev_lse, torch.float32, total * h, dev))
+          and kv.dtype is torch.bfloat16 and kv.numel() >= rows * DQK and kv.is_contiguous() and kv.get_device() == dev)
+    # whole numbers that ctypes would cut to 32 bits
+    _need(fn, ws.dtype is torch.uint8 and ws.is_contiguous() and ws.get_device() == dev and 0 <= window < 1 << 31
+          and 0 <= sinks < 1 << 31 and -1 << 31 <= batch < 1 << 31)
+    _call(fn, dev, stream, (ctypes.byref(dims.c()), batch, total, q.data_ptr(), q_start.data_ptr(), kv.data_ptr(),
+                            _ptr(page_table), ctx_len.data_ptr(), scale, window, sinks, _ptr(prev_out), _ptr(prev_lse),
+                            out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel()))
 
 
 def get_device_status(ws: torch.Tensor, stream=None) -> int:

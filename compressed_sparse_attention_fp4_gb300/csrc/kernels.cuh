@@ -147,8 +147,37 @@ struct AppendArgs {
   uint16_t* entry;
 };
 
+struct WindowAppendArgs {
+  csa2_rope cfg;
+  const uint16_t* x;
+  int64_t n, x_stride;
+  const uint16_t* norm_w;
+  float eps;
+  const int32_t* pos;
+  const int64_t* dst_rows;
+  uint16_t* kv;
+  int64_t cache_rows;
+};
+
+struct IdxAppendArgs {
+  bool rotate;
+  csa2_rope cfg;
+  int32_t kind, offset, norm;
+  const void* x;
+  int64_t n, x_stride;
+  const void* norm_w;
+  const void* norm_b;
+  float eps;
+  const int32_t* pos;
+  const int64_t* dst_rows;
+  void* idx_k;
+  int64_t cache_rows;
+};
+
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_window_append(const WindowAppendArgs& a, cudaStream_t st);
+cudaError_t launch_idx_append(const IdxAppendArgs& a, cudaStream_t st);
 cudaError_t launch_quantize(const uint16_t* x, int64_t n, const int64_t* dst_rows, uint8_t* codes,
                             uint8_t* scales, bool early, cudaStream_t st);
 cudaError_t launch_quantize_idx(const uint16_t* x, int64_t n, const int64_t* dst_rows, uint8_t* idx_k,

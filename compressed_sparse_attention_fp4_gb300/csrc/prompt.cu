@@ -1,5 +1,5 @@
 // prompt.cu -- C entry points of the prompt-side calls: rotary positions, the
-// cache append and dense chunk attention.  As in api.cu, every call validates on
+// appends (FP4 rows, exact rows, indexer keys), dense and window attention of a chunk.  As in api.cu, every call validates on
 // the host and launches nothing when an argument is wrong.
 #include <cmath>
 #include <cstdint>
@@ -8,6 +8,7 @@
 #include "dense.cuh"
 #include "kernels.cuh"
 #include "rope.cuh"
+#include "window.cuh"
 
 using namespace csa2;
 
@@ -31,6 +32,13 @@ int64_t extent(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t h
   return e > (__int128(1) << 59) ? -1 : int64_t(e);
 }
 
+// Whether two blocks of bytes share any.
+bool overlap(const void* a, __int128 a_bytes, const void* b, __int128 b_bytes) {
+  const __int128 x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+// Sizes of a chunk call: heads, contexts, rows counted in 32 bits.
 csa2_status check_dense_dims(const csa2_dims* d, int32_t batch, int64_t total_q) {
   if (!d || batch < 0 || total_q < 0) return CSA2_ERR_INVALID_ARG;
   if (d->heads < 1 || d->heads > kMaxHeads) return CSA2_ERR_UNSUPPORTED_SHAPE;
@@ -178,6 +186,140 @@ csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t tot
   a.part_lse = reinterpret_cast<float*>(w + L.part_lse);
   a.part_o = reinterpret_cast<float*>(w + L.part_o);
   return from_cuda(launch_dense(a, as_stream(stream)));
+}
+
+csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n, int64_t x_stride,
+                               const uint16_t* norm_w, float eps, const int32_t* pos, const int64_t* dst_rows,
+                               uint16_t* kv, int64_t cache_rows, void* stream) {
+  csa2_status st = check_rope(r);
+  if (st != CSA2_OK) return st;
+  if (r->rot != kRope) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (n < 0 || cache_rows < 0 || (norm_w && !(eps > 0.0f && eps <= 1.0f))) return CSA2_ERR_INVALID_ARG;
+  if (n == 0) return CSA2_OK;
+  if (!x || !pos || !dst_rows || !kv) return CSA2_ERR_INVALID_ARG;
+  if (!is_aligned(x, 16) || !is_aligned(kv, 16) || !is_aligned(pos, 4) || !is_aligned(dst_rows, 8) ||
+      (norm_w && !is_aligned(norm_w, 16)))
+    return CSA2_ERR_INVALID_ARG;
+  if (n > 1 && (x_stride < kDqk || x_stride % 8 != 0)) return CSA2_ERR_INVALID_ARG;
+  const __int128 last = __int128(n - 1) * (n > 1 ? x_stride : 0) + kDqk;
+  if (last > (__int128(1) << 59) || cache_rows > (int64_t(1) << 49)) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (overlap(x, last * 2, kv, __int128(cache_rows) * kDqk * 2)) return CSA2_ERR_INVALID_ARG;
+  WindowAppendArgs a = {};
+  a.cfg = *r;
+  a.x = x;
+  a.n = n;
+  a.x_stride = n > 1 ? x_stride : 0;
+  a.norm_w = norm_w;
+  a.eps = eps;
+  a.pos = pos;
+  a.dst_rows = dst_rows;
+  a.kv = kv;
+  a.cache_rows = cache_rows;
+  return from_cuda(launch_window_append(a, as_stream(stream)));
+}
+
+csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const void* x, int64_t n, int64_t x_stride,
+                              int32_t offset, int32_t norm, const void* norm_w, const void* norm_b, float eps,
+                              const int32_t* pos, const int64_t* dst_rows, void* idx_k, int64_t cache_rows,
+                              void* stream) {
+  csa2_status st = r ? check_rope(r) : CSA2_OK;
+  if (st != CSA2_OK) return st;
+  if (idx_k_dtype != CSA2_IDXK_E4M3 && idx_k_dtype != CSA2_IDXK_F32 && idx_k_dtype != CSA2_IDXK_FP4) return CSA2_ERR_INVALID_ARG;
+  if (norm < CSA2_IDX_NORM_NONE || norm > CSA2_IDX_NORM_LAYER) return CSA2_ERR_INVALID_ARG;
+  const int64_t dim = idx_k_dtype == CSA2_IDXK_F32 ? 64 : 128, size = idx_k_dtype == CSA2_IDXK_F32 ? 4 : 2;
+  if (offset < 0 || int64_t(offset) + (r ? r->rot : 0) > dim || (!r && offset != 0)) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (n < 0 || cache_rows < 0) return CSA2_ERR_INVALID_ARG;
+  // from 2^-40 on eps needs no scaling of small rows: squares that fp32 loses are nothing beside it
+  if (norm != CSA2_IDX_NORM_NONE ? !norm_w || !(eps >= 9.094947017729282e-13f && eps <= 1.0f) : norm_w != nullptr)
+    return CSA2_ERR_INVALID_ARG;
+  if (norm_b && norm != CSA2_IDX_NORM_LAYER) return CSA2_ERR_INVALID_ARG;
+  if (n == 0) return CSA2_OK;
+  if (!x || (r && !pos) || !dst_rows || !idx_k) return CSA2_ERR_INVALID_ARG;
+  if (!is_aligned(x, 16) || !is_aligned(idx_k, 16) || (pos && !is_aligned(pos, 4)) || !is_aligned(dst_rows, 8) ||
+      (norm_w && !is_aligned(norm_w, 16)) || (norm_b && !is_aligned(norm_b, 16)))
+    return CSA2_ERR_INVALID_ARG;
+  if (n > 1 && (x_stride < dim || x_stride % (16 / size) != 0)) return CSA2_ERR_INVALID_ARG;
+  const __int128 last = __int128(n - 1) * (n > 1 ? x_stride : 0) + dim;
+  if (last > (__int128(1) << 59) || cache_rows > (int64_t(1) << 49)) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  const int64_t row = idx_k_dtype == CSA2_IDXK_F32 ? 256 : idx_k_dtype == CSA2_IDXK_FP4 ? 72 : 128;
+  if (overlap(x, last * size, idx_k, __int128(cache_rows) * row)) return CSA2_ERR_INVALID_ARG;
+  IdxAppendArgs a = {};
+  a.rotate = r != nullptr;
+  if (r) a.cfg = *r;
+  a.kind = idx_k_dtype;
+  a.offset = offset;
+  a.norm = norm;
+  a.x = x;
+  a.n = n;
+  a.x_stride = n > 1 ? x_stride : 0;
+  a.norm_w = norm_w;
+  a.norm_b = norm_b;
+  a.eps = eps;
+  a.pos = r ? pos : nullptr;
+  a.dst_rows = dst_rows;
+  a.idx_k = idx_k;
+  a.cache_rows = cache_rows;
+  return from_cuda(launch_idx_append(a, as_stream(stream)));
+}
+
+csa2_status csa2_window_attn_workspace_size(const csa2_dims* d, int32_t batch, int64_t total_q, size_t* bytes) {
+  if (!bytes) return CSA2_ERR_INVALID_ARG;
+  const csa2_status st = check_dense_dims(d, batch, total_q);
+  if (st != CSA2_OK) return st;
+  *bytes = size_t(make_window_layout().total);
+  return CSA2_OK;
+}
+
+csa2_status csa2_window_attn_chunk(const csa2_dims* d, int32_t batch, int64_t total_q, const uint16_t* q,
+                                   const int32_t* q_start, const uint16_t* kv, const int32_t* page_table,
+                                   const int32_t* ctx_len, float scale, int32_t window, int32_t sinks,
+                                   const uint16_t* prev_out, const float* prev_lse, uint16_t* out, float* lse,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  csa2_status st = check_dense_dims(d, batch, total_q);
+  if (st != CSA2_OK) return st;
+  if (window < 1 || sinks < 0 || !std::isfinite(scale) || (prev_out == nullptr) != (prev_lse == nullptr))
+    return CSA2_ERR_INVALID_ARG;
+  if (window > kMaxCtx || sinks > kMaxCtx) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_paging(d, page_table)) != CSA2_OK) return st;
+  if (!ws || !is_aligned(ws, 256)) return CSA2_ERR_INVALID_ARG;
+  const WindowLayout L = make_window_layout();
+  if (ws_bytes < size_t(L.total)) return CSA2_ERR_WORKSPACE_TOO_SMALL;
+  // the cache is addressed by 32-bit row coordinates, and one row behind it (read as zeros)
+  const __int128 rows = page_table ? __int128(d->num_pages) * kPage : __int128(batch) * d->max_ctx;
+  if (rows > INT32_MAX) return CSA2_ERR_UNSUPPORTED_SHAPE;
+  if (batch == 0 || total_q == 0) return CSA2_OK;
+  if (!q || !q_start || !kv || !ctx_len || !out || !lse) return CSA2_ERR_INVALID_ARG;
+  if (!is_aligned(q, 16) || !is_aligned(q_start, 4) || !is_aligned(kv, 16) || !is_aligned(ctx_len, 4) ||
+      !is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(prev_out, 16) || !is_aligned(prev_lse, 4))
+    return CSA2_ERR_INVALID_ARG;
+  const __int128 n = __int128(total_q) * d->heads;
+  if (overlap(out, n * kLatent * 2, q, n * kDqk * 2) || overlap(out, n * kLatent * 2, kv, rows * kDqk * 2) ||
+      (prev_out && prev_out != out && overlap(out, n * kLatent * 2, prev_out, n * kLatent * 2)) ||
+      (prev_lse && prev_lse != lse && overlap(lse, n * 4, prev_lse, n * 4)))
+    return CSA2_ERR_INVALID_ARG;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  WindowArgs a = {};
+  a.d = *d;
+  a.batch = batch;
+  a.total_q = int(total_q);
+  a.window = window;
+  a.sinks = sinks;
+  a.q = q;
+  a.q_start = q_start;
+  a.kv = kv;
+  a.page_table = page_table;
+  a.ctx_len = ctx_len;
+  a.scale = scale;
+  a.prev_out = prev_out;
+  a.prev_lse = prev_lse;
+  a.out = out;
+  a.lse = lse;
+  a.ws = w;
+  a.head = reinterpret_cast<int*>(w + L.head);
+  a.tiles = reinterpret_cast<int2*>(w + L.tiles);
+  a.part_lse = reinterpret_cast<float*>(w + L.part_lse);
+  a.part_o = reinterpret_cast<float*>(w + L.part_o);
+  return from_cuda(launch_window(a, as_stream(stream)));
 }
 
 }  // extern "C"

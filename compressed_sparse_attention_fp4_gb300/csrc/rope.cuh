@@ -70,8 +70,8 @@ inline csa2_status check_rope(const csa2_rope* r) {
 // is taken to within an eighth of a turn of a multiple of a quarter, where the Taylor
 // series about 0 to the 9th and 8th power are right to 2.5e-8 (the first terms left out,
 // (pi/4)^11 / 11! and (pi/4)^10 / 10!).
-__device__ inline float2 rope_cs(const RopeTable& t, int i, int32_t pos) {
-  const uint32_t a = uint32_t((uint64_t(int64_t(pos)) * t.turn[i]) >> 32);      // modulo one turn
+__device__ inline float2 rope_cs(uint64_t turn, float mscale, int32_t pos) {
+  const uint32_t a = uint32_t((uint64_t(int64_t(pos)) * turn) >> 32);           // modulo one turn
   const uint32_t q = (a + 0x20000000u) >> 30;                                    // nearest quarter
   const float x = float(int32_t(a - (q << 30))) * 1.4629180792671596e-9f;        // 2 pi / 2^32
   const float z = x * x;
@@ -79,7 +79,8 @@ __device__ inline float2 rope_cs(const RopeTable& t, int i, int32_t pos) {
   const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
   // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
   const float u = (q & 1) ? s : c, v = (q & 1) ? c : s;
-  return make_float2(((q + 1) & 2) ? -u * t.mscale : u * t.mscale, (q & 2) ? -v * t.mscale : v * t.mscale);
+  return make_float2(((q + 1) & 2) ? -u * mscale : u * mscale, (q & 2) ? -v * mscale : v * mscale);
 }
+__device__ inline float2 rope_cs(const RopeTable& t, int i, int32_t pos) { return rope_cs(t.turn[i], t.mscale, pos); }
 
 }  // namespace csa2

@@ -475,6 +475,78 @@ csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t tot
                                   float scale, int32_t window, int32_t flags, uint16_t* out, float* lse, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* Append of exact rows: row i of x (bf16, x + i * x_stride, 576 channels: 512 latent, then 64
+ * rotary) is normed and rotated as by csa2_kv_append and written in bf16, unquantized, to row
+ * dst_rows[i] of the window cache kv (bf16 [cache_rows][576]: what csa2_window_attn_chunk reads;
+ * positions map to rows as elsewhere, by a page table or b * max_ctx + t).  A row whose destination
+ * is negative or not below cache_rows is skipped.  Destinations must differ from each other.
+ * For a decode step of csa2_sparse_attn_decode, whose window is swa_kv [B][W][576] in any order:
+ * write position t to row b * W + t % W.
+ *   x, norm_w, eps, pos, dst_rows, r: as csa2_kv_append;  kv: 16-byte aligned, no part of it
+ *   within x
+ * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (rot != 64), CSA2_ERR_CUDA. */
+csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n, int64_t x_stride,
+                               const uint16_t* norm_w, float eps, const int32_t* pos, const int64_t* dst_rows,
+                               uint16_t* kv, int64_t cache_rows, void* stream);
+
+/* Append of indexer keys: row i of x is normed, rotated and written to row dst_rows[i] of the
+ * indexer-K cache in one pass.
+ *   idx_k_dtype: csa2_idxk_dtype.  CSA2_IDXK_E4M3, CSA2_IDXK_FP4: x bf16, 128 channels;
+ *     CSA2_IDXK_F32: x fp32, 64 channels.
+ *   norm: CSA2_IDX_NORM_NONE; CSA2_IDX_NORM_RMS, x w / sqrt(mean(x^2) + eps);
+ *     CSA2_IDX_NORM_LAYER, (x - mean) w / sqrt(mean((x - mean)^2) + eps) + b
+ *   r: rotary on channels [offset, offset + r->rot) of the normed row (r->rot + offset at most its
+ *     channels), or NULL: none (then pos may be NULL and offset is 0)
+ *   key: E4M3, rounded to nearest even, saturating at 448; FP4, the bytes that
+ *     fp4_idx_k_quantize_scatter forms of the row rounded to bf16; fp32.  All before it is fp32.
+ *   x: 16-byte aligned, row stride x_stride a multiple of 16 bytes and at least a row for n > 1
+ *   norm_w, norm_b: device, of x's type and channels, 16-byte aligned; norm_w NULL without a norm,
+ *     norm_b with CSA2_IDX_NORM_LAYER only, or NULL
+ *   eps: 2^-40 .. 1 with a norm;  pos: device int32 [n];  dst_rows: device int64 [n], as above
+ *   idx_k, cache_rows: the indexer-K buffer (16-byte aligned) and its rows, no part of it within x
+ * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (offset, rot), CSA2_ERR_CUDA. */
+typedef enum { CSA2_IDX_NORM_NONE = 0, CSA2_IDX_NORM_RMS = 1, CSA2_IDX_NORM_LAYER = 2 } csa2_idx_norm;
+csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const void* x, int64_t n, int64_t x_stride,
+                              int32_t offset, int32_t norm, const void* norm_w, const void* norm_b, float eps,
+                              const int32_t* pos, const int64_t* dst_rows, void* idx_k, int64_t cache_rows,
+                              void* stream);
+
+/* Attention of a chunk of new tokens over a sliding window of exact bf16 rows, with the first
+ * positions that stay visible (sinks).  Queries and sequences are packed as for
+ * csa2_dense_attn_chunk; token i (0-based, of n) of sequence b stands at p = ctx_len[b] - n + i and
+ * sees the positions t <= p with t > p - window or t < sinks (each once).  With kv_t the row of
+ * position t, for each head:
+ *   logit_t = scale * q . kv_t,  out = sum_t softmax(logit)_t kv_t[0..511],  lse = ln sum_t exp(logit_t);
+ *   a token that sees nothing: out 0, lse -inf.
+ * With prev_out and prev_lse, what another attention over other rows gave the same queries (the
+ * layer's FP4 entries, by csa2_dense_attn_chunk), out and lse are those of one softmax over both:
+ *   lse = ln(e^lse_own + e^prev_lse),  out = e^(lse_own - lse) out_own + e^(prev_lse - lse) prev_out.
+ * The new tokens' own rows have been written before (csa2_window_append).  Rows and pages that no new
+ * token sees are not read: a page table may hold anything there, and pages may come round (a ring).
+ *   Dimensions read: heads, max_ctx, max_pages, num_pages (the window cache's own).
+ *   q, q_start, ctx_len, out, lse: as csa2_dense_attn_chunk, out and lse not within q or kv
+ *   kv:        device bf16 [rows][576], 16-byte aligned; rows and page_table as elsewhere (rows =
+ *              batch * max_ctx, or num_pages * 64).  A position whose page id is out of range is
+ *              skipped and reported.
+ *   prev_out, prev_lse: device, as out and lse; both or neither; out and lse themselves (joined in
+ *              place) or buffers apart from them
+ *   window:    1 .. 2^20 positions;  sinks: 0 .. 2^20
+ *   ws:        workspace of csa2_window_attn_workspace_size bytes, its first 256 the error word as
+ *              elsewhere.  Calls that may run at the same time need a workspace each.
+ *   A q_start that falls back or leaves 0 .. total_q is reported and the call writes nothing.
+ *   An infinity or a NaN in a row reaches only the outputs of tokens that see it (all their channels
+ *   may then be NaN), in a query only that token and head.
+ *   P is rounded to bf16 (2^-8) and the output to bf16; everything between is fp32.
+ * Results do not change from call to call.  Limits: total_q * H <= 2^30, batch <= 2^20, rows < 2^31.
+ * Make the first call on a device before any stream capture.
+ * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE, CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
+csa2_status csa2_window_attn_workspace_size(const csa2_dims* d, int32_t batch, int64_t total_q, size_t* bytes);
+csa2_status csa2_window_attn_chunk(const csa2_dims* d, int32_t batch, int64_t total_q, const uint16_t* q,
+                                   const int32_t* q_start, const uint16_t* kv, const int32_t* page_table,
+                                   const int32_t* ctx_len, float scale, int32_t window, int32_t sinks,
+                                   const uint16_t* prev_out, const float* prev_lse, uint16_t* out, float* lse,
+                                   void* ws, size_t ws_bytes, void* stream);
+
 /* Kernel timing, a tracing aid.  While enabled, the library brackets every
  * kernel it launches with a pair of CUDA events on the launching stream
  * (not for use during stream capture).  Enabling (or disabling) clears the
