@@ -26,34 +26,35 @@ namespace csa2 {
 namespace {
 
 constexpr int kRowWarps = 8;                         // softmax and outputs: lane quarter w % 4, half of the rows w / 4
-constexpr int kMmaWarp = kRowWarps;                  // the last warp copies
-constexpr int kWinThreads = (kRowWarps + 2) * 32;
+constexpr int kMmaWarp = kRowWarps;
+constexpr int kGroups = 5;                           // channel groups, a copying warp each: 4 x 128 latent, 64 rope
+constexpr int kLoadWarp0 = kMmaWarp + 1;
+constexpr int kWinThreads = (kLoadWarp0 + kGroups) * 32;
 
 constexpr int kKReg = kWinPos * 128;                 // 64 channels of a block's positions: 16 KB
 constexpr int kQReg = kWinRows * 128;                // 64 channels of a tile's rows: 8 KB
 constexpr int kKBytes = 9 * kKReg, kQBytes = 9 * kQReg;
-constexpr int kPOff = 8 * kKReg;                     // P takes the place of the block's rope channels
-constexpr int kQOff = kKBytes, kStageOff = kQOff + kQBytes;
-constexpr int kStageWarp = 8 * 64;                   // 8 rows x 32 channels of outputs
-constexpr int kWinSmem = kStageOff + kRowWarps * kStageWarp;
-constexpr int kGroups = 5;                           // channel groups of a block: 4 x 128 latent, 64 rope
+constexpr int kPHalf = 64 * 128;                     // P of 64 positions: 8 KB
+constexpr int kQOff = kKBytes, kPOff = kQOff + kQBytes;
+constexpr int kWinSmem = kPOff + kPHalf;
 constexpr uint32_t kOCol = 64;                       // tensor memory: S^T 64 columns, O^T 4 x 64
 constexpr uint32_t kCols = 512;
 constexpr int kMinSplit = 3;                         // least blocks a tile's positions are split from
 
 struct WinSmall {
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, q8_full, q8_empty;       // queries: latent channels, rope channels
   uint64_t k_full[kGroups], k_empty[kGroups];
   uint64_t s_full, p_full, o_full, o_empty, drain;
   uint32_t tmem_slot;
   int abort;
   int bad;                                           // q_start out of order
+  uint32_t hidden;                                   // 1 + the last block in which hide_values has changed the places
   int tiles, blocks;                                 // tiles of the call; most blocks of one
-  __align__(16) float ref[kRowWarps][32];            // softmax reference of the warp's rows, for all its lanes
-  __align__(16) float alpha[kRowWarps][32];
-  __align__(16) int pos[kRowWarps][32];              // positions of the warp's rows (-1: no such row)
-  __align__(16) float top[2][4][kWinRows];           // maxima of a block by lane quarter
-  __align__(16) float sum[4][kWinRows];
+  // of the rows of a half, for all lanes of its four warps, which write the same values
+  __align__(16) float ref[2][32];                    // softmax reference
+  __align__(16) float alpha[2][32];
+  __align__(16) int pos[2][32];                      // positions (-1: no such row)
+  __align__(16) float top[2][4][kWinRows];           // maxima of a block by lane quarter; sums at the end
 };
 static_assert(kWinSmem + (sizeof(WinSmall) + 1023) / 1024 * 1024 <= 232448, "shared memory; the dynamic part starts on a multiple of its alignment");
 
@@ -89,23 +90,14 @@ __device__ inline bool elect_one() {
 }
 __device__ inline void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// Four rows of a tensor map, 64 channels each (the map's box is one row high).
-__device__ inline void tma_gather4(const CUtensorMap* map, uint32_t dst, int x, int4 y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(tc::smem_u32(bar))
-      : "memory");
-}
+struct WindowMaps {
+  CUtensorMap q;
+  CUtensorMap kv[7];                                 // boxes of 64 channels x 2^i rows
+};
 
 __device__ inline float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ inline float max_over_warp(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ inline uint32_t bf16x2_rn(float lo, float hi) {
@@ -114,18 +106,37 @@ __device__ inline uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
-// 32 values a lane summed over the warp: lane l gets the sum of value l (31 shuffles).
-__device__ inline float butterfly_sum(float (&v)[32], int lane) {
+// 32 values a lane reduced over the warp: lane l gets the sum or maximum of value l (31 shuffles; 130
+// cycles, where 32 reductions by redux take 2,950).
+template <bool kMax>
+__device__ inline float butterfly(const float (&x)[32], int lane) {
+  float v[16];
 #pragma unroll
   for (int half = 16; half >= 1; half >>= 1) {
     const bool up = lane & half;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
-      const float keep = up ? v[half + i] : v[i], give = up ? v[i] : v[half + i];
-      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half);
+      const float lo = half == 16 ? x[i] : v[i], hi = half == 16 ? x[half + i] : v[half + i];
+      const float keep = up ? hi : lo, give = up ? lo : hi;
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, give, half);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
   return v[0];
+}
+
+// One step of a transposition: register bit K goes to lane bit B and back.
+template <int N, int K, int B, typename T>
+__device__ inline void exchange(T (&v)[N], int lane) {
+  const bool up = lane >> B & 1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i & K) continue;
+    const T give = up ? v[i] : v[i | K];
+    const T got = __shfl_xor_sync(0xFFFFFFFFu, give, 1 << B);
+    if (up) v[i] = got;
+    else v[i | K] = got;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -138,68 +149,78 @@ __device__ inline int context(const WindowArgs& a, int b) {
 }
 __device__ inline int tiles_of(const WindowArgs& a, int len) { return (len * a.d.heads + kWinRows - 1) / kWinRows; }
 
-// One piece of a tile's work: what its rows see, as a list of positions (first the sinks
-// that the window has left behind, then the window of all its tokens), cut into blocks of 128.
+// One piece of a tile's work.  Its tokens see the positions lo .. last and the sinks before lo.
+//   Compact calls (`compact`, below): all of them fit a block of 128 places.  Position t has place
+//     t (t < sinks) or sinks + (t - sinks) % (128 - sinks), so that the rows of consecutive tiles
+//     stay where they are and a tile's new positions take the places of those that the window has left.
+//   Other calls: whole pages of 64 positions, the sinks' (sp of them) and then the window's, two a block.
 struct Piece {
   int seq, from, len, ctx;      // sequence: first query token, query tokens, context
   int row0;                     // first row in the sequence
-  int lo, ns, nv;               // first position of the window; sinks before it; positions of the list
+  int lo, last;
+  int sp, np;
   int blk, n;                   // blocks of this piece
-  __device__ int pos(int v) const { return v < ns ? v : lo + v - ns; }     // of list entry v < nv
 };
 
+// Position of place e of block j of a piece (-1: none).
+__device__ inline int place_position(const WindowArgs& a, const Piece& p, int j, int e) {
+  if (a.compact) {
+    if (e < a.sinks) return e <= p.last ? e : -1;
+    const int c = kWinPos - a.sinks, d = (p.last - a.sinks) % c - (e - a.sinks);      // places from e on to the last position's
+    const int t = p.last - (d < 0 ? d + c : d);
+    return t >= max(p.lo, a.sinks) ? t : -1;
+  }
+  const int i = 2 * (p.blk + j) + (e >> 6);
+  const int t = (i < p.sp ? i : p.lo / kPage + i - p.sp) * kPage + (e & (kPage - 1));
+  return i < p.np && t <= p.last ? t : -1;
+}
+
+// A warp's way through the tiles.  It keeps 32 sequences, one a lane.
 struct Walk {
   const WindowArgs& a;
-  int b, base, nt, from, len, lane;                  // sequence, tiles before it, its tiles
-  __device__ Walk(const WindowArgs& args, int l) : a(args), b(-1), base(0), nt(0), from(0), len(0), lane(l) {}
-  // Goes on to the sequence of tile t (not before the present one), 32 sequences at a time.
-  __device__ bool seek(int t) {
-    if (t < base + nt) return true;
-    int at = base + nt;
-    for (int b0 = b + 1; b0 < a.batch; b0 += 32) {
-      const int i = b0 + lane;
-      int f = 0, l = 0, k = 0;
-      if (i < a.batch) {
-        f = __ldg(a.q_start + i);
-        l = __ldg(a.q_start + i + 1) - f;
-        k = tiles_of(a, l);
-      }
-      int x = k;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, at + x > t);
-      if (past) {
-        const int w = __ffs(past) - 1;
-        b = b0 + w;
-        nt = __shfl_sync(0xFFFFFFFFu, k, w);
-        base = at + __shfl_sync(0xFFFFFFFFu, x, w) - nt;
-        from = __shfl_sync(0xFFFFFFFFu, f, w);
-        len = __shfl_sync(0xFFFFFFFFu, l, w);
-        return true;
-      }
-      at += __shfl_sync(0xFFFFFFFFu, x, 31);
+  int lane;
+  int b0, base;                                      // first sequence kept, tiles before it
+  int from, len, ctx, upto;                          // the lane's sequence; tiles up to its end from b0 on
+  __device__ Walk(const WindowArgs& args, int l) : a(args), lane(l), b0(0), base(0) { load(); }
+  __device__ void load() {
+    const int i = b0 + lane;
+    from = len = ctx = upto = 0;
+    if (i < a.batch) {
+      from = __ldg(a.q_start + i);
+      len = __ldg(a.q_start + i + 1) - from;
+      ctx = context(a, i);
+      upto = tiles_of(a, len);
     }
-    return false;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
   }
-  // Piece s of n of tile t.
+  // Piece s of n of tile t (not before the one asked for last); false behind the last.
   __device__ bool piece(int t, int s, int n, Piece& p) {
-    if (!seek(t)) return false;
-    p.seq = b;
-    p.from = from;
-    p.len = len;
-    p.ctx = context(a, b);
-    p.row0 = (t - base) * kWinRows;
-    const int tok0 = p.row0 / a.d.heads, tok1 = min(len - 1, (p.row0 + kWinRows - 1) / a.d.heads);
-    const int last = p.ctx - len + tok1;
-    p.lo = max(0, p.ctx - len + tok0 - a.window + 1);
-    p.ns = min(a.sinks, p.lo);
-    p.nv = last < 0 ? 0 : p.ns + last + 1 - p.lo;
-    const int nb = (p.nv + kWinPos - 1) / kWinPos;
-    p.blk = nb * s / n;
-    p.n = nb * (s + 1) / n - p.blk;
+    uint32_t past;
+    while ((past = __ballot_sync(0xFFFFFFFFu, base + upto > t)) == 0) {
+      base += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      b0 += 32;
+      if (b0 >= a.batch) return false;
+      load();
+    }
+    const int w = __ffs(past) - 1;
+    p.seq = b0 + w;
+    p.from = __shfl_sync(0xFFFFFFFFu, from, w);
+    p.len = __shfl_sync(0xFFFFFFFFu, len, w);
+    p.ctx = __shfl_sync(0xFFFFFFFFu, ctx, w);
+    const int before = __shfl_sync(0xFFFFFFFFu, upto, max(w - 1, 0));
+    p.row0 = (t - base - (w > 0 ? before : 0)) * kWinRows;
+    const int tok0 = p.row0 / a.d.heads, tok1 = min(p.len - 1, (p.row0 + kWinRows - 1) / a.d.heads);
+    p.last = p.ctx - p.len + tok1;
+    p.lo = max(0, p.ctx - p.len + tok0 - a.window + 1);
+    p.sp = min((a.sinks + kPage - 1) / kPage, p.lo / kPage);
+    p.np = p.last < 0 ? 0 : p.sp + p.last / kPage - p.lo / kPage + 1;
+    const int nb = a.compact ? p.last >= 0 : (p.np + 1) / 2;
+    p.blk = n == 1 ? 0 : nb * s / n;
+    p.n = n == 1 ? nb : nb * (s + 1) / n - p.blk;
     return true;
   }
 };
@@ -217,7 +238,7 @@ __device__ inline int row_of(const WindowArgs& a, int seq, int t) {
 // The position's values, if an infinity or NaN is among them, become 0: its weight in the rows that
 // do not see it is 0, and so must be 0 times its values.  The rows that do see it are NaN by its
 // score, which holds the same channels.
-__device__ __noinline__ void hide_values(uint8_t* base, int e) {
+__device__ __noinline__ void hide_values(WinSmall& sm, uint8_t* base, int e, uint32_t block) {
   bool whole = true;
 #pragma unroll 1
   for (int c = 0; c < 64; ++c) {
@@ -227,6 +248,7 @@ __device__ __noinline__ void hide_values(uint8_t* base, int e) {
     for (int i = 0; i < 4; ++i) whole = whole && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
   }
   if (whole) return;
+  *reinterpret_cast<volatile uint32_t*>(&sm.hidden) = block + 1;
 #pragma unroll 1
   for (int c = 0; c < 64; ++c)
     *reinterpret_cast<uint4*>(base + (c >> 3) * kKReg + tc::sw128_offset(e, c & 7)) = make_uint4(0, 0, 0, 0);
@@ -236,58 +258,137 @@ struct Span {
   int first, units, step, pieces;                    // the CTA's units: first, first + step, ... below units
 };
 
-// Copies queries and cache rows.  A lane has four rows of a block.
-__device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int lane,
-                                 const CUtensorMap* qmap, const CUtensorMap* kmap) {
+// A box of 2^lg rows (lg -1: none) from cache row `row` on, for the places from `slot` on.
+struct Box {
+  int slot, row, lg;
+};
+
+// The positions first .. last of a compact tile as boxes, one a lane from lane `k` on: runs of
+// rows, cut at pages and where the places come round, in powers of two (a tile has at most 6 runs
+// of 128 rows together: at most 23 boxes).  `page`: lane i has the page ids of the first two pages
+// (lanes 0, 1) and of the window's (lanes 2 .. 5).  Returns their rows.
+__device__ inline int boxes(const WindowArgs& a, const Piece& p, int first, int last, int page, int lane, int& k, Box& mine,
+                            bool& lost) {
+  int rows = 0;
+  for (int t = first; t <= last;) {
+    const int at = t / kPage;
+    int slot = t < a.sinks ? t : a.sinks + (t - a.sinks) % (kWinPos - a.sinks);
+    int n = min(last - t + 1, kWinPos - slot), row;
+    if (a.page_table) {
+      n = min(n, kPage - t % kPage);
+      const int pg = __shfl_sync(0xFFFFFFFFu, page, at < 2 ? at : 2 + at - p.lo / kPage);
+      row = pg < 0 || pg >= a.d.num_pages ? -1 : pg * kPage + t % kPage;
+    } else {
+      row = int(int64_t(p.seq) * a.d.max_ctx + t);
+    }
+    t += n;
+    if (row < 0) {
+      lost = true;
+      continue;
+    }
+    rows += n;
+    while (n > 0) {
+      const int lg = min(6, 31 - __clz(n));
+      if (k == lane) mine = {slot, row, lg};
+      ++k;
+      slot += 1 << lg;
+      row += 1 << lg;
+      n -= 1 << lg;
+    }
+  }
+  return rows;
+}
+// What a compact tile sees from position `from` on.
+__device__ inline int tile_boxes(const WindowArgs& a, const Piece& p, int from, int lane, Box& mine, bool& lost) {
+  int page = -1, k = 0;
+  if (a.page_table && lane < 6) {
+    const int i = lane < 2 ? lane : p.lo / kPage + lane - 2;
+    if (i < a.d.max_pages && i * kPage <= p.last) page = __ldg(a.page_table + int64_t(p.seq) * a.d.max_pages + i);
+  }
+  mine.lg = -1;
+  const int rows = boxes(a, p, from, min(a.sinks - 1, p.last), page, lane, k, mine, lost);
+  return rows + boxes(a, p, max(from, max(p.lo, a.sinks)), p.last, page, lane, k, mine, lost);
+}
+
+// Where P of a block's first and last 64 positions goes: over the block's rope channels, which only
+// the scores need; in a compact call, whose rows stay, into a place of its own and over the queries'
+// rope channels, which no other block of the tile needs.
+__device__ inline uint32_t p_offset(const WindowArgs& a, int half) {
+  return a.compact ? (half == 0 ? kPOff : kQOff + 8 * kQReg) : 8 * kKReg + half * kPHalf;
+}
+
+// Copies channel group g of the queries and the cache rows.  (One warp for all groups takes 650 cycles
+// for the few copies of one: what it waits for is the issue, not the copies.)
+__device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int g, int lane,
+                                 const WindowMaps& m) {
   Walk walk(a, lane);
   Piece p;
-  const int none = int(a.page_table ? a.d.num_pages * kPage : int64_t(a.batch) * a.d.max_ctx);   // a row outside: zeros
-  const uint32_t k0 = tc::smem_u32(base) + lane * 512;
   uint32_t nq = 0, nk = 0;
+  int was_seq = -1, was_last = 0;                    // what the places hold
+  const int regions = g < 4 ? 2 : 1;
+  uint64_t* q_full = g < 4 ? &sm.q_full : &sm.q8_full;
+  uint64_t* q_empty = g < 4 ? &sm.q_empty : &sm.q8_empty;
   for (int u = w.first; u < w.units; u += w.step) {
     if (!walk.piece(u / w.pieces, u % w.pieces, w.pieces, p)) return;
+    if (p.n == 0) continue;
+    // a compact tile's boxes: what the tile before has not left there, or all of it
+    Box box;
+    int rows = 0;
+    bool lost = false;
+    if (a.compact) {
+      rows = tile_boxes(a, p, p.seq == was_seq ? was_last + 1 : 0, lane, box, lost);
+      was_seq = p.seq;
+      was_last = p.last;
+    }
     for (int j = 0; j < p.n; ++j, ++nk) {
-      int y[4];
-      bool lost = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int v = (p.blk + j) * kWinPos + 4 * lane + i;
-        y[i] = none;
-        if (v < p.nv) {
-          const int r = row_of(a, p.seq, p.pos(v));
-          if (r >= 0) y[i] = r;
-          else lost = true;
+      int row = -1;                                  // lane's half of the block (lane & 1)
+      if (!a.compact) {
+        const int t = place_position(a, p, j, kPage * (lane & 1));
+        if (t >= 0) {
+          row = row_of(a, p.seq, t);
+          lost = row < 0;
         }
       }
-      if (lost) raise_err(a.ws, CSA2_DEV_PAGE_ID);
+      if (g == 0 && lost) raise_err(a.ws, CSA2_DEV_PAGE_ID);
       if (j == 0) {
-        if (!wait_warp(sm, &sm.q_empty, (nq & 1) ^ 1, a.ws)) return;
-        if (lane == 0) tc::mbar_expect_tx(&sm.q_full, kQBytes);
+        if (!wait_warp(sm, q_empty, (nq & 1) ^ 1, a.ws)) return;
+        if (lane == 0) tc::mbar_expect_tx(q_full, uint32_t(regions * kQReg));
         __syncwarp();
-        if (lane < 9)
-          tc::tma_load_2d(qmap, base + kQOff + lane * kQReg, 64 * lane, p.from * a.d.heads + p.row0, &sm.q_full);
+        if (lane < regions)
+          tc::tma_load_2d(&m.q, base + kQOff + (2 * g + lane) * kQReg, 64 * (2 * g + lane), p.from * a.d.heads + p.row0, q_full);
         ++nq;
       }
-#pragma unroll 1
-      for (int g = 0; g < kGroups; ++g) {
-        if (!wait_warp(sm, &sm.k_empty[g], (nk & 1) ^ 1, a.ws)) return;
-        const int regions = g < 4 ? 2 : 1;
-        if (lane == 0) tc::mbar_expect_tx(&sm.k_full[g], uint32_t(regions * kKReg));
+      if (!wait_warp(sm, &sm.k_empty[g], (nk & 1) ^ 1, a.ws)) return;
+      if (a.compact) {
+        // values of the tile before may have been taken out of their places
+        if (g < 4 && nk > 0 && *reinterpret_cast<volatile uint32_t*>(&sm.hidden) == nk)
+          rows = tile_boxes(a, p, 0, lane, box, lost);
+        if (lane == 0) tc::mbar_expect_tx(&sm.k_full[g], uint32_t(regions * rows * 128));
         __syncwarp();
-        for (int r = 2 * g; r < 2 * g + regions; ++r)
-          tma_gather4(kmap, k0 + r * kKReg, 64 * r, make_int4(y[0], y[1], y[2], y[3]), &sm.k_full[g]);
+        if (box.lg >= 0)
+          for (int r = 2 * g; r < 2 * g + regions; ++r)
+            tc::tma_load_2d(&m.kv[box.lg], base + r * kKReg + box.slot * 128, 64 * r, box.row, &sm.k_full[g]);
+      } else {
+        const int halves = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0) & 3u);
+        if (lane == 0) tc::mbar_expect_tx(&sm.k_full[g], uint32_t(regions * halves * (kKReg / 2)));
+        __syncwarp();
+        const int r = 2 * g + (lane >> 1);
+        if (lane < 2 * regions && row >= 0)
+          tc::tma_load_2d(&m.kv[6], base + r * kKReg + (lane & 1) * (kKReg / 2), 64 * r, row, &sm.k_full[g]);
       }
     }
   }
 }
 
-// Issues the products.
+// Issues the products.  The offsets are constants: a product takes 58 cycles, and formed at run time
+// they take longer than that.
 __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int lane, uint32_t tmem) {
   constexpr uint32_t id_s = tc::idesc_bf16(kWinPos, kWinRows, 0, 0);
   constexpr uint32_t id_o = tc::idesc_bf16(kWinPos, kWinRows, 1, 1);
-  const uint32_t k_at = tc::smem_u32(base);
-  const uint64_t ks = tc::smem_desc(k_at, 16, 1024, 2), qs = tc::smem_desc(k_at + kQOff, 16, 1024, 2);
-  const uint64_t vs = tc::smem_desc(k_at, kKReg, 1024, 2), ps = tc::smem_desc(k_at + kPOff, kKReg, 1024, 2);
+  const uint32_t at = tc::smem_u32(base);
+  const uint64_t ks = tc::smem_desc(at, 16, 1024, 2), qs = tc::smem_desc(at + kQOff, 16, 1024, 2);
+  const uint64_t vs = tc::smem_desc(at, kKReg, 1024, 2);
+  const uint64_t p0 = tc::smem_desc(at + p_offset(a, 0), kPHalf, 1024, 2), p1 = tc::smem_desc(at + p_offset(a, 1), kPHalf, 1024, 2);
   const bool leader = elect_one();
   Walk walk(a, lane);
   Piece p;
@@ -297,13 +398,14 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
     if (p.n == 0) continue;
     if (!wait_warp(sm, &sm.q_full, nq & 1, a.ws)) return;
     for (int j = 0; j < p.n; ++j, ++nk) {
-#pragma unroll 1
+#pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         if (!wait_warp(sm, &sm.k_full[g], nk & 1, a.ws)) return;
+        if (g == 4 && j == 0 && !wait_warp(sm, &sm.q8_full, nq & 1, a.ws)) return;
         tc::tc_fence_after_sync();
         if (leader) {
-          const int last = g < 4 ? 8 : 4;
-          for (int i = 0; i < last; ++i) {
+#pragma unroll
+          for (int i = 0; i < (g < 4 ? 8 : 4); ++i) {
             const uint32_t kb = 2 * g + (i >> 2), off = (i & 3) * 32;
             tc::mma_bf16(tmem, ks + ((kb * kKReg + off) >> 4), qs + ((kb * kQReg + off) >> 4), id_s, g + i > 0);
           }
@@ -312,21 +414,27 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       }
       if (leader) {
         tc::mma_commit(&sm.s_full);
-        if (j == p.n - 1) tc::mma_commit(&sm.q_empty);
+        if (a.compact) tc::mma_commit(&sm.k_empty[4]);
+        if (j == p.n - 1) {
+          tc::mma_commit(&sm.q_empty);
+          if (!a.compact) tc::mma_commit(&sm.q8_empty);
+        }
       }
       __syncwarp();
       if (!wait_warp(sm, &sm.p_full, nk & 1, a.ws)) return;
       if (j == 0 && !wait_warp(sm, &sm.o_empty, (nq & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
       if (leader) {
-#pragma unroll 1
+        const bool more = j > 0;
+#pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            tc::mma_bf16(tmem + kOCol + 64 * mt, vs + ((2 * mt * kKReg + k * 2048) >> 4), ps + ((k * 2048) >> 4), id_o, j + k > 0);
+            tc::mma_bf16(tmem + kOCol + 64 * mt, vs + ((2 * mt * kKReg + k * 2048) >> 4), (k < 4 ? p0 : p1) + (((k & 3) * 2048) >> 4),
+                         id_o, more || k > 0);
           tc::mma_commit(&sm.k_empty[mt]);
         }
-        tc::mma_commit(&sm.k_empty[4]);
+        tc::mma_commit(a.compact ? &sm.q8_empty : &sm.k_empty[4]);
         if (j == p.n - 1) tc::mma_commit(&sm.o_full);
       }
       __syncwarp();
@@ -335,9 +443,30 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
   }
 }
 
+// What a row warp has to know of a piece before its scores come.
+struct Ahead {
+  Piece p;
+  bool have;
+  int mine;                                          // position of the lane's row, -1: no such row
+  int t, row;                                        // position in the lane's place of the first block (-1: none), its row
+};
+__device__ inline void place_seen(const WindowArgs& a, const Piece& p, int j, int e, int& t, int& row) {
+  t = place_position(a, p, j, e);
+  row = t >= 0 ? row_of(a, p.seq, t) : -1;
+}
+__device__ inline void look_ahead(const WindowArgs& a, Walk& walk, const Span& w, int u, int half, int e, int lane, Ahead& n) {
+  n.have = u < w.units && walk.piece(u / w.pieces, u % w.pieces, w.pieces, n.p);
+  if (!n.have) return;
+  const int lr = n.p.row0 + 32 * half + lane;
+  n.mine = lr < n.p.len * a.d.heads ? n.p.ctx - n.p.len + lr / a.d.heads : -1;
+  if (n.p.n > 0) place_seen(a, n.p, 0, e, n.t, n.row);
+}
+
 // Softmax over a block's positions (tensor-memory lanes) and the outputs.  Warp rw has the
 // lanes 32 (rw % 4) .. + 31 and the rows 32 (rw / 4) .. + 31; lane i keeps the state of row i of
 // these (alike in the four warps of a half, but for the sum, which is of its own lanes).
+// Shared memory is the products': they take five sixths of its bandwidth, so values cross the lanes
+// by shuffles.
 // A wait that gives up leaves the warp in the loop, without waits or results: its hardware
 // barriers have no limit, and all eight warps pass the same ones.
 __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int rw, int lane,
@@ -345,25 +474,25 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
   const int quarter = rw & 3, half = rw >> 2, e = 32 * quarter + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(32 * half);
   const float c2 = a.scale * 1.4426950408889634f;
-  uint8_t* stage = base + kStageOff + rw * kStageWarp;
+  uint8_t* const p_at = base + p_offset(a, quarter >> 1);
   bool dead = false;
   Walk walk(a, lane);
-  Piece p;
+  Ahead now;
+  look_ahead(a, walk, w, w.first, half, e, lane, now);
   uint32_t nq = 0, nk = 0;
-  for (int u = w.first; u < w.units; u += w.step) {
-    if (!walk.piece(u / w.pieces, u % w.pieces, w.pieces, p)) return;
-    const int lr = p.row0 + 32 * half + lane, rows = p.len * a.d.heads;
-    const int mine = lr < rows ? p.ctx - p.len + lr / a.d.heads : -1;       // position of the lane's row
-    __syncwarp();
-    sm.pos[rw][lane] = mine;
+  for (int u = w.first; now.have; u += w.step) {
+    const Piece p = now.p;
+    const int mine = now.mine, rows = p.len * a.d.heads;
+    const int lr = p.row0 + 32 * half + lane;
+    sm.pos[half][lane] = mine;
     __syncwarp();
     const int p_max = __reduce_max_sync(0xFFFFFFFFu, mine);
     const int p_min = __reduce_min_sync(0xFFFFFFFFu, lr < rows ? mine : p_max);
     float ref = -INFINITY, sum = 0.0f;
+    int t = now.t, row = now.row;
     for (int j = 0; j < p.n; ++j, ++nk) {
-      const int v = (p.blk + j) * kWinPos + e;
-      int t = v < p.nv ? p.pos(v) : -1;
-      if (t >= 0 && row_of(a, p.seq, t) < 0) t = -1;
+      if (j > 0) place_seen(a, p, j, e, t, row);
+      if (row < 0) t = -1;
       const bool all = t >= 0 && t <= p_min && (t > p_max - a.window || t < a.sinks);
       const bool edge = !__all_sync(0xFFFFFFFFu, all);
       if (!dead && !wait_warp(sm, &sm.s_full, nk & 1, a.ws)) dead = true;
@@ -376,7 +505,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         bool odd = false;                            // some score of a row that does not see the position is no number
 #pragma unroll
         for (int i4 = 0; i4 < 8; ++i4) {
-          const int4 pr = reinterpret_cast<const int4*>(sm.pos[rw])[i4];
+          const int4 pr = reinterpret_cast<const int4*>(sm.pos[half])[i4];
           const int q4[4] = {pr.x, pr.y, pr.z, pr.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -387,14 +516,10 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
             x[i] = see ? (fine ? x[i] : NAN) : -INFINITY;
           }
         }
-        if (odd) hide_values(base, e);
+        if (odd) hide_values(sm, base, e, nk);
+        __syncwarp();
       }
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float m = max_over_warp(x[i]);
-        if (lane == i) top = m;
-      }
+      float top = butterfly<true>(x, lane);
       sm.top[nk & 1][quarter][32 * half + lane] = top;
       bar_sync(1 + half, 128);
 #pragma unroll
@@ -405,13 +530,13 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         if (ref != -INFINITY) alpha = ex2(ref - to);
         ref = to;
       }
-      sm.ref[rw][lane] = ref == -INFINITY ? 0.0f : ref;
+      sm.ref[half][lane] = ref == -INFINITY ? 0.0f : ref;
       const bool turn = __any_sync(0xFFFFFFFFu, alpha != 1.0f);
-      if (turn) sm.alpha[rw][lane] = alpha;
+      if (turn) sm.alpha[half][lane] = alpha;
       __syncwarp();
       if (turn) {
-        // the outputs so far to the new reference (the block's rope channels, which the scores
-        // waited for, came after the last product)
+        // the outputs so far to the new reference (this block's scores came after the last product: the
+        // copies that they needed waited for it)
         sum *= alpha;
 #pragma unroll 1
         for (int mt = 0; mt < 4; ++mt)
@@ -420,7 +545,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
             float o[8];
             tc::tmem_ld8(lanes + kOCol + 64 * mt + c, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= sm.alpha[rw][c + i];
+            for (int i = 0; i < 8; ++i) o[i] *= sm.alpha[half][c + i];
             tc::tmem_st8(lanes + kOCol + 64 * mt + c, o);
           }
       }
@@ -429,7 +554,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         uint32_t pk[4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float4 r4 = reinterpret_cast<const float4*>(sm.ref[rw])[2 * i8 + k];
+          const float4 r4 = reinterpret_cast<const float4*>(sm.ref[half])[2 * i8 + k];
           const int i = 8 * i8 + 4 * k;
           x[i] = ex2(x[i] - r4.x);
           x[i + 1] = ex2(x[i + 1] - r4.y);
@@ -438,24 +563,26 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
           pk[2 * k] = bf16x2_rn(x[i], x[i + 1]);
           pk[2 * k + 1] = bf16x2_rn(x[i + 2], x[i + 3]);
         }
-        *reinterpret_cast<uint4*>(base + kPOff + tc::sw128_offset(e, 4 * half + i8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4*>(p_at + tc::sw128_offset(e & 63, 4 * half + i8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive(&sm.p_full);
-      sum += butterfly_sum(x, lane);
+      sum += butterfly<false>(x, lane);
     }
+    look_ahead(a, walk, w, u + w.step, half, e, lane, now);
     // outputs: sums of the four lane quarters, joined with the other attention's
     const bool join = a.prev_out != nullptr && w.pieces == 1;
     const int64_t row0 = int64_t(p.from) * a.d.heads + p.row0 + 32 * half;
     float prev = -INFINITY;
     if (join && lr < rows) prev = a.prev_lse[row0 + lane];
-    sm.sum[quarter][32 * half + lane] = sum;
+    float (&sums)[4][kWinRows] = sm.top[nk & 1];     // (the other one may still be read)
+    sums[quarter][32 * half + lane] = sum;
     bar_sync(1 + half, 128);
     float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) total += sm.sum[k][32 * half + lane];
+    for (int k = 0; k < 4; ++k) total += sums[k][32 * half + lane];
     float own = total != 0.0f ? 1.0f / total : 0.0f, other = 0.0f;
     float lse = total != 0.0f ? ((ref == -INFINITY ? 0.0f : ref) + log2f(total)) * 0.6931471805599453f : -INFINITY;
     if (join && prev != -INFINITY) {
@@ -464,12 +591,25 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       other = x1 / (x0 + x1);
       lse = most + logf(x0 + x1);
     }
+    sm.ref[half][lane] = own;
+    // after the transposition a lane has 8 channels of the rows 8 k + lane % 8
+    const int ch = 32 * quarter + 8 * (lane >> 3);
+    const int64_t at = (row0 + (lane & 7)) * kLatent + ch;
+    const int left = rows - (p.row0 + 32 * half) - (lane & 7);              // row 8 k exists: 8 k < left
+    uint4 old[4];
+    float share[4];
+    if (join) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        share[k] = __shfl_sync(0xFFFFFFFFu, other, 8 * k + (lane & 7));
+        old[k] = make_uint4(0, 0, 0, 0);
+        if (share[k] != 0.0f && 8 * k < left) old[k] = *reinterpret_cast<const uint4*>(a.prev_out + at + 8 * k * kLatent);
+      }
+    }
     if (p.n > 0) {
       if (!dead && !wait_warp(sm, &sm.o_full, nq & 1, a.ws)) dead = true;
       tc::tc_fence_after_sync();
     }
-    sm.ref[rw][lane] = own;
-    sm.alpha[rw][lane] = other;
     __syncwarp();
     if (w.pieces > 1) {
       // a piece: its own softmax in fp32, for the merge
@@ -487,7 +627,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
             float* dst = a.part_o + (int64_t(u) * kWinRows + 32 * half) * kLatent + 128 * mt + e;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (p.row0 + 32 * half + i < rows) dst[i * kLatent] = o[i] * sm.ref[rw][i];
+              if (p.row0 + 32 * half + i < rows) dst[i * kLatent] = o[i] * sm.ref[half][i];
           }
         }
       }
@@ -498,38 +638,49 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         float o[32];
         if (p.n > 0) {
           tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
+#pragma unroll
+          for (int i4 = 0; i4 < 8; ++i4) {
+            const float4 f = reinterpret_cast<const float4*>(sm.ref[half])[i4];
+            o[4 * i4] *= f.x;
+            o[4 * i4 + 1] *= f.y;
+            o[4 * i4 + 2] *= f.z;
+            o[4 * i4 + 3] *= f.w;
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.0f;
         }
-        // 8 rows x 32 channels at a time through shared memory: 64 bytes of a row for four lanes
-        const int ch = 128 * mt + 32 * quarter + 8 * (lane & 3);
+        uint32_t y[16];                              // 4 rows of 8 channels
+        if (join) {
+          exchange<32, 1, 0>(o, lane);
+          exchange<32, 2, 1>(o, lane);
+          exchange<32, 4, 2>(o, lane);
 #pragma unroll
-        for (int i8 = 0; i8 < 4; ++i8) {
-          const int r = 8 * i8 + (lane >> 2);
-          const bool have = p.row0 + 32 * half + r < rows;
-          const int64_t at = (row0 + r) * kLatent + ch;
-          __syncwarp();
-          if (join) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (have) v = *reinterpret_cast<const uint4*>(a.prev_out + at);
-            *reinterpret_cast<uint4*>(stage + lane * 16) = v;
-            __syncwarp();
-          }
-          uint16_t* col = reinterpret_cast<uint16_t*>(stage) + lane;
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x[4] = {old[k].x, old[k].y, old[k].z, old[k].w};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int i = 8 * i8 + k;
-            float y = p.n > 0 ? o[i] * sm.ref[rw][i] : 0.0f;
-            if (join) {
-              const float f = sm.alpha[rw][i];
-              if (f != 0.0f) y = fmaf(f, bf16_to_f32(col[32 * k]), y);
-            }
-            col[32 * k] = uint16_t(bf16x2_rn(y, 0.0f));
+            for (int i = 0; i < 4; ++i)
+              y[4 * k + i] = bf16x2_rn(fmaf(share[k], __uint_as_float(x[i] << 16), o[8 * k + 2 * i]),
+                                       fmaf(share[k], __uint_as_float(x[i] & 0xFFFF0000u), o[8 * k + 2 * i + 1]));
+            // the next channels' come while these go
+            if (mt < 3 && share[k] != 0.0f && 8 * k < left)
+              old[k] = *reinterpret_cast<const uint4*>(a.prev_out + at + 8 * k * kLatent + 128 * (mt + 1));
           }
-          __syncwarp();
-          if (have) *reinterpret_cast<uint4*>(a.out + at) = *reinterpret_cast<const uint4*>(stage + lane * 16);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t z = bf16x2_rn(o[2 * i], o[2 * i + 1]);          // two rows of the lane's channel
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, z, 1);
+            y[i] = lane & 1 ? __byte_perm(got, z, 0x7632) : __byte_perm(z, got, 0x5410);
+          }
+          exchange<16, 1, 1>(y, lane);
+          exchange<16, 2, 2>(y, lane);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (8 * k < left)
+            *reinterpret_cast<uint4*>(a.out + at + 8 * k * kLatent + 128 * mt) =
+                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
     }
     if (p.n > 0) {
@@ -538,13 +689,12 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       if (lane == 0) arrive(&sm.o_empty);
       ++nq;
     }
-    bar_sync(1 + half, 128);                         // the sums have been read
+    bar_sync(1 + half, 128);                         // the sums and factors have been read
   }
 }
 
 __global__ void __launch_bounds__(kWinThreads, 1)
-    window_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ CUtensorMap qmap,
-                  const __grid_constant__ CUtensorMap kmap) {
+    window_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ WindowMaps m) {
   extern __shared__ __align__(1024) uint8_t base[];  // 1024-byte aligned: checked below
   __shared__ WinSmall sm;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -555,8 +705,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   }
   if (wid == kMmaWarp) tc::tmem_alloc(&sm.tmem_slot, kCols);
   if (tid == 0) {
-    tc::mbar_init(&sm.q_full, 1);
+    tc::mbar_init(&sm.q_full, kGroups - 1);
     tc::mbar_init(&sm.q_empty, 1);
+    tc::mbar_init(&sm.q8_full, 1);
+    tc::mbar_init(&sm.q8_empty, 1);
     for (int g = 0; g < kGroups; ++g) {
       tc::mbar_init(&sm.k_full[g], 1);
       tc::mbar_init(&sm.k_empty[g], 1);
@@ -569,6 +721,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     tc::fence_mbar_init();
     sm.abort = 0;
     sm.bad = 0;
+    sm.hidden = 0;
     sm.tiles = 0;
     sm.blocks = 0;
   }
@@ -610,9 +763,16 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   Span w;
   w.pieces = 1;
   if (a.may_split && tiles > 0 && 2 * tiles <= grid && sm.blocks >= kMinSplit) w.pieces = min(grid / tiles, sm.blocks);
-  w.first = blockIdx.x;
-  w.units = tiles * w.pieces;
-  w.step = grid;
+  if (a.compact) {
+    // consecutive tiles share most of their rows
+    w.first = int(int64_t(tiles) * blockIdx.x / grid);
+    w.units = int(int64_t(tiles) * (blockIdx.x + 1) / grid);
+    w.step = 1;
+  } else {
+    w.first = blockIdx.x;
+    w.units = tiles * w.pieces;
+    w.step = grid;
+  }
   if (blockIdx.x == 0 && tid == 0) {
     if (sm.bad) raise_err(a.ws, CSA2_DEV_Q_START);
     a.head[0] = tiles;
@@ -620,7 +780,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   }
   if (wid < kRowWarps) row_role(a, sm, base, w, wid, lane, tmem);
   else if (wid == kMmaWarp) mma_role(a, sm, base, w, lane, tmem);
-  else load_role(a, sm, base, w, lane, &qmap, &kmap);
+  else load_role(a, sm, base, w, wid - kLoadWarp0, lane, m);
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
   __syncwarp();
   if (wid == kMmaWarp) {
@@ -720,19 +880,22 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }  // namespace
 
 cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
-  CUtensorMap q, kv;
+  const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;   // most tokens of a tile
+  a.compact = int64_t(a.window) + span - 1 + a.sinks <= kWinPos;
+  WindowMaps m;
   const auto enc = tensor_map_encoder();
   const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
-  if (!encode_2d_cached(enc, &q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, uint64_t(a.total_q) * a.d.heads, kDqk * 2,
-                        64, kWinRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-      !encode_2d_cached(enc, &kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kDqk, rows, kDqk * 2, 64, 1,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+  if (!encode_2d_cached(enc, &m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, uint64_t(a.total_q) * a.d.heads, kDqk * 2,
+                        64, kWinRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
+  for (int i = a.compact ? 0 : 6; i < 7; ++i)
+    if (!encode_2d_cached(enc, &m.kv[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kDqk, rows, kDqk * 2, 64, 1u << i,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+      return cudaErrorUnknown;
   static KernelAttrs attrs;
   cudaError_t e = prepare_kernel(window_kernel, size_t(kWinSmem), false, attrs);
   if (e != cudaSuccess) return e;
   // bounds of what the device will find: tiles, and blocks of one
-  const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;
   int odd = H;                                       // 64 less the greatest common divisor: what a sequence's last tile may lack
   for (int b = kWinRows; b != 0;) {
     const int r = odd % b;
@@ -747,7 +910,7 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   // fewer tiles than half of the SMs, at least: their positions may be split
   a.may_split = blocks >= kMinSplit && 2 * (int64_t(a.total_q) * H / kWinRows) <= grid;
   CSA2_PROFILED(st, "window_attn",
-                (e = launch_pdl(window_kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, q, kv)));
+                (e = launch_pdl(window_kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, m)));
   if (e != cudaSuccess || !a.may_split) return e;
   CSA2_PROFILED(st, "window_merge",
                 (e = launch_pdl(window_merge_kernel, dim3(kWinRows / kMergeRows, unsigned(min64(tiles, grid / 2))),

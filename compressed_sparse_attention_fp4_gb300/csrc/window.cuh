@@ -11,7 +11,9 @@ constexpr int kWinMaxCtas = 152;         // most pieces of a call whose tiles ar
 
 struct WindowArgs {
   csa2_dims d;
-  int batch, total_q, window, sinks, may_split;
+  int batch, total_q, window, sinks;
+  int may_split;       // pieces of few tiles may be split and merged
+  int compact;         // what a tile's tokens see fits one block of 128 places (see window.cu)
   const uint16_t* q;
   const int32_t* q_start;
   const uint16_t* kv;
