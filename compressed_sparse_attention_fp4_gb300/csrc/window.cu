@@ -13,6 +13,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -25,11 +26,14 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kRowWarps = 8;                         // softmax and outputs: lane quarter w % 4, half of the rows w / 4
-constexpr int kMmaWarp = kRowWarps;
+constexpr int kRowWarps = 8;                         // softmax: lane quarter w % 4, half of the rows w / 4
+constexpr int kOutWarp0 = kRowWarps, kOutWarps = 8;  // outputs: likewise
+constexpr int kMmaWarp = kOutWarp0 + kOutWarps;
 constexpr int kGroups = 5;                           // channel groups, a copying warp each: 4 x 128 latent, 64 rope
 constexpr int kLoadWarp0 = kMmaWarp + 1;
-constexpr int kWinThreads = (kLoadWarp0 + kGroups) * 32;
+constexpr int kPlanWarp = kLoadWarp0 + kGroups;      // (one more makes them a warpgroup)
+constexpr int kWinThreads = (kMmaWarp + 8) * 32;
+constexpr int kReaders = kPlanWarp;                  // warps that follow the plan
 
 constexpr int kKReg = kWinPos * 128;                 // 64 channels of a block's positions: 16 KB
 constexpr int kQReg = kWinRows * 128;                // 64 channels of a tile's rows: 8 KB
@@ -40,21 +44,44 @@ constexpr int kWinSmem = kPOff + kPHalf;
 constexpr uint32_t kOCol = 64;                       // tensor memory: S^T 64 columns, O^T 4 x 64
 constexpr uint32_t kCols = 512;
 constexpr int kMinSplit = 3;                         // least blocks a tile's positions are split from
+constexpr int kPlanSlots = 4;
+
+// One piece of a tile's work.  Its tokens see the positions lo .. last and the sinks before lo.
+//   Compact calls: all of them fit a block of 128 places.  Position t has place t (t < sinks) or
+//     sinks + (t - sinks) % (128 - sinks), so that the rows of consecutive tiles stay where they are and
+//     a tile's new positions take the places of those that the window has left.
+//   Other calls: whole pages of 64 positions, the sinks' (sp of them) and then the window's, two a block.
+struct __align__(16) Piece {
+  int n;                        // blocks, -1 behind the last piece
+  int row, have;                // first row of q, rows (64, or what is left of the sequence)
+  int seq;
+  int lo, last;
+  int pos, rem;                 // the first row's token position and head
+  int blk, np;                  // first block; pages (sinks' and window's)
+  int sp, fresh;                // sinks' pages; compact: first position that the tile before has not left in its place (0: none left)
+  int turn;                     // compact: (last - sinks) % (128 - sinks), -1 where last < sinks
+  int unit;
+  int spare[2];
+};
 
 struct WinSmall {
-  uint64_t q_full, q_empty, q8_full, q8_empty;       // queries: latent channels, rope channels
+  uint64_t q_full[kGroups], q_empty[kGroups];        // queries and cache rows by channel group
   uint64_t k_full[kGroups], k_empty[kGroups];
   uint64_t s_full, p_full, o_full, o_empty, drain;
+  uint64_t stat_full, stat_empty;
+  uint64_t meet[2], out_meet[2];                     // the four warps of a half
+  uint64_t plan_full[kPlanSlots], plan_empty[kPlanSlots];
   uint32_t tmem_slot;
   int abort;
   int bad;                                           // q_start out of order
   uint32_t hidden;                                   // 1 + the last block in which hide_values has changed the places
   int tiles, blocks;                                 // tiles of the call; most blocks of one
+  Piece plan[kPlanSlots];
   // of the rows of a half, for all lanes of its four warps, which write the same values
   __align__(16) float ref[2][32];                    // softmax reference
-  __align__(16) float alpha[2][32];
-  __align__(16) int pos[2][32];                      // positions (-1: no such row)
-  __align__(16) float top[2][4][kWinRows];           // maxima of a block by lane quarter; sums at the end
+  __align__(16) float own[2][32];                    // factor of the outputs
+  __align__(16) float top[4][kWinRows];              // maxima of a block by lane quarter; at the end of a piece the sums
+  __align__(16) float sum_ref[kWinRows];             // their reference
 };
 static_assert(kWinSmem + (sizeof(WinSmall) + 1023) / 1024 * 1024 <= 232448, "shared memory; the dynamic part starts on a multiple of its alignment");
 
@@ -88,12 +115,20 @@ __device__ inline bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-__device__ inline void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 struct WindowMaps {
   CUtensorMap q;
   CUtensorMap kv[7];                                 // boxes of 64 channels x 2^i rows
 };
+
+// Registers a thread of the calling warpgroup: what a role gives below the launch's 80, another takes.
+template <int n>
+__device__ inline void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
+template <int n>
+__device__ inline void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
+constexpr int kWinRegs = 80, kRowRegs = 104, kOutRegs = 80, kMoveRegs = 56;
+static_assert(kRowWarps * kRowRegs + kOutWarps * kOutRegs + 8 * kMoveRegs <= kWinRegs * (kWinThreads / 32),
+              "a split above what was launched would wait for ever");
 
 __device__ inline float ex2(float x) {
   float y;
@@ -139,91 +174,13 @@ __device__ inline void exchange(T (&v)[N], int lane) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// Tiles: 64 rows of a sequence each, the sequences' tiles one after the other.
-// ---------------------------------------------------------------------------
 // Context of sequence b (bad ones are reported by the first CTA's count, and taken as 0).
 __device__ inline int context(const WindowArgs& a, int b) {
   const int n = __ldg(a.ctx_len + b);
   return n < 0 || n > a.d.max_ctx || (a.page_table && n > int64_t(a.d.max_pages) * kPage) ? 0 : n;
 }
+// Tiles of a sequence of len tokens: 64 rows each.
 __device__ inline int tiles_of(const WindowArgs& a, int len) { return (len * a.d.heads + kWinRows - 1) / kWinRows; }
-
-// One piece of a tile's work.  Its tokens see the positions lo .. last and the sinks before lo.
-//   Compact calls (`compact`, below): all of them fit a block of 128 places.  Position t has place
-//     t (t < sinks) or sinks + (t - sinks) % (128 - sinks), so that the rows of consecutive tiles
-//     stay where they are and a tile's new positions take the places of those that the window has left.
-//   Other calls: whole pages of 64 positions, the sinks' (sp of them) and then the window's, two a block.
-struct Piece {
-  int seq, from, len, ctx;      // sequence: first query token, query tokens, context
-  int row0;                     // first row in the sequence
-  int lo, last;
-  int sp, np;
-  int blk, n;                   // blocks of this piece
-};
-
-// Position of place e of block j of a piece (-1: none).
-__device__ inline int place_position(const WindowArgs& a, const Piece& p, int j, int e) {
-  if (a.compact) {
-    if (e < a.sinks) return e <= p.last ? e : -1;
-    const int c = kWinPos - a.sinks, d = (p.last - a.sinks) % c - (e - a.sinks);      // places from e on to the last position's
-    const int t = p.last - (d < 0 ? d + c : d);
-    return t >= max(p.lo, a.sinks) ? t : -1;
-  }
-  const int i = 2 * (p.blk + j) + (e >> 6);
-  const int t = (i < p.sp ? i : p.lo / kPage + i - p.sp) * kPage + (e & (kPage - 1));
-  return i < p.np && t <= p.last ? t : -1;
-}
-
-// A warp's way through the tiles.  It keeps 32 sequences, one a lane.
-struct Walk {
-  const WindowArgs& a;
-  int lane;
-  int b0, base;                                      // first sequence kept, tiles before it
-  int from, len, ctx, upto;                          // the lane's sequence; tiles up to its end from b0 on
-  __device__ Walk(const WindowArgs& args, int l) : a(args), lane(l), b0(0), base(0) { load(); }
-  __device__ void load() {
-    const int i = b0 + lane;
-    from = len = ctx = upto = 0;
-    if (i < a.batch) {
-      from = __ldg(a.q_start + i);
-      len = __ldg(a.q_start + i + 1) - from;
-      ctx = context(a, i);
-      upto = tiles_of(a, len);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += y;
-    }
-  }
-  // Piece s of n of tile t (not before the one asked for last); false behind the last.
-  __device__ bool piece(int t, int s, int n, Piece& p) {
-    uint32_t past;
-    while ((past = __ballot_sync(0xFFFFFFFFu, base + upto > t)) == 0) {
-      base += __shfl_sync(0xFFFFFFFFu, upto, 31);
-      b0 += 32;
-      if (b0 >= a.batch) return false;
-      load();
-    }
-    const int w = __ffs(past) - 1;
-    p.seq = b0 + w;
-    p.from = __shfl_sync(0xFFFFFFFFu, from, w);
-    p.len = __shfl_sync(0xFFFFFFFFu, len, w);
-    p.ctx = __shfl_sync(0xFFFFFFFFu, ctx, w);
-    const int before = __shfl_sync(0xFFFFFFFFu, upto, max(w - 1, 0));
-    p.row0 = (t - base - (w > 0 ? before : 0)) * kWinRows;
-    const int tok0 = p.row0 / a.d.heads, tok1 = min(p.len - 1, (p.row0 + kWinRows - 1) / a.d.heads);
-    p.last = p.ctx - p.len + tok1;
-    p.lo = max(0, p.ctx - p.len + tok0 - a.window + 1);
-    p.sp = min((a.sinks + kPage - 1) / kPage, p.lo / kPage);
-    p.np = p.last < 0 ? 0 : p.sp + p.last / kPage - p.lo / kPage + 1;
-    const int nb = a.compact ? p.last >= 0 : (p.np + 1) / 2;
-    p.blk = n == 1 ? 0 : nb * s / n;
-    p.n = n == 1 ? nb : nb * (s + 1) / n - p.blk;
-    return true;
-  }
-};
 
 // Cache row of position t (-1: its page id is out of range).
 __device__ inline int row_of(const WindowArgs& a, int seq, int t) {
@@ -232,9 +189,21 @@ __device__ inline int row_of(const WindowArgs& a, int seq, int t) {
   return pg < 0 || pg >= a.d.num_pages ? -1 : pg * kPage + t % kPage;
 }
 
-// ---------------------------------------------------------------------------
-// Roles
-// ---------------------------------------------------------------------------
+// Position of place e of block j of a piece (-1: none).
+template <bool kCompact>
+__device__ inline int place_position(const WindowArgs& a, const Piece& p, int j, int e) {
+  if (kCompact) {
+    if (e < a.sinks) return e <= p.last ? e : -1;
+    int d = p.turn - (e - a.sinks);                  // places from e on to the last position's
+    if (d < 0) d += kWinPos - a.sinks;
+    const int t = p.last - d;
+    return p.turn >= 0 && t >= max(p.lo, a.sinks) ? t : -1;
+  }
+  const int i = 2 * (p.blk + j) + (e >> 6);
+  const int t = (i < p.sp ? i : p.lo / kPage + i - p.sp) * kPage + (e & (kPage - 1));
+  return i < p.np && t <= p.last ? t : -1;
+}
+
 // The position's values, if an infinity or NaN is among them, become 0: its weight in the rows that
 // do not see it is 0, and so must be 0 times its values.  The rows that do see it are NaN by its
 // score, which holds the same channels.
@@ -254,10 +223,108 @@ __device__ __noinline__ void hide_values(WinSmall& sm, uint8_t* base, int e, uin
     *reinterpret_cast<uint4*>(base + (c >> 3) * kKReg + tc::sw128_offset(e, c & 7)) = make_uint4(0, 0, 0, 0);
 }
 
+// ---------------------------------------------------------------------------
+// Plan: one warp walks the CTA's tiles and tells the others what to do, a few pieces ahead.
+// ---------------------------------------------------------------------------
+// A CTA's units of work (pieces of tiles): first, first + step, ... below units.
 struct Span {
-  int first, units, step, pieces;                    // the CTA's units: first, first + step, ... below units
+  int first, units, step, pieces;
 };
 
+template <bool kCompact>
+__device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& w, int lane) {
+  // 32 sequences, one a lane: from b0 on, `base` tiles before them
+  int b0 = 0, base = 0, from = 0, len = 0, ctx = 0, upto = 0;
+  const auto load = [&]() {
+    const int i = b0 + lane;
+    from = len = ctx = upto = 0;
+    if (i < a.batch) {
+      from = __ldg(a.q_start + i);
+      len = __ldg(a.q_start + i + 1) - from;
+      ctx = context(a, i);
+      upto = tiles_of(a, len);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
+  };
+  load();
+  int was_seq = -1, was_last = 0;
+  uint32_t k = 0;
+  for (int u = w.first;; u += w.step, ++k) {
+    Piece p = {};
+    p.n = -1;
+    if (u < w.units) {
+      const int t = u / w.pieces, s = u - t * w.pieces;
+      uint32_t past;
+      while ((past = __ballot_sync(0xFFFFFFFFu, base + upto > t)) == 0) {
+        base += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        b0 += 32;
+        load();
+      }
+      const int i = __ffs(past) - 1;
+      const int tokens = __shfl_sync(0xFFFFFFFFu, len, i), c = __shfl_sync(0xFFFFFFFFu, ctx, i);
+      const int before = i > 0 ? __shfl_sync(0xFFFFFFFFu, upto, i - 1) : 0;
+      const int r0 = (t - base - before) * kWinRows, tok0 = r0 / a.d.heads;
+      const int tok1 = min(tokens - 1, (r0 + kWinRows - 1) / a.d.heads);
+      p.row = __shfl_sync(0xFFFFFFFFu, from, i) * a.d.heads + r0;
+      p.have = min(kWinRows, tokens * a.d.heads - r0);
+      p.seq = b0 + i;
+      p.pos = c - tokens + tok0;
+      p.rem = r0 - tok0 * a.d.heads;
+      p.last = c - tokens + tok1;
+      p.lo = max(0, p.pos - a.window + 1);
+      p.unit = u;
+      if (kCompact) {
+        p.n = p.last >= 0;
+        p.fresh = p.seq == was_seq ? was_last + 1 : 0;
+        p.turn = p.last >= a.sinks ? (p.last - a.sinks) % (kWinPos - a.sinks) : -1;
+        if (p.n > 0) {
+          was_seq = p.seq;
+          was_last = p.last;
+        }
+      } else {
+        p.sp = min((a.sinks + kPage - 1) / kPage, p.lo / kPage);
+        p.np = p.last < 0 ? 0 : p.sp + p.last / kPage - p.lo / kPage + 1;
+        const int nb = (p.np + 1) / 2;
+        p.blk = nb * s / w.pieces;
+        p.n = nb * (s + 1) / w.pieces - p.blk;
+      }
+    }
+    const uint32_t slot = k % kPlanSlots;
+    if (!wait_warp(sm, &sm.plan_empty[slot], ((k / kPlanSlots) & 1) ^ 1, a.ws)) return;
+    if (lane == 0) {
+      sm.plan[slot] = p;
+      arrive(&sm.plan_full[slot]);
+    }
+    __syncwarp();
+    if (p.n < 0) return;
+  }
+}
+
+// The next piece, for a converged warp; false behind the last.
+__device__ inline bool next_piece(WinSmall& sm, uint32_t& k, int lane, uint8_t* ws, Piece& p) {
+  const uint32_t slot = k % kPlanSlots;
+  if (!wait_warp(sm, &sm.plan_full[slot], (k / kPlanSlots) & 1, ws)) return false;
+  p = sm.plan[slot];
+  __syncwarp();
+  if (lane == 0) arrive(&sm.plan_empty[slot]);
+  ++k;
+  return p.n >= 0;
+}
+
+// The four warps of a half meet (bounded, unlike a hardware barrier).
+__device__ inline bool meet(WinSmall& sm, uint64_t* bar, uint32_t& n, int lane, uint8_t* ws) {
+  __syncwarp();
+  if (lane == 0) arrive(bar);
+  return wait_warp(sm, bar, n++ & 1, ws);
+}
+
+// ---------------------------------------------------------------------------
+// Copies
+// ---------------------------------------------------------------------------
 // A box of 2^lg rows (lg -1: none) from cache row `row` on, for the places from `slot` on.
 struct Box {
   int slot, row, lg;
@@ -267,7 +334,7 @@ struct Box {
 // rows, cut at pages and where the places come round, in powers of two (a tile has at most 6 runs
 // of 128 rows together: at most 23 boxes).  `page`: lane i has the page ids of the first two pages
 // (lanes 0, 1) and of the window's (lanes 2 .. 5).  Returns their rows.
-__device__ inline int boxes(const WindowArgs& a, const Piece& p, int first, int last, int page, int lane, int& k, Box& mine,
+__device__ inline int boxes(const WindowArgs& a, int seq, int lo, int first, int last, int page, int lane, int& k, Box& mine,
                             bool& lost) {
   int rows = 0;
   for (int t = first; t <= last;) {
@@ -276,10 +343,10 @@ __device__ inline int boxes(const WindowArgs& a, const Piece& p, int first, int 
     int n = min(last - t + 1, kWinPos - slot), row;
     if (a.page_table) {
       n = min(n, kPage - t % kPage);
-      const int pg = __shfl_sync(0xFFFFFFFFu, page, at < 2 ? at : 2 + at - p.lo / kPage);
+      const int pg = __shfl_sync(0xFFFFFFFFu, page, at < 2 ? at : 2 + at - lo / kPage);
       row = pg < 0 || pg >= a.d.num_pages ? -1 : pg * kPage + t % kPage;
     } else {
-      row = int(int64_t(p.seq) * a.d.max_ctx + t);
+      row = int(int64_t(seq) * a.d.max_ctx + t);
     }
     t += n;
     if (row < 0) {
@@ -298,232 +365,294 @@ __device__ inline int boxes(const WindowArgs& a, const Piece& p, int first, int 
   }
   return rows;
 }
-// What a compact tile sees from position `from` on.
-__device__ inline int tile_boxes(const WindowArgs& a, const Piece& p, int from, int lane, Box& mine, bool& lost) {
+// All that a compact tile sees.
+__device__ __noinline__ int tile_boxes(const WindowArgs& a, int seq, int lo, int last, int lane, Box& mine, bool& lost) {
   int page = -1, k = 0;
   if (a.page_table && lane < 6) {
-    const int i = lane < 2 ? lane : p.lo / kPage + lane - 2;
-    if (i < a.d.max_pages && i * kPage <= p.last) page = __ldg(a.page_table + int64_t(p.seq) * a.d.max_pages + i);
+    const int i = lane < 2 ? lane : lo / kPage + lane - 2;
+    if (i < a.d.max_pages && i * kPage <= last) page = __ldg(a.page_table + int64_t(seq) * a.d.max_pages + i);
   }
   mine.lg = -1;
-  const int rows = boxes(a, p, from, min(a.sinks - 1, p.last), page, lane, k, mine, lost);
-  return rows + boxes(a, p, max(from, max(p.lo, a.sinks)), p.last, page, lane, k, mine, lost);
+  int rows = 0;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part)
+    rows += boxes(a, seq, lo, part == 0 ? 0 : max(lo, a.sinks), part == 0 ? min(a.sinks - 1, last) : last, page, lane, k, mine, lost);
+  return rows;
 }
 
 // Where P of a block's first and last 64 positions goes: over the block's rope channels, which only
 // the scores need; in a compact call, whose rows stay, into a place of its own and over the queries'
 // rope channels, which no other block of the tile needs.
-__device__ inline uint32_t p_offset(const WindowArgs& a, int half) {
-  return a.compact ? (half == 0 ? kPOff : kQOff + 8 * kQReg) : 8 * kKReg + half * kPHalf;
+template <bool kCompact>
+__device__ inline uint32_t p_offset(int half) {
+  return kCompact ? (half == 0 ? kPOff : kQOff + 8 * kQReg) : 8 * kKReg + half * kPHalf;
 }
 
 // Copies channel group g of the queries and the cache rows.  (One warp for all groups takes 650 cycles
 // for the few copies of one: what it waits for is the issue, not the copies.)
-__device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int g, int lane,
-                                 const WindowMaps& m) {
-  Walk walk(a, lane);
+//
+// A few rows are fetched into registers while their places are still in use, and stored when they are
+// free: a copy by TMA from then on takes 700 cycles of the chain.  More rows go as boxes.
+constexpr int kFewRows = 4, kFewChunks = kFewRows * 16 / 32;
+
+template <bool kCompact>
+__device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, int g, int lane, const WindowMaps& m) {
+  const int regions = g < 4 ? 2 : 1, shift = g < 4 ? 4 : 3;            // (16-byte pieces of a row: 1 << shift)
   Piece p;
-  uint32_t nq = 0, nk = 0;
-  int was_seq = -1, was_last = 0;                    // what the places hold
-  const int regions = g < 4 ? 2 : 1;
-  uint64_t* q_full = g < 4 ? &sm.q_full : &sm.q8_full;
-  uint64_t* q_empty = g < 4 ? &sm.q_empty : &sm.q8_empty;
-  for (int u = w.first; u < w.units; u += w.step) {
-    if (!walk.piece(u / w.pieces, u % w.pieces, w.pieces, p)) return;
+  uint32_t nu = 0, nq = 0, nk = 0;
+  while (next_piece(sm, nu, lane, a.ws, p)) {
     if (p.n == 0) continue;
-    // a compact tile's boxes: what the tile before has not left there, or all of it
     Box box;
     int rows = 0;
-    bool lost = false;
-    if (a.compact) {
-      rows = tile_boxes(a, p, p.seq == was_seq ? was_last + 1 : 0, lane, box, lost);
-      was_seq = p.seq;
-      was_last = p.last;
-    }
-    for (int j = 0; j < p.n; ++j, ++nk) {
-      int row = -1;                                  // lane's half of the block (lane & 1)
-      if (!a.compact) {
-        const int t = place_position(a, p, j, kPage * (lane & 1));
-        if (t >= 0) {
-          row = row_of(a, p.seq, t);
-          lost = row < 0;
+    bool lost = false, few = false;
+    uint4 v[kFewChunks];
+    uint32_t to[kFewChunks];                         // offsets in the block, ~0: none
+    if (kCompact) {
+      few = p.fresh > 0 && p.last - p.fresh < kFewRows;
+      if (few) {
+#pragma unroll
+        for (int i = 0; i < kFewChunks; ++i) {
+          const int c = lane + 32 * i, t = p.fresh + (c >> shift), r = 2 * g + (c >> 3 & (regions - 1));
+          to[i] = ~0u;
+          if (t > p.last) continue;
+          const int row = row_of(a, p.seq, t);
+          if (row < 0) {
+            lost = true;
+            continue;
+          }
+          int d = p.turn - (p.last - t);
+          if (d < 0) d += kWinPos - a.sinks;
+          to[i] = r * kKReg + tc::sw128_offset(t < a.sinks ? t : a.sinks + d, c & 7);
+          v[i] = __ldg(reinterpret_cast<const uint4*>(a.kv + int64_t(row) * kDqk + 64 * r) + (c & 7));
         }
+      } else {
+        rows = tile_boxes(a, p.seq, p.lo, p.last, lane, box, lost);
       }
-      if (g == 0 && lost) raise_err(a.ws, CSA2_DEV_PAGE_ID);
-      if (j == 0) {
-        if (!wait_warp(sm, q_empty, (nq & 1) ^ 1, a.ws)) return;
-        if (lane == 0) tc::mbar_expect_tx(q_full, uint32_t(regions * kQReg));
-        __syncwarp();
-        if (lane < regions)
-          tc::tma_load_2d(&m.q, base + kQOff + (2 * g + lane) * kQReg, 64 * (2 * g + lane), p.from * a.d.heads + p.row0, q_full);
-        ++nq;
-      }
+    }
+    if (!wait_warp(sm, &sm.q_empty[g], (nq++ & 1) ^ 1, a.ws)) return;
+    if (lane == 0) {
+      tc::mbar_expect_tx(&sm.q_full[g], uint32_t(regions * kQReg));
+#pragma unroll 1
+      for (int r = 2 * g; r < 2 * g + regions; ++r)
+        tc::tma_load_2d(&m.q, base + kQOff + r * kQReg, 64 * r, p.row, &sm.q_full[g]);
+      // the next tile's queries are the next rows: to L2
+      const int64_t more = min64(kWinRows, int64_t(a.total_q) * a.d.heads - p.row - kWinRows);
+      if (kCompact && g == 4 && more > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(a.q + (int64_t(p.row) + kWinRows) * kDqk), "r"(uint32_t(more * kDqk * 2)) : "memory");
+    }
+    __syncwarp();
+    if (kCompact) {
       if (!wait_warp(sm, &sm.k_empty[g], (nk & 1) ^ 1, a.ws)) return;
-      if (a.compact) {
-        // values of the tile before may have been taken out of their places
-        if (g < 4 && nk > 0 && *reinterpret_cast<volatile uint32_t*>(&sm.hidden) == nk)
-          rows = tile_boxes(a, p, 0, lane, box, lost);
+      // values of the tile before may have been taken out of their places
+      if (few && g < 4 && nk > 0 && *reinterpret_cast<volatile uint32_t*>(&sm.hidden) == nk) {
+        few = false;
+        rows = tile_boxes(a, p.seq, p.lo, p.last, lane, box, lost);
+      }
+      if (few) {
+#pragma unroll
+        for (int i = 0; i < kFewChunks; ++i)
+          if (to[i] != ~0u) *reinterpret_cast<uint4*>(base + to[i]) = v[i];
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive(&sm.k_full[g]);
+      } else {
         if (lane == 0) tc::mbar_expect_tx(&sm.k_full[g], uint32_t(regions * rows * 128));
         __syncwarp();
         if (box.lg >= 0)
+#pragma unroll 1
           for (int r = 2 * g; r < 2 * g + regions; ++r)
             tc::tma_load_2d(&m.kv[box.lg], base + r * kKReg + box.slot * 128, 64 * r, box.row, &sm.k_full[g]);
-      } else {
+      }
+      ++nk;
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < p.n; ++j, ++nk) {
+        // lane: half of the block (lane & 1), region
+        const int h = lane & 1, r = 2 * g + (lane >> 1), t = place_position<false>(a, p, j, kPage * h);
+        const int row = t >= 0 ? row_of(a, p.seq, t) : -1;
+        lost = lost || (t >= 0 && row < 0);
         const int halves = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0) & 3u);
+        if (!wait_warp(sm, &sm.k_empty[g], (nk & 1) ^ 1, a.ws)) return;
         if (lane == 0) tc::mbar_expect_tx(&sm.k_full[g], uint32_t(regions * halves * (kKReg / 2)));
         __syncwarp();
-        const int r = 2 * g + (lane >> 1);
         if (lane < 2 * regions && row >= 0)
-          tc::tma_load_2d(&m.kv[6], base + r * kKReg + (lane & 1) * (kKReg / 2), 64 * r, row, &sm.k_full[g]);
+          tc::tma_load_2d(&m.kv[6], base + r * kKReg + h * (kKReg / 2), 64 * r, row, &sm.k_full[g]);
       }
     }
+    if (g == 0 && lost) raise_err(a.ws, CSA2_DEV_PAGE_ID);
   }
 }
 
-// Issues the products.  The offsets are constants: a product takes 58 cycles, and formed at run time
-// they take longer than that.
-__device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int lane, uint32_t tmem) {
+// ---------------------------------------------------------------------------
+// Products
+// ---------------------------------------------------------------------------
+// tc::mma_bf16 with descriptors as low words (address, leading offset); their high words are one
+// constant: rows of 8 are 1,024 bytes apart, 128-byte swizzle.  Called by the whole warp, done by
+// the thread with `leader`: what the operands are formed from is then the same for the warp to the
+// compiler, which keeps it in uniform registers.
+template <bool kFirst>
+__device__ inline void mma_lo(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(leader), "n"((1024 >> 4) | 1 << 14 | 2 << 29), "n"(kFirst ? 0 : 1)
+      : "memory");
+}
+__device__ inline void commit_lo(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(tc::smem_u32(bar)), "r"(leader) : "memory");
+}
+
+template <bool kCompact>
+__device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, int lane, uint32_t tmem) {
   constexpr uint32_t id_s = tc::idesc_bf16(kWinPos, kWinRows, 0, 0);
   constexpr uint32_t id_o = tc::idesc_bf16(kWinPos, kWinRows, 1, 1);
   const uint32_t at = tc::smem_u32(base);
-  const uint64_t ks = tc::smem_desc(at, 16, 1024, 2), qs = tc::smem_desc(at + kQOff, 16, 1024, 2);
-  const uint64_t vs = tc::smem_desc(at, kKReg, 1024, 2);
-  const uint64_t p0 = tc::smem_desc(at + p_offset(a, 0), kPHalf, 1024, 2), p1 = tc::smem_desc(at + p_offset(a, 1), kPHalf, 1024, 2);
-  const bool leader = elect_one();
-  Walk walk(a, lane);
+  const uint32_t k_lo = uint32_t(tc::smem_desc(at, 16, 1024, 2)), q_lo = uint32_t(tc::smem_desc(at + kQOff, 16, 1024, 2));
+  const uint32_t v_lo = uint32_t(tc::smem_desc(at, kKReg, 1024, 2));
+  const uint32_t p_lo[2] = {uint32_t(tc::smem_desc(at + p_offset<kCompact>(0), kPHalf, 1024, 2)),
+                            uint32_t(tc::smem_desc(at + p_offset<kCompact>(1), kPHalf, 1024, 2))};
+  const uint32_t leader = elect_one();
   Piece p;
-  uint32_t nq = 0, nk = 0;
-  for (int u = w.first; u < w.units; u += w.step) {
-    if (!walk.piece(u / w.pieces, u % w.pieces, w.pieces, p)) return;
-    if (p.n == 0) continue;
-    if (!wait_warp(sm, &sm.q_full, nq & 1, a.ws)) return;
-    for (int j = 0; j < p.n; ++j, ++nk) {
+  uint32_t nu = 0, nq = 0, nk = 0;
+  while (next_piece(sm, nu, lane, a.ws, p)) {
+    const int n = p.n;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j, ++nk) {
+      // a channel group at a time: two regions, rope one
+      const auto scores = [&](int g, auto first, auto regions) {
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        if (!wait_warp(sm, &sm.k_full[g], nk & 1, a.ws)) return;
-        if (g == 4 && j == 0 && !wait_warp(sm, &sm.q8_full, nq & 1, a.ws)) return;
+        for (int i = 0; i < 4 * regions; ++i) {
+          const uint32_t ks = k_lo + (((2 * g + (i >> 2)) * kKReg + (i & 3) * 32) >> 4), qs = q_lo + (((2 * g + (i >> 2)) * kQReg + (i & 3) * 32) >> 4);
+          if (first && i == 0) mma_lo<true>(leader, tmem, ks, qs, id_s);
+          else mma_lo<false>(leader, tmem, ks, qs, id_s);
+        }
+        // the next tile's queries come group by group (P goes over the rope channels in a compact call)
+        if (j == n - 1 && (g < 4 || !kCompact)) commit_lo(leader, &sm.q_empty[g]);
+      };
+      const auto ready = [&](int g) {
+        if (j == 0 && !wait_warp(sm, &sm.q_full[g], nq & 1, a.ws)) return false;
+        if (!wait_warp(sm, &sm.k_full[g], nk & 1, a.ws)) return false;
         tc::tc_fence_after_sync();
-        if (leader) {
-#pragma unroll
-          for (int i = 0; i < (g < 4 ? 8 : 4); ++i) {
-            const uint32_t kb = 2 * g + (i >> 2), off = (i & 3) * 32;
-            tc::mma_bf16(tmem, ks + ((kb * kKReg + off) >> 4), qs + ((kb * kQReg + off) >> 4), id_s, g + i > 0);
-          }
-        }
-        __syncwarp();
+        return true;
+      };
+      if (!ready(0)) return;
+      scores(0, std::true_type{}, std::integral_constant<int, 2>{});
+#pragma unroll 1
+      for (int g = 1; g < 4; ++g) {
+        if (!ready(g)) return;
+        scores(g, std::false_type{}, std::integral_constant<int, 2>{});
       }
-      if (leader) {
-        tc::mma_commit(&sm.s_full);
-        if (a.compact) tc::mma_commit(&sm.k_empty[4]);
-        if (j == p.n - 1) {
-          tc::mma_commit(&sm.q_empty);
-          if (!a.compact) tc::mma_commit(&sm.q8_empty);
-        }
-      }
-      __syncwarp();
+      if (!ready(4)) return;
+      scores(4, std::false_type{}, std::integral_constant<int, 1>{});
+      commit_lo(leader, &sm.s_full);
+      if (kCompact) commit_lo(leader, &sm.k_empty[4]);
       if (!wait_warp(sm, &sm.p_full, nk & 1, a.ws)) return;
       if (j == 0 && !wait_warp(sm, &sm.o_empty, (nq & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
-      if (leader) {
-        const bool more = j > 0;
+#pragma unroll 1
+      for (int mt = 0; mt < 4; ++mt) {
+        const uint32_t vs = v_lo + mt * (2 * kKReg >> 4), d = tmem + kOCol + 64 * mt;
+        if (j == 0) mma_lo<true>(leader, d, vs, p_lo[0], id_o);
+        else mma_lo<false>(leader, d, vs, p_lo[0], id_o);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc::mma_bf16(tmem + kOCol + 64 * mt, vs + ((2 * mt * kKReg + k * 2048) >> 4), (k < 4 ? p0 : p1) + (((k & 3) * 2048) >> 4),
-                         id_o, more || k > 0);
-          tc::mma_commit(&sm.k_empty[mt]);
-        }
-        tc::mma_commit(a.compact ? &sm.q8_empty : &sm.k_empty[4]);
-        if (j == p.n - 1) tc::mma_commit(&sm.o_full);
+        for (int k = 1; k < 8; ++k) mma_lo<false>(leader, d, vs + (k * 2048 >> 4), p_lo[k >> 2] + ((k & 3) * 2048 >> 4), id_o);
+        commit_lo(leader, &sm.k_empty[mt]);
       }
-      __syncwarp();
+      commit_lo(leader, kCompact ? &sm.q_empty[4] : &sm.k_empty[4]);
+      if (j == n - 1) commit_lo(leader, &sm.o_full);
     }
-    ++nq;
+    if (n > 0) ++nq;
   }
 }
 
-// What a row warp has to know of a piece before its scores come.
-struct Ahead {
-  Piece p;
-  bool have;
-  int mine;                                          // position of the lane's row, -1: no such row
-  int t, row;                                        // position in the lane's place of the first block (-1: none), its row
-};
-__device__ inline void place_seen(const WindowArgs& a, const Piece& p, int j, int e, int& t, int& row) {
-  t = place_position(a, p, j, e);
-  row = t >= 0 ? row_of(a, p.seq, t) : -1;
-}
-__device__ inline void look_ahead(const WindowArgs& a, Walk& walk, const Span& w, int u, int half, int e, int lane, Ahead& n) {
-  n.have = u < w.units && walk.piece(u / w.pieces, u % w.pieces, w.pieces, n.p);
-  if (!n.have) return;
-  const int lr = n.p.row0 + 32 * half + lane;
-  n.mine = lr < n.p.len * a.d.heads ? n.p.ctx - n.p.len + lr / a.d.heads : -1;
-  if (n.p.n > 0) place_seen(a, n.p, 0, e, n.t, n.row);
+// ---------------------------------------------------------------------------
+// Softmax
+// ---------------------------------------------------------------------------
+// Scores of a position t that not every row sees: those of rows that do not see it become -inf.
+// `pos`, `rem`: the first row's token position and head; tokens are `heads` rows each.  (Rows that do
+// not exist take part as if they did: nothing of theirs is used.)
+__device__ inline void mask_scores(const WindowArgs& a, WinSmall& sm, uint8_t* base, float (&x)[32], int t, int pos, int rem, int e,
+                                   uint32_t block) {
+  const uint32_t span = t < 0 ? 0u : t < a.sinks ? 0x7FFFFFFFu : uint32_t(a.window);   // seen by tokens t .. t + span - 1
+  float any = 0.0f;                                  // 0, or NaN where a score is no number
+  int p = pos, h = rem;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    any = fmaf(x[i], 0.0f, any);
+    x[i] = uint32_t(p - t) < span ? x[i] : -INFINITY;
+    if (++h == a.d.heads) {
+      h = 0;
+      ++p;
+    }
+  }
+  if (any == 0.0f) return;
+  // an infinity or NaN: rows that see the position become NaN; is it hidden from others, its values go
+  bool odd = false;
+  p = pos;
+  h = rem;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const bool see = uint32_t(p - t) < span;
+    odd = odd || !see;
+    if (see && !(fabsf(x[i]) < INFINITY)) x[i] = NAN;
+    if (++h == a.d.heads) {
+      h = 0;
+      ++p;
+    }
+  }
+  if (odd) hide_values(sm, base, e, block);
 }
 
-// Softmax over a block's positions (tensor-memory lanes) and the outputs.  Warp rw has the
-// lanes 32 (rw % 4) .. + 31 and the rows 32 (rw / 4) .. + 31; lane i keeps the state of row i of
-// these (alike in the four warps of a half, but for the sum, which is of its own lanes).
-// Shared memory is the products': they take five sixths of its bandwidth, so values cross the lanes
-// by shuffles.
-// A wait that gives up leaves the warp in the loop, without waits or results: its hardware
-// barriers have no limit, and all eight warps pass the same ones.
-__device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, const Span& w, int rw, int lane,
-                                uint32_t tmem) {
+// Softmax over a block's positions (tensor-memory lanes).  Warp rw has the lanes 32 (rw % 4) .. + 31
+// and the rows 32 (rw / 4) .. + 31; lane i keeps the state of row i of these (alike in the four warps
+// of a half, but for the sum, which is of its own lanes).
+template <bool kCompact>
+__device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, int rw, int lane, uint32_t tmem) {
   const int quarter = rw & 3, half = rw >> 2, e = 32 * quarter + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(32 * half);
   const float c2 = a.scale * 1.4426950408889634f;
-  uint8_t* const p_at = base + p_offset(a, quarter >> 1);
-  bool dead = false;
-  Walk walk(a, lane);
-  Ahead now;
-  look_ahead(a, walk, w, w.first, half, e, lane, now);
-  uint32_t nq = 0, nk = 0;
-  for (int u = w.first; now.have; u += w.step) {
-    const Piece p = now.p;
-    const int mine = now.mine, rows = p.len * a.d.heads;
-    const int lr = p.row0 + 32 * half + lane;
-    sm.pos[half][lane] = mine;
-    __syncwarp();
-    const int p_max = __reduce_max_sync(0xFFFFFFFFu, mine);
-    const int p_min = __reduce_min_sync(0xFFFFFFFFu, lr < rows ? mine : p_max);
+  uint8_t* const p_at = base + p_offset<kCompact>(quarter >> 1);
+  Piece p;
+  uint32_t nu = 0, nk = 0, nm = 0;
+  while (next_piece(sm, nu, lane, a.ws, p)) {
+    // tokens of the warp's rows: the first one's position and its row's head, the last one's position
+    const int r0 = p.rem + 32 * half, tok = r0 / a.d.heads, rem = r0 - tok * a.d.heads;
+    const int p_min = p.pos + tok, p_max = p.pos + (p.rem + max(min(32 * half + 31, p.have - 1), 0)) / a.d.heads;
     float ref = -INFINITY, sum = 0.0f;
-    int t = now.t, row = now.row;
+    int t, row;
+    const auto look = [&](int j) {
+      t = place_position<kCompact>(a, p, j, e);
+      row = t >= 0 ? row_of(a, p.seq, t) : -1;
+    };
+    look(0);
+    // the last piece's sums, which stand where the maxima go, have been read
+    if (!wait_warp(sm, &sm.stat_empty, nu & 1, a.ws)) return;
+#pragma unroll 1
     for (int j = 0; j < p.n; ++j, ++nk) {
-      if (j > 0) place_seen(a, p, j, e, t, row);
       if (row < 0) t = -1;
       const bool all = t >= 0 && t <= p_min && (t > p_max - a.window || t < a.sinks);
       const bool edge = !__all_sync(0xFFFFFFFFu, all);
-      if (!dead && !wait_warp(sm, &sm.s_full, nk & 1, a.ws)) dead = true;
+      if (!wait_warp(sm, &sm.s_full, nk & 1, a.ws)) return;
       tc::tc_fence_after_sync();
       float x[32];
       tc::tmem_ld32(lanes, x);
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] *= c2;
       if (edge) {
-        bool odd = false;                            // some score of a row that does not see the position is no number
-#pragma unroll
-        for (int i4 = 0; i4 < 8; ++i4) {
-          const int4 pr = reinterpret_cast<const int4*>(sm.pos[half])[i4];
-          const int q4[4] = {pr.x, pr.y, pr.z, pr.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = 4 * i4 + k;
-            const bool see = t >= 0 && t <= q4[k] && (t > q4[k] - a.window || t < a.sinks);
-            const bool fine = fabsf(x[i]) < INFINITY;
-            odd = odd || !(see || fine);
-            x[i] = see ? (fine ? x[i] : NAN) : -INFINITY;
-          }
-        }
-        if (odd) hide_values(sm, base, e, nk);
+        mask_scores(a, sm, base, x, t, p_min, rem, e, nk);
         __syncwarp();
       }
       float top = butterfly<true>(x, lane);
-      sm.top[nk & 1][quarter][32 * half + lane] = top;
-      bar_sync(1 + half, 128);
+      sm.top[quarter][32 * half + lane] = top;       // (read before the other warps' P, which these scores came after)
+      if (!meet(sm, &sm.meet[half], nm, lane, a.ws)) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, sm.top[nk & 1][k][32 * half + lane]);
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, sm.top[k][32 * half + lane]);
       float alpha = 1.0f;
       if (top > ref + 8.0f) {
         const float to = ceilf(top);
@@ -531,21 +660,19 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         ref = to;
       }
       sm.ref[half][lane] = ref == -INFINITY ? 0.0f : ref;
-      const bool turn = __any_sync(0xFFFFFFFFu, alpha != 1.0f);
-      if (turn) sm.alpha[half][lane] = alpha;
       __syncwarp();
-      if (turn) {
+      if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
         // the outputs so far to the new reference (this block's scores came after the last product: the
         // copies that they needed waited for it)
         sum *= alpha;
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt)
+        for (int c = 0; c < 32; c += 8)
 #pragma unroll 1
-          for (int c = 0; c < 32; c += 8) {
+          for (int mt = 0; mt < 4; ++mt) {
             float o[8];
             tc::tmem_ld8(lanes + kOCol + 64 * mt + c, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= sm.alpha[half][c + i];
+            for (int i = 0; i < 8; ++i) o[i] *= __shfl_sync(0xFFFFFFFFu, alpha, c + i);
             tc::tmem_st8(lanes + kOCol + 64 * mt + c, o);
           }
       }
@@ -570,19 +697,41 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       __syncwarp();
       if (lane == 0) arrive(&sm.p_full);
       sum += butterfly<false>(x, lane);
+      if (j + 1 < p.n) look(j + 1);
     }
-    look_ahead(a, walk, w, u + w.step, half, e, lane, now);
-    // outputs: sums of the four lane quarters, joined with the other attention's
-    const bool join = a.prev_out != nullptr && w.pieces == 1;
-    const int64_t row0 = int64_t(p.from) * a.d.heads + p.row0 + 32 * half;
+    // all have read the maxima: the sums go in their place
+    if (!meet(sm, &sm.meet[half], nm, lane, a.ws)) return;
+    sm.top[quarter][32 * half + lane] = sum;
+    if (quarter == 0) sm.sum_ref[32 * half + lane] = ref;
+    __syncwarp();
+    if (lane == 0) arrive(&sm.stat_full);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Outputs, from tensor memory: lanes are channels, columns are rows.  The products take five sixths of
+// shared memory's bandwidth, so values cross the lanes by shuffles, few of them.
+// ---------------------------------------------------------------------------
+template <bool kCompact, bool kJoin>
+__device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, int ow, int lane, uint32_t tmem) {
+  const int quarter = ow & 3, half = ow >> 2, e = 32 * quarter + lane;
+  const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(32 * half);
+  const bool whole = kCompact || pieces == 1, join = kJoin && whole;
+  Piece p;
+  uint32_t nu = 0, nq = 0, nm = 0;
+  while (next_piece(sm, nu, lane, a.ws, p)) {
+    const int have = p.have - 32 * half;             // rows of this half
+    const int64_t row0 = int64_t(p.row) + 32 * half;
+    // after the transposition a lane has 8 channels of the rows 8 k + lane % 8
+    const int64_t at = (row0 + (lane & 7)) * kLatent + 32 * quarter + 8 * (lane >> 3);
+    const int left = have - (lane & 7);              // row 8 k exists: 8 k < left
     float prev = -INFINITY;
-    if (join && lr < rows) prev = a.prev_lse[row0 + lane];
-    float (&sums)[4][kWinRows] = sm.top[nk & 1];     // (the other one may still be read)
-    sums[quarter][32 * half + lane] = sum;
-    bar_sync(1 + half, 128);
+    if (join && lane < have) prev = a.prev_lse[row0 + lane];
+    if (!wait_warp(sm, &sm.stat_full, (nu - 1) & 1, a.ws)) return;
     float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) total += sums[k][32 * half + lane];
+    for (int k = 0; k < 4; ++k) total += sm.top[k][32 * half + lane];
+    const float ref = sm.sum_ref[32 * half + lane];
     float own = total != 0.0f ? 1.0f / total : 0.0f, other = 0.0f;
     float lse = total != 0.0f ? ((ref == -INFINITY ? 0.0f : ref) + log2f(total)) * 0.6931471805599453f : -INFINITY;
     if (join && prev != -INFINITY) {
@@ -591,11 +740,11 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       other = x1 / (x0 + x1);
       lse = most + logf(x0 + x1);
     }
-    sm.ref[half][lane] = own;
-    // after the transposition a lane has 8 channels of the rows 8 k + lane % 8
-    const int ch = 32 * quarter + 8 * (lane >> 3);
-    const int64_t at = (row0 + (lane & 7)) * kLatent + ch;
-    const int left = rows - (p.row0 + 32 * half) - (lane & 7);              // row 8 k exists: 8 k < left
+    // all four have read prev_lse (lse may be the same place) and the last piece's factors
+    if (!meet(sm, &sm.out_meet[half], nm, lane, a.ws)) return;
+    sm.own[half][lane] = own;
+    __syncwarp();
+    if (lane == 0) arrive(&sm.stat_empty);
     uint4 old[4];
     float share[4];
     if (join) {
@@ -607,32 +756,11 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       }
     }
     if (p.n > 0) {
-      if (!dead && !wait_warp(sm, &sm.o_full, nq & 1, a.ws)) dead = true;
+      if (!wait_warp(sm, &sm.o_full, nq & 1, a.ws)) return;
       tc::tc_fence_after_sync();
     }
-    __syncwarp();
-    if (w.pieces > 1) {
-      // a piece: its own softmax in fp32, for the merge
-      if (!dead) {
-        if (quarter == 0) {
-          a.part_lse[u * kWinRows + 32 * half + lane] = lse;
-          if (u % w.pieces == 0 && rw == 0 && lane == 0)
-            a.tiles[u / w.pieces] = make_int2(int(row0), min(kWinRows, rows - p.row0));
-        }
-        if (p.n > 0) {
-#pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
-            float o[32];
-            tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
-            float* dst = a.part_o + (int64_t(u) * kWinRows + 32 * half) * kLatent + 128 * mt + e;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (p.row0 + 32 * half + i < rows) dst[i * kLatent] = o[i] * sm.ref[half][i];
-          }
-        }
-      }
-    } else if (!dead) {
-      if (quarter == 0 && lr < rows) a.lse[row0 + lane] = lse;
+    if (whole) {
+      if (quarter == 0 && lane < have) a.lse[row0 + lane] = lse;
 #pragma unroll 1
       for (int mt = 0; mt < 4; ++mt) {
         float o[32];
@@ -640,7 +768,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
           tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
 #pragma unroll
           for (int i4 = 0; i4 < 8; ++i4) {
-            const float4 f = reinterpret_cast<const float4*>(sm.ref[half])[i4];
+            const float4 f = reinterpret_cast<const float4*>(sm.own[half])[i4];
             o[4 * i4] *= f.x;
             o[4 * i4 + 1] *= f.y;
             o[4 * i4 + 2] *= f.z;
@@ -682,6 +810,24 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
             *reinterpret_cast<uint4*>(a.out + at + 8 * k * kLatent + 128 * mt) =
                 make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
+    } else {
+      // a piece: its own softmax in fp32, for the merge
+      const int u = p.unit;
+      if (quarter == 0) {
+        a.part_lse[u * kWinRows + 32 * half + lane] = lse;
+        if (u % pieces == 0 && ow == 0 && lane == 0) a.tiles[u / pieces] = make_int2(p.row, p.have);
+      }
+      if (p.n > 0) {
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          float o[32];
+          tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
+          float* dst = a.part_o + (int64_t(u) * kWinRows + 32 * half) * kLatent + 128 * mt + e;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < have) dst[i * kLatent] = o[i] * sm.own[half][i];
+        }
+      }
     }
     if (p.n > 0) {
       tc::tc_fence_before_sync();
@@ -689,15 +835,15 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       if (lane == 0) arrive(&sm.o_empty);
       ++nq;
     }
-    bar_sync(1 + half, 128);                         // the sums and factors have been read
   }
 }
 
+template <bool kCompact, bool kJoin>
 __global__ void __launch_bounds__(kWinThreads, 1)
     window_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ WindowMaps m) {
   extern __shared__ __align__(1024) uint8_t base[];  // 1024-byte aligned: checked below
   __shared__ WinSmall sm;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // the same for the warp, to the compiler too
   if (tc::smem_u32(base) & 1023u) {                  // never, as laid out
     pdl_wait();
     if (tid == 0) raise_err(a.ws, CSA2_DEV_TIMEOUT);
@@ -705,19 +851,27 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   }
   if (wid == kMmaWarp) tc::tmem_alloc(&sm.tmem_slot, kCols);
   if (tid == 0) {
-    tc::mbar_init(&sm.q_full, kGroups - 1);
-    tc::mbar_init(&sm.q_empty, 1);
-    tc::mbar_init(&sm.q8_full, 1);
-    tc::mbar_init(&sm.q8_empty, 1);
     for (int g = 0; g < kGroups; ++g) {
+      tc::mbar_init(&sm.q_full[g], 1);
+      tc::mbar_init(&sm.q_empty[g], 1);
       tc::mbar_init(&sm.k_full[g], 1);
       tc::mbar_init(&sm.k_empty[g], 1);
     }
     tc::mbar_init(&sm.s_full, 1);
     tc::mbar_init(&sm.p_full, kRowWarps);
     tc::mbar_init(&sm.o_full, 1);
-    tc::mbar_init(&sm.o_empty, kRowWarps);
+    tc::mbar_init(&sm.o_empty, kOutWarps);
     tc::mbar_init(&sm.drain, 1);
+    tc::mbar_init(&sm.stat_full, kRowWarps);
+    tc::mbar_init(&sm.stat_empty, kOutWarps);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.meet[i], 4);
+      tc::mbar_init(&sm.out_meet[i], 4);
+    }
+    for (int i = 0; i < kPlanSlots; ++i) {
+      tc::mbar_init(&sm.plan_full[i], 1);
+      tc::mbar_init(&sm.plan_empty[i], kReaders);
+    }
     tc::fence_mbar_init();
     sm.abort = 0;
     sm.bad = 0;
@@ -742,7 +896,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
       if (blockIdx.x == 0) check_ctx(__ldg(a.ctx_len + b), a.d, paged, a.ws);
       tiles += tiles_of(a, s1 - s0);
-      if (s1 > s0) {
+      if (!kCompact && s1 > s0) {
         const int64_t see = min64(context(a, b), int64_t(a.window) + min(span, s1 - s0) - 1 + a.sinks);
         blocks = max(blocks, int((see + kWinPos - 1) / kWinPos));
       }
@@ -750,9 +904,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     if (bad) atomicOr(&sm.bad, 1);
     tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
     blocks = __reduce_max_sync(0xFFFFFFFFu, blocks);
-    if (lane == 0) {
+    if (lane == 0 && tiles > 0) {
       atomicAdd(&sm.tiles, tiles);
-      atomicMax(&sm.blocks, blocks);
+      if (!kCompact) atomicMax(&sm.blocks, blocks);
     }
   }
   tc::tc_fence_before_sync();
@@ -762,25 +916,35 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   const int tiles = sm.bad ? 0 : sm.tiles, grid = gridDim.x;
   Span w;
   w.pieces = 1;
-  if (a.may_split && tiles > 0 && 2 * tiles <= grid && sm.blocks >= kMinSplit) w.pieces = min(grid / tiles, sm.blocks);
-  if (a.compact) {
+  if (kCompact) {
     // consecutive tiles share most of their rows
     w.first = int(int64_t(tiles) * blockIdx.x / grid);
     w.units = int(int64_t(tiles) * (blockIdx.x + 1) / grid);
     w.step = 1;
   } else {
+    if (a.may_split && tiles > 0 && 2 * tiles <= grid && sm.blocks >= kMinSplit) w.pieces = min(grid / tiles, sm.blocks);
     w.first = blockIdx.x;
     w.units = tiles * w.pieces;
     w.step = grid;
   }
   if (blockIdx.x == 0 && tid == 0) {
     if (sm.bad) raise_err(a.ws, CSA2_DEV_Q_START);
-    a.head[0] = tiles;
-    a.head[1] = w.pieces;
+    if (!kCompact) {
+      a.head[0] = tiles;
+      a.head[1] = w.pieces;
+    }
   }
-  if (wid < kRowWarps) row_role(a, sm, base, w, wid, lane, tmem);
-  else if (wid == kMmaWarp) mma_role(a, sm, base, w, lane, tmem);
-  else load_role(a, sm, base, w, wid - kLoadWarp0, lane, m);
+  if (wid < kRowWarps) {
+    regs_up<kRowRegs>();
+    row_role<kCompact>(a, sm, base, wid, lane, tmem);
+  } else if (wid < kMmaWarp) {
+    out_role<kCompact, kJoin>(a, sm, w.pieces, wid - kOutWarp0, lane, tmem);
+  } else {
+    regs_down<kMoveRegs>();
+    if (wid == kMmaWarp) mma_role<kCompact>(a, sm, base, lane, tmem);
+    else if (wid < kPlanWarp) load_role<kCompact>(a, sm, base, wid - kLoadWarp0, lane, m);
+    else if (wid == kPlanWarp) plan_role<kCompact>(a, sm, w, lane);
+  }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
   __syncwarp();
   if (wid == kMmaWarp) {
@@ -892,8 +1056,11 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
     if (!encode_2d_cached(enc, &m.kv[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kDqk, rows, kDqk * 2, 64, 1u << i,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return cudaErrorUnknown;
-  static KernelAttrs attrs;
-  cudaError_t e = prepare_kernel(window_kernel, size_t(kWinSmem), false, attrs);
+  static KernelAttrs attrs[4];
+  const int which = (a.compact ? 2 : 0) + (a.prev_out ? 1 : 0);
+  auto kernel = which == 0 ? window_kernel<false, false> : which == 1 ? window_kernel<false, true>
+                : which == 2 ? window_kernel<true, false> : window_kernel<true, true>;
+  cudaError_t e = prepare_kernel(kernel, size_t(kWinSmem), false, attrs[which]);
   if (e != cudaSuccess) return e;
   // bounds of what the device will find: tiles, and blocks of one
   int odd = H;                                       // 64 less the greatest common divisor: what a sequence's last tile may lack
@@ -908,9 +1075,9 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   const int64_t see = min64(ctx, int64_t(a.window) + span - 1 + a.sinks), blocks = (see + kWinPos - 1) / kWinPos;
   const int64_t grid = min64(min64(device_sms(), kWinMaxCtas), max64(1, tiles * blocks));
   // fewer tiles than half of the SMs, at least: their positions may be split
-  a.may_split = blocks >= kMinSplit && 2 * (int64_t(a.total_q) * H / kWinRows) <= grid;
+  a.may_split = !a.compact && blocks >= kMinSplit && 2 * (int64_t(a.total_q) * H / kWinRows) <= grid;
   CSA2_PROFILED(st, "window_attn",
-                (e = launch_pdl(window_kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, m)));
+                (e = launch_pdl(kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, m)));
   if (e != cudaSuccess || !a.may_split) return e;
   CSA2_PROFILED(st, "window_merge",
                 (e = launch_pdl(window_merge_kernel, dim3(kWinRows / kMergeRows, unsigned(min64(tiles, grid / 2))),
