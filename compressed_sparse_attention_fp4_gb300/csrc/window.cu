@@ -44,7 +44,7 @@ constexpr int kWinSmem = kPOff + kPHalf;
 constexpr uint32_t kOCol = 64;                       // tensor memory: S^T 64 columns, O^T 4 x 64
 constexpr uint32_t kCols = 512;
 constexpr int kMinSplit = 3;                         // least blocks a tile's positions are split from
-constexpr int kPlanSlots = 4;
+constexpr int kPlanSlots = 3;
 
 // One piece of a tile's work.  Its tokens see the positions lo .. last and the sinks before lo.
 //   Compact calls: all of them fit a block of 128 places.  Position t has place t (t < sinks) or
@@ -58,14 +58,16 @@ struct __align__(16) Piece {
   int lo, last;
   int pos, rem;                 // the first row's token position and head
   int blk, np;                  // first block; pages (sinks' and window's)
-  int sp, fresh;                // sinks' pages; compact: first position that the tile before has not left in its place (0: none left)
-  int turn;                     // compact: (last - sinks) % (128 - sinks), -1 where last < sinks
+  int sp;                       // sinks' pages
   int unit;
-  int spare[2];
+  // compact calls have in place of the last four:
+  __device__ int& fresh() { return blk; }            // first position that the tile before has not left in its place (0: none left)
+  __device__ int& turn() { return np; }              // (last - sinks) % (128 - sinks), -1 where last < sinks
+  __device__ int turn() const { return np; }
 };
 
 struct WinSmall {
-  uint64_t q_full[kGroups], q_empty[kGroups];        // queries and cache rows by channel group
+  uint64_t q_full[2], q_empty[kGroups];              // queries and cache rows by channel group (full: latent, rope channels)
   uint64_t k_full[kGroups], k_empty[kGroups];
   uint64_t s_full, p_full, o_full, o_empty, drain;
   uint64_t stat_full, stat_empty;
@@ -77,9 +79,8 @@ struct WinSmall {
   uint32_t hidden;                                   // 1 + the last block in which hide_values has changed the places
   int tiles, blocks;                                 // tiles of the call; most blocks of one
   Piece plan[kPlanSlots];
-  // of the rows of a half, for all lanes of its four warps, which write the same values
-  __align__(16) float ref[2][32];                    // softmax reference
-  __align__(16) float own[2][32];                    // factor of the outputs
+  __align__(16) float factor[kRowWarps][32];         // of a warp's weights, by row
+  __align__(16) float own[2][32];                    // of the outputs of a half's rows (its four warps write the same values)
   __align__(16) float top[4][kWinRows];              // maxima of a block by lane quarter; at the end of a piece the sums
   __align__(16) float sum_ref[kWinRows];             // their reference
 };
@@ -126,7 +127,7 @@ template <int n>
 __device__ inline void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
 template <int n>
 __device__ inline void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
-constexpr int kWinRegs = 80, kRowRegs = 104, kOutRegs = 80, kMoveRegs = 56;
+constexpr int kWinRegs = 80, kRowRegs = 96, kOutRegs = 88, kMoveRegs = 56;
 static_assert(kRowWarps * kRowRegs + kOutWarps * kOutRegs + 8 * kMoveRegs <= kWinRegs * (kWinThreads / 32),
               "a split above what was launched would wait for ever");
 
@@ -141,10 +142,13 @@ __device__ inline uint32_t bf16x2_rn(float lo, float hi) {
   return r;
 }
 
-// 32 values a lane reduced over the warp: lane l gets the sum or maximum of value l (31 shuffles; 130
-// cycles, where 32 reductions by redux take 2,950).
-template <bool kMax>
-__device__ inline float butterfly(const float (&x)[32], int lane) {
+__device__ inline float max_over_warp(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 32 values a lane summed over the warp: lane l gets the sum of value l (31 shuffles).
+__device__ inline float butterfly_sum(const float (&x)[32], int lane) {
   float v[16];
 #pragma unroll
   for (int half = 16; half >= 1; half >>= 1) {
@@ -153,8 +157,7 @@ __device__ inline float butterfly(const float (&x)[32], int lane) {
     for (int i = 0; i < half; ++i) {
       const float lo = half == 16 ? x[i] : v[i], hi = half == 16 ? x[half + i] : v[half + i];
       const float keep = up ? hi : lo, give = up ? lo : hi;
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, give, half);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, half);
     }
   }
   return v[0];
@@ -194,10 +197,10 @@ template <bool kCompact>
 __device__ inline int place_position(const WindowArgs& a, const Piece& p, int j, int e) {
   if (kCompact) {
     if (e < a.sinks) return e <= p.last ? e : -1;
-    int d = p.turn - (e - a.sinks);                  // places from e on to the last position's
+    int d = p.turn() - (e - a.sinks);                  // places from e on to the last position's
     if (d < 0) d += kWinPos - a.sinks;
     const int t = p.last - d;
-    return p.turn >= 0 && t >= max(p.lo, a.sinks) ? t : -1;
+    return p.turn() >= 0 && t >= max(p.lo, a.sinks) ? t : -1;
   }
   const int i = 2 * (p.blk + j) + (e >> 6);
   const int t = (i < p.sp ? i : p.lo / kPage + i - p.sp) * kPage + (e & (kPage - 1));
@@ -279,8 +282,8 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
       p.unit = u;
       if (kCompact) {
         p.n = p.last >= 0;
-        p.fresh = p.seq == was_seq ? was_last + 1 : 0;
-        p.turn = p.last >= a.sinks ? (p.last - a.sinks) % (kWinPos - a.sinks) : -1;
+        p.fresh() = p.seq == was_seq ? was_last + 1 : 0;
+        p.turn() = p.last >= a.sinks ? (p.last - a.sinks) % (kWinPos - a.sinks) : -1;
         if (p.n > 0) {
           was_seq = p.seq;
           was_last = p.last;
@@ -315,12 +318,12 @@ __device__ inline bool next_piece(WinSmall& sm, uint32_t& k, int lane, uint8_t* 
   return p.n >= 0;
 }
 
-// The four warps of a half meet (bounded, unlike a hardware barrier).
-__device__ inline bool meet(WinSmall& sm, uint64_t* bar, uint32_t& n, int lane, uint8_t* ws) {
+// The four warps of a half meet (bounded, unlike a hardware barrier), in two steps.
+__device__ inline void meet_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) arrive(bar);
-  return wait_warp(sm, bar, n++ & 1, ws);
 }
+__device__ inline bool meet_wait(WinSmall& sm, uint64_t* bar, uint32_t& n, uint8_t* ws) { return wait_warp(sm, bar, n++ & 1, ws); }
 
 // ---------------------------------------------------------------------------
 // Copies
@@ -398,6 +401,7 @@ constexpr int kFewRows = 4, kFewChunks = kFewRows * 16 / 32;
 template <bool kCompact>
 __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, int g, int lane, const WindowMaps& m) {
   const int regions = g < 4 ? 2 : 1, shift = g < 4 ? 4 : 3;            // (16-byte pieces of a row: 1 << shift)
+  uint64_t* const q_full = &sm.q_full[g == 4];
   Piece p;
   uint32_t nu = 0, nq = 0, nk = 0;
   while (next_piece(sm, nu, lane, a.ws, p)) {
@@ -408,11 +412,11 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
     uint4 v[kFewChunks];
     uint32_t to[kFewChunks];                         // offsets in the block, ~0: none
     if (kCompact) {
-      few = p.fresh > 0 && p.last - p.fresh < kFewRows;
+      few = p.fresh() > 0 && p.last - p.fresh() < kFewRows;
       if (few) {
 #pragma unroll
         for (int i = 0; i < kFewChunks; ++i) {
-          const int c = lane + 32 * i, t = p.fresh + (c >> shift), r = 2 * g + (c >> 3 & (regions - 1));
+          const int c = lane + 32 * i, t = p.fresh() + (c >> shift), r = 2 * g + (c >> 3 & (regions - 1));
           to[i] = ~0u;
           if (t > p.last) continue;
           const int row = row_of(a, p.seq, t);
@@ -420,7 +424,7 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
             lost = true;
             continue;
           }
-          int d = p.turn - (p.last - t);
+          int d = p.turn() - (p.last - t);
           if (d < 0) d += kWinPos - a.sinks;
           to[i] = r * kKReg + tc::sw128_offset(t < a.sinks ? t : a.sinks + d, c & 7);
           v[i] = __ldg(reinterpret_cast<const uint4*>(a.kv + int64_t(row) * kDqk + 64 * r) + (c & 7));
@@ -431,10 +435,10 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
     }
     if (!wait_warp(sm, &sm.q_empty[g], (nq++ & 1) ^ 1, a.ws)) return;
     if (lane == 0) {
-      tc::mbar_expect_tx(&sm.q_full[g], uint32_t(regions * kQReg));
+      tc::mbar_expect_tx(q_full, uint32_t(regions * kQReg));
 #pragma unroll 1
       for (int r = 2 * g; r < 2 * g + regions; ++r)
-        tc::tma_load_2d(&m.q, base + kQOff + r * kQReg, 64 * r, p.row, &sm.q_full[g]);
+        tc::tma_load_2d(&m.q, base + kQOff + r * kQReg, 64 * r, p.row, q_full);
       // the next tile's queries are the next rows: to L2
       const int64_t more = min64(kWinRows, int64_t(a.total_q) * a.d.heads - p.row - kWinRows);
       if (kCompact && g == 4 && more > 0)
@@ -520,8 +524,10 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
   const uint32_t leader = elect_one();
   Piece p;
   uint32_t nu = 0, nq = 0, nk = 0;
-  while (next_piece(sm, nu, lane, a.ws, p)) {
+  bool more = next_piece(sm, nu, lane, a.ws, p);
+  while (more) {
     const int n = p.n;
+    if (n == 0) more = next_piece(sm, nu, lane, a.ws, p);
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++nk) {
       // a channel group at a time: two regions, rope one
@@ -536,11 +542,11 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         if (j == n - 1 && (g < 4 || !kCompact)) commit_lo(leader, &sm.q_empty[g]);
       };
       const auto ready = [&](int g) {
-        if (j == 0 && !wait_warp(sm, &sm.q_full[g], nq & 1, a.ws)) return false;
         if (!wait_warp(sm, &sm.k_full[g], nk & 1, a.ws)) return false;
         tc::tc_fence_after_sync();
         return true;
       };
+      if (j == 0 && !wait_warp(sm, &sm.q_full[0], nq & 1, a.ws)) return;
       if (!ready(0)) return;
       scores(0, std::true_type{}, std::integral_constant<int, 2>{});
 #pragma unroll 1
@@ -548,10 +554,12 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         if (!ready(g)) return;
         scores(g, std::false_type{}, std::integral_constant<int, 2>{});
       }
+      if (j == 0 && !wait_warp(sm, &sm.q_full[1], nq & 1, a.ws)) return;
       if (!ready(4)) return;
       scores(4, std::false_type{}, std::integral_constant<int, 1>{});
       commit_lo(leader, &sm.s_full);
       if (kCompact) commit_lo(leader, &sm.k_empty[4]);
+      if (j == n - 1) more = next_piece(sm, nu, lane, a.ws, p);           // ahead: nothing between this piece's last product and its scores
       if (!wait_warp(sm, &sm.p_full, nk & 1, a.ws)) return;
       if (j == 0 && !wait_warp(sm, &sm.o_empty, (nq & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
@@ -611,12 +619,14 @@ __device__ inline void mask_scores(const WindowArgs& a, WinSmall& sm, uint8_t* b
 
 // Softmax over a block's positions (tensor-memory lanes).  Warp rw has the lanes 32 (rw % 4) .. + 31
 // and the rows 32 (rw / 4) .. + 31; lane i keeps the state of row i of these (alike in the four warps
-// of a half, but for the sum, which is of its own lanes).
+// of a half, but for the sum, which is of its own lanes).  A warp's weights are formed under its own
+// maxima while it waits for the other warps', and then brought to the common reference.
+constexpr float kNone = -3.0e38f;                    // maximum of no scores
 template <bool kCompact>
 __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, int rw, int lane, uint32_t tmem) {
   const int quarter = rw & 3, half = rw >> 2, e = 32 * quarter + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(32 * half);
-  const float c2 = a.scale * 1.4426950408889634f;
+  const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);        // logits in base 2 per score
   uint8_t* const p_at = base + p_offset<kCompact>(quarter >> 1);
   Piece p;
   uint32_t nu = 0, nk = 0, nm = 0;
@@ -624,7 +634,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
     // tokens of the warp's rows: the first one's position and its row's head, the last one's position
     const int r0 = p.rem + 32 * half, tok = r0 / a.d.heads, rem = r0 - tok * a.d.heads;
     const int p_min = p.pos + tok, p_max = p.pos + (p.rem + max(min(32 * half + 31, p.have - 1), 0)) / a.d.heads;
-    float ref = -INFINITY, sum = 0.0f;
+    float ref = kNone, sum = 0.0f;
     int t, row;
     const auto look = [&](int j) {
       t = place_position<kCompact>(a, p, j, e);
@@ -642,38 +652,56 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       tc::tc_fence_after_sync();
       float x[32];
       tc::tmem_ld32(lanes, x);
+      if (a.scale < 0.0f) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] *= c2;
+        for (int i = 0; i < 32; ++i) x[i] = -x[i];
+      }
       if (edge) {
         mask_scores(a, sm, base, x, t, p_min, rem, e, nk);
         __syncwarp();
       }
-      float top = butterfly<true>(x, lane);
-      sm.top[quarter][32 * half + lane] = top;       // (read before the other warps' P, which these scores came after)
-      if (!meet(sm, &sm.meet[half], nm, lane, a.ws)) return;
+      float top = kNone;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, sm.top[k][32 * half + lane]);
+      for (int i = 0; i < 32; ++i) {
+        const float m = max_over_warp(x[i]);
+        if (lane == i) top = m;
+      }
+      top = fmaxf(top * c, kNone);
+      sm.top[quarter][32 * half + lane] = top;       // (read before the other warps' P, which these scores came after)
+      meet_arrive(&sm.meet[half], lane);
+#pragma unroll
+      for (int i4 = 0; i4 < 8; ++i4) {
+        const float4 m = reinterpret_cast<const float4*>(&sm.top[quarter][32 * half])[i4];
+        x[4 * i4] = ex2(fmaf(x[4 * i4], c, -m.x));
+        x[4 * i4 + 1] = ex2(fmaf(x[4 * i4 + 1], c, -m.y));
+        x[4 * i4 + 2] = ex2(fmaf(x[4 * i4 + 2], c, -m.z));
+        x[4 * i4 + 3] = ex2(fmaf(x[4 * i4 + 3], c, -m.w));
+      }
+      if (!meet_wait(sm, &sm.meet[half], nm, a.ws)) return;
+      float most = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) most = fmaxf(most, sm.top[k][32 * half + lane]);
       float alpha = 1.0f;
-      if (top > ref + 8.0f) {
-        const float to = ceilf(top);
-        if (ref != -INFINITY) alpha = ex2(ref - to);
+      if (most > ref + 8.0f) {
+        const float to = ceilf(most);
+        if (ref != kNone) alpha = ex2(ref - to);
         ref = to;
       }
-      sm.ref[half][lane] = ref == -INFINITY ? 0.0f : ref;
+      sm.factor[rw][lane] = ex2(top - fmaxf(ref, -1.0e38f));
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
         // the outputs so far to the new reference (this block's scores came after the last product: the
         // copies that they needed waited for it)
         sum *= alpha;
 #pragma unroll 1
-        for (int c = 0; c < 32; c += 8)
+        for (int col = 0; col < 32; col += 8)
 #pragma unroll 1
           for (int mt = 0; mt < 4; ++mt) {
             float o[8];
-            tc::tmem_ld8(lanes + kOCol + 64 * mt + c, o);
+            tc::tmem_ld8(lanes + kOCol + 64 * mt + col, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= __shfl_sync(0xFFFFFFFFu, alpha, c + i);
-            tc::tmem_st8(lanes + kOCol + 64 * mt + c, o);
+            for (int i = 0; i < 8; ++i) o[i] *= __shfl_sync(0xFFFFFFFFu, alpha, col + i);
+            tc::tmem_st8(lanes + kOCol + 64 * mt + col, o);
           }
       }
 #pragma unroll
@@ -681,12 +709,12 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         uint32_t pk[4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float4 r4 = reinterpret_cast<const float4*>(sm.ref[half])[2 * i8 + k];
+          const float4 f = reinterpret_cast<const float4*>(sm.factor[rw])[2 * i8 + k];
           const int i = 8 * i8 + 4 * k;
-          x[i] = ex2(x[i] - r4.x);
-          x[i + 1] = ex2(x[i + 1] - r4.y);
-          x[i + 2] = ex2(x[i + 2] - r4.z);
-          x[i + 3] = ex2(x[i + 3] - r4.w);
+          x[i] *= f.x;
+          x[i + 1] *= f.y;
+          x[i + 2] *= f.z;
+          x[i + 3] *= f.w;
           pk[2 * k] = bf16x2_rn(x[i], x[i + 1]);
           pk[2 * k + 1] = bf16x2_rn(x[i + 2], x[i + 3]);
         }
@@ -696,11 +724,12 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       tc::tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive(&sm.p_full);
-      sum += butterfly<false>(x, lane);
+      sum += butterfly_sum(x, lane);
       if (j + 1 < p.n) look(j + 1);
     }
     // all have read the maxima: the sums go in their place
-    if (!meet(sm, &sm.meet[half], nm, lane, a.ws)) return;
+    meet_arrive(&sm.meet[half], lane);
+    if (!meet_wait(sm, &sm.meet[half], nm, a.ws)) return;
     sm.top[quarter][32 * half + lane] = sum;
     if (quarter == 0) sm.sum_ref[32 * half + lane] = ref;
     __syncwarp();
@@ -710,8 +739,21 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 
 // ---------------------------------------------------------------------------
 // Outputs, from tensor memory: lanes are channels, columns are rows.  The products take five sixths of
-// shared memory's bandwidth, so values cross the lanes by shuffles, few of them.
+// shared memory's bandwidth, which shuffles share, so values go out as they lie, 64 bytes of a row an
+// instruction.  (Eight channels of four rows a lane, by 32 shuffles for 32 x 32 values: as many lines
+// for the stores, and the shuffles beside them.)  Joined outputs do take that way: the other attention's
+// come in 16-byte pieces (two bytes a lane: a decode batch in 29 us instead of 17).
 // ---------------------------------------------------------------------------
+__device__ inline void load_factors(const float (&own)[32], float (&f)[32]) {
+#pragma unroll
+  for (int i4 = 0; i4 < 8; ++i4) {
+    const float4 v = reinterpret_cast<const float4*>(own)[i4];
+    f[4 * i4] = v.x;
+    f[4 * i4 + 1] = v.y;
+    f[4 * i4 + 2] = v.z;
+    f[4 * i4 + 3] = v.w;
+  }
+}
 template <bool kCompact, bool kJoin>
 __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, int ow, int lane, uint32_t tmem) {
   const int quarter = ow & 3, half = ow >> 2, e = 32 * quarter + lane;
@@ -722,9 +764,6 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
   while (next_piece(sm, nu, lane, a.ws, p)) {
     const int have = p.have - 32 * half;             // rows of this half
     const int64_t row0 = int64_t(p.row) + 32 * half;
-    // after the transposition a lane has 8 channels of the rows 8 k + lane % 8
-    const int64_t at = (row0 + (lane & 7)) * kLatent + 32 * quarter + 8 * (lane >> 3);
-    const int left = have - (lane & 7);              // row 8 k exists: 8 k < left
     float prev = -INFINITY;
     if (join && lane < have) prev = a.prev_lse[row0 + lane];
     if (!wait_warp(sm, &sm.stat_full, (nu - 1) & 1, a.ws)) return;
@@ -733,7 +772,7 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
     for (int k = 0; k < 4; ++k) total += sm.top[k][32 * half + lane];
     const float ref = sm.sum_ref[32 * half + lane];
     float own = total != 0.0f ? 1.0f / total : 0.0f, other = 0.0f;
-    float lse = total != 0.0f ? ((ref == -INFINITY ? 0.0f : ref) + log2f(total)) * 0.6931471805599453f : -INFINITY;
+    float lse = total != 0.0f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
     if (join && prev != -INFINITY) {
       const float most = fmaxf(lse, prev), x0 = expf(lse - most), x1 = expf(prev - most);
       own *= x0 / (x0 + x1);
@@ -741,10 +780,14 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
       lse = most + logf(x0 + x1);
     }
     // all four have read prev_lse (lse may be the same place) and the last piece's factors
-    if (!meet(sm, &sm.out_meet[half], nm, lane, a.ws)) return;
+    meet_arrive(&sm.out_meet[half], lane);
+    if (!meet_wait(sm, &sm.out_meet[half], nm, a.ws)) return;
     sm.own[half][lane] = own;
     __syncwarp();
     if (lane == 0) arrive(&sm.stat_empty);
+    // joined outputs: after the transposition below a lane has 8 channels of the rows 8 k + lane % 8
+    const int64_t at = (row0 + (lane & 7)) * kLatent + 32 * quarter + 8 * (lane >> 3);
+    const int left = have - (lane & 7);              // row 8 k exists: 8 k < left
     uint4 old[4];
     float share[4];
     if (join) {
@@ -755,30 +798,27 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
         if (share[k] != 0.0f && 8 * k < left) old[k] = *reinterpret_cast<const uint4*>(a.prev_out + at + 8 * k * kLatent);
       }
     }
+    float f[32];
+    if (!join) load_factors(sm.own[half], f);
     if (p.n > 0) {
       if (!wait_warp(sm, &sm.o_full, nq & 1, a.ws)) return;
       tc::tc_fence_after_sync();
     }
     if (whole) {
       if (quarter == 0 && lane < have) a.lse[row0 + lane] = lse;
+      uint16_t* dst = a.out + row0 * kLatent + e;
 #pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt) {
+      for (int mt = 0; mt < 4; ++mt, dst += 128) {
         float o[32];
         if (p.n > 0) {
           tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
-#pragma unroll
-          for (int i4 = 0; i4 < 8; ++i4) {
-            const float4 f = reinterpret_cast<const float4*>(sm.own[half])[i4];
-            o[4 * i4] *= f.x;
-            o[4 * i4 + 1] *= f.y;
-            o[4 * i4 + 2] *= f.z;
-            o[4 * i4 + 3] *= f.w;
-          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.0f;
         }
-        uint32_t y[16];                              // 4 rows of 8 channels
+        if (join) load_factors(sm.own[half], f);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= f[i];
         if (join) {
           exchange<32, 1, 0>(o, lane);
           exchange<32, 2, 1>(o, lane);
@@ -786,29 +826,29 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t x[4] = {old[k].x, old[k].y, old[k].z, old[k].w};
+            uint32_t y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              y[4 * k + i] = bf16x2_rn(fmaf(share[k], __uint_as_float(x[i] << 16), o[8 * k + 2 * i]),
-                                       fmaf(share[k], __uint_as_float(x[i] & 0xFFFF0000u), o[8 * k + 2 * i + 1]));
+              y[i] = bf16x2_rn(fmaf(share[k], __uint_as_float(x[i] << 16), o[8 * k + 2 * i]),
+                               fmaf(share[k], __uint_as_float(x[i] & 0xFFFF0000u), o[8 * k + 2 * i + 1]));
             // the next channels' come while these go
             if (mt < 3 && share[k] != 0.0f && 8 * k < left)
               old[k] = *reinterpret_cast<const uint4*>(a.prev_out + at + 8 * k * kLatent + 128 * (mt + 1));
+            if (8 * k < left)
+              *reinterpret_cast<uint4*>(a.out + at + 8 * k * kLatent + 128 * mt) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (have >= 32) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint32_t y = bf16x2_rn(o[i], o[i + 1]);
+            dst[i * kLatent] = uint16_t(y);
+            dst[(i + 1) * kLatent] = uint16_t(y >> 16);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t z = bf16x2_rn(o[2 * i], o[2 * i + 1]);          // two rows of the lane's channel
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, z, 1);
-            y[i] = lane & 1 ? __byte_perm(got, z, 0x7632) : __byte_perm(z, got, 0x5410);
-          }
-          exchange<16, 1, 1>(y, lane);
-          exchange<16, 2, 2>(y, lane);
+          for (int i = 0; i < 32; ++i)
+            if (i < have) dst[i * kLatent] = uint16_t(bf16x2_rn(o[i], 0.0f));
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (8 * k < left)
-            *reinterpret_cast<uint4*>(a.out + at + 8 * k * kLatent + 128 * mt) =
-                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
     } else {
       // a piece: its own softmax in fp32, for the merge
@@ -825,7 +865,7 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
           float* dst = a.part_o + (int64_t(u) * kWinRows + 32 * half) * kLatent + 128 * mt + e;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (i < have) dst[i * kLatent] = o[i] * sm.own[half][i];
+            if (i < have) dst[i * kLatent] = o[i] * f[i];
         }
       }
     }
@@ -851,8 +891,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   }
   if (wid == kMmaWarp) tc::tmem_alloc(&sm.tmem_slot, kCols);
   if (tid == 0) {
+    tc::mbar_init(&sm.q_full[0], kGroups - 1);
+    tc::mbar_init(&sm.q_full[1], 1);
     for (int g = 0; g < kGroups; ++g) {
-      tc::mbar_init(&sm.q_full[g], 1);
       tc::mbar_init(&sm.q_empty[g], 1);
       tc::mbar_init(&sm.k_full[g], 1);
       tc::mbar_init(&sm.k_empty[g], 1);
@@ -938,6 +979,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     regs_up<kRowRegs>();
     row_role<kCompact>(a, sm, base, wid, lane, tmem);
   } else if (wid < kMmaWarp) {
+    regs_up<kOutRegs>();
     out_role<kCompact, kJoin>(a, sm, w.pieces, wid - kOutWarp0, lane, tmem);
   } else {
     regs_down<kMoveRegs>();
