@@ -77,12 +77,11 @@ struct WinSmall {
   int abort;
   int bad;                                           // q_start out of order
   uint32_t hidden;                                   // 1 + the last block in which hide_values has changed the places
-  int tiles, blocks;                                 // tiles of the call; most blocks of one
+  int tiles, tokens, most;                           // tiles of the call; most tokens of one, most positions that one sees
   Piece plan[kPlanSlots];
-  __align__(16) float factor[kRowWarps][32];         // of a warp's weights, by row
-  __align__(16) float own[2][32];                    // of the outputs of a half's rows (its four warps write the same values)
+  __align__(16) float factor[kRowWarps][32];         // of a warp's weights, by row; at the end of a piece the first warp's of a half: reference
+  __align__(16) float own[2][32], other[2][32];      // of the outputs of a half's rows, of the other attention's (its four warps write the same values)
   __align__(16) float top[4][kWinRows];              // maxima of a block by lane quarter; at the end of a piece the sums
-  __align__(16) float sum_ref[kWinRows];             // their reference
 };
 static_assert(kWinSmem + (sizeof(WinSmall) + 1023) / 1024 * 1024 <= 232448, "shared memory; the dynamic part starts on a multiple of its alignment");
 
@@ -127,7 +126,7 @@ template <int n>
 __device__ inline void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
 template <int n>
 __device__ inline void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
-constexpr int kWinRegs = 80, kRowRegs = 96, kOutRegs = 88, kMoveRegs = 56;
+constexpr int kWinRegs = 80, kRowRegs = 96, kOutRegs = 96, kMoveRegs = 48;
 static_assert(kRowWarps * kRowRegs + kOutWarps * kOutRegs + 8 * kMoveRegs <= kWinRegs * (kWinThreads / 32),
               "a split above what was launched would wait for ever");
 
@@ -163,25 +162,13 @@ __device__ inline float butterfly_sum(const float (&x)[32], int lane) {
   return v[0];
 }
 
-// One step of a transposition: register bit K goes to lane bit B and back.
-template <int N, int K, int B, typename T>
-__device__ inline void exchange(T (&v)[N], int lane) {
-  const bool up = lane >> B & 1;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i & K) continue;
-    const T give = up ? v[i] : v[i | K];
-    const T got = __shfl_xor_sync(0xFFFFFFFFu, give, 1 << B);
-    if (up) v[i] = got;
-    else v[i | K] = got;
-  }
-}
-
 // Context of sequence b (bad ones are reported by the first CTA's count, and taken as 0).
 __device__ inline int context(const WindowArgs& a, int b) {
   const int n = __ldg(a.ctx_len + b);
   return n < 0 || n > a.d.max_ctx || (a.page_table && n > int64_t(a.d.max_pages) * kPage) ? 0 : n;
 }
+// Row number over heads: a.by_heads = ceil(2^64 / heads), exact below 2^31 rows (0 for one head).
+__device__ inline int over_heads(const WindowArgs& a, int row) { return a.by_heads ? int(__umul64hi(uint64_t(row), a.by_heads)) : row; }
 // Tiles of a sequence of len tokens: 64 rows each.
 __device__ inline int tiles_of(const WindowArgs& a, int len) { return (len * a.d.heads + kWinRows - 1) / kWinRows; }
 
@@ -234,11 +221,10 @@ struct Span {
   int first, units, step, pieces;
 };
 
-template <bool kCompact>
-__device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& w, int lane) {
-  // 32 sequences, one a lane: from b0 on, `base` tiles before them
-  int b0 = 0, base = 0, from = 0, len = 0, ctx = 0, upto = 0;
-  const auto load = [&]() {
+// 32 sequences, one a lane: from b0 on, with `base` tiles before them.
+struct Sequences {
+  int b0, base, from, len, ctx, upto;
+  __device__ void load(const WindowArgs& a, int lane) {
     const int i = b0 + lane;
     from = len = ctx = upto = 0;
     if (i < a.batch) {
@@ -247,34 +233,42 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
       ctx = context(a, i);
       upto = tiles_of(a, len);
     }
+  }
+  __device__ void count(int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += y;
     }
-  };
-  load();
+  }
+};
+
+// `q`: the first 32 sequences, loaded.
+template <bool kCompact>
+__device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& w, Sequences& q, int lane) {
+  q.count(lane);
   int was_seq = -1, was_last = 0;
   uint32_t k = 0;
   for (int u = w.first;; u += w.step, ++k) {
     Piece p = {};
     p.n = -1;
     if (u < w.units) {
-      const int t = u / w.pieces, s = u - t * w.pieces;
+      const int t = w.pieces == 1 ? u : u / w.pieces, s = u - t * w.pieces;
       uint32_t past;
-      while ((past = __ballot_sync(0xFFFFFFFFu, base + upto > t)) == 0) {
-        base += __shfl_sync(0xFFFFFFFFu, upto, 31);
-        b0 += 32;
-        load();
+      while ((past = __ballot_sync(0xFFFFFFFFu, q.base + q.upto > t)) == 0) {
+        q.base += __shfl_sync(0xFFFFFFFFu, q.upto, 31);
+        q.b0 += 32;
+        q.load(a, lane);
+        q.count(lane);
       }
       const int i = __ffs(past) - 1;
-      const int tokens = __shfl_sync(0xFFFFFFFFu, len, i), c = __shfl_sync(0xFFFFFFFFu, ctx, i);
-      const int before = i > 0 ? __shfl_sync(0xFFFFFFFFu, upto, i - 1) : 0;
-      const int r0 = (t - base - before) * kWinRows, tok0 = r0 / a.d.heads;
-      const int tok1 = min(tokens - 1, (r0 + kWinRows - 1) / a.d.heads);
-      p.row = __shfl_sync(0xFFFFFFFFu, from, i) * a.d.heads + r0;
+      const int tokens = __shfl_sync(0xFFFFFFFFu, q.len, i), c = __shfl_sync(0xFFFFFFFFu, q.ctx, i);
+      const int before = i > 0 ? __shfl_sync(0xFFFFFFFFu, q.upto, i - 1) : 0;
+      const int r0 = (t - q.base - before) * kWinRows, tok0 = over_heads(a, r0);
+      const int tok1 = min(tokens - 1, over_heads(a, r0 + kWinRows - 1));
+      p.row = __shfl_sync(0xFFFFFFFFu, q.from, i) * a.d.heads + r0;
       p.have = min(kWinRows, tokens * a.d.heads - r0);
-      p.seq = b0 + i;
+      p.seq = q.b0 + i;
       p.pos = c - tokens + tok0;
       p.rem = r0 - tok0 * a.d.heads;
       p.last = c - tokens + tok1;
@@ -292,8 +286,8 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
         p.sp = min((a.sinks + kPage - 1) / kPage, p.lo / kPage);
         p.np = p.last < 0 ? 0 : p.sp + p.last / kPage - p.lo / kPage + 1;
         const int nb = (p.np + 1) / 2;
-        p.blk = nb * s / w.pieces;
-        p.n = nb * (s + 1) / w.pieces - p.blk;
+        p.blk = w.pieces == 1 ? 0 : nb * s / w.pieces;
+        p.n = w.pieces == 1 ? nb : nb * (s + 1) / w.pieces - p.blk;
       }
     }
     const uint32_t slot = k % kPlanSlots;
@@ -333,54 +327,26 @@ struct Box {
   int slot, row, lg;
 };
 
-// The positions first .. last of a compact tile as boxes, one a lane from lane `k` on: runs of
-// rows, cut at pages and where the places come round, in powers of two (a tile has at most 6 runs
-// of 128 rows together: at most 23 boxes).  `page`: lane i has the page ids of the first two pages
-// (lanes 0, 1) and of the window's (lanes 2 .. 5).  Returns their rows.
-__device__ inline int boxes(const WindowArgs& a, int seq, int lo, int first, int last, int page, int lane, int& k, Box& mine,
-                            bool& lost) {
-  int rows = 0;
-  for (int t = first; t <= last;) {
-    const int at = t / kPage;
-    int slot = t < a.sinks ? t : a.sinks + (t - a.sinks) % (kWinPos - a.sinks);
-    int n = min(last - t + 1, kWinPos - slot), row;
-    if (a.page_table) {
-      n = min(n, kPage - t % kPage);
-      const int pg = __shfl_sync(0xFFFFFFFFu, page, at < 2 ? at : 2 + at - lo / kPage);
-      row = pg < 0 || pg >= a.d.num_pages ? -1 : pg * kPage + t % kPage;
-    } else {
-      row = int(int64_t(seq) * a.d.max_ctx + t);
-    }
-    t += n;
-    if (row < 0) {
-      lost = true;
-      continue;
-    }
-    rows += n;
-    while (n > 0) {
-      const int lg = min(6, 31 - __clz(n));
-      if (k == lane) mine = {slot, row, lg};
-      ++k;
-      slot += 1 << lg;
-      row += 1 << lg;
-      n -= 1 << lg;
-    }
+// The positions first .. last (at most 128) of a sequence as boxes, one a lane: they are cut where
+// pages end and at `turn` (where the places come round) into up to four runs, each of them a sum of
+// powers of two; lane = 8 * run + 6 - power.  The place of a position is `shift` more than it before
+// `turn`, `shift - back` from there on.
+__device__ inline Box make_box(const WindowArgs& a, int seq, int first, int last, int turn, int shift, int back, int lane, bool& lost) {
+  const int end = last + 1, c1 = min((first / kPage + 1) * kPage, end), c2 = min(c1 + kPage, end);
+  const int c3 = min(max(turn, first), end);         // cuts: first, c1, c2, c3, end
+  const int lo = min(c1, c3), hi = max(c2, c3), mid = c1 + c2 + c3 - lo - hi;
+  const int r = lane >> 3, lg = 6 - (lane & 7);
+  const int from = r == 0 ? first : r == 1 ? lo : r == 2 ? mid : hi, to = r == 0 ? lo : r == 1 ? mid : r == 2 ? hi : end;
+  const int n = to - from;
+  Box box = {0, 0, -1};
+  if (n > 0 && lg >= 0 && (n >> lg & 1)) {
+    const int t = from + (n & ~((2 << lg) - 1));     // behind the larger powers
+    box.row = row_of(a, seq, t);
+    box.slot = t + shift - (t >= turn ? back : 0);
+    if (box.row >= 0) box.lg = lg;
+    else lost = true;
   }
-  return rows;
-}
-// All that a compact tile sees.
-__device__ __noinline__ int tile_boxes(const WindowArgs& a, int seq, int lo, int last, int lane, Box& mine, bool& lost) {
-  int page = -1, k = 0;
-  if (a.page_table && lane < 6) {
-    const int i = lane < 2 ? lane : lo / kPage + lane - 2;
-    if (i < a.d.max_pages && i * kPage <= last) page = __ldg(a.page_table + int64_t(seq) * a.d.max_pages + i);
-  }
-  mine.lg = -1;
-  int rows = 0;
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part)
-    rows += boxes(a, seq, lo, part == 0 ? 0 : max(lo, a.sinks), part == 0 ? min(a.sinks - 1, last) : last, page, lane, k, mine, lost);
-  return rows;
+  return box;
 }
 
 // Where P of a block's first and last 64 positions goes: over the block's rope channels, which only
@@ -406,11 +372,19 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
   uint32_t nu = 0, nq = 0, nk = 0;
   while (next_piece(sm, nu, lane, a.ws, p)) {
     if (p.n == 0) continue;
-    Box box;
+    Box box[2];                                      // the window's, the sinks'
     int rows = 0;
     bool lost = false, few = false;
     uint4 v[kFewChunks];
     uint32_t to[kFewChunks];                         // offsets in the block, ~0: none
+    const auto whole = [&]() {
+      const int first = max(p.lo, a.sinks), c = kWinPos - a.sinks;
+      // the last position has place sinks + turn(): `turn()` positions before it is the first place
+      box[0] = make_box(a, p.seq, first, max(p.last, first - 1), p.last - p.turn(), a.sinks + p.turn() - p.last + c, c, lane, lost);
+      box[1].lg = -1;
+      if (a.sinks > 0) box[1] = make_box(a, p.seq, 0, min(a.sinks - 1, p.last), 1 << 30, 0, 0, lane, lost);
+      rows = __reduce_add_sync(0xFFFFFFFFu, (box[0].lg >= 0 ? 1 << box[0].lg : 0) + (box[1].lg >= 0 ? 1 << box[1].lg : 0));
+    };
     if (kCompact) {
       few = p.fresh() > 0 && p.last - p.fresh() < kFewRows;
       if (few) {
@@ -430,7 +404,7 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
           v[i] = __ldg(reinterpret_cast<const uint4*>(a.kv + int64_t(row) * kDqk + 64 * r) + (c & 7));
         }
       } else {
-        rows = tile_boxes(a, p.seq, p.lo, p.last, lane, box, lost);
+        whole();
       }
     }
     if (!wait_warp(sm, &sm.q_empty[g], (nq++ & 1) ^ 1, a.ws)) return;
@@ -451,7 +425,7 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
       // values of the tile before may have been taken out of their places
       if (few && g < 4 && nk > 0 && *reinterpret_cast<volatile uint32_t*>(&sm.hidden) == nk) {
         few = false;
-        rows = tile_boxes(a, p.seq, p.lo, p.last, lane, box, lost);
+        whole();
       }
       if (few) {
 #pragma unroll
@@ -463,10 +437,14 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
       } else {
         if (lane == 0) tc::mbar_expect_tx(&sm.k_full[g], uint32_t(regions * rows * 128));
         __syncwarp();
-        if (box.lg >= 0)
 #pragma unroll 1
-          for (int r = 2 * g; r < 2 * g + regions; ++r)
-            tc::tma_load_2d(&m.kv[box.lg], base + r * kKReg + box.slot * 128, 64 * r, box.row, &sm.k_full[g]);
+        for (int part = 0; part < 2; ++part) {
+          const Box b = part == 0 ? box[0] : box[1];
+          if (b.lg >= 0)
+#pragma unroll 1
+            for (int r = 2 * g; r < 2 * g + regions; ++r)
+              tc::tma_load_2d(&m.kv[b.lg], base + r * kKReg + b.slot * 128, 64 * r, b.row, &sm.k_full[g]);
+        }
       }
       ++nk;
     } else {
@@ -582,39 +560,32 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 // ---------------------------------------------------------------------------
 // Softmax
 // ---------------------------------------------------------------------------
-// Scores of a position t that not every row sees: those of rows that do not see it become -inf.
-// `pos`, `rem`: the first row's token position and head; tokens are `heads` rows each.  (Rows that do
-// not exist take part as if they did: nothing of theirs is used.)
-__device__ inline void mask_scores(const WindowArgs& a, WinSmall& sm, uint8_t* base, float (&x)[32], int t, int pos, int rem, int e,
-                                   uint32_t block) {
-  const uint32_t span = t < 0 ? 0u : t < a.sinks ? 0x7FFFFFFFu : uint32_t(a.window);   // seen by tokens t .. t + span - 1
+// Which of the warp's 32 rows see position t (bit i: row i).  `pos`, `rem`: the first row's token
+// position and head; tokens are `heads` rows each.  (Rows that do not exist take part as if they did:
+// nothing of theirs is used.)
+__device__ inline uint32_t seen_by(const WindowArgs& a, int t, int pos, int rem) {
+  if (t < 0) return 0u;
+  // rows from the first of token t on, to the last of token t + window - 1 (any, for a sink)
+  const int lo = (t - pos) * a.d.heads - rem, hi = t < a.sinks ? 32 : lo + a.window * a.d.heads;
+  if (lo >= 32 || hi <= 0) return 0u;
+  const uint32_t from = lo <= 0 ? ~0u : ~0u << lo;
+  return hi >= 32 ? from : from & ((1u << hi) - 1u);
+}
+
+// The scores of rows that do not see the lane's position become -inf.
+__device__ inline void mask_scores(WinSmall& sm, uint8_t* base, float (&x)[32], uint32_t see, int e, uint32_t block) {
   float any = 0.0f;                                  // 0, or NaN where a score is no number
-  int p = pos, h = rem;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     any = fmaf(x[i], 0.0f, any);
-    x[i] = uint32_t(p - t) < span ? x[i] : -INFINITY;
-    if (++h == a.d.heads) {
-      h = 0;
-      ++p;
-    }
+    x[i] = see >> i & 1 ? x[i] : -INFINITY;
   }
   if (any == 0.0f) return;
   // an infinity or NaN: rows that see the position become NaN; is it hidden from others, its values go
-  bool odd = false;
-  p = pos;
-  h = rem;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const bool see = uint32_t(p - t) < span;
-    odd = odd || !see;
-    if (see && !(fabsf(x[i]) < INFINITY)) x[i] = NAN;
-    if (++h == a.d.heads) {
-      h = 0;
-      ++p;
-    }
-  }
-  if (odd) hide_values(sm, base, e, block);
+  for (int i = 0; i < 32; ++i)
+    if ((see >> i & 1) && !(fabsf(x[i]) < INFINITY)) x[i] = NAN;
+  if (see != ~0u) hide_values(sm, base, e, block);
 }
 
 // Softmax over a block's positions (tensor-memory lanes).  Warp rw has the lanes 32 (rw % 4) .. + 31
@@ -631,9 +602,8 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
   Piece p;
   uint32_t nu = 0, nk = 0, nm = 0;
   while (next_piece(sm, nu, lane, a.ws, p)) {
-    // tokens of the warp's rows: the first one's position and its row's head, the last one's position
-    const int r0 = p.rem + 32 * half, tok = r0 / a.d.heads, rem = r0 - tok * a.d.heads;
-    const int p_min = p.pos + tok, p_max = p.pos + (p.rem + max(min(32 * half + 31, p.have - 1), 0)) / a.d.heads;
+    // the warp's first row: its token's position, its head
+    const int r0 = p.rem + 32 * half, tok = over_heads(a, r0), rem = r0 - tok * a.d.heads, pos = p.pos + tok;
     float ref = kNone, sum = 0.0f;
     int t, row;
     const auto look = [&](int j) {
@@ -646,8 +616,8 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 #pragma unroll 1
     for (int j = 0; j < p.n; ++j, ++nk) {
       if (row < 0) t = -1;
-      const bool all = t >= 0 && t <= p_min && (t > p_max - a.window || t < a.sinks);
-      const bool edge = !__all_sync(0xFFFFFFFFu, all);
+      const uint32_t see = seen_by(a, t, pos, rem);
+      const bool edge = !__all_sync(0xFFFFFFFFu, see == ~0u);
       if (!wait_warp(sm, &sm.s_full, nk & 1, a.ws)) return;
       tc::tc_fence_after_sync();
       float x[32];
@@ -657,7 +627,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         for (int i = 0; i < 32; ++i) x[i] = -x[i];
       }
       if (edge) {
-        mask_scores(a, sm, base, x, t, p_min, rem, e, nk);
+        mask_scores(sm, base, x, see, e, nk);
         __syncwarp();
       }
       float top = kNone;
@@ -731,7 +701,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
     meet_arrive(&sm.meet[half], lane);
     if (!meet_wait(sm, &sm.meet[half], nm, a.ws)) return;
     sm.top[quarter][32 * half + lane] = sum;
-    if (quarter == 0) sm.sum_ref[32 * half + lane] = ref;
+    if (quarter == 0) sm.factor[rw][lane] = ref;
     __syncwarp();
     if (lane == 0) arrive(&sm.stat_full);
   }
@@ -741,8 +711,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 // Outputs, from tensor memory: lanes are channels, columns are rows.  The products take five sixths of
 // shared memory's bandwidth, which shuffles share, so values go out as they lie, 64 bytes of a row an
 // instruction.  (Eight channels of four rows a lane, by 32 shuffles for 32 x 32 values: as many lines
-// for the stores, and the shuffles beside them.)  Joined outputs do take that way: the other attention's
-// come in 16-byte pieces (two bytes a lane: a decode batch in 29 us instead of 17).
+// for the stores, and the shuffles beside them.)
 // ---------------------------------------------------------------------------
 __device__ inline void load_factors(const float (&own)[32], float (&f)[32]) {
 #pragma unroll
@@ -754,11 +723,11 @@ __device__ inline void load_factors(const float (&own)[32], float (&f)[32]) {
     f[4 * i4 + 3] = v.w;
   }
 }
-template <bool kCompact, bool kJoin>
+template <bool kJoin>
 __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, int ow, int lane, uint32_t tmem) {
   const int quarter = ow & 3, half = ow >> 2, e = 32 * quarter + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(32 * half);
-  const bool whole = kCompact || pieces == 1, join = kJoin && whole;
+  const bool whole = pieces == 1, join = kJoin && whole;
   Piece p;
   uint32_t nu = 0, nq = 0, nm = 0;
   while (next_piece(sm, nu, lane, a.ws, p)) {
@@ -766,11 +735,29 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
     const int64_t row0 = int64_t(p.row) + 32 * half;
     float prev = -INFINITY;
     if (join && lane < have) prev = a.prev_lse[row0 + lane];
+    // Joined outputs: the other attention's of the lane's four channels, two rows a word, come while the
+    // scores and products are formed (but for rows of which it has seen nothing: they may be anything).
+    // Loops that shift the registers: straight code that runs once waits for its instructions.
+    uint32_t old[kJoin ? 64 : 1];
+    if constexpr (kJoin) {
+      const uint32_t use = __ballot_sync(0xFFFFFFFFu, prev != -INFINITY);
+      const uint16_t* src = a.prev_out + row0 * kLatent + e;
+#pragma unroll 1
+      for (int mt = 0; mt < 4; ++mt, src += 128) {
+#pragma unroll
+        for (int i = 0; i < 48; ++i) old[i] = old[i + 16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const uint32_t x = use >> i & 1 ? src[i * kLatent] : 0, y = use >> i & 2 ? src[(i + 1) * kLatent] : 0;
+          old[48 + i / 2] = x | y << 16;
+        }
+      }
+    }
     if (!wait_warp(sm, &sm.stat_full, (nu - 1) & 1, a.ws)) return;
     float total = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) total += sm.top[k][32 * half + lane];
-    const float ref = sm.sum_ref[32 * half + lane];
+    const float ref = sm.factor[4 * half][lane];
     float own = total != 0.0f ? 1.0f / total : 0.0f, other = 0.0f;
     float lse = total != 0.0f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
     if (join && prev != -INFINITY) {
@@ -783,23 +770,11 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
     meet_arrive(&sm.out_meet[half], lane);
     if (!meet_wait(sm, &sm.out_meet[half], nm, a.ws)) return;
     sm.own[half][lane] = own;
+    if (kJoin) sm.other[half][lane] = other;
     __syncwarp();
     if (lane == 0) arrive(&sm.stat_empty);
-    // joined outputs: after the transposition below a lane has 8 channels of the rows 8 k + lane % 8
-    const int64_t at = (row0 + (lane & 7)) * kLatent + 32 * quarter + 8 * (lane >> 3);
-    const int left = have - (lane & 7);              // row 8 k exists: 8 k < left
-    uint4 old[4];
-    float share[4];
-    if (join) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        share[k] = __shfl_sync(0xFFFFFFFFu, other, 8 * k + (lane & 7));
-        old[k] = make_uint4(0, 0, 0, 0);
-        if (share[k] != 0.0f && 8 * k < left) old[k] = *reinterpret_cast<const uint4*>(a.prev_out + at + 8 * k * kLatent);
-      }
-    }
-    float f[32];
-    if (!join) load_factors(sm.own[half], f);
+    float f[kJoin ? 1 : 32];
+    if constexpr (!kJoin) load_factors(sm.own[half], f);
     if (p.n > 0) {
       if (!wait_warp(sm, &sm.o_full, nq & 1, a.ws)) return;
       tc::tc_fence_after_sync();
@@ -807,47 +782,60 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
     if (whole) {
       if (quarter == 0 && lane < have) a.lse[row0 + lane] = lse;
       uint16_t* dst = a.out + row0 * kLatent + e;
+      if constexpr (kJoin) {
 #pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt, dst += 128) {
-        float o[32];
-        if (p.n > 0) {
-          tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
-        } else {
+        for (int mt = 0; mt < 4; ++mt, dst += 128) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          for (int i8 = 0; i8 < 32; i8 += 8) {
+            float o[8];
+            if (p.n > 0) {
+              tc::tmem_ld8(lanes + kOCol + 64 * mt + i8, o);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i4 = 0; i4 < 8; i4 += 4) {
+              const float4 u = *reinterpret_cast<const float4*>(&sm.own[half][i8 + i4]);
+              const float4 v = *reinterpret_cast<const float4*>(&sm.other[half][i8 + i4]);
+              const float own4[4] = {u.x, u.y, u.z, u.w}, other4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t w = old[(i8 + i4 + i) / 2];
+                o[i4 + i] = fmaf(other4[i], __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16), o[i4 + i] * own4[i]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i8 + i < have) dst[(i8 + i) * kLatent] = uint16_t(bf16x2_rn(o[i], 0.0f));
+          }
+#pragma unroll
+          for (int i = 0; i < 48; ++i) old[i] = old[i + 16];
         }
-        if (join) load_factors(sm.own[half], f);
+      } else {
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt, dst += 128) {
+          float o[32];
+          if (p.n > 0) {
+            tc::tmem_ld32(lanes + kOCol + 64 * mt, o);
+          } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= f[i];
-        if (join) {
-          exchange<32, 1, 0>(o, lane);
-          exchange<32, 2, 1>(o, lane);
-          exchange<32, 4, 2>(o, lane);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x[4] = {old[k].x, old[k].y, old[k].z, old[k].w};
-            uint32_t y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              y[i] = bf16x2_rn(fmaf(share[k], __uint_as_float(x[i] << 16), o[8 * k + 2 * i]),
-                               fmaf(share[k], __uint_as_float(x[i] & 0xFFFF0000u), o[8 * k + 2 * i + 1]));
-            // the next channels' come while these go
-            if (mt < 3 && share[k] != 0.0f && 8 * k < left)
-              old[k] = *reinterpret_cast<const uint4*>(a.prev_out + at + 8 * k * kLatent + 128 * (mt + 1));
-            if (8 * k < left)
-              *reinterpret_cast<uint4*>(a.out + at + 8 * k * kLatent + 128 * mt) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int i = 0; i < 32; ++i) o[i] = 0.0f;
           }
-        } else if (have >= 32) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const uint32_t y = bf16x2_rn(o[i], o[i + 1]);
-            dst[i * kLatent] = uint16_t(y);
-            dst[(i + 1) * kLatent] = uint16_t(y >> 16);
+          for (int i = 0; i < 32; ++i) o[i] *= f[i];
+          if (have >= 32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const uint32_t y = bf16x2_rn(o[i], o[i + 1]);
+              dst[i * kLatent] = uint16_t(y);
+              dst[(i + 1) * kLatent] = uint16_t(y >> 16);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < have) dst[i * kLatent] = uint16_t(bf16x2_rn(o[i], 0.0f));
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < have) dst[i * kLatent] = uint16_t(bf16x2_rn(o[i], 0.0f));
         }
       }
     } else {
@@ -865,7 +853,7 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
           float* dst = a.part_o + (int64_t(u) * kWinRows + 32 * half) * kLatent + 128 * mt + e;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (i < have) dst[i * kLatent] = o[i] * f[i];
+            if (i < have) dst[i * kLatent] = o[i] * sm.own[half][i];
         }
       }
     }
@@ -878,7 +866,7 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
   }
 }
 
-template <bool kCompact, bool kJoin>
+template <bool kJoin>
 __global__ void __launch_bounds__(kWinThreads, 1)
     window_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ WindowMaps m) {
   extern __shared__ __align__(1024) uint8_t base[];  // 1024-byte aligned: checked below
@@ -918,16 +906,20 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     sm.bad = 0;
     sm.hidden = 0;
     sm.tiles = 0;
-    sm.blocks = 0;
+    sm.tokens = 0;
+    sm.most = 0;
   }
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  // count the tiles; starts out of order are reported and the call writes nothing
+  Sequences first = {0, 0, 0, 0, 0, 0};
+  if (wid == kPlanWarp) first.load(a, lane);         // on their way while the tiles are counted
+  // Count the tiles, and what most their rows see.  Starts out of order are reported and the call
+  // writes nothing.
   {
     const bool paged = a.page_table != nullptr;
     const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;   // most tokens of a tile
-    int tiles = 0, blocks = 0;
+    int tiles = 0, tokens = 0, most = 0;
     bool bad = false;
     for (int b = tid; b < a.batch; b += kWinThreads) {
       const int s0 = __ldg(a.q_start + b), s1 = __ldg(a.q_start + b + 1);
@@ -937,17 +929,17 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
       if (blockIdx.x == 0) check_ctx(__ldg(a.ctx_len + b), a.d, paged, a.ws);
       tiles += tiles_of(a, s1 - s0);
-      if (!kCompact && s1 > s0) {
-        const int64_t see = min64(context(a, b), int64_t(a.window) + min(span, s1 - s0) - 1 + a.sinks);
-        blocks = max(blocks, int((see + kWinPos - 1) / kWinPos));
-      }
+      tokens = max(tokens, min(span, s1 - s0));
+      if (a.may_split && s1 > s0) most = max(most, int(min64(context(a, b), int64_t(a.window) + min(span, s1 - s0) - 1 + a.sinks)));
     }
     if (bad) atomicOr(&sm.bad, 1);
     tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
-    blocks = __reduce_max_sync(0xFFFFFFFFu, blocks);
+    tokens = __reduce_max_sync(0xFFFFFFFFu, tokens);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
     if (lane == 0 && tiles > 0) {
       atomicAdd(&sm.tiles, tiles);
-      if (!kCompact) atomicMax(&sm.blocks, blocks);
+      atomicMax(&sm.tokens, tokens);
+      if (a.may_split) atomicMax(&sm.most, most);
     }
   }
   tc::tc_fence_before_sync();
@@ -955,37 +947,47 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   tc::tc_fence_after_sync();
   const uint32_t tmem = sm.tmem_slot;
   const int tiles = sm.bad ? 0 : sm.tiles, grid = gridDim.x;
+  const bool compact = int64_t(a.window) + sm.tokens - 1 + a.sinks <= kWinPos;
   Span w;
   w.pieces = 1;
-  if (kCompact) {
+  if (compact) {
     // consecutive tiles share most of their rows
     w.first = int(int64_t(tiles) * blockIdx.x / grid);
     w.units = int(int64_t(tiles) * (blockIdx.x + 1) / grid);
     w.step = 1;
   } else {
-    if (a.may_split && tiles > 0 && 2 * tiles <= grid && sm.blocks >= kMinSplit) w.pieces = min(grid / tiles, sm.blocks);
+    const int blocks = (sm.most + kWinPos - 1) / kWinPos;
+    if (a.may_split && tiles > 0 && 2 * tiles <= grid && blocks >= kMinSplit) w.pieces = min(grid / tiles, blocks);
     w.first = blockIdx.x;
     w.units = tiles * w.pieces;
     w.step = grid;
   }
   if (blockIdx.x == 0 && tid == 0) {
     if (sm.bad) raise_err(a.ws, CSA2_DEV_Q_START);
-    if (!kCompact) {
+    if (a.may_split) {
       a.head[0] = tiles;
       a.head[1] = w.pieces;
     }
   }
   if (wid < kRowWarps) {
     regs_up<kRowRegs>();
-    row_role<kCompact>(a, sm, base, wid, lane, tmem);
+    if (compact) row_role<true>(a, sm, base, wid, lane, tmem);
+    else row_role<false>(a, sm, base, wid, lane, tmem);
   } else if (wid < kMmaWarp) {
     regs_up<kOutRegs>();
-    out_role<kCompact, kJoin>(a, sm, w.pieces, wid - kOutWarp0, lane, tmem);
+    out_role<kJoin>(a, sm, w.pieces, wid - kOutWarp0, lane, tmem);
   } else {
     regs_down<kMoveRegs>();
-    if (wid == kMmaWarp) mma_role<kCompact>(a, sm, base, lane, tmem);
-    else if (wid < kPlanWarp) load_role<kCompact>(a, sm, base, wid - kLoadWarp0, lane, m);
-    else if (wid == kPlanWarp) plan_role<kCompact>(a, sm, w, lane);
+    if (wid == kMmaWarp) {
+      if (compact) mma_role<true>(a, sm, base, lane, tmem);
+      else mma_role<false>(a, sm, base, lane, tmem);
+    } else if (wid < kPlanWarp) {
+      if (compact) load_role<true>(a, sm, base, wid - kLoadWarp0, lane, m);
+      else load_role<false>(a, sm, base, wid - kLoadWarp0, lane, m);
+    } else if (wid == kPlanWarp) {
+      if (compact) plan_role<true>(a, sm, w, first, lane);
+      else plan_role<false>(a, sm, w, first, lane);
+    }
   }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)
   __syncwarp();
@@ -1015,59 +1017,63 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 constexpr int kMergeRows = 4, kMergeThreads = kMergeRows * kLatent / 8;
 
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __grid_constant__ WindowArgs a) {
+  __shared__ float s_part[kMergeRows][kWinMaxCtas];
   pdl_wait();
   pdl_launch_dependents();
-  const int tiles = a.head[0], n = a.head[1], t = blockIdx.y;
+  const int tiles = __ldg(a.head), n = __ldg(a.head + 1), t = blockIdx.y;
   if (n <= 1 || t >= tiles) return;
-  const int2 tile = a.tiles[t];
-  const int r = blockIdx.x * kMergeRows + threadIdx.x / (kLatent / 8), c = threadIdx.x % (kLatent / 8) * 8;
+  const int2 tile = __ldg(a.tiles + t);
+  const int y = threadIdx.x / (kLatent / 8), r = blockIdx.x * kMergeRows + y, x = threadIdx.x % (kLatent / 8);
   const bool have = r < tile.y;
   const int64_t row = int64_t(tile.x) + r;
-  float top = -INFINITY, prev = -INFINITY;
-  if (have) {
-    for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_lse[(t * n + s) * kWinRows + r]);
-    if (a.prev_out) prev = a.prev_lse[row];
-  }
-  const float most = fmaxf(top, prev);
+  if (blockIdx.x * kMergeRows >= tile.y) return;
+  // weights of the pieces and of the other attention, by row
+  for (int s = x; s < n; s += kLatent / 8) s_part[y][s] = __ldg(a.part_lse + (t * n + s) * kWinRows + r);
+  const float prev = have && a.prev_out ? a.prev_lse[row] : -INFINITY;
+  uint4 old = make_uint4(0, 0, 0, 0);
+  if (prev != -INFINITY) old = *reinterpret_cast<const uint4*>(a.prev_out + row * kLatent + 8 * x);
+  __syncthreads();                                   // (and every row's prev_lse has been read: lse may be the same place)
+  if (!have) return;
+  float most = prev;
+  for (int s = 0; s < n; ++s) most = fmaxf(most, s_part[y][s]);
   float o[8], total = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) o[k] = 0.0f;
-  if (have) {
-    for (int s = 0; s < n; ++s) {
-      const float l = a.part_lse[(t * n + s) * kWinRows + r];
-      if (l == -INFINITY) continue;                  // (that piece has written no outputs)
-      const float f = expf(l - most);
-      total += f;
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + (int64_t(t * n + s) * kWinRows + r) * kLatent + c);
-      const float4 u = src[0], v = src[1];
-      o[0] = fmaf(f, u.x, o[0]);
-      o[1] = fmaf(f, u.y, o[1]);
-      o[2] = fmaf(f, u.z, o[2]);
-      o[3] = fmaf(f, u.w, o[3]);
-      o[4] = fmaf(f, v.x, o[4]);
-      o[5] = fmaf(f, v.y, o[5]);
-      o[6] = fmaf(f, v.z, o[6]);
-      o[7] = fmaf(f, v.w, o[7]);
+  const float* src = a.part_o + (int64_t(t) * n * kWinRows + r) * kLatent + 8 * x;
+#pragma unroll 8
+  for (int s = 0; s < n; ++s) {
+    const float l = s_part[y][s];
+    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+    if (l != -INFINITY) {                            // (else that piece has written no outputs)
+      u = __ldg(reinterpret_cast<const float4*>(src + int64_t(s) * kWinRows * kLatent));
+      v = __ldg(reinterpret_cast<const float4*>(src + int64_t(s) * kWinRows * kLatent) + 1);
     }
-    if (prev != -INFINITY) {
-      const float f = expf(prev - most);
-      total += f;
-      const uint4 v = *reinterpret_cast<const uint4*>(a.prev_out + row * kLatent + c);
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    const float f = l != -INFINITY ? expf(l - most) : 0.0f;
+    total += f;
+    o[0] = fmaf(f, u.x, o[0]);
+    o[1] = fmaf(f, u.y, o[1]);
+    o[2] = fmaf(f, u.z, o[2]);
+    o[3] = fmaf(f, u.w, o[3]);
+    o[4] = fmaf(f, v.x, o[4]);
+    o[5] = fmaf(f, v.y, o[5]);
+    o[6] = fmaf(f, v.z, o[6]);
+    o[7] = fmaf(f, v.w, o[7]);
+  }
+  if (prev != -INFINITY) {
+    const float f = expf(prev - most);
+    total += f;
+    const uint32_t z[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        o[2 * k] = fmaf(f, __uint_as_float(x[k] << 16), o[2 * k]);
-        o[2 * k + 1] = fmaf(f, __uint_as_float(x[k] & 0xFFFF0000u), o[2 * k + 1]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      o[2 * k] = fmaf(f, __uint_as_float(z[k] << 16), o[2 * k]);
+      o[2 * k + 1] = fmaf(f, __uint_as_float(z[k] & 0xFFFF0000u), o[2 * k + 1]);
     }
   }
-  __syncthreads();                                   // every row's prev_lse has been read (lse may be the same place)
-  if (!have) return;
   const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-  *reinterpret_cast<uint4*>(a.out + row * kLatent + c) =
+  *reinterpret_cast<uint4*>(a.out + row * kLatent + 8 * x) =
       make_uint4(bf16x2_rn(o[0] * inv, o[1] * inv), bf16x2_rn(o[2] * inv, o[3] * inv), bf16x2_rn(o[4] * inv, o[5] * inv),
                  bf16x2_rn(o[6] * inv, o[7] * inv));
-  if (c == 0) a.lse[row] = total != 0.0f ? most + logf(total) : -INFINITY;
+  if (x == 0) a.lse[row] = total != 0.0f ? most + logf(total) : -INFINITY;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -1087,22 +1093,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;   // most tokens of a tile
-  a.compact = int64_t(a.window) + span - 1 + a.sinks <= kWinPos;
+  a.by_heads = H > 1 ? ~uint64_t(0) / H + 1 : 0;     // (for powers of two, too: 2^64 / H)
   WindowMaps m;
   const auto enc = tensor_map_encoder();
   const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
   if (!encode_2d_cached(enc, &m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, uint64_t(a.total_q) * a.d.heads, kDqk * 2,
                         64, kWinRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
     return cudaErrorUnknown;
-  for (int i = a.compact ? 0 : 6; i < 7; ++i)
+  for (int i = 0; i < 7; ++i)
     if (!encode_2d_cached(enc, &m.kv[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kDqk, rows, kDqk * 2, 64, 1u << i,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return cudaErrorUnknown;
-  static KernelAttrs attrs[4];
-  const int which = (a.compact ? 2 : 0) + (a.prev_out ? 1 : 0);
-  auto kernel = which == 0 ? window_kernel<false, false> : which == 1 ? window_kernel<false, true>
-                : which == 2 ? window_kernel<true, false> : window_kernel<true, true>;
-  cudaError_t e = prepare_kernel(kernel, size_t(kWinSmem), false, attrs[which]);
+  static KernelAttrs attrs[2];
+  auto kernel = a.prev_out ? window_kernel<true> : window_kernel<false>;
+  cudaError_t e = prepare_kernel(kernel, size_t(kWinSmem), false, attrs[a.prev_out ? 1 : 0]);
   if (e != cudaSuccess) return e;
   // bounds of what the device will find: tiles, and blocks of one
   int odd = H;                                       // 64 less the greatest common divisor: what a sequence's last tile may lack
@@ -1117,7 +1121,7 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   const int64_t see = min64(ctx, int64_t(a.window) + span - 1 + a.sinks), blocks = (see + kWinPos - 1) / kWinPos;
   const int64_t grid = min64(min64(device_sms(), kWinMaxCtas), max64(1, tiles * blocks));
   // fewer tiles than half of the SMs, at least: their positions may be split
-  a.may_split = !a.compact && blocks >= kMinSplit && 2 * (int64_t(a.total_q) * H / kWinRows) <= grid;
+  a.may_split = blocks >= kMinSplit && 2 * (int64_t(a.total_q) * H / kWinRows) <= grid;
   CSA2_PROFILED(st, "window_attn",
                 (e = launch_pdl(kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, m)));
   if (e != cudaSuccess || !a.may_split) return e;

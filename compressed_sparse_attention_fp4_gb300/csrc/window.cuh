@@ -13,7 +13,7 @@ struct WindowArgs {
   csa2_dims d;
   int batch, total_q, window, sinks;
   int may_split;       // pieces of few tiles may be split and merged
-  int compact;         // what a tile's tokens see fits one block of 128 places (see window.cu)
+  uint64_t by_heads;   // see over_heads
   const uint16_t* q;
   const int32_t* q_start;
   const uint16_t* kv;
