@@ -127,8 +127,9 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
@@ -214,9 +215,10 @@ def fp4_idx_k_quantize_scatter(x: torch.Tensor, idx_k: torch.Tensor, cache_rows:
 
 def fp4_idx_k_planes(idx_k: torch.Tensor, cache_rows: int):
     """Views (codes [rows, 64], scales [rows, 8]) of a two-plane FP4 indexer-K buffer."""
-    flat = idx_k.reshape(-1)
-    return (flat[:cache_rows * 64].view(cache_rows, 64),
-            flat[cache_rows * 64:cache_rows * 72].view(cache_rows, 8))
+    flat = idx_k if idx_k.dim() == 1 and idx_k.is_contiguous() else idx_k.reshape(-1)
+    _need("fp4_idx_k_planes", 0 <= cache_rows * 72 <= flat.numel())
+    at = flat.storage_offset()
+    return flat.as_strided((cache_rows, 64), (64, 1), at), flat.as_strided((cache_rows, 8), (8, 1), at + cache_rows * 64)
 
 
 def fp4_kv_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor | None = None,
@@ -442,6 +444,7 @@ def csa2_window_append(cfg: Rope, x: torch.Tensor, pos: torch.Tensor, dst_rows: 
                             kv.data_ptr(), rows))
 
 
+# an indexer key: type and channels of its row before the append, bytes of it in the cache
 _KEY_ROW = {IDXK_E4M3: (torch.bfloat16, 128, 128), IDXK_F32: (torch.float32, 64, 256), IDXK_FP4: (torch.bfloat16, 128, 72)}
 
 
@@ -455,14 +458,14 @@ def csa2_idx_k_append(cfg: Rope | None, kind: int, x: torch.Tensor, pos: torch.T
     fn = "csa2_idx_k_append"
     _need(fn, kind in _KEY_ROW)
     dt, dim, size = _KEY_ROW[kind]
-    _need(fn, x.dim() == 2 and x.shape[1] == dim and x.dtype is dt and x.stride(1) == 1)
-    n, dev = x.shape[0], x.get_device()
-    # whole numbers that ctypes would cut to 32 bits
-    _need(fn, 0 <= offset < 1 << 31 and 0 <= norm < 1 << 31 and _plane(dst_rows, torch.int64, n, dev)
-          and (pos is None or _plane(pos, torch.int32, n, dev)) and (norm_w is None or _plane(norm_w, dt, dim, dev))
-          and (norm_b is None or _plane(norm_b, dt, dim, dev)) and idx_k.is_contiguous() and idx_k.get_device() == dev
-          and idx_k.numel() * idx_k.element_size() == cache_rows * size)
-    _call(fn, dev, stream, (None if cfg is None else cfg.ref(), kind, x.data_ptr(), n, x.stride(0), offset, norm, _ptr(norm_w),
+    n, dev = x.numel() // dim, x.get_device()
+    strides = x.stride()
+    # (whole numbers that ctypes would cut to 32 bits, too)
+    _need(fn, x.dtype is dt and len(strides) == 2 and x.shape[1] == dim and strides[1] == 1 and 0 <= offset < 1 << 31
+          and 0 <= norm < 1 << 31 and _plane(dst_rows, torch.int64, n, dev) and (pos is None or _plane(pos, torch.int32, n, dev))
+          and (norm_w is None or _plane(norm_w, dt, dim, dev)) and (norm_b is None or _plane(norm_b, dt, dim, dev))
+          and idx_k.numel() * idx_k.element_size() == cache_rows * size and idx_k.is_contiguous() and idx_k.get_device() == dev)
+    _call(fn, dev, stream, (None if cfg is None else cfg.ref(), kind, x.data_ptr(), n, strides[0], offset, norm, _ptr(norm_w),
                             _ptr(norm_b), eps, _ptr(pos), dst_rows.data_ptr(), idx_k.data_ptr(), cache_rows))
 
 

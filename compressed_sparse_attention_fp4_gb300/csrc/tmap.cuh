@@ -25,7 +25,7 @@ inline bool encode_2d_cached(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* 
     int dtype, swizzle, l2;
     CUtensorMap map;
   };
-  constexpr int kEntries = 64;
+  constexpr int kEntries = 16;
   static std::mutex mu;
   static Entry cache[kEntries];
   static int next = 0;

@@ -19,7 +19,6 @@
 #include "kernels.cuh"
 #include "profile.cuh"
 #include "tc.cuh"
-#include "tmap.cuh"
 #include "window.cuh"
 
 namespace csa2 {
@@ -1089,21 +1088,50 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// The maps of a call, a pure function of the arguments here: encoding them takes longer than the call's
+// other work on the host, so the last ones are remembered (as tmap.cuh does for single maps).
+bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_rows, WindowMaps* out) {
+  struct Entry {
+    bool used;
+    const void *q, *kv;
+    uint64_t q_rows, kv_rows;
+    WindowMaps maps;
+  };
+  constexpr int kEntries = 16;
+  static std::mutex mu;
+  static Entry cache[kEntries];
+  static int next = 0;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Entry& e : cache)
+    if (e.used && e.q == q && e.kv == kv && e.q_rows == q_rows && e.kv_rows == kv_rows) {
+      *out = e.maps;
+      return true;
+    }
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const auto encode = [&](CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+    const cuuint64_t dim[2] = {kDqk, rows}, stride[1] = {kDqk * 2};
+    const cuuint32_t box[2] = {64, box_rows}, step[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  bool ok = encode(&out->q, q, q_rows, kWinRows);
+  for (int i = 0; i < 7; ++i) ok = ok && encode(&out->kv[i], kv, kv_rows, 1u << i);
+  if (!ok) return false;
+  Entry& e = cache[next];
+  next = (next + 1) % kEntries;
+  e = {true, q, kv, q_rows, kv_rows, *out};
+  return true;
+}
+
 }  // namespace
 
 cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;   // most tokens of a tile
   a.by_heads = H > 1 ? ~uint64_t(0) / H + 1 : 0;     // (for powers of two, too: 2^64 / H)
   WindowMaps m;
-  const auto enc = tensor_map_encoder();
   const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
-  if (!encode_2d_cached(enc, &m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kDqk, uint64_t(a.total_q) * a.d.heads, kDqk * 2,
-                        64, kWinRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-    return cudaErrorUnknown;
-  for (int i = 0; i < 7; ++i)
-    if (!encode_2d_cached(enc, &m.kv[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, kDqk, rows, kDqk * 2, 64, 1u << i,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-      return cudaErrorUnknown;
+  if (!window_maps(a.q, uint64_t(a.total_q) * a.d.heads, a.kv, rows, &m)) return cudaErrorUnknown;
   static KernelAttrs attrs[2];
   auto kernel = a.prev_out ? window_kernel<true> : window_kernel<false>;
   cudaError_t e = prepare_kernel(kernel, size_t(kWinSmem), false, attrs[a.prev_out ? 1 : 0]);
