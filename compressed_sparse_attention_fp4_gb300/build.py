@@ -50,14 +50,20 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
-def check_registers(source: str, ptxas: str):
-    """Raises where ptxas gave a dense attention kernel another number of registers than the split
-    among its roles counts on (kLaunchRegs): the library would refuse every call, without this reason."""
-    want = int(re.search(r"kLaunchRegs = (\d+)", source).group(1))
-    for name, got in re.findall(r"entry function '\w*?(dense_kernel|dense_pair_kernel)E\w*'.*?Used (\d+) registers", ptxas, re.S):
+# kernels whose roles share out the registers of the launch: source, its constant, their names
+ROLE_SPLITS = {"dense.cu": ("kLaunchRegs", "dense_kernel|dense_pair_kernel"), "window.cu": ("kWinRegs", "window_kernel")}
+
+
+def check_registers(source: str, ptxas: str, file: str = "dense.cu"):
+    """Raises where ptxas gave a kernel of `file` (the dense attention's, the window attention's) another
+    number of registers than the split among its roles counts on (the constant in `source`): the library
+    would refuse every call, without this reason."""
+    constant, kernels = ROLE_SPLITS[file]
+    want = int(re.search(rf"{constant} = (\d+)", source).group(1))
+    for name, got in re.findall(rf"entry function '\w*?\d({kernels})[EI]\w*'.*?Used (\d+) registers", ptxas, re.S):
         if int(got) != want:
-            raise RuntimeError(f"{name}: {got} registers a thread, but its role split (csrc/dense.cu) is for {want}: "
-                               "build with the CUDA toolkit it was written for, or change kLaunchRegs and the split")
+            raise RuntimeError(f"{name}: {got} registers a thread, but its role split (csrc/{file}) is for {want}: "
+                               f"build with the CUDA toolkit it was written for, or change {constant} and the split")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -76,9 +82,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         if verbose:
             sys.stderr.write(r.stderr)
-        if os.path.basename(src) == "dense.cu":
+        if os.path.basename(src) in ROLE_SPLITS:
             with open(src) as f:
-                check_registers(f.read(), r.stderr)
+                check_registers(f.read(), r.stderr, os.path.basename(src))
         return obj
 
     srcs = sources()

@@ -12,6 +12,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -1136,6 +1137,13 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   auto kernel = a.prev_out ? window_kernel<true> : window_kernel<false>;
   cudaError_t e = prepare_kernel(kernel, size_t(kWinSmem), false, attrs[a.prev_out ? 1 : 0]);
   if (e != cudaSuccess) return e;
+  static std::atomic<bool> split[2];                 // the register split of the roles counts on this many a thread
+  if (!split[a.prev_out ? 1 : 0].load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    if (fa.numRegs != kWinRegs) return cudaErrorInvalidConfiguration;
+    split[a.prev_out ? 1 : 0].store(true, std::memory_order_relaxed);
+  }
   // bounds of what the device will find: tiles, and blocks of one
   int odd = H;                                       // 64 less the greatest common divisor: what a sequence's last tile may lack
   for (int b = kWinRows; b != 0;) {
