@@ -3,12 +3,14 @@
 The dense form, for a prompt, a context no longer than the Top-K, or a verification
 of draft tokens: rotary positions on the queries, the new tokens' rows normed,
 rotated, quantized and appended to the FP4 cache, then attention of the chunk
-over every visible position of it.  Three library calls; no arithmetic here.
+over every visible position of it.  With `exact` and `keys`, what a layer has beside
+that: the window of exact rows, joined in one softmax, and the indexer's keys.
+Library calls in order; no arithmetic here.
 
-Attention reads FP4 rows alone.  The decode step (``step.py``) joins them with the
-exact bf16 rows of the newest tokens where its layer has a window (``swa`` > 0): the
-two are the same function only for a layer without one (``swa`` 0) whose Top-K set
-holds every position.  ``entry`` keeps the exact rows for a decode step's window.
+The decode step (``step.py``) attends to the FP4 rows of its Top-K set and, where its
+layer has a window (``swa`` > 0), to the exact bf16 rows of the newest tokens.  The two are
+the same function for a Top-K set that holds every position, with `exact` of a window of
+``swa`` positions, or without it for ``swa`` 0.
 """
 from __future__ import annotations
 
@@ -17,6 +19,36 @@ from dataclasses import dataclass
 import torch
 
 from . import csa2
+
+
+@dataclass
+class ExactRows:
+    """A layer's window over exact bf16 rows: where the chunk's rows go, and what it reads of earlier ones."""
+    kv: torch.Tensor                # bf16 [rows, 576], written and read
+    dst_rows: torch.Tensor          # int64 [total] its rows for the new tokens (cache_rows)
+    window: int                     # positions that a token sees, its own among them
+    sinks: int = 0                  # first positions that stay visible
+    dims: csa2.Dims | None = None   # of this cache (heads, max_ctx, pages); None: the chunk's
+    page_table: torch.Tensor | None = None
+    # the same rows for a decode step's window, in place (window_rows); both or neither
+    swa: torch.Tensor | None = None          # bf16 [B, W, 576]
+    swa_rows: torch.Tensor | None = None     # int64 [total]
+    ws: torch.Tensor = None
+
+
+@dataclass
+class IndexerKeys:
+    """The new tokens' indexer keys: written to the cache rows of their FP4 rows."""
+    x: torch.Tensor                 # bf16 [total, 128], fp32 [total, 64] for IDXK_F32: projections
+    idx_k: torch.Tensor             # the indexer-K buffer
+    cache_rows: int                 # its rows
+    kind: int = csa2.IDXK_E4M3
+    rope: csa2.Rope | None = None   # on channels [offset, offset + rope.rot)
+    offset: int = 0
+    norm: int = csa2.IDX_NORM_NONE
+    norm_w: torch.Tensor | None = None
+    norm_b: torch.Tensor | None = None
+    eps: float = 1e-6
 
 
 @dataclass
@@ -46,12 +78,17 @@ class ChunkBuffers:
     out: torch.Tensor = None        # bf16 [total, H, 512]
     lse: torch.Tensor = None        # fp32 [total, H]
     ws: torch.Tensor = None
+    # what else the layer has
+    exact: ExactRows | None = None
+    keys: IndexerKeys | None = None
 
     def allocate_outputs(self):
         total, h, dev = self.q.shape[0], self.dims.heads, self.q.device
         self.out = torch.empty((total, h, csa2.LATENT), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((total, h), dtype=torch.float32, device=dev)
         self.ws = csa2.alloc_dense_attn_workspace(self.dims, self.batch, total, device=dev)
+        if self.exact is not None:
+            self.exact.ws = csa2.alloc_window_attn_workspace(self.exact.dims or self.dims, self.batch, total, device=dev)
         return self
 
 
@@ -81,10 +118,38 @@ def cache_rows(ctx_len, q_start, page_table=None, max_ctx: int = 0, total: int |
     return pos.to(torch.int32), torch.where(own & (pos == at), rows, torch.full_like(rows, -1))
 
 
+def window_rows(ctx_len, q_start, window: int, total: int | None = None):
+    """Rows (int64 [total]) of a chunk's tokens in a decode step's window [B, window, 576]: position t of
+    sequence b at row b * window + t % window.  Tokens that newer ones of the chunk push out of the
+    window have none (of several query tokens, decode_mq, each sees another window: in the order of
+    their positions, not this one), nor have padding tokens and positions below 0 (ctx_len, q_start, total: as cache_rows)."""
+    csa2._need("window_rows", window > 0)
+    pos, own = cache_rows(ctx_len, q_start, max_ctx=1 << 31, total=total)
+    if ctx_len.numel() == 0:
+        return own
+    b = torch.searchsorted(q_start.long()[1:].contiguous(), torch.arange(pos.numel(), device=pos.device), right=True)
+    b = b.clamp(max=ctx_len.numel() - 1)
+    return torch.where((own >= 0) & (pos >= ctx_len[b] - window), b * window + pos % window, torch.full_like(own, -1))
+
+
 def run_chunk(cb: ChunkBuffers, stream=None):
-    """Enqueue the chunk: three library calls in order on one stream."""
+    """Enqueue the chunk: three library calls in order on one stream, up to four more for `exact` and `keys`."""
+    ex, keys = cb.exact, cb.keys
+    csa2._need("run_chunk", ex is None or (ex.swa is None) == (ex.swa_rows is None))
     csa2.csa2_rope_apply(cb.rope, cb.q, cb.pos, y=cb.q, offset=csa2.LATENT, stream=stream)
+    if ex is not None:
+        csa2.csa2_window_append(cb.rope, cb.x, cb.pos, ex.dst_rows, ex.kv, norm_w=cb.norm_w, eps=cb.eps, stream=stream)
+        if ex.swa is not None:
+            csa2.csa2_window_append(cb.rope, cb.x, cb.pos, ex.swa_rows, ex.swa, norm_w=cb.norm_w, eps=cb.eps, stream=stream)
+    if keys is not None:
+        csa2.csa2_idx_k_append(keys.rope, keys.kind, keys.x, None if keys.rope is None else cb.pos, cb.dst_rows, keys.idx_k,
+                               keys.cache_rows, offset=keys.offset, norm=keys.norm, norm_w=keys.norm_w, norm_b=keys.norm_b,
+                               eps=keys.eps, stream=stream)
     csa2.csa2_kv_append(cb.rope, cb.x, cb.pos, cb.dst_rows, cb.kv_codes, cb.kv_scales, cb.kv_rope, norm_w=cb.norm_w,
                         eps=cb.eps, entry=cb.entry, stream=stream)
     csa2.csa2_dense_attn_chunk(cb.dims, cb.batch, cb.q, cb.q_start, cb.kv_codes, cb.kv_scales, cb.kv_rope, cb.page_table,
                                cb.ctx_len, cb.scale, cb.out, cb.lse, cb.ws, window=cb.window, stream=stream)
+    if ex is not None:                               # joined in place
+        csa2.csa2_window_attn_chunk(ex.dims or cb.dims, cb.batch, cb.q, cb.q_start, ex.kv, ex.page_table, cb.ctx_len, cb.scale,
+                                    ex.window, cb.out, cb.lse, ex.ws, sinks=ex.sinks, prev_out=cb.out, prev_lse=cb.lse,
+                                    stream=stream)
