@@ -21,6 +21,7 @@
 #include "profile.cuh"
 #include "tc.cuh"
 #include "window.cuh"
+#include "window_tiles.cuh"
 
 namespace csa2 {
 
@@ -162,23 +163,6 @@ __device__ inline float butterfly_sum(const float (&x)[32], int lane) {
   return v[0];
 }
 
-// Context of sequence b (bad ones are reported by the first CTA's count, and taken as 0).
-__device__ inline int context(const WindowArgs& a, int b) {
-  const int n = __ldg(a.ctx_len + b);
-  return n < 0 || n > a.d.max_ctx || (a.page_table && n > int64_t(a.d.max_pages) * kPage) ? 0 : n;
-}
-// Row number over heads: a.by_heads = ceil(2^64 / heads), exact below 2^31 rows (0 for one head).
-__device__ inline int over_heads(const WindowArgs& a, int row) { return a.by_heads ? int(__umul64hi(uint64_t(row), a.by_heads)) : row; }
-// Tiles of a sequence of len tokens: 64 rows each.
-__device__ inline int tiles_of(const WindowArgs& a, int len) { return (len * a.d.heads + kWinRows - 1) / kWinRows; }
-
-// Cache row of position t (-1: its page id is out of range).
-__device__ inline int row_of(const WindowArgs& a, int seq, int t) {
-  if (!a.page_table) return int(int64_t(seq) * a.d.max_ctx + t);
-  const int pg = __ldg(a.page_table + int64_t(seq) * a.d.max_pages + t / kPage);
-  return pg < 0 || pg >= a.d.num_pages ? -1 : pg * kPage + t % kPage;
-}
-
 // Position of place e of block j of a piece (-1: none).
 template <bool kCompact>
 __device__ inline int place_position(const WindowArgs& a, const Piece& p, int j, int e) {
@@ -221,31 +205,9 @@ struct Span {
   int first, units, step, pieces;
 };
 
-// 32 sequences, one a lane: from b0 on, with `base` tiles before them.
-struct Sequences {
-  int b0, base, from, len, ctx, upto;
-  __device__ void load(const WindowArgs& a, int lane) {
-    const int i = b0 + lane;
-    from = len = ctx = upto = 0;
-    if (i < a.batch) {
-      from = __ldg(a.q_start + i);
-      len = __ldg(a.q_start + i + 1) - from;
-      ctx = context(a, i);
-      upto = tiles_of(a, len);
-    }
-  }
-  __device__ void count(int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-      if (lane >= o) upto += y;
-    }
-  }
-};
-
 // `q`: the first 32 sequences, loaded.
 template <bool kCompact>
-__device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& w, Sequences& q, int lane) {
+__device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& w, Sequences<kWinRows>& q, int lane) {
   q.count(lane);
   int was_seq = -1, was_last = 0;
   uint32_t k = 0;
@@ -254,25 +216,14 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
     p.n = -1;
     if (u < w.units) {
       const int t = w.pieces == 1 ? u : u / w.pieces, s = u - t * w.pieces;
-      uint32_t past;
-      while ((past = __ballot_sync(0xFFFFFFFFu, q.base + q.upto > t)) == 0) {
-        q.base += __shfl_sync(0xFFFFFFFFu, q.upto, 31);
-        q.b0 += 32;
-        q.load(a, lane);
-        q.count(lane);
-      }
-      const int i = __ffs(past) - 1;
-      const int tokens = __shfl_sync(0xFFFFFFFFu, q.len, i), c = __shfl_sync(0xFFFFFFFFu, q.ctx, i);
-      const int before = i > 0 ? __shfl_sync(0xFFFFFFFFu, q.upto, i - 1) : 0;
-      const int r0 = (t - q.base - before) * kWinRows, tok0 = over_heads(a, r0);
-      const int tok1 = min(tokens - 1, over_heads(a, r0 + kWinRows - 1));
-      p.row = __shfl_sync(0xFFFFFFFFu, q.from, i) * a.d.heads + r0;
-      p.have = min(kWinRows, tokens * a.d.heads - r0);
-      p.seq = q.b0 + i;
-      p.pos = c - tokens + tok0;
-      p.rem = r0 - tok0 * a.d.heads;
-      p.last = c - tokens + tok1;
-      p.lo = max(0, p.pos - a.window + 1);
+      const Tile tile = find_tile(a, q, t, lane);
+      p.row = tile.row;
+      p.have = tile.have;
+      p.seq = tile.seq;
+      p.pos = tile.pos;
+      p.rem = tile.rem;
+      p.last = tile.last;
+      p.lo = tile.lo;
       p.unit = u;
       if (kCompact) {
         p.n = p.last >= 0;
@@ -283,8 +234,9 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
           was_last = p.last;
         }
       } else {
-        p.sp = min((a.sinks + kPage - 1) / kPage, p.lo / kPage);
-        p.np = p.last < 0 ? 0 : p.sp + p.last / kPage - p.lo / kPage + 1;
+        const TilePages pages = pages_of(a, p.lo, p.last);
+        p.sp = pages.sinks;
+        p.np = pages.all;
         const int nb = (p.np + 1) / 2;
         p.blk = w.pieces == 1 ? 0 : nb * s / w.pieces;
         p.n = w.pieces == 1 ? nb : nb * (s + 1) / w.pieces - p.blk;
@@ -912,13 +864,13 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  Sequences first = {0, 0, 0, 0, 0, 0};
+  Sequences<kWinRows> first = {0, 0, 0, 0, 0, 0};
   if (wid == kPlanWarp) first.load(a, lane);         // on their way while the tiles are counted
   // Count the tiles, and what most their rows see.  Starts out of order are reported and the call
   // writes nothing.
   {
     const bool paged = a.page_table != nullptr;
-    const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;   // most tokens of a tile
+    const int H = a.d.heads, span = tile_tokens(H, kWinRows);
     int tiles = 0, tokens = 0, most = 0;
     bool bad = false;
     for (int b = tid; b < a.batch; b += kWinThreads) {
@@ -928,7 +880,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         continue;
       }
       if (blockIdx.x == 0) check_ctx(__ldg(a.ctx_len + b), a.d, paged, a.ws);
-      tiles += tiles_of(a, s1 - s0);
+      tiles += tiles_of<kWinRows>(a, s1 - s0);
       tokens = max(tokens, min(span, s1 - s0));
       if (a.may_split && s1 > s0) most = max(most, int(min64(context(a, b), int64_t(a.window) + min(span, s1 - s0) - 1 + a.sinks)));
     }
@@ -1091,12 +1043,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // The maps of a call, a pure function of the arguments here: encoding them takes longer than the call's
 // other work on the host, so the last ones are remembered (as tmap.cuh does for single maps).
-bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_rows, WindowMaps* out) {
+bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_rows, WindowMaps* out, WindowLongMaps* out_long) {
   struct Entry {
     bool used;
     const void *q, *kv;
     uint64_t q_rows, kv_rows;
     WindowMaps maps;
+    WindowLongMaps longs;
   };
   constexpr int kEntries = 16;
   static std::mutex mu;
@@ -1106,6 +1059,7 @@ bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_row
   for (const Entry& e : cache)
     if (e.used && e.q == q && e.kv == kv && e.q_rows == q_rows && e.kv_rows == kv_rows) {
       *out = e.maps;
+      *out_long = e.longs;
       return true;
     }
   const auto enc = tensor_map_encoder();
@@ -1118,21 +1072,35 @@ bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_row
   };
   bool ok = encode(&out->q, q, q_rows, kWinRows);
   for (int i = 0; i < 7; ++i) ok = ok && encode(&out->kv[i], kv, kv_rows, 1u << i);
+  ok = ok && encode(&out_long->q, q, q_rows, 32);
   if (!ok) return false;
+  out_long->keys = out->kv[5];
+  out_long->values = out->kv[6];
   Entry& e = cache[next];
   next = (next + 1) % kEntries;
-  e = {true, q, kv, q_rows, kv_rows, *out};
+  e = {true, q, kv, q_rows, kv_rows, *out, *out_long};
   return true;
+}
+
+// Whether a call takes window_long.cu's tiles.
+bool window_is_long(const WindowArgs& a, int span) {
+  const int64_t rows = int64_t(a.total_q) * a.d.heads;
+  return int64_t(a.window) + span - 1 + a.sinks > kWinPos && rows >= int64_t(kLongRows) * a.batch && rows >= kLongRows * 38;
 }
 
 }  // namespace
 
 cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
-  const int H = a.d.heads, span = kWinRows % H == 0 ? kWinRows / H : (H + 62) / H + 1;   // most tokens of a tile
+  const int H = a.d.heads, span = tile_tokens(H, kWinRows);
   a.by_heads = H > 1 ? ~uint64_t(0) / H + 1 : 0;     // (for powers of two, too: 2^64 / H)
   WindowMaps m;
+  WindowLongMaps ml;
   const uint64_t rows = a.page_table ? uint64_t(a.d.num_pages) * kPage : uint64_t(a.batch) * uint64_t(a.d.max_ctx);
-  if (!window_maps(a.q, uint64_t(a.total_q) * a.d.heads, a.kv, rows, &m)) return cudaErrorUnknown;
+  if (!window_maps(a.q, uint64_t(a.total_q) * a.d.heads, a.kv, rows, &m, &ml)) return cudaErrorUnknown;
+  if (window_is_long(a, span)) {
+    a.may_split = 0;
+    return launch_window_long(a, ml, (int64_t(a.total_q) * H + kLongRows - 1) / kLongRows + a.batch, st);
+  }
   static KernelAttrs attrs[2];
   auto kernel = a.prev_out ? window_kernel<true> : window_kernel<false>;
   cudaError_t e = prepare_kernel(kernel, size_t(kWinSmem), false, attrs[a.prev_out ? 1 : 0]);

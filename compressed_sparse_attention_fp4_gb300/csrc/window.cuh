@@ -6,6 +6,7 @@
 namespace csa2 {
 
 constexpr int kWinRows = 64;             // rows (query token, head) of a tile: the MMA's N
+constexpr int kLongRows = 256;          // rows of a tile of window_long.cu
 constexpr int kWinPos = 128;             // cache positions of a block: the MMA's M
 constexpr int kWinMaxCtas = 152;         // most pieces of a call whose tiles are split
 
