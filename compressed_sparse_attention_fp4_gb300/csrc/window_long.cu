@@ -71,7 +71,7 @@ struct LongSmall {
   uint64_t q_place[4];                               // 32 query rows have come to their place in the ring
   uint64_t k_ready[kStages];                         // leading scores CTA: the other's half of a block is there
   uint64_t s_full[kSBufs], s_empty[kSBufs];
-  uint64_t q_full;
+  uint64_t q_full, q_free;                           // queries in tensor memory (both CTAs); read by the tile's last product
   uint64_t ref_full[2][4];                           // reference of a row, from the warp of one block to that of the next
   uint64_t p_free[kPSlots];                          // scores CTA: slot read by the values CTA (remote arrival)
   uint64_t p_full[kPSlots];                          // values CTA: bytes of P and meta have arrived
@@ -308,11 +308,8 @@ __device__ inline void query_role(const WindowArgs& a, LongSmall& sm, uint8_t* b
   uint32_t nu = 0, nt = 0, n = 0;
   while (next_piece(sm, nu, lane, a.ws, p)) {
     if (p.n == 0) continue;
-    // all four places: they include that of the tile before's last block, whose product read the queries before
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i)
-      if (!wait_warp(sm, &sm.q_place[i], nt & 1, a.ws)) return;
-    ++nt;
+    if (!wait_warp(sm, &sm.q_place[k], nt & 1, a.ws)) return;
+    if (!wait_warp(sm, &sm.q_free, (nt++ & 1) ^ 1, a.ws)) return;
     tc::tc_fence_after_sync();
     const uint32_t st = (n + k) % kStages, src = tc::smem_u32(base) + kRingOff + st * kKStage;
     const uint32_t to = tmem + (uint32_t(32 * k) << 16);
@@ -378,6 +375,7 @@ __device__ inline void scores_mma_role(const WindowArgs& a, LongSmall& sm, uint8
           for (int k4 = 0; k4 < 4; ++k4) mma_ts(d, tmem + g * 32 + k4 * 8, bd + ((g * 4096 + k4 * 32) >> 4), id, g + k4 > 0);
         commit_to(&sm.empty[st], 0x3);
         commit_to(&sm.s_full[buf], 0x3);
+        if (j == p.n - 1) commit_to(&sm.q_free, 0x3);
       }
       __syncwarp();
     }
@@ -734,6 +732,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kLongThreads, 1)
       tc::mbar_init(&sm.s_empty[i], 8);              // four warps in each CTA
     }
     tc::mbar_init(&sm.q_full, 8);
+    tc::mbar_init(&sm.q_free, 1);
     for (int i = 0; i < 8; ++i) tc::mbar_init(&sm.ref_full[i >> 2][i & 3], 1);
     for (int i = 0; i < kPSlots; ++i) {
       tc::mbar_init(&sm.p_free[i], 1);
