@@ -970,7 +970,6 @@ constexpr int kMergeRows = 4, kMergeThreads = kMergeRows * kLatent / 8;
 
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __grid_constant__ WindowArgs a) {
   __shared__ float s_part[kMergeRows][kWinMaxCtas];
-  pdl_wait();
   pdl_launch_dependents();
   const int tiles = __ldg(a.head), n = __ldg(a.head + 1), t = blockIdx.y;
   if (n <= 1 || t >= tiles) return;
@@ -1134,9 +1133,11 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   CSA2_PROFILED(st, "window_attn",
                 (e = launch_pdl(kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, m)));
   if (e != cudaSuccess || !a.may_split) return e;
+  // Launched only when the pieces are done.  (Ahead of that, by pdl_launch_dependents, its CTAs all go to the
+  // few SMs that the attention leaves free and stay there: 24.0 us in place of 18.6 for 8 tokens over 2,048 positions.)
   CSA2_PROFILED(st, "window_merge",
-                (e = launch_pdl(window_merge_kernel, dim3(kWinRows / kMergeRows, unsigned(min64(tiles, grid / 2))),
-                                dim3(kMergeThreads), 0, st, 1, a)));
+                (window_merge_kernel<<<dim3(kWinRows / kMergeRows, unsigned(min64(tiles, grid / 2))), dim3(kMergeThreads), 0, st>>>(a),
+                 e = cudaGetLastError()));
   return e;
 }
 
