@@ -73,18 +73,19 @@ __global__ void __launch_bounds__(kWinAppThreads, kWinAppBlocks)
 // All in fp32: the keys' formats are coarse beside its roundings (2^-22 of a row's size), so no
 // compensated sums as for the latent rows.
 //
-// What bounds it is instructions: 16 values a lane and row, and a third of them for the angles, whose
-// (cos, sin) are formed once a row, spread over the warp, two rows at a time.  So values are held in
-// pairs, for two fp32 operations an instruction, and the angles' results and the values that half-split
-// pairs exchange go through shared memory, laid out so that the eight lanes of a row read 128 bytes
-// in a row.
+// What bounds it is instructions and shared memory's cycles, both: 16 values a lane and row, and a third of
+// the work for the angles, whose (cos, sin) are formed once a row, spread over the warp, two rows at a time.
+// So values are held in pairs, for two fp32 operations an instruction, and the angles' results and the values
+// that half-split pairs exchange go through shared memory, laid out so that the eight lanes of a row read 128
+// bytes in a row.
 //
-// A million rows (layer norm, 64 of 128 channels turned, E4M3): 135 us, 464 instructions a warp for four
-// rows, issued in 70 % of the cycles, shared memory and shuffles busy in 67 %.  With the same arithmetic on
-// single values and angles formed by the lanes that use them it took 206 us.
+// A million rows (layer norm, 64 of 128 channels turned, E4M3): 111 us.  It took 206 us with arithmetic on
+// single values and angles formed by the lanes that use them, 135 with polynomials for all sines, 120 with
+// the weights in shared memory (four wavefronts a load, 87 % of its cycles) at 4 blocks of 256 threads, 114
+// at 3.
 // ---------------------------------------------------------------------------
-constexpr int kKeyThreads = 256;
-constexpr int kKeyBlocks = 4;                        // resident on an SM (3: 136 us)
+constexpr int kKeyThreads = 128;
+constexpr int kKeyBlocks = 4;                        // resident on an SM: 128 registers a thread hold the weights, too (5: 120 us)
 constexpr int kKeyPairs = 64;                        // most pairs of a key
 
 using f32x2 = uint64_t;                              // low half first
@@ -214,7 +215,6 @@ __global__ void __launch_bounds__(kKeyThreads, kKeyBlocks)
   constexpr int C = Piece<T>::kC, D = 16 * C, P = C / 2;               // channels and pairs of a piece
   __shared__ __align__(16) float s_c[kKeyThreads / 32][4][kCsRow], s_s[kKeyThreads / 32][2][4][kCsRow];   // (sin: and -sin)
   __shared__ __align__(16) float s_y[kKeyThreads / 32][4][D];
-  __shared__ uint4 s_w[16], s_b[16];                 // (in registers these and the frequencies would take a fourth of the warps)
   __shared__ uint64_t s_turn[kKeyPairs];
   const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3, wid = threadIdx.x >> 5;
   const int64_t warp = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -223,9 +223,12 @@ __global__ void __launch_bounds__(kKeyThreads, kKeyBlocks)
   const int pairs = tab.pairs, rot = 2 * pairs;
   pdl_wait();
   pdl_launch_dependents();
-  if (kNorm != CSA2_IDX_NORM_NONE && threadIdx.x < 16) s_w[threadIdx.x] = __ldg(static_cast<const uint4*>(wv) + threadIdx.x);
-  if (kNorm == CSA2_IDX_NORM_LAYER && threadIdx.x >= 32 && threadIdx.x < 48)
-    s_b[threadIdx.x - 32] = bv ? __ldg(static_cast<const uint4*>(bv) + threadIdx.x - 32) : make_uint4(0, 0, 0, 0);
+  uint4 wr[2], br[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (kNorm != CSA2_IDX_NORM_NONE) wr[j] = __ldg(static_cast<const uint4*>(wv) + l + 8 * j);
+    if (kNorm == CSA2_IDX_NORM_LAYER) br[j] = bv ? __ldg(static_cast<const uint4*>(bv) + l + 8 * j) : make_uint4(0, 0, 0, 0);
+  }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + kKeyPairs) s_turn[threadIdx.x - 64] = tab.turn[threadIdx.x - 64];
   __syncthreads();
   if (4 * warp >= n) return;
@@ -271,8 +274,8 @@ __global__ void __launch_bounds__(kKeyThreads, kKeyBlocks)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         f32x2 w[P], b[P];
-        Piece<T>::get(s_w[l + 8 * j], w);
-        if (kNorm == CSA2_IDX_NORM_LAYER) Piece<T>::get(s_b[l + 8 * j], b);
+        Piece<T>::get(wr[j], w);
+        if (kNorm == CSA2_IDX_NORM_LAYER) Piece<T>::get(br[j], b);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const f32x2 t = mul2(y[j * P + i], rs);
@@ -421,7 +424,7 @@ cudaError_t launch_idx_append(const IdxAppendArgs& a, cudaStream_t st) {
   const bool half = a.rotate && a.cfg.layout == CSA2_ROPE_HALF;
   const int c = a.kind == CSA2_IDXK_F32 ? 4 : 8, rot = a.rotate ? a.cfg.rot : 0;
   const int vec = a.offset % c == 0 && (half ? rot / 2 : rot) % c == 0;
-  const int64_t want = (a.n + 31) / 32, cap = int64_t(device_sms()) * kKeyBlocks;
+  const int64_t want = (a.n + kKeyThreads / 8 - 1) / (kKeyThreads / 8), cap = int64_t(device_sms()) * kKeyBlocks;
   uint8_t* keys = static_cast<uint8_t*>(a.idx_k);
   uint8_t* scales = a.kind == CSA2_IDXK_FP4 ? keys + a.cache_rows * 64 : nullptr;
   const IdxKernel kernel = a.kind == CSA2_IDXK_E4M3  ? (half ? idx_kernel<CSA2_IDXK_E4M3, true>(a.norm) : idx_kernel<CSA2_IDXK_E4M3, false>(a.norm))
