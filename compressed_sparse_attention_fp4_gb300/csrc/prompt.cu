@@ -292,10 +292,13 @@ csa2_status csa2_window_attn_chunk(const csa2_dims* d, int32_t batch, int64_t to
   if (!is_aligned(q, 16) || !is_aligned(q_start, 4) || !is_aligned(kv, 16) || !is_aligned(ctx_len, 4) ||
       !is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(prev_out, 16) || !is_aligned(prev_lse, 4))
     return CSA2_ERR_INVALID_ARG;
-  const __int128 n = __int128(total_q) * d->heads;
-  if (overlap(out, n * kLatent * 2, q, n * kDqk * 2) || overlap(out, n * kLatent * 2, kv, rows * kDqk * 2) ||
-      (prev_out && prev_out != out && overlap(out, n * kLatent * 2, prev_out, n * kLatent * 2)) ||
-      (prev_lse && prev_lse != lse && overlap(lse, n * 4, prev_lse, n * 4)))
+  const __int128 n = __int128(total_q) * d->heads, out_bytes = n * kLatent * 2, lse_bytes = n * 4;
+  if (overlap(out, out_bytes, q, n * kDqk * 2) || overlap(out, out_bytes, kv, rows * kDqk * 2) || overlap(out, out_bytes, lse, lse_bytes) ||
+      overlap(lse, lse_bytes, q, n * kDqk * 2) || overlap(lse, lse_bytes, kv, rows * kDqk * 2) || overlap(ws, L.total, out, out_bytes) ||
+      overlap(ws, L.total, lse, lse_bytes))
+    return CSA2_ERR_INVALID_ARG;
+  if (prev_out && ((prev_out != out && overlap(out, out_bytes, prev_out, out_bytes)) || overlap(lse, lse_bytes, prev_out, out_bytes) ||
+                   (prev_lse != lse && overlap(lse, lse_bytes, prev_lse, lse_bytes)) || overlap(out, out_bytes, prev_lse, lse_bytes)))
     return CSA2_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
   WindowArgs a = {};

@@ -65,6 +65,7 @@ __device__ inline Tile find_tile(const WindowArgs& a, Sequences<kRows>& q, int t
   Tile p;
   uint32_t past;
   while ((past = __ballot_sync(0xFFFFFFFFu, q.base + q.upto > t)) == 0) {
+    if (q.b0 >= a.batch) return {0, 0, 0, 0, -1, 0, 0};                // the starts have changed since they were counted
     q.base += __shfl_sync(0xFFFFFFFFu, q.upto, 31);
     q.b0 += 32;
     q.load(a, lane);

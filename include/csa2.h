@@ -521,10 +521,12 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
  * With prev_out and prev_lse, what another attention over other rows gave the same queries (the
  * layer's FP4 entries, by csa2_dense_attn_chunk), out and lse are those of one softmax over both:
  *   lse = ln(e^lse_own + e^prev_lse),  out = e^(lse_own - lse) out_own + e^(prev_lse - lse) prev_out.
- * The new tokens' own rows have been written before (csa2_window_append).  Rows and pages that no new
- * token sees are not read: a page table may hold anything there, and pages may come round (a ring).
+ * The new tokens' own rows have been written before (csa2_window_append).  Of the page table only
+ * the entries of pages that a new token sees a position of are read: it may hold anything elsewhere,
+ * and pages may come round (a ring).  Rows that no new token sees may hold anything.
  *   Dimensions read: heads, max_ctx, max_pages, num_pages (the window cache's own).
- *   q, q_start, ctx_len, out, lse: as csa2_dense_attn_chunk, out and lse not within q or kv
+ *   q, q_start, ctx_len, out, lse: as csa2_dense_attn_chunk, out and lse apart from q, kv, ws and
+ *              each other
  *   kv:        device bf16 [rows][576], 16-byte aligned; rows and page_table as elsewhere (rows =
  *              batch * max_ctx, or num_pages * 64).  A position whose page id is out of range is
  *              skipped and reported.
@@ -536,7 +538,8 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
  *   A q_start that falls back or leaves 0 .. total_q is reported and the call writes nothing.
  *   An infinity or a NaN in a row reaches only the outputs of tokens that see it (all their channels
  *   may then be NaN), in a query only that token and head.
- *   P is rounded to bf16 (2^-8) and the output to bf16; everything between is fp32.
+ *   P is rounded to bf16 (2^-8) and the output to bf16; everything between is fp32, where weights
+ *   are kept up to 2^8 times too large: values above 2^99 may pass its range.
  * Results do not change from call to call.  Limits: total_q * H <= 2^30, batch <= 2^20, rows < 2^31.
  * Make the first call on a device before any stream capture.
  * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE, CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
