@@ -425,14 +425,13 @@ __device__ inline void load_role(const WindowArgs& a, WinSmall& sm, uint8_t* bas
 // constant: rows of 8 are 1,024 bytes apart, 128-byte swizzle.  Called by the whole warp, done by
 // the thread with `leader`: what the operands are formed from is then the same for the warp to the
 // compiler, which keeps it in uniform registers.
-template <bool kFirst>
-__device__ inline void mma_lo(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+__device__ inline void mma_lo(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
       "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(leader), "n"((1024 >> 4) | 1 << 14 | 2 << 29), "n"(kFirst ? 0 : 1)
+      ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(leader), "n"((1024 >> 4) | 1 << 14 | 2 << 29), "r"(add)
       : "memory");
 }
 __device__ inline void commit_lo(uint32_t leader, uint64_t* bar) {
@@ -460,50 +459,38 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
     if (n == 0) more = next_piece(sm, nu, lane, a.ws, p);
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++nk) {
-      // a channel group at a time: two regions, rope one
-      const auto scores = [&](int g, auto first, auto regions) {
-#pragma unroll
-        for (int i = 0; i < 4 * regions; ++i) {
-          const uint32_t ks = k_lo + (((2 * g + (i >> 2)) * kKReg + (i & 3) * 32) >> 4), qs = q_lo + (((2 * g + (i >> 2)) * kQReg + (i & 3) * 32) >> 4);
-          if (first && i == 0) mma_lo<true>(leader, tmem, ks, qs, id_s);
-          else mma_lo<false>(leader, tmem, ks, qs, id_s);
-        }
-        // the next tile's queries come group by group (P goes over the rope channels in a compact call)
-        if (j == n - 1 && (g < 4 || !kCompact)) commit_lo(leader, &sm.q_empty[g]);
-      };
-      const auto ready = [&](int g) {
-        if (!wait_warp(sm, &sm.k_full[g], nk & 1, a.ws)) return false;
-        tc::tc_fence_after_sync();
-        return true;
-      };
-      if (j == 0 && !wait_warp(sm, &sm.q_full[0], nq & 1, a.ws)) return;
-      if (!ready(0)) return;
-      scores(0, std::true_type{}, std::integral_constant<int, 2>{});
+      const bool end = j == n - 1;
 #pragma unroll 1
-      for (int g = 1; g < 4; ++g) {
-        if (!ready(g)) return;
-        scores(g, std::false_type{}, std::integral_constant<int, 2>{});
+      for (int t = 0; t < 9; ++t) {                  // regions of 64 channels
+        const int g = t >> 1;
+        if ((t & 1) == 0) {
+          if (j == 0 && (t == 0 || t == 8) && !wait_warp(sm, &sm.q_full[t >> 3], nq & 1, a.ws)) return;
+          if (!wait_warp(sm, &sm.k_full[g], nk & 1, a.ws)) return;
+          tc::tc_fence_after_sync();
+        }
+        const uint32_t x = k_lo + t * (kKReg >> 4), y = q_lo + t * (kQReg >> 4);
+        mma_lo(leader, tmem, x, y, id_s, t);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) mma_lo(leader, tmem, x + k * (32 >> 4), y + k * (32 >> 4), id_s, 1);
+        // the next tile's queries come group by group (P goes over the rope channels in a compact call)
+        if (end && ((t & 1) || (t == 8 && !kCompact))) commit_lo(leader, &sm.q_empty[g]);
       }
-      if (j == 0 && !wait_warp(sm, &sm.q_full[1], nq & 1, a.ws)) return;
-      if (!ready(4)) return;
-      scores(4, std::false_type{}, std::integral_constant<int, 1>{});
       commit_lo(leader, &sm.s_full);
       if (kCompact) commit_lo(leader, &sm.k_empty[4]);
-      if (j == n - 1) more = next_piece(sm, nu, lane, a.ws, p);           // ahead: nothing between this piece's last product and its scores
+      if (end) more = next_piece(sm, nu, lane, a.ws, p);                    // ahead: nothing between this piece's last product and its scores
       if (!wait_warp(sm, &sm.p_full, nk & 1, a.ws)) return;
       if (j == 0 && !wait_warp(sm, &sm.o_empty, (nq & 1) ^ 1, a.ws)) return;
       tc::tc_fence_after_sync();
 #pragma unroll 1
       for (int mt = 0; mt < 4; ++mt) {
         const uint32_t vs = v_lo + mt * (2 * kKReg >> 4), d = tmem + kOCol + 64 * mt;
-        if (j == 0) mma_lo<true>(leader, d, vs, p_lo[0], id_o);
-        else mma_lo<false>(leader, d, vs, p_lo[0], id_o);
+        mma_lo(leader, d, vs, p_lo[0], id_o, j);
 #pragma unroll
-        for (int k = 1; k < 8; ++k) mma_lo<false>(leader, d, vs + (k * 2048 >> 4), p_lo[k >> 2] + ((k & 3) * 2048 >> 4), id_o);
+        for (int k = 1; k < 8; ++k) mma_lo(leader, d, vs + (k * 2048 >> 4), p_lo[k >> 2] + ((k & 3) * 2048 >> 4), id_o, 1);
         commit_lo(leader, &sm.k_empty[mt]);
       }
       commit_lo(leader, kCompact ? &sm.q_empty[4] : &sm.k_empty[4]);
-      if (j == n - 1) commit_lo(leader, &sm.o_full);
+      if (end) commit_lo(leader, &sm.o_full);
     }
     if (n > 0) ++nq;
   }
