@@ -848,6 +848,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     sm.tokens = 0;
     sm.most = 0;
   }
+  // Places that no row is copied to (short contexts, a last block of one page) hold zeros: what else the
+  // memory held might be no numbers, which costs a look through them (decode steps over windows of 300 to 400
+  // positions 19 us in place of 14, 4 tokens over 64 positions 28 in place of 16).
+  for (int i = tid; i < kKBytes / 16; i += kWinThreads) reinterpret_cast<uint4*>(base)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
