@@ -9,6 +9,24 @@
 // (the layer's FP4 entries: one softmax over main KV and exact SWA rows, foosynaptic atlas
 // "DeepSeek-V4.1-Flash 梗概", section 3.2, figure "异构 KV"):
 //   lse = log(e^l + e^l'),  out = e^(l - lse) out + e^(l' - lse) out'.
+//
+// Tiles of 64 rows, one SM each: with transposed products the rows are the MMAs' columns, so that a single
+// token of 64 heads wastes nothing (S^T [128 positions x 64 rows] = K . Q^T, O^T [4 x 128 channels x 64 rows] =
+// V^T . P^T, both from one copy of the cache rows in shared memory: 128 x 1,152 B, with the queries' 72 KB
+// all that an SM has).  A position is a tensor-memory lane: the softmax's maxima and sums go across lanes.
+// The rows of a window of 128 are copied once for a run of tiles and then row by row (compact calls); longer
+// windows go through the same memory block by block, and where there are few tiles their blocks are shared
+// out among the SMs and merged.  (Many tokens over long windows: window_long.cu.)
+//
+// Roles of a CTA's 24 warps: 8 softmax, 8 outputs, one that issues the MMAs, 5 that copy a channel group
+// each, one that plans.  They meet at mbarriers, group by group, so that the next tile's queries and rows come
+// while this one's outputs are formed.
+//
+// What bounds it: the chain of a tile, about 8,000 cycles: scores 3,000 (2,100 of products at the rate at which
+// shared memory feeds 64 columns, 5/6 of its bandwidth), softmax 2,200, outputs 1,900, and the hand-overs
+// between.  Measured (GB300, 64 heads): whole prompts of 8,872 tokens, window 128, 262 us (0.7 of the copy rate
+// on queries and outputs); 64 decode tokens joined with another attention 12.5 us, one token 9.4-10 us (launch,
+// plan, copies, products, outputs one after the other); 8 tokens over 2,048 positions 18.7 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -44,7 +62,13 @@ constexpr int kQOff = kKBytes, kPOff = kQOff + kQBytes;
 constexpr int kWinSmem = kPOff + kPHalf;
 constexpr uint32_t kOCol = 64;                       // tensor memory: S^T 64 columns, O^T 4 x 64
 constexpr uint32_t kCols = 512;
-constexpr int kMinSplit = 3;                         // least blocks a tile's positions are split from
+// Least blocks a tile's positions are split from, into three pieces or more; into two, as many as here.
+// Measured, 64 heads, single tokens, split / whole: 1 sequence over 300, 500, 2,000 positions 13.8 / 15.0,
+// 14.2 / 17.4, 15.8 / 50.2 us; 32 sequences 15.8 / 15.3, 16.2 / 17.7, 29.6 / 54.9; 70 sequences, in two pieces,
+// 21.0 / 16.0, 22.1 / 19.5, 53.8 / 62.4 (1,000 positions, 8 or 9 blocks: 35.4 / 33.5).
+__host__ __device__ inline bool splits(int64_t tiles, int64_t blocks, int64_t grid) {
+  return blocks >= 3 && (3 * tiles <= grid || (2 * tiles <= grid && blocks >= 12));
+}
 constexpr int kPlanSlots = 3;
 
 // One piece of a tile's work.  Its tokens see the positions lo .. last and the sinks before lo.
@@ -891,7 +915,12 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   tc::tc_fence_after_sync();
   const uint32_t tmem = sm.tmem_slot;
   const int tiles = sm.bad ? 0 : sm.tiles, grid = gridDim.x;
-  const bool compact = int64_t(a.window) + sm.tokens - 1 + a.sinks <= kWinPos;
+  // Compact where a tile's positions fit a block.  As whole pages they might be three, in two blocks (window
+  // 128, 64 heads: 8,000 tokens of prompts 233 us compact, 384 by pages; 64 sequences of 4 tokens 16.9, 20.9),
+  // unless they are no more than a page and one: then one block by pages, too, which is copied without a look
+  // at each position (window 64: 244, 229; 16.7, 14.3).
+  const int64_t seen = int64_t(a.window) + sm.tokens - 1;
+  const bool compact = seen + a.sinks <= kWinPos && (a.sinks > 0 || seen > kPage + 1);
   Span w;
   w.pieces = 1;
   if (compact) {
@@ -901,7 +930,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     w.step = 1;
   } else {
     const int blocks = (sm.most + kWinPos - 1) / kWinPos;
-    if (a.may_split && tiles > 0 && 2 * tiles <= grid && blocks >= kMinSplit) w.pieces = min(grid / tiles, blocks);
+    if (a.may_split && tiles > 0 && splits(tiles, blocks, grid)) w.pieces = min(grid / tiles, blocks);
     w.first = blockIdx.x;
     w.units = tiles * w.pieces;
     w.step = grid;
@@ -1120,8 +1149,8 @@ cudaError_t launch_window(WindowArgs a, cudaStream_t st) {
   const int64_t ctx = a.page_table ? min64(a.d.max_ctx, int64_t(a.d.max_pages) * kPage) : a.d.max_ctx;
   const int64_t see = min64(ctx, int64_t(a.window) + span - 1 + a.sinks), blocks = (see + kWinPos - 1) / kWinPos;
   const int64_t grid = min64(min64(device_sms(), kWinMaxCtas), max64(1, tiles * blocks));
-  // fewer tiles than half of the SMs, at least: their positions may be split
-  a.may_split = blocks >= kMinSplit && 2 * (int64_t(a.total_q) * H / kWinRows) <= grid;
+  // (By the tokens of the call: of padding tokens, which make no tiles, it would be seen on the device only.)
+  a.may_split = splits(int64_t(a.total_q) * H / kWinRows, blocks, grid);
   CSA2_PROFILED(st, "window_attn",
                 (e = launch_pdl(kernel, dim3(unsigned(grid)), dim3(kWinThreads), size_t(kWinSmem), st, 1, a, m)));
   if (e != cudaSuccess || !a.may_split) return e;
