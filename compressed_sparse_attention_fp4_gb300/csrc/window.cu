@@ -616,9 +616,8 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
       for (int k = 0; k < 4; ++k) most = fmaxf(most, sm.top[k][32 * half + lane]);
       float alpha = 1.0f;
       if (most > ref + 8.0f) {
-        const float to = ceilf(most);
-        if (ref != kNone) alpha = ex2(ref - to);
-        ref = to;
+        if (ref != kNone) alpha = ex2(ref - most);
+        ref = most;                                  // the largest weight is 1, which bf16 holds exactly
       }
       sm.factor[rw][lane] = ex2(top - fmaxf(ref, -1.0e38f));
       __syncwarp();

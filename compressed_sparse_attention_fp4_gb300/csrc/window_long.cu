@@ -15,13 +15,18 @@
 // buffers, 3 blocks of P).  Tensor work of a block: 1,152 and 1,024 cycles, at the tensor cores' own rate:
 // the pair's operands are read once for 256 rows.
 //
-// The softmax reference is kept per row as an integer (base 2) and raised only when a block's maximum
-// passes it by more than 8: outputs are rarely rescaled, and then by a power of two.  Sums are fp32, of
-// the unrounded P.
+// The softmax reference is kept per row and raised to a block's maximum only when that passes it by more
+// than 8 (base 2), so that outputs are rarely rescaled.  Sums are fp32, of the unrounded P.
 //
 // Masks are formed only in blocks that some row of the tile does not see whole.  There, positions whose
 // scores are no numbers are passed on with P, and the values CTAs make zeros of those whose values are
 // not either (0 * P would be NaN in rows that do not see them).
+//
+// Measured (GB300, 64 heads): 2,048 tokens at 32,768, window 2,048, 4 sinks 400-413 us, 1.4-1.5 PFLOP/s on what
+// the rows see (window.cu's tiles: 705), bound by the tensor cores: a block takes 1,130-1,170 cycles of the 1,152
+// of its scores; of a tile's 35 blocks four or five are half masked; a tile's queries (147 KB a CTA) leave a gap
+// of about 3,300 cycles between its products and those of the tile before; and 512 tiles are 15 rounds of the 36
+// clusters that fit.  Two slots of P in place of three: 524 us, two score buffers: 407.
 #include <cuda.h>
 
 #include <atomic>
@@ -455,7 +460,7 @@ __device__ inline void softmax_role(const WindowArgs& a, LongSmall& sm, uint8_t*
       }
       float ref = before, alpha = 1.0f;
       if (top > ref + 8.0f) {
-        ref = ceilf(top);
+        ref = top;                                   // the largest weight so far is 1, which bf16 holds exactly
         if (before != -INFINITY) alpha = ex2(before - ref);
       }
       sm.ref[half][r] = ref;

@@ -459,8 +459,9 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
  *   The product of a row of q, scaled by the power of two that brings its largest value
  *   to 2^14, with a key has to stay within fp32 (rope keys below 2^100 do).
  * A CSA2 layer with a window (dims.swa > 0) joins the FP4 entries with exact bf16 rows in
- * one softmax (csa2_sparse_attn_decode); this call has no such operand and reads FP4 rows
- * alone, as that one does with swa 0 and every position in its Top-K set.
+ * one softmax (csa2_sparse_attn_decode).  This call reads FP4 rows alone, as that one does
+ * with swa 0 and every position in its Top-K set; csa2_window_attn_chunk adds the exact rows
+ * to its out and lse.
  * Limits: total_q * H <= 2^30, batch <= 2^20, cache rows (batch * max_ctx, or num_pages *
  * 64) < 2^31.
  * Make the first call on a device before any stream capture.
@@ -481,7 +482,7 @@ csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t tot
  * positions map to rows as elsewhere, by a page table or b * max_ctx + t).  A row whose destination
  * is negative or not below cache_rows is skipped.  Destinations must differ from each other.
  * For a decode step of csa2_sparse_attn_decode, whose window is swa_kv [B][W][576] in any order:
- * write position t to row b * W + t % W.
+ * write position t to row b * W + t % W.  (csa2_sparse_attn_decode_mq wants them oldest first.)
  *   x, norm_w, eps, pos, dst_rows, r: as csa2_kv_append;  kv: 16-byte aligned, no part of it
  *   within x
  * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (rot != 64), CSA2_ERR_CUDA. */
@@ -498,7 +499,8 @@ csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n,
  *   r: rotary on channels [offset, offset + r->rot) of the normed row (r->rot + offset at most its
  *     channels), or NULL: none (then pos may be NULL and offset is 0)
  *   key: E4M3, rounded to nearest even, saturating at 448; FP4, the bytes that
- *     fp4_idx_k_quantize_scatter forms of the row rounded to bf16; fp32.  All before it is fp32.
+ *     fp4_idx_k_quantize_scatter forms of the row rounded to bf16; fp32.  All before it is fp32,
+ *     with sines and cosines within 2^-21 for E4M3 and FP4 keys.
  *   x: 16-byte aligned, row stride x_stride a multiple of 16 bytes and at least a row for n > 1
  *   norm_w, norm_b: device, of x's type and channels, 16-byte aligned; norm_w NULL without a norm,
  *     norm_b with CSA2_IDX_NORM_LAYER only, or NULL
