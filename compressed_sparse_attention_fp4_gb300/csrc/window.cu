@@ -271,6 +271,10 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
     if (lane == 0) {
       sm.plan[slot] = p;
       arrive(&sm.plan_full[slot]);
+      // the other attention's outputs of a tile to come (one piece of memory) to L2
+      if (a.prev_out && p.n >= 0 && w.pieces == 1)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(a.prev_out + int64_t(p.row) * kLatent), "r"(uint32_t(p.have * kLatent * 2)) : "memory");
     }
     __syncwarp();
     if (p.n < 0) return;
@@ -697,23 +701,20 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
     const int64_t row0 = int64_t(p.row) + 32 * half;
     float prev = -INFINITY;
     if (join && lane < have) prev = a.prev_lse[row0 + lane];
-    // Joined outputs: the other attention's of the lane's four channels, two rows a word, come while the
-    // scores and products are formed (but for rows of which it has seen nothing: they may be anything).
-    // Loops that shift the registers: straight code that runs once waits for its instructions.
-    uint32_t old[kJoin ? 64 : 1];
+    // Joined outputs: the other attention's of the lane's first channel come while the scores and products are
+    // formed, those of the next channel while one is stored (but for rows of which it has seen nothing: they
+    // may be anything).  All four at once leave too few registers to have them on their way together (8,000
+    // tokens: 127 us).
+    uint32_t raw[kJoin ? 32 : 1], use = 0;
+    const uint16_t* src = nullptr;
+    const auto fetch = [&]() {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) raw[kJoin ? i : 0] = use >> i & 1 ? src[i * kLatent] : 0;
+    };
     if constexpr (kJoin) {
-      const uint32_t use = __ballot_sync(0xFFFFFFFFu, prev != -INFINITY);
-      const uint16_t* src = a.prev_out + row0 * kLatent + e;
-#pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt, src += 128) {
-#pragma unroll
-        for (int i = 0; i < 48; ++i) old[i] = old[i + 16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const uint32_t x = use >> i & 1 ? src[i * kLatent] : 0, y = use >> i & 2 ? src[(i + 1) * kLatent] : 0;
-          old[48 + i / 2] = x | y << 16;
-        }
-      }
+      use = __ballot_sync(0xFFFFFFFFu, prev != -INFINITY);
+      src = a.prev_out + row0 * kLatent + e;
+      fetch();
     }
     if (!wait_warp(sm, &sm.stat_full, (nu - 1) & 1, a.ws)) return;
     float total = 0.0f;
@@ -747,6 +748,11 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
       if constexpr (kJoin) {
 #pragma unroll 1
         for (int mt = 0; mt < 4; ++mt, dst += 128) {
+          uint32_t old[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) old[i] = raw[2 * i] | raw[2 * i + 1] << 16;
+          src += 128;
+          if (mt < 3) fetch();
 #pragma unroll
           for (int i8 = 0; i8 < 32; i8 += 8) {
             float o[8];
@@ -771,8 +777,6 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
             for (int i = 0; i < 8; ++i)
               if (i8 + i < have) dst[(i8 + i) * kLatent] = uint16_t(bf16x2_rn(o[i], 0.0f));
           }
-#pragma unroll
-          for (int i = 0; i < 48; ++i) old[i] = old[i + 16];
         }
       } else {
 #pragma unroll 1

@@ -226,7 +226,7 @@ __device__ inline bool next_piece(LongSmall& sm, uint32_t& k, int lane, uint8_t*
 }
 
 // One warp of each CTA walks the cluster's tiles and tells the others, a few tiles ahead.
-__device__ inline void plan_role(const WindowArgs& a, LongSmall& sm, int first, int tiles, int step, Sequences<kLongRows>& q, int lane) {
+__device__ inline void plan_role(const WindowArgs& a, LongSmall& sm, int first, int tiles, int step, int values, Sequences<kLongRows>& q, int lane) {
   q.count(lane);
   uint32_t k = 0;
   for (int t = first;; t += step, ++k) {
@@ -243,6 +243,11 @@ __device__ inline void plan_role(const WindowArgs& a, LongSmall& sm, int first, 
     if (lane == 0) {
       sm.plan[slot] = p;
       arrive(&sm.plan_full[slot]);
+      // values CTAs: the other attention's outputs of their rows (one piece of memory) to L2
+      const int rows = p.n < 0 || values < 0 ? 0 : min(kHalfRows, p.t.have - kHalfRows * values);
+      if (a.prev_out && rows > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(a.prev_out + (int64_t(p.t.row) + kHalfRows * values) * kLatent), "r"(rows * kLatent * 2) : "memory");
     }
     __syncwarp();
     if (p.n < 0) return;
@@ -647,19 +652,28 @@ __device__ inline void output_role(const WindowArgs& a, LongSmall& sm, uint8_t* 
     const auto chunk_at = [&](int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); };
     const int ch = lane & 7;
     const int64_t at = g0 * kLatent + 8 * ch;
+    // the other attention's outputs, whole rows of 128 bytes an instruction, a step ahead (not those of rows of
+    // which it has seen nothing, or that do not exist: their bit in `use` is 0)
+    const auto channel_of = [&](int col) { return (col0 >> 1) + (col & 127) + ((col & 128) << 1); };
+    const uint32_t use = kJoin ? __ballot_sync(0xFFFFFFFFu, prev != -INFINITY) : 0;
+    uint4 ahead[kJoin ? 8 : 1];
+    const auto fetch = [&](int col) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + lane / 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (use >> row & 1) v = *reinterpret_cast<const uint4*>(a.prev_out + at + int64_t(row) * kLatent + channel_of(col));
+        ahead[kJoin ? i : 0] = v;
+      }
+    };
+    if (kJoin) fetch(0);
 #pragma unroll 1
     for (int col = 0; col < 256; col += 64) {
-      const int channel = (col0 >> 1) + (col & 127) + ((col & 128) << 1);
+      const int channel = channel_of(col);
       if (kJoin) {
-        // the other attention's outputs, whole rows of 128 bytes an instruction (not those of rows of which it has seen nothing)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + lane / 8;
-          const float was = __shfl_sync(0xFFFFFFFFu, prev, row);             // (-inf, too, where there is no row)
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (was != -INFINITY) v = *reinterpret_cast<const uint4*>(a.prev_out + at + int64_t(row) * kLatent + channel);
-          *reinterpret_cast<uint4*>(stage + chunk_at(row, ch)) = v;
-        }
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(stage + chunk_at(4 * i + lane / 8, ch)) = ahead[i];
+        if (col < 192) fetch(col + 64);
         __syncwarp();
       }
 #pragma unroll
@@ -793,7 +807,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kLongThreads, 1)
   const int tiles = sm.bad ? 0 : sm.tiles, cluster = blockIdx.x / 4, clusters = gridDim.x / 4;
   if (blockIdx.x == 0 && tid == 0 && sm.bad) raise_err(a.ws, CSA2_DEV_Q_START);
   if (wid == kPlanWarp) {
-    plan_role(a, sm, cluster, tiles, clusters, first, lane);
+    plan_role(a, sm, cluster, tiles, clusters, scores ? -1 : part, first, lane);
   } else if (scores) {
     if (wid < kRowWarps) softmax_role(a, sm, base, part, wid, lane, tmem);
     else if (wid < kMmaWarp) query_role(a, sm, base, wid - kQueryWarp0, lane, tmem);
