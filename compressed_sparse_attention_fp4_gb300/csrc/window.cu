@@ -230,7 +230,7 @@ struct Span {
 };
 
 // `q`: the first 32 sequences, loaded.
-template <bool kCompact>
+template <bool kCompact, bool kJoin>
 __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& w, Sequences<kWinRows>& q, int lane) {
   q.count(lane);
   int was_seq = -1, was_last = 0;
@@ -271,8 +271,8 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
     if (lane == 0) {
       sm.plan[slot] = p;
       arrive(&sm.plan_full[slot]);
-      // the other attention's outputs of a tile to come (one piece of memory) to L2
-      if (a.prev_out && p.n >= 0 && w.pieces == 1)
+      // the other attention's outputs of a later tile (one piece of memory) to L2
+      if (kJoin && k > 0 && p.n >= 0 && w.pieces == 1)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
                      ::"l"(a.prev_out + int64_t(p.row) * kLatent), "r"(uint32_t(p.have * kLatent * 2)) : "memory");
     }
@@ -619,7 +619,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 #pragma unroll
       for (int k = 0; k < 4; ++k) most = fmaxf(most, sm.top[k][32 * half + lane]);
       float alpha = 1.0f;
-      if (most > ref + 8.0f) {
+      if (most > ref + kWinSlack) {
         if (ref != kNone) alpha = ex2(ref - most);
         ref = most;                                  // the largest weight is 1, which bf16 holds exactly
       }
@@ -701,19 +701,21 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
     const int64_t row0 = int64_t(p.row) + 32 * half;
     float prev = -INFINITY;
     if (join && lane < have) prev = a.prev_lse[row0 + lane];
-    // Joined outputs: the other attention's of the lane's first channel come while the scores and products are
-    // formed, those of the next channel while one is stored (but for rows of which it has seen nothing: they
-    // may be anything).  All four at once leave too few registers to have them on their way together (8,000
-    // tokens: 127 us).
-    uint32_t raw[kJoin ? 32 : 1], use = 0;
-    const uint16_t* src = nullptr;
+    // Joined outputs go by pairs of lanes: of rows 2 i and 2 i + 1 the even lane takes both channels of the one,
+    // the odd lane both of the other, so that loads and stores are 32 bits.  The other attention's come a step
+    // ahead, the first while the scores and products are formed (but for rows of which it has seen nothing: they
+    // may be anything).  4,000 tokens of 16 heads, joined: 61 us (41 alone); with values of 16 bits 66, and all
+    // fetched ahead, which leaves too few registers to be on their way together, 127.
+    const int odd = lane & 1;
+    uint32_t raw[kJoin ? 16 : 1], use = 0;
+    const uint32_t* src = nullptr;
     const auto fetch = [&]() {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) raw[kJoin ? i : 0] = use >> i & 1 ? src[i * kLatent] : 0;
+      for (int i = 0; i < 16; ++i) raw[kJoin ? i : 0] = use >> (2 * i) & 1 ? src[i * kLatent] : 0;
     };
     if constexpr (kJoin) {
-      use = __ballot_sync(0xFFFFFFFFu, prev != -INFINITY);
-      src = a.prev_out + row0 * kLatent + e;
+      use = __ballot_sync(0xFFFFFFFFu, prev != -INFINITY) >> odd;
+      src = reinterpret_cast<const uint32_t*>(a.prev_out + (row0 + odd) * kLatent + (e - odd));
       fetch();
     }
     if (!wait_warp(sm, &sm.stat_full, (nu - 1) & 1, a.ws)) return;
@@ -746,36 +748,38 @@ __device__ inline void out_role(const WindowArgs& a, WinSmall& sm, int pieces, i
       if (quarter == 0 && lane < have) a.lse[row0 + lane] = lse;
       uint16_t* dst = a.out + row0 * kLatent + e;
       if constexpr (kJoin) {
+        uint32_t* to = reinterpret_cast<uint32_t*>(dst + (odd ? kLatent - 1 : 0));
+        float fo[16], go[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          fo[i] = sm.own[half][2 * i + odd];
+          go[i] = sm.other[half][2 * i + odd];
+        }
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt, dst += 128) {
+        for (int mt = 0; mt < 4; ++mt, to += 64) {
           uint32_t old[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) old[i] = raw[2 * i] | raw[2 * i + 1] << 16;
-          src += 128;
+          for (int i = 0; i < 16; ++i) old[i] = raw[i];
+          src += 64;
           if (mt < 3) fetch();
 #pragma unroll
-          for (int i8 = 0; i8 < 32; i8 += 8) {
-            float o[8];
+          for (int i8 = 0; i8 < 32; i8 += 16) {
+            float o[16];
             if (p.n > 0) {
-              tc::tmem_ld8(lanes + kOCol + 64 * mt + i8, o);
+              tc::tmem_ld16(lanes + kOCol + 64 * mt + i8, o);
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+              for (int i = 0; i < 16; ++i) o[i] = 0.0f;
             }
 #pragma unroll
-            for (int i4 = 0; i4 < 8; i4 += 4) {
-              const float4 u = *reinterpret_cast<const float4*>(&sm.own[half][i8 + i4]);
-              const float4 v = *reinterpret_cast<const float4*>(&sm.other[half][i8 + i4]);
-              const float own4[4] = {u.x, u.y, u.z, u.w}, other4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t w = old[(i8 + i4 + i) / 2];
-                o[i4 + i] = fmaf(other4[i], __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16), o[i4 + i] * own4[i]);
-              }
+            for (int i = 0; i < 16; i += 2) {
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[i] : o[i + 1], 1);
+              const float f = fo[(i8 + i) / 2], g = go[(i8 + i) / 2];
+              const uint32_t w = old[(i8 + i) / 2];
+              const float x = fmaf(g, __uint_as_float(w << 16), (odd ? got : o[i]) * f);
+              const float y = fmaf(g, __uint_as_float(w & 0xFFFF0000u), (odd ? o[i + 1] : got) * f);
+              if (i8 + i + odd < have) to[(i8 + i) / 2 * kLatent] = bf16x2_rn(x, y);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i8 + i < have) dst[(i8 + i) * kLatent] = uint16_t(bf16x2_rn(o[i], 0.0f));
           }
         }
       } else {
@@ -961,8 +965,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (compact) load_role<true>(a, sm, base, wid - kLoadWarp0, lane, m);
       else load_role<false>(a, sm, base, wid - kLoadWarp0, lane, m);
     } else if (wid == kPlanWarp) {
-      if (compact) plan_role<true>(a, sm, w, first, lane);
-      else plan_role<false>(a, sm, w, first, lane);
+      if (compact) plan_role<true, kJoin>(a, sm, w, first, lane);
+      else plan_role<false, kJoin>(a, sm, w, first, lane);
     }
   }
   // the thread that issued the MMAs sees them done (they are, unless a wait gave up)

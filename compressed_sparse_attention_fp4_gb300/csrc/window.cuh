@@ -8,6 +8,9 @@ namespace csa2 {
 constexpr int kWinRows = 64;             // rows (query token, head) of a tile: the MMA's N
 constexpr int kLongRows = 256;          // rows of a tile of window_long.cu
 constexpr int kWinPos = 128;             // cache positions of a block: the MMA's M
+// How far (base 2) a block's maximum may pass a row's reference before the outputs so far are rescaled.  Weights
+// up to 2^16 cost no precision, only range: with 2^20 positions, values up to 2^91 stay within fp32.
+constexpr float kWinSlack = 16.0f;
 constexpr int kWinMaxCtas = 152;         // most pieces of a call whose tiles are split
 
 struct WindowArgs {

@@ -541,7 +541,7 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
  *   An infinity or a NaN in a row reaches only the outputs of tokens that see it (all their channels
  *   may then be NaN), in a query only that token and head.
  *   P is rounded to bf16 (2^-8) and the output to bf16; everything between is fp32, where weights
- *   are kept up to 2^8 times too large: values above 2^99 may pass its range.
+ *   are kept up to 2^16 times too large: values above 2^91 may pass its range.
  * Results do not change from call to call.  Limits: total_q * H <= 2^30, batch <= 2^20, rows < 2^31.
  * Make the first call on a device before any stream capture.
  * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE, CSA2_ERR_WORKSPACE_TOO_SMALL, CSA2_ERR_CUDA. */
