@@ -24,8 +24,8 @@
 //
 // What bounds it: the chain of a tile, about 8,000 cycles: scores 3,000 (2,100 of products at the rate at which
 // shared memory feeds 64 columns, 5/6 of its bandwidth), softmax 2,200, outputs 1,900, and the hand-overs
-// between.  Measured (GB300, 64 heads): whole prompts of 8,872 tokens, window 128, 262 us (0.7 of the copy rate
-// on queries and outputs); 64 decode tokens joined with another attention 12.5 us, one token 9.4-10 us (launch,
+// between.  Measured (GB300, 64 heads): whole prompts of 8,872 tokens, window 128, 257 us (0.72 of the copy rate
+// on queries and outputs); 64 decode tokens joined with another attention 12.0 us, one token 9.4-10 us (launch,
 // plan, copies, products, outputs one after the other); 8 tokens over 2,048 positions 18.7 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
