@@ -272,7 +272,7 @@ __device__ inline void plan_role(const WindowArgs& a, WinSmall& sm, const Span& 
       sm.plan[slot] = p;
       arrive(&sm.plan_full[slot]);
       // the other attention's outputs of a later tile (one piece of memory) to L2
-      if (kJoin && k > 0 && p.n >= 0 && w.pieces == 1)
+      if (kJoin && k > 0 && p.n >= 0 && p.have > 0 && w.pieces == 1)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
                      ::"l"(a.prev_out + int64_t(p.row) * kLatent), "r"(uint32_t(p.have * kLatent * 2)) : "memory");
     }
