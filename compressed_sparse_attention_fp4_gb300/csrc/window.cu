@@ -1114,9 +1114,12 @@ bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_row
 //     25.9 / 21.8, 37.2 / 27.4, 104 / 58 us; 81,920 rows 73 / 60, 99 / 72, 150 / 96, 473 / 235 us;
 //   fewer, where tiles take many blocks: 4,096 rows 24.0 / 19.2 us over 512 positions, 42 / 33 over 2,048
 //     (256: 16.0 / 16.8); 2,560 rows 20.3 / 18.2, 32.0 / 32.8;
+//   joined, where the longer pass over the outputs holds up the next tile: 64,000 rows over windows of 128, 192,
+//     256, 512 positions 71 / 83, 71 / 88, 90 / 89, 128 / 108 us;
 //   sequences of fewer rows than a tile: 64 of 128 rows 14 / 20, 17 / 24, 24 / 31, 67 / 73 us.
 bool window_is_long(const WindowArgs& a, int span) {
   const int64_t rows = int64_t(a.total_q) * a.d.heads, see = int64_t(a.window) + a.sinks;
+  if (a.prev_out && see < 200) return false;
   return see + span - 1 > kWinPos && rows >= int64_t(kLongRows) * a.batch && (rows > 152 * kWinRows || (rows >= 4096 && see >= 512));
 }
 

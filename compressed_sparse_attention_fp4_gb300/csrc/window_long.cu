@@ -680,6 +680,11 @@ __device__ inline void output_role(const WindowArgs& a, LongSmall& sm, uint8_t* 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
+        uint4 o[kJoin ? 4 : 1];
+        if (kJoin) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const uint4*>(stage + chunk_at(lane, 4 * h + i));
+        }
         if (p.n > 0) {
           tc::tmem_ld32(lanes + col + 32 * h, v);
         } else {
@@ -688,11 +693,10 @@ __device__ inline void output_role(const WindowArgs& a, LongSmall& sm, uint8_t* 
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint4* to = reinterpret_cast<uint4*>(stage + chunk_at(lane, 4 * h + i));
           uint32_t w[4] = {0, 0, 0, 0};
           if (kJoin) {
-            const uint4 o = *to;
-            w[0] = o.x; w[1] = o.y; w[2] = o.z; w[3] = o.w;
+            const uint4 x = o[kJoin ? i : 0];
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -703,7 +707,7 @@ __device__ inline void output_role(const WindowArgs& a, LongSmall& sm, uint8_t* 
             }
             w[k] = bf16x2_rn(lo, up);
           }
-          *to = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + chunk_at(lane, 4 * h + i)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       __syncwarp();
