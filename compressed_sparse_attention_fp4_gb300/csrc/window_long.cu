@@ -74,7 +74,9 @@ struct __align__(16) LongPiece {
 
 struct LongSmall {
   uint64_t full[kStages], empty[kStages];            // ring (full: of keys or values)
-  uint64_t q_place[4];                               // 32 query rows have come to their place in the ring
+  // 32 query rows have come to their place in the ring: barriers apart from `full`, as a wait by parity needs all
+  // of a barrier's phases, and those who copy the queries see none of the blocks between
+  uint64_t q_place[4];
   uint64_t k_ready[kStages];                         // leading scores CTA: the other's half of a block is there
   uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint64_t q_full, q_free;                           // queries in tensor memory (both CTAs); read by the tile's last product
