@@ -217,8 +217,9 @@ def fp4_idx_k_planes(idx_k: torch.Tensor, cache_rows: int):
     """Views (codes [rows, 64], scales [rows, 8]) of a two-plane FP4 indexer-K buffer."""
     flat = idx_k if idx_k.dim() == 1 and idx_k.is_contiguous() else idx_k.reshape(-1)
     _need("fp4_idx_k_planes", 0 <= cache_rows * 72 <= flat.numel())
-    at = flat.storage_offset()
-    return flat.as_strided((cache_rows, 64), (64, 1), at), flat.as_strided((cache_rows, 8), (8, 1), at + cache_rows * 64)
+    at, step = flat.storage_offset(), flat.stride(0)
+    return (flat.as_strided((cache_rows, 64), (64 * step, step), at),
+            flat.as_strided((cache_rows, 8), (8 * step, step), at + cache_rows * 64 * step))
 
 
 def fp4_kv_dequantize(codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor | None = None,
