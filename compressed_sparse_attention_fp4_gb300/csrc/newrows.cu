@@ -79,13 +79,14 @@ __global__ void __launch_bounds__(kWinAppThreads, kWinAppBlocks)
 // that half-split pairs exchange go through shared memory, laid out so that the eight lanes of a row read 128
 // bytes in a row.
 //
-// A million rows (layer norm, 64 of 128 channels turned, E4M3): 111 us.  It took 206 us with arithmetic on
-// single values and angles formed by the lanes that use them, 135 with polynomials for all sines, 120 with
-// the weights in shared memory (four wavefronts a load, 87 % of its cycles) at 4 blocks of 256 threads, 114
-// at 3.
+// A million rows (layer norm, 64 of 128 channels turned, E4M3): 122 us.  It took 206 us with arithmetic on
+// single values and angles formed by the lanes that use them, 135 with the weights in shared memory (four
+// wavefronts a load, 87 % of its cycles) at 4 blocks of 256 threads.  (With the hardware's sine and cosine, which
+// are off by 2^-21 and more whatever they are themselves, 112: E4M3 keys then come out a step off next to a
+// rounding border, by many steps where a large channel meets a small sine.)
 // ---------------------------------------------------------------------------
 constexpr int kKeyThreads = 128;
-constexpr int kKeyBlocks = 4;                        // resident on an SM: 128 registers a thread hold the weights, too (5: 120 us)
+constexpr int kKeyBlocks = 4;                        // resident on an SM: 128 registers a thread hold the weights, too (5: 135 us)
 constexpr int kKeyPairs = 64;                        // most pairs of a key
 
 using f32x2 = uint64_t;                              // low half first
@@ -187,16 +188,6 @@ __device__ inline void rope_cs2(uint64_t turn, f32x2 mscale, int32_t p0, int32_t
   s.y = __uint_as_float(__float_as_uint(q1 & 1 ? u.y : v.y) ^ (q1 << 30 & 0x80000000u));
 }
 
-// The same for keys of 4 and 8 bits: the exact part of a turn, then the hardware's sine and cosine, which are
-// within 2^-21 of 1 there (1.0 in 2^18 is lost at most; E4M3 keys round by 2^-4 of themselves).
-__device__ inline void rope_cs2_fast(uint64_t turn, float mscale, int32_t p0, int32_t p1, float2& c, float2& s) {
-  const float unit = 1.4629180792671596e-9f;                                                // 2 pi / 2^32
-  const float x0 = float(int32_t(uint32_t((uint64_t(int64_t(p0)) * turn) >> 32))) * unit;
-  const float x1 = float(int32_t(uint32_t((uint64_t(int64_t(p1)) * turn) >> 32))) * unit;
-  c = make_float2(__cosf(x0) * mscale, __cosf(x1) * mscale);
-  s = make_float2(__sinf(x0) * mscale, __sinf(x1) * mscale);
-}
-
 // Places (floats) of a row's channel c and pair p in shared memory: where pieces have two quads of
 // channels, the first quads of eight pieces stand before their second ones (pairs, 48 apart: the 32
 // lanes that store them meet all banks).
@@ -293,8 +284,7 @@ __global__ void __launch_bounds__(kKeyThreads, kKeyBlocks)
         for (int r = 0; r < 4; r += 2) {
           float2 c, s;
           const int32_t p0 = __shfl_sync(0xFFFFFFFFu, now.pos, 8 * r), p1 = __shfl_sync(0xFFFFFFFFu, now.pos, 8 * r + 8);
-          if constexpr (kKind == CSA2_IDXK_F32) rope_cs2(turn, mscale, p0, p1, c, s);
-          else rope_cs2_fast(turn, tab.mscale, p0, p1, c, s);
+          rope_cs2(turn, mscale, p0, p1, c, s);
           if (i < pairs) {
             const int to = cs_place<C, kHalf>(i);
             s_c[wid][r][to] = c.x;

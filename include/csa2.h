@@ -500,7 +500,7 @@ csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n,
  *     channels), or NULL: none (then pos may be NULL and offset is 0)
  *   key: E4M3, rounded to nearest even, saturating at 448; FP4, the bytes that
  *     fp4_idx_k_quantize_scatter forms of the row rounded to bf16; fp32.  All before it is fp32,
- *     with sines and cosines within 2^-21 for E4M3 and FP4 keys.
+ *     sines and cosines as of csa2_rope_apply.
  *   x: 16-byte aligned, row stride x_stride a multiple of 16 bytes and at least a row for n > 1
  *   norm_w, norm_b: device, of x's type and channels, 16-byte aligned; norm_w NULL without a norm,
  *     norm_b with CSA2_IDX_NORM_LAYER only, or NULL
