@@ -555,16 +555,28 @@ __device__ inline void mask_scores(WinSmall& sm, uint8_t* base, float (&x)[32], 
   if (see != ~0u) hide_values(sm, base, e, block);
 }
 
+// Two scores as weights under their rows' maxima (a pair, low half first).
+__device__ inline void weights2(float& x, float& y, uint64_t m, float c) {
+  asm("{\n\t.reg .b64 v, k;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 k, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, %2, k, v;\n\tmov.b64 k, {%4, %4};\n\tmul.rn.f32x2 v, v, k;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y) : "l"(m), "f"(-1.0f), "f"(c));
+  x = ex2(x);
+  y = ex2(y);
+}
+
 // Softmax over a block's positions (tensor-memory lanes).  Warp rw has the lanes 32 (rw % 4) .. + 31
 // and the rows 32 (rw / 4) .. + 31; lane i keeps the state of row i of these (alike in the four warps
 // of a half, but for the sum, which is of its own lanes).  A warp's weights are formed under its own
 // maxima while it waits for the other warps', and then brought to the common reference.
-constexpr float kNone = -3.0e38f;                    // maximum of no scores
+// Maxima and references are scores, not yet times `c`: the difference of two scores is exact where it matters, and 0
+// for the largest, whatever their size.  (c x less a rounded c x is not: half a unit of it, past any weight from 2^31 on.)
+constexpr float kNone = -3.402823466e38f;            // maximum of no scores
 template <bool kCompact>
 __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base, int rw, int lane, uint32_t tmem) {
   const int quarter = rw & 3, half = rw >> 2, e = 32 * quarter + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(32 * half);
-  const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);        // logits in base 2 per score
+  const float c = score_to_log2(a);
   uint8_t* const p_at = base + p_offset<kCompact>(quarter >> 1);
   Piece p;
   uint32_t nu = 0, nk = 0, nm = 0;
@@ -603,27 +615,25 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         const float m = max_over_warp(x[i]);
         if (lane == i) top = m;
       }
-      top = fmaxf(top * c, kNone);
+      top = fmaxf(top, kNone);
       sm.top[quarter][32 * half + lane] = top;       // (read before the other warps' P, which these scores came after)
       meet_arrive(&sm.meet[half], lane);
 #pragma unroll
       for (int i4 = 0; i4 < 8; ++i4) {
-        const float4 m = reinterpret_cast<const float4*>(&sm.top[quarter][32 * half])[i4];
-        x[4 * i4] = ex2(fmaf(x[4 * i4], c, -m.x));
-        x[4 * i4 + 1] = ex2(fmaf(x[4 * i4 + 1], c, -m.y));
-        x[4 * i4 + 2] = ex2(fmaf(x[4 * i4 + 2], c, -m.z));
-        x[4 * i4 + 3] = ex2(fmaf(x[4 * i4 + 3], c, -m.w));
+        const ulonglong2 m = reinterpret_cast<const ulonglong2*>(&sm.top[quarter][32 * half])[i4];
+        weights2(x[4 * i4], x[4 * i4 + 1], m.x, c);
+        weights2(x[4 * i4 + 2], x[4 * i4 + 3], m.y, c);
       }
       if (!meet_wait(sm, &sm.meet[half], nm, a.ws)) return;
       float most = top;
 #pragma unroll
       for (int k = 0; k < 4; ++k) most = fmaxf(most, sm.top[k][32 * half + lane]);
       float alpha = 1.0f;
-      if (most > ref + kWinSlack) {
-        if (ref != kNone) alpha = ex2(ref - most);
+      if ((most - ref) * c > kWinSlack || (ref == kNone && most > kNone)) {
+        if (ref != kNone) alpha = ex2((ref - most) * c);
         ref = most;                                  // the largest weight is 1, which bf16 holds exactly
       }
-      sm.factor[rw][lane] = ex2(top - fmaxf(ref, -1.0e38f));
+      sm.factor[rw][lane] = ex2((top - ref) * c);
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
         // the outputs so far to the new reference (this block's scores came after the last product: the
@@ -667,7 +677,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
     meet_arrive(&sm.meet[half], lane);
     if (!meet_wait(sm, &sm.meet[half], nm, a.ws)) return;
     sm.top[quarter][32 * half + lane] = sum;
-    if (quarter == 0) sm.factor[rw][lane] = ref;
+    if (quarter == 0) sm.factor[rw][lane] = ref * c;
     __syncwarp();
     if (lane == 0) arrive(&sm.stat_full);
   }

@@ -15,9 +15,9 @@
 // buffers, 3 blocks of P).  Tensor work of a block: 1,152 and 1,024 cycles, at the tensor cores' own rate:
 // the pair's operands are read once for 256 rows.
 //
-// The softmax reference is kept per row and raised to a block's maximum only when that passes it by more
-// than 16 (base 2), so that outputs are rarely rescaled (8: 430 in place of 410 us for the call below).  Sums
-// are fp32, of the unrounded P.
+// The softmax reference is a score of the row (window.cu says why not a logit), raised to a block's maximum only
+// when that passes it by more than 16 (base 2), so that outputs are rarely rescaled (8: 430 in place of 410 us for
+// the call below).  Sums are fp32, of the unrounded P.
 //
 // Masks are formed only in blocks that some row of the tile does not see whole.  There, positions whose
 // scores are no numbers are passed on with P, and the values CTAs make zeros of those whose values are
@@ -196,9 +196,9 @@ __device__ inline uint64_t pack2(float lo, float hi) {
   return r;
 }
 __device__ inline void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+__device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ inline uint64_t add2(uint64_t a, uint64_t b) {
@@ -402,7 +402,7 @@ __device__ inline void scores_mma_role(const WindowArgs& a, LongSmall& sm, uint8
 __device__ inline void softmax_role(const WindowArgs& a, LongSmall& sm, uint8_t* base, int part, int rw, int lane, uint32_t tmem) {
   const int wq = rw & 3, half = rw >> 2, r = 32 * wq + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * wq) << 16);
-  const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);        // logits in base 2 per score
+  const float c = score_to_log2(a);
   LongPiece p;
   uint32_t nu = 0, n = 0;
   while (next_piece(sm, nu, lane, a.ws, p)) {
@@ -460,21 +460,21 @@ __device__ inline void softmax_role(const WindowArgs& a, LongSmall& sm, uint8_t*
       for (int i = 4; i < 64; i += 4)
 #pragma unroll
         for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], x[i + k]);
-      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
       float before = -INFINITY;
       if (n > 0) {
         if (!wait_warp(sm, &sm.ref_full[half ^ 1][wq], ((n - 1) >> 1) & 1, a.ws)) return;
         if (n != n0) before = sm.ref[half ^ 1][r];
       }
       float ref = before, alpha = 1.0f;
-      if (top > ref + kWinSlack) {
+      if ((top - ref) * c > kWinSlack) {             // (no score yet: NaN, or inf)
         ref = top;                                   // the largest weight so far is 1, which bf16 holds exactly
-        if (before != -INFINITY) alpha = ex2(before - ref);
+        if (before != -INFINITY) alpha = ex2((before - ref) * c);
       }
       sm.ref[half][r] = ref;
       __syncwarp();
       if (lane == 0) arrive(&sm.ref_full[half][wq]);
-      if (own != ref && own != -INFINITY) sum *= ex2(own - ref);     // (no reference yet: 0, or NaN)
+      if (own != ref && own != -INFINITY) sum *= ex2((own - ref) * c);     // (no reference yet: 0, or NaN)
       own = ref;
       const float sub = ref == -INFINITY ? 0.0f : ref;
       if (!wait_warp(sm, &sm.p_free[slot], ((n / kPSlots) & 1) ^ 1, a.ws)) return;
@@ -486,7 +486,7 @@ __device__ inline void softmax_role(const WindowArgs& a, LongSmall& sm, uint8_t*
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float p0, p1;
-          unpack2(fma2(pack2(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]), cc, ss), p0, p1);
+          unpack2(mul2(add2(pack2(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]), ss), cc), p0, p1);
           p0 = ex2(p0);
           p1 = ex2(p1);
           acc[k & 1] = add2(acc[k & 1], pack2(p0, p1));
@@ -589,6 +589,7 @@ template <bool kJoin>
 __device__ inline void output_role(const WindowArgs& a, LongSmall& sm, uint8_t* base, int part, int rw, int lane, uint32_t tmem) {
   const int wq = rw & 3, col0 = 256 * (rw >> 2), r = 32 * wq + lane;
   const uint32_t lanes = tmem + (uint32_t(32 * wq) << 16) + uint32_t(col0);
+  const float c = score_to_log2(a);
   uint8_t* stage = base + kOutOff + rw * 4096;
   LongPiece p;
   uint32_t nu = 0, n = 0;
@@ -659,9 +660,9 @@ __device__ inline void output_role(const WindowArgs& a, LongSmall& sm, uint8_t* 
       if (!wait_warp(sm, &sm.pv_done[m % kPSlots], (m / kPSlots) & 1, a.ws)) return;
       tc::tc_fence_after_sync();
     }
-    if (sum_b != 0.0f) sum += sum_b * ex2(sub_b - sub);
+    if (sum_b != 0.0f) sum += sum_b * ex2((sub_b - sub) * c);
     float mine = sum != 0.0f ? 1.0f / sum : 0.0f, other = 0.0f;          // NaN stays NaN
-    float lse = sum != 0.0f ? (sub + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    float lse = sum != 0.0f ? fmaf(sub, c, log2f(sum)) * 0.6931471805599453f : -INFINITY;
     if (kJoin && prev != -INFINITY) {
       const float most = fmaxf(lse, prev), x0 = expf(lse - most), x1 = expf(prev - most);
       mine *= x0 / (x0 + x1);

@@ -86,6 +86,9 @@ __device__ inline Tile find_tile(const WindowArgs& a, Sequences<kRows>& q, int t
   return p;
 }
 
+// Logits in base 2 per score (but for its sign; not 0, which would make NaN of a masked score).
+__device__ inline float score_to_log2(const WindowArgs& a) { return fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f); }
+
 // Pages of 64 positions that a tile sees: `sinks` of them first, then the window's.
 struct TilePages {
   int sinks, all;
