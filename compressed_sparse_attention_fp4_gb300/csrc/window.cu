@@ -202,23 +202,29 @@ __device__ inline int place_position(const WindowArgs& a, const Piece& p, int j,
   return i < p.np && t <= p.last ? t : -1;
 }
 
-// The position's values, if an infinity or NaN is among them, become 0: its weight in the rows that
-// do not see it is 0, and so must be 0 times its values.  The rows that do see it are NaN by its
-// score, which holds the same channels.
-__device__ __noinline__ void hide_values(WinSmall& sm, uint8_t* base, int e, uint32_t block) {
+// For a position whose scores are no numbers, of cache row `row`, at place e, which the rows `see` of the warp's see.
+// Its values, if an infinity or NaN is among them, become 0 where a row does not see them: the weight there is 0, and
+// so must be 0 times its values.  Returns the rows that do see such values.  (Looked up in the cache, as the other
+// half's warp may have hidden them.)
+__device__ __noinline__ uint32_t hide_values(const WindowArgs& a, WinSmall& sm, uint8_t* base, uint32_t see, int row, int e, uint32_t block) {
+  uint32_t lost = 0;
+  if (see != 0u) {
+    const uint4* at = reinterpret_cast<const uint4*>(a.kv + int64_t(row) * kDqk);
+#pragma unroll 1
+    for (int c = 0; c < 64; ++c)
+      if (!bf16x8_finite(__ldg(at + c))) lost = see;
+  }
+  if (see == ~0u) return lost;
   bool whole = true;
 #pragma unroll 1
-  for (int c = 0; c < 64; ++c) {
-    const uint4 x = *reinterpret_cast<const uint4*>(base + (c >> 3) * kKReg + tc::sw128_offset(e, c & 7));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) whole = whole && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
-  }
-  if (whole) return;
+  for (int c = 0; c < 64; ++c)
+    whole = whole && bf16x8_finite(*reinterpret_cast<const uint4*>(base + (c >> 3) * kKReg + tc::sw128_offset(e, c & 7)));
+  if (whole) return lost;
   *reinterpret_cast<volatile uint32_t*>(&sm.hidden) = block + 1;
 #pragma unroll 1
   for (int c = 0; c < 64; ++c)
     *reinterpret_cast<uint4*>(base + (c >> 3) * kKReg + tc::sw128_offset(e, c & 7)) = make_uint4(0, 0, 0, 0);
+  return lost;
 }
 
 // ---------------------------------------------------------------------------
@@ -527,20 +533,23 @@ __device__ inline void mma_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 // ---------------------------------------------------------------------------
 // Softmax
 // ---------------------------------------------------------------------------
-// Which of the warp's 32 rows see position t (bit i: row i).  `pos`, `rem`: the first row's token
-// position and head; tokens are `heads` rows each.  (Rows that do not exist take part as if they did:
-// nothing of theirs is used.)
-__device__ inline uint32_t seen_by(const WindowArgs& a, int t, int pos, int rem) {
+// Which of the warp's 32 rows see position t (bit i: row i), and whether all 64 rows of the tile do, of which
+// `before` come before the warp's.  `pos`, `rem`: the first row's token position and head; tokens are `heads` rows
+// each.  (Rows that do not exist take part as if they did: nothing of theirs is used.)
+__device__ inline uint32_t seen_by(const WindowArgs& a, int t, int pos, int rem, int before, bool& all) {
+  all = false;
   if (t < 0) return 0u;
   // rows from the first of token t on, to the last of token t + window - 1 (any, for a sink)
-  const int lo = (t - pos) * a.d.heads - rem, hi = t < a.sinks ? 32 : lo + a.window * a.d.heads;
+  const int lo = (t - pos) * a.d.heads - rem, hi = t < a.sinks ? kWinRows : lo + a.window * a.d.heads;
+  all = lo <= -before && hi >= kWinRows - before;
   if (lo >= 32 || hi <= 0) return 0u;
   const uint32_t from = lo <= 0 ? ~0u : ~0u << lo;
   return hi >= 32 ? from : from & ((1u << hi) - 1u);
 }
 
-// The scores of rows that do not see the lane's position become -inf.
-__device__ inline void mask_scores(WinSmall& sm, uint8_t* base, float (&x)[32], uint32_t see, int e, uint32_t block) {
+// The scores of rows that do not see the lane's position become -inf.  `row`: its cache row.
+__device__ inline void mask_scores(const WindowArgs& a, WinSmall& sm, uint8_t* base, float (&x)[32], uint32_t see, int row, int e,
+                                   uint32_t block) {
   float any = 0.0f;                                  // 0, or NaN where a score is no number
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
@@ -548,11 +557,12 @@ __device__ inline void mask_scores(WinSmall& sm, uint8_t* base, float (&x)[32], 
     x[i] = see >> i & 1 ? x[i] : -INFINITY;
   }
   if (any == 0.0f) return;
-  // an infinity or NaN: rows that see the position become NaN; is it hidden from others, its values go
+  // An infinity or NaN: values that are no numbers go where a row does not see them, and the rows that do become NaN.
+  // (Of values that are numbers a score of -inf, by the rotary channels alone, is weight 0, and one of +inf makes NaN
+  // by itself.)
+  const uint32_t lost = hide_values(a, sm, base, see, row, e, block);
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if ((see >> i & 1) && !(fabsf(x[i]) < INFINITY)) x[i] = NAN;
-  if (see != ~0u) hide_values(sm, base, e, block);
+  for (int i = 0; i < 32; ++i) x[i] = lost >> i & 1 ? NAN : x[i];
 }
 
 // Two scores as weights under their rows' maxima (a pair, low half first).
@@ -595,8 +605,9 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
 #pragma unroll 1
     for (int j = 0; j < p.n; ++j, ++nk) {
       if (row < 0) t = -1;
-      const uint32_t see = seen_by(a, t, pos, rem);
-      const bool edge = !__all_sync(0xFFFFFFFFu, see == ~0u);
+      bool all;
+      const uint32_t see = seen_by(a, t, pos, rem, 32 * half, all);
+      const bool edge = !__all_sync(0xFFFFFFFFu, all);     // the same for both halves: what one hides, the other must know of
       if (!wait_warp(sm, &sm.s_full, nk & 1, a.ws)) return;
       tc::tc_fence_after_sync();
       float x[32];
@@ -606,7 +617,7 @@ __device__ inline void row_role(const WindowArgs& a, WinSmall& sm, uint8_t* base
         for (int i = 0; i < 32; ++i) x[i] = -x[i];
       }
       if (edge) {
-        mask_scores(sm, base, x, see, e, nk);
+        mask_scores(a, sm, base, x, see, row, e, nk);
         __syncwarp();
       }
       float top = kNone;

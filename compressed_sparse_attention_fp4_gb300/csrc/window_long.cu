@@ -21,7 +21,7 @@
 //
 // Masks are formed only in blocks that some row of the tile does not see whole.  There, positions whose
 // scores are no numbers are passed on with P, and the values CTAs make zeros of those whose values are
-// not either (0 * P would be NaN in rows that do not see them).
+// not either (0 * P would be NaN in rows that do not see them); rows that do see them become NaN by their sums.
 //
 // Measured (GB300, 64 heads): 2,048 tokens at 32,768, window 2,048, 4 sinks 400-413 us, 1.4-1.5 PFLOP/s on what
 // the rows see (window.cu's tiles: 705), bound by the tensor cores: a block takes 1,130-1,170 cycles of the 1,152
@@ -395,6 +395,22 @@ __device__ inline void scores_mma_role(const WindowArgs& a, LongSmall& sm, uint8
   }
 }
 
+// The lowest n bits.
+__device__ inline uint64_t below(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+// Of the block's positions in `among` (the same for the warp), up to the last, those whose cache rows (the first's:
+// `row`) hold values that are no numbers.
+__device__ __noinline__ uint64_t not_finite(const WindowArgs& a, int row, int last, uint64_t among, int lane) {
+  uint64_t found = 0;
+#pragma unroll 1
+  for (int e = 0; e < kBlk && e <= last; ++e) {
+    if (!(among >> e & 1)) continue;
+    const uint4* at = reinterpret_cast<const uint4*>(a.kv + (int64_t(row) + e) * kDqk);
+    const bool finite = bf16x8_finite(__ldg(at + lane)) && bf16x8_finite(__ldg(at + 32 + lane));
+    if (!__all_sync(0xFFFFFFFFu, finite)) found |= 1ull << e;
+  }
+  return found;
+}
+
 // Warp rw: rows 32 (rw % 4) .. + 31 of the CTA's (one a lane), of every block n with n % 2 = rw / 4: the two
 // warps of a row take turns, each with two block periods for the latencies of a block.  What must go in
 // order is the reference: block n's warp takes it from block n - 1's as soon as that one has its maximum,
@@ -446,11 +462,13 @@ __device__ inline void softmax_role(const WindowArgs& a, LongSmall& sm, uint8_t*
         for (int i = 0; i < 64; ++i) any = fmaf(x[i], 0.0f, any);
         if (__any_sync(0xFFFFFFFFu, any != 0.0f)) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const bool no = !(fabsf(x[i]) < INFINITY);
-            if (__any_sync(0xFFFFFFFFu, no)) hidden[i >> 5] |= 1u << (i & 31);
-            if (no) x[i] = NAN;
-          }
+          for (int i = 0; i < 64; ++i)
+            if (__any_sync(0xFFFFFFFFu, !(fabsf(x[i]) < INFINITY))) hidden[i >> 5] |= 1u << (i & 31);
+          // Of those whose values are not numbers either, which the values CTAs hide from all rows, the rows that
+          // see them become NaN by their sums.  (Else a score of -inf, by the rotary channels alone, is weight 0, and
+          // one of +inf makes NaN by itself.)
+          const uint64_t see = below(hi + 1) & (~below(lo) | below(sk));
+          if (!lost && (not_finite(a, row_of(a, p.t.seq, t0), p.t.last - t0, uint64_t(hidden[1]) << 32 | hidden[0], lane) & see)) sum = NAN;
         }
 #pragma unroll
         for (int i = 0; i < 64; ++i) x[i] = i <= hi && (i >= lo || i < sk) ? x[i] : -INFINITY;
@@ -573,12 +591,7 @@ __device__ __noinline__ void hide_values(uint8_t* stage, uint64_t hidden, int rw
   for (int e = rw; e < kBlk; e += kRowWarps) {
     if (!(hidden >> e & 1)) continue;
     uint4* at = reinterpret_cast<uint4*>(stage + (lane >> 3) * 8192 + tc::sw128_offset(e, lane & 7));
-    const uint4 v = *at;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) finite = finite && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
-    if (!finite) *at = make_uint4(0, 0, 0, 0);
+    if (!bf16x8_finite(*at)) *at = make_uint4(0, 0, 0, 0);
   }
   tc::fence_proxy_async_smem();
 }

@@ -89,6 +89,15 @@ __device__ inline Tile find_tile(const WindowArgs& a, Sequences<kRows>& q, int t
 // Logits in base 2 per score (but for its sign; not 0, which would make NaN of a masked score).
 __device__ inline float score_to_log2(const WindowArgs& a) { return fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f); }
 
+// Whether four 32-bit words hold eight finite bf16 values.
+__device__ inline bool bf16x8_finite(uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) finite = finite && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
+  return finite;
+}
+
 // Pages of 64 positions that a tile sees: `sinks` of them first, then the window's.
 struct TilePages {
   int sinks, all;

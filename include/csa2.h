@@ -538,8 +538,11 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
  *   ws:        workspace of csa2_window_attn_workspace_size bytes, its first 256 the error word as
  *              elsewhere.  Calls that may run at the same time need a workspace each.
  *   A q_start that falls back or leaves 0 .. total_q is reported and the call writes nothing.
- *   An infinity or a NaN in a row reaches only the outputs of tokens that see it (all their channels
- *   may then be NaN), in a query only that token and head.
+ *   An infinity or a NaN in a row reaches only the outputs of tokens that see it: among the row's values
+ *   (channels 0..511) they are no numbers in those channels at least (their others and lse may be none);
+ *   among its rotary channels alone the formula holds: a logit of -inf is weight 0 (of a token left with
+ *   no weight: as if it saw nothing), one of +inf or NaN leaves no number in out and lse.  In a query
+ *   they reach only that token and head.
  *   P is rounded to bf16 (2^-8) and the output to bf16; everything between is fp32, where weights
  *   are kept up to 2^16 times too large: values above 2^91 may pass its range.
  * Results do not change from call to call.  Limits: total_q * H <= 2^30, batch <= 2^20, rows < 2^31.
