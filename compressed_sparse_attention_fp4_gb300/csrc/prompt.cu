@@ -38,6 +38,19 @@ bool overlap(const void* a, __int128 a_bytes, const void* b, __int128 b_bytes) {
   return x < y + b_bytes && y < x + a_bytes;
 }
 
+// A block of bytes that a call reads (may be NULL: none).
+struct Bytes {
+  const void* at;
+  __int128 n;
+};
+// Whether [p, p + n), which a call writes, shares any byte with what it reads.
+template <int kCount>
+bool overlaps_any(const void* p, __int128 n, const Bytes (&reads)[kCount]) {
+  for (const Bytes& r : reads)
+    if (r.at && overlap(p, n, r.at, r.n)) return true;
+  return false;
+}
+
 // Sizes of a chunk call: heads, contexts, rows counted in 32 bits.
 csa2_status check_dense_dims(const csa2_dims* d, int32_t batch, int64_t total_q) {
   if (!d || batch < 0 || total_q < 0) return CSA2_ERR_INVALID_ARG;
@@ -203,7 +216,8 @@ csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n,
   if (n > 1 && (x_stride < kDqk || x_stride % 8 != 0)) return CSA2_ERR_INVALID_ARG;
   const __int128 last = __int128(n - 1) * (n > 1 ? x_stride : 0) + kDqk;
   if (last > (__int128(1) << 59) || cache_rows > (int64_t(1) << 49)) return CSA2_ERR_UNSUPPORTED_SHAPE;
-  if (overlap(x, last * 2, kv, __int128(cache_rows) * kDqk * 2)) return CSA2_ERR_INVALID_ARG;
+  const Bytes reads[] = {{x, last * 2}, {pos, __int128(n) * 4}, {dst_rows, __int128(n) * 8}, {norm_w, kLatent * 2}};
+  if (overlaps_any(kv, __int128(cache_rows) * kDqk * 2, reads)) return CSA2_ERR_INVALID_ARG;
   WindowAppendArgs a = {};
   a.cfg = *r;
   a.x = x;
@@ -242,7 +256,9 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
   const __int128 last = __int128(n - 1) * (n > 1 ? x_stride : 0) + dim;
   if (last > (__int128(1) << 59) || cache_rows > (int64_t(1) << 49)) return CSA2_ERR_UNSUPPORTED_SHAPE;
   const int64_t row = idx_k_dtype == CSA2_IDXK_F32 ? 256 : idx_k_dtype == CSA2_IDXK_FP4 ? 72 : 128;
-  if (overlap(x, last * size, idx_k, __int128(cache_rows) * row)) return CSA2_ERR_INVALID_ARG;
+  const Bytes reads[] = {{x, last * size}, {r ? pos : nullptr, __int128(n) * 4}, {dst_rows, __int128(n) * 8},
+                         {norm_w, dim * size}, {norm_b, dim * size}};
+  if (overlaps_any(idx_k, __int128(cache_rows) * row, reads)) return CSA2_ERR_INVALID_ARG;
   IdxAppendArgs a = {};
   a.rotate = r != nullptr;
   if (r) a.cfg = *r;
@@ -284,7 +300,7 @@ csa2_status csa2_window_attn_chunk(const csa2_dims* d, int32_t batch, int64_t to
   if (!ws || !is_aligned(ws, 256)) return CSA2_ERR_INVALID_ARG;
   const WindowLayout L = make_window_layout();
   if (ws_bytes < size_t(L.total)) return CSA2_ERR_WORKSPACE_TOO_SMALL;
-  // the cache is addressed by 32-bit row coordinates, and one row behind it (read as zeros)
+  // the cache is addressed by 32-bit row coordinates
   const __int128 rows = page_table ? __int128(d->num_pages) * kPage : __int128(batch) * d->max_ctx;
   if (rows > INT32_MAX) return CSA2_ERR_UNSUPPORTED_SHAPE;
   if (batch == 0 || total_q == 0) return CSA2_OK;
@@ -293,12 +309,17 @@ csa2_status csa2_window_attn_chunk(const csa2_dims* d, int32_t batch, int64_t to
       !is_aligned(out, 16) || !is_aligned(lse, 4) || !is_aligned(prev_out, 16) || !is_aligned(prev_lse, 4))
     return CSA2_ERR_INVALID_ARG;
   const __int128 n = __int128(total_q) * d->heads, out_bytes = n * kLatent * 2, lse_bytes = n * 4;
-  if (overlap(out, out_bytes, q, n * kDqk * 2) || overlap(out, out_bytes, kv, rows * kDqk * 2) || overlap(out, out_bytes, lse, lse_bytes) ||
-      overlap(lse, lse_bytes, q, n * kDqk * 2) || overlap(lse, lse_bytes, kv, rows * kDqk * 2) || overlap(ws, L.total, out, out_bytes) ||
-      overlap(ws, L.total, lse, lse_bytes))
-    return CSA2_ERR_INVALID_ARG;
-  if (prev_out && ((prev_out != out && overlap(out, out_bytes, prev_out, out_bytes)) || overlap(lse, lse_bytes, prev_out, out_bytes) ||
-                   (prev_lse != lse && overlap(lse, lse_bytes, prev_lse, lse_bytes)) || overlap(out, out_bytes, prev_lse, lse_bytes)))
+  // outputs and workspace apart from what the call reads and from each other; joined in place, out and lse are read as well
+  const Bytes reads[] = {{q, n * kDqk * 2},
+                         {kv, rows * kDqk * 2},
+                         {q_start, (__int128(batch) + 1) * 4},
+                         {ctx_len, __int128(batch) * 4},
+                         {page_table, __int128(batch) * d->max_pages * 4},
+                         {prev_out != out ? prev_out : nullptr, out_bytes},
+                         {prev_lse != lse ? prev_lse : nullptr, lse_bytes}};
+  const Bytes outputs[] = {{out, out_bytes}, {lse, lse_bytes}};
+  if (overlaps_any(out, out_bytes, reads) || overlaps_any(lse, lse_bytes, reads) || overlaps_any(ws, L.total, reads) ||
+      overlaps_any(ws, L.total, outputs) || overlap(out, out_bytes, lse, lse_bytes))
     return CSA2_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
   WindowArgs a = {};

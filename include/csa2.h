@@ -483,8 +483,8 @@ csa2_status csa2_dense_attn_chunk(const csa2_dims* d, int32_t batch, int64_t tot
  * is negative or not below cache_rows is skipped.  Destinations must differ from each other.
  * For a decode step of csa2_sparse_attn_decode, whose window is swa_kv [B][W][576] in any order:
  * write position t to row b * W + t % W.  (csa2_sparse_attn_decode_mq wants them oldest first.)
- *   x, norm_w, eps, pos, dst_rows, r: as csa2_kv_append;  kv: 16-byte aligned, no part of it
- *   within x
+ *   x, norm_w, eps, pos, dst_rows, r: as csa2_kv_append;  kv: 16-byte aligned, apart from all that
+ *   the call reads
  * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (rot != 64), CSA2_ERR_CUDA. */
 csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n, int64_t x_stride,
                                const uint16_t* norm_w, float eps, const int32_t* pos, const int64_t* dst_rows,
@@ -505,7 +505,8 @@ csa2_status csa2_window_append(const csa2_rope* r, const uint16_t* x, int64_t n,
  *   norm_w, norm_b: device, of x's type and channels, 16-byte aligned; norm_w NULL without a norm,
  *     norm_b with CSA2_IDX_NORM_LAYER only, or NULL
  *   eps: 2^-40 .. 1 with a norm;  pos: device int32 [n];  dst_rows: device int64 [n], as above
- *   idx_k, cache_rows: the indexer-K buffer (16-byte aligned) and its rows, no part of it within x
+ *   idx_k, cache_rows: the indexer-K buffer (16-byte aligned) and its rows, apart from all that the
+ *     call reads
  * Errors: CSA2_ERR_INVALID_ARG, CSA2_ERR_UNSUPPORTED_SHAPE (offset, rot), CSA2_ERR_CUDA. */
 typedef enum { CSA2_IDX_NORM_NONE = 0, CSA2_IDX_NORM_RMS = 1, CSA2_IDX_NORM_LAYER = 2 } csa2_idx_norm;
 csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const void* x, int64_t n, int64_t x_stride,
@@ -527,8 +528,8 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
  * the entries of pages that a new token sees a position of are read: it may hold anything elsewhere,
  * and pages may come round (a ring).  Rows that no new token sees may hold anything.
  *   Dimensions read: heads, max_ctx, max_pages, num_pages (the window cache's own).
- *   q, q_start, ctx_len, out, lse: as csa2_dense_attn_chunk, out and lse apart from q, kv, ws and
- *              each other
+ *   q, q_start, ctx_len, out, lse: as csa2_dense_attn_chunk; out, lse and ws apart from each other
+ *              and from all that the call reads (but prev_out, prev_lse: below)
  *   kv:        device bf16 [rows][576], 16-byte aligned; rows and page_table as elsewhere (rows =
  *              batch * max_ctx, or num_pages * 64).  A position whose page id is out of range is
  *              skipped and reported.
