@@ -28,7 +28,8 @@ class ExactRows:
     dst_rows: torch.Tensor          # int64 [total] its rows for the new tokens (cache_rows)
     window: int                     # positions that a token sees, its own among them
     sinks: int = 0                  # first positions that stay visible
-    dims: csa2.Dims | None = None   # of this cache (heads, max_ctx, pages); None: the chunk's
+    # of this cache (heads, max_ctx, pages); None: the chunk's, and its page table where none is given here
+    dims: csa2.Dims | None = None
     page_table: torch.Tensor | None = None
     # the same rows for a decode step's window, in place (window_rows); both or neither
     swa: torch.Tensor | None = None          # bf16 [B, W, 576]
@@ -150,6 +151,7 @@ def run_chunk(cb: ChunkBuffers, stream=None):
     csa2.csa2_dense_attn_chunk(cb.dims, cb.batch, cb.q, cb.q_start, cb.kv_codes, cb.kv_scales, cb.kv_rope, cb.page_table,
                                cb.ctx_len, cb.scale, cb.out, cb.lse, cb.ws, window=cb.window, stream=stream)
     if ex is not None:                               # joined in place
-        csa2.csa2_window_attn_chunk(ex.dims or cb.dims, cb.batch, cb.q, cb.q_start, ex.kv, ex.page_table, cb.ctx_len, cb.scale,
+        table = cb.page_table if ex.dims is None and ex.page_table is None else ex.page_table
+        csa2.csa2_window_attn_chunk(ex.dims or cb.dims, cb.batch, cb.q, cb.q_start, ex.kv, table, cb.ctx_len, cb.scale,
                                     ex.window, cb.out, cb.lse, ex.ws, sinks=ex.sinks, prev_out=cb.out, prev_lse=cb.lse,
                                     stream=stream)
