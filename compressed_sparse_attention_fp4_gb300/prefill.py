@@ -35,6 +35,10 @@ class ExactRows:
     swa: torch.Tensor | None = None          # bf16 [B, W, 576]
     swa_rows: torch.Tensor | None = None     # int64 [total]
     ws: torch.Tensor = None
+    # positions after which the pages of a sequence come round, whole pages (0: they do not).  All rows of a chunk are
+    # written before its attention, so a ring holds what its first token sees and all new tokens: run_chunk
+    # refuses a chunk of more than ring - window + 1 tokens of a sequence.
+    ring: int = 0
 
 
 @dataclass
@@ -82,6 +86,7 @@ class ChunkBuffers:
     # what else the layer has
     exact: ExactRows | None = None
     keys: IndexerKeys | None = None
+    longest: int = 0                     # most new tokens of a sequence (0: they may all be one's); for rings of pages
 
     def allocate_outputs(self):
         total, h, dev = self.q.shape[0], self.dims.heads, self.q.device
@@ -137,6 +142,8 @@ def run_chunk(cb: ChunkBuffers, stream=None):
     """Enqueue the chunk: three library calls in order on one stream, up to four more for `exact` and `keys`."""
     ex, keys = cb.exact, cb.keys
     csa2._need("run_chunk", ex is None or (ex.swa is None) == (ex.swa_rows is None))
+    if ex is not None and ex.ring != 0:
+        csa2._need("run_chunk", ex.ring > 0 and ex.ring % csa2.PAGE == 0 and (cb.longest or cb.q.shape[0]) + ex.window - 1 <= ex.ring)
     csa2.csa2_rope_apply(cb.rope, cb.q, cb.pos, y=cb.q, offset=csa2.LATENT, stream=stream)
     if ex is not None:
         csa2.csa2_window_append(cb.rope, cb.x, cb.pos, ex.dst_rows, ex.kv, norm_w=cb.norm_w, eps=cb.eps, stream=stream)

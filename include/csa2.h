@@ -526,7 +526,9 @@ csa2_status csa2_idx_k_append(const csa2_rope* r, int32_t idx_k_dtype, const voi
  *   lse = ln(e^lse_own + e^prev_lse),  out = e^(lse_own - lse) out_own + e^(prev_lse - lse) prev_out.
  * The new tokens' own rows have been written before (csa2_window_append).  Of the page table only
  * the entries of pages that a new token sees a position of are read: it may hold anything elsewhere,
- * and pages may come round (a ring).  Rows that no new token sees may hold anything.
+ * and pages may come round (a ring, of at least window + n - 1 positions for n new tokens of a
+ * sequence: their rows have all been written, the first token's window stands beside them; pages of
+ * sinks stay).  Rows that no new token sees may hold anything.
  *   Dimensions read: heads, max_ctx, max_pages, num_pages (the window cache's own).
  *   q, q_start, ctx_len, out, lse: as csa2_dense_attn_chunk; out, lse and ws apart from each other
  *              and from all that the call reads (but prev_out, prev_lse: below)

@@ -55,3 +55,30 @@ def test_a_cache_without_pages(pre):
     cb = chunk(pre, pre.ExactRows(e, e, 128))
     pre.run_chunk(cb)
     assert attention(pre) == (cb.dims, None)
+
+
+@pytest.mark.parametrize("window,ring,tokens,longest,fits", [
+    (128, 128, 1, 0, True), (128, 128, 2, 0, False), (128, 192, 65, 0, True), (128, 192, 66, 0, False), (1, 64, 64, 0, True),
+    (1, 64, 65, 0, False), (100, 192, 500, 93, True), (100, 192, 500, 94, False), (128, 6 * 64, 256, 256, True), (128, 0, 5000, 0, True),
+    (128, 200, 4, 0, False), (128, -64, 4, 0, False)])
+def test_a_chunk_that_its_ring_does_not_hold_is_refused(pre, window, ring, tokens, longest, fits):
+    """Before anything is enqueued: its first tokens would read rows that its last ones have taken."""
+    from compressed_sparse_attention_fp4_gb300 import csa2
+    e = torch.empty(0)
+    cb = chunk(pre, pre.ExactRows(e, e, window, ring=ring), tokens=tokens, longest=longest, batch=8 if longest else 1)
+    if fits:
+        pre.run_chunk(cb)
+        assert "csa2_window_attn_chunk" in [c[0] for c in pre.calls]
+    else:
+        with pytest.raises(csa2.Csa2Error, match="run_chunk"):
+            pre.run_chunk(cb)
+        assert not pre.calls
+
+
+@pytest.mark.parametrize("window,ring", [(1, 64), (37, 128), (128, 192)])
+def test_the_longest_chunk_of_a_ring_is_just_that(window, ring):
+    """Positions that the chunk writes and those that its tokens see keep places of their own up to it, and not beyond."""
+    for n, fits in ((ring - window + 1, True), (ring - window + 2, False)):
+        c = 1000
+        live = set(range(c - n - window + 1, c))              # seen by some new token, or new
+        assert (len({t % ring for t in live}) == len(live)) == fits
