@@ -22,11 +22,15 @@
 // each, one that plans.  They meet at mbarriers, group by group, so that the next tile's queries and rows come
 // while this one's outputs are formed.
 //
+// P is rounded to bf16, as a product's operands have one type and the rows are bf16: outputs are off by 1.8-2.0e-3
+// relative against 64 bits, of which their own rounding to bf16 is 1.65e-3.  (P in two parts would take the second products
+// twice: 1,900 cycles more in the chain below.)  The largest weight of a row is 1, which bf16 holds exactly.
+//
 // What bounds it: the chain of a tile, about 8,000 cycles: scores 3,000 (2,100 of products at the rate at which
 // shared memory feeds 64 columns, 5/6 of its bandwidth), softmax 2,200, outputs 1,900, and the hand-overs
-// between.  Measured (GB300, 64 heads): whole prompts of 8,872 tokens, window 128, 257 us (0.72 of the copy rate
-// on queries and outputs); 64 decode tokens joined with another attention 12.0 us, one token 9.4-10 us (launch,
-// plan, copies, products, outputs one after the other); 8 tokens over 2,048 positions 18.7 us.
+// between.  Measured (GB300, 64 heads): whole prompts of 8,872 tokens, window 128, 260 us (0.71 of the copy rate
+// on queries and outputs); 64 decode tokens joined with another attention 11.9 us, one token 9.4-10 us (launch,
+// plan, copies, products, outputs one after the other); 8 tokens over 2,048 positions 18.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1141,7 +1145,7 @@ bool window_maps(const void* q, uint64_t q_rows, const void* kv, uint64_t kv_row
 bool window_is_long(const WindowArgs& a, int span) {
   const int64_t rows = int64_t(a.total_q) * a.d.heads, see = int64_t(a.window) + a.sinks;
   if (a.prev_out && see < 200) return false;
-  return see + span - 1 > kWinPos && rows >= int64_t(kLongRows) * a.batch && (rows > 152 * kWinRows || (rows >= 4096 && see >= 512));
+  return see + span - 1 > kWinPos && rows >= int64_t(kLongRows) * a.batch && (rows > int64_t(device_sms()) * kWinRows || (rows >= 4096 && see >= 512));
 }
 
 }  // namespace
