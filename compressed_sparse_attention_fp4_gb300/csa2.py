@@ -127,7 +127,7 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream=None) -> int:
-    if stream is None:
+    if stream is None:                                # (torch.cuda.current_stream() takes 2.9 us of host time, this 0.2)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 

@@ -23,11 +23,14 @@
 // scores are no numbers are passed on with P, and the values CTAs make zeros of those whose values are
 // not either (0 * P would be NaN in rows that do not see them); rows that do see them become NaN by their sums.
 //
-// Measured (GB300, 64 heads): 2,048 tokens at 32,768, window 2,048, 4 sinks 400-413 us, 1.4-1.5 PFLOP/s on what
-// the rows see (window.cu's tiles: 705), bound by the tensor cores: a block takes 1,130-1,170 cycles of the 1,152
-// of its scores; of a tile's 35 blocks four or five are half masked; a tile's queries (147 KB a CTA) leave a gap
-// of about 3,300 cycles between its products and those of the tile before; and 512 tiles are 15 rounds of the 36
-// clusters that fit.  Two slots of P in place of three: 524 us, two score buffers: 407.
+// P is rounded to bf16, as the rows are (window.cu): in two parts it would take 2,048 cycles of values a block.
+//
+// Measured (GB300, 64 heads): 2,048 tokens at 32,768, window 2,048, 4 sinks 384-415 us (the clock gives way to power
+// within a second), 1.4-1.5 PFLOP/s on what the rows see (window.cu's tiles: 705), bound by the tensor cores: a block takes
+// 1,280-1,340 cycles for the 1,152 of its scores (one more block a tile costs 0.66-0.69 us in 15 rounds of tiles,
+// windows of 2,048 to 8,192 positions, at 1.85-1.94 GHz); of a tile's 35 blocks four or five are half masked; a tile's
+// queries (147 KB a CTA) leave a gap of 3,000 to 4,000 cycles between its products and those of the tile before; and 512
+// tiles are 15 rounds of the 36 clusters that fit.  Two slots of P in place of three: 524 us, two score buffers: 407.
 #include <cuda.h>
 
 #include <atomic>

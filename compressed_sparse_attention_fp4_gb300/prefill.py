@@ -139,7 +139,10 @@ def window_rows(ctx_len, q_start, window: int, total: int | None = None):
 
 
 def run_chunk(cb: ChunkBuffers, stream=None):
-    """Enqueue the chunk: three library calls in order on one stream, up to four more for `exact` and `keys`."""
+    """Enqueue the chunk: three library calls in order on one stream, up to four more for `exact` and `keys`.
+
+    With `exact` the dense attention's outputs pass through bf16 on their way into the joined ones: those are rounded
+    once more than a decode step's, which joins in fp32 (by 2^-8 of the dense part)."""
     ex, keys = cb.exact, cb.keys
     csa2._need("run_chunk", ex is None or (ex.swa is None) == (ex.swa_rows is None))
     if ex is not None and ex.ring != 0:

@@ -457,7 +457,9 @@ csa2_status csa2_kv_append(const csa2_rope* r, const uint16_t* x, int64_t n, int
  *             time need a workspace each.
  *   P is rounded to fp16 (2^-11) and the output to bf16; everything between is fp32.
  *   The product of a row of q, scaled by the power of two that brings its largest value
- *   to 2^14, with a key has to stay within fp32 (rope keys below 2^100 do).
+ *   to 2^14, with a key has to stay within fp32 (rope keys below 2^100 do), and logits of
+ *   positions that a token sees within 2^23: the softmax reference is a rounded logit, and from
+ *   there on its rounding passes a weight's range (out and lse may then be no numbers).
  * A CSA2 layer with a window (dims.swa > 0) joins the FP4 entries with exact bf16 rows in
  * one softmax (csa2_sparse_attn_decode).  This call reads FP4 rows alone, as that one does
  * with swa 0 and every position in its Top-K set; csa2_window_attn_chunk adds the exact rows
